@@ -1,6 +1,6 @@
 """What the 8-bit row operators are measured on: norm, gated activation, cache store and read, product.
 
-The operators (``include/xsymv.h``, the x*q8 entry points) keep a row of n numbers as n signed
+The operators (``include/xsymv.h``, the xsymv_q8 entry points) keep a row of n numbers as n signed
 8-bit codes and one 32-bit scale: with a = max(max_j |v_j|, 2^-100),
 
     code_j = round_half_even(v_j * (127 / a)),   scale = a / 127,   value_j = code_j * scale.
@@ -196,25 +196,25 @@ def _own(s):
     t = LETTER[s["type"]]
     if op == "gemm":
         a, w, c = s["a"], s["wt"], s["c"]
-        getattr(X, "xgemmq8_" + t)(m, n, s["k"], a, a.stride(0), s["sa"], w, w.stride(0), s["sw"], s["bias"], c, n)
+        getattr(X, "xsymv_q8gemm_" + t)(m, n, s["k"], a, a.stride(0), s["sa"], w, w.stride(0), s["sw"], s["bias"], c, n)
         return {"c": c}
     v = s["values"]
-    read = getattr(X, "xreadq8_" + LETTER[s["vtype"]])
+    read = getattr(X, "xsymv_q8read_" + LETTER[s["vtype"]])
     if op in ("store", "read"):
         if op == "store":
             x = s["x"]
-            getattr(X, "xstoreq8_" + t)(m, n, x, x.stride(0), s["slot"], s["cap"], s["cache"], n, s["cscale"])
+            getattr(X, "xsymv_q8store_" + t)(m, n, x, x.stride(0), s["slot"], s["cap"], s["cache"], n, s["cscale"])
         read(m, n, s["cache"], s["cache"].stride(0), s["cscale"], s["slot"], s["cap"], v, n)
         return {"values": v}
     q, scale = s["q"], s["scale"]
     if op == "norm":
         x, r, h = s["x"], s["r"], s["h"]
-        getattr(X, "xnormq8_" + t)(m, n, x, x.stride(0), LETTER[s["res"]], r, r.stride(0), t, s["w"], EPS,
+        getattr(X, "xsymv_q8norm_" + t)(m, n, x, x.stride(0), LETTER[s["res"]], r, r.stride(0), t, s["w"], EPS,
                                    h, n, q, n, scale)
         read(m, n, q, n, scale, None, m, v, n)
         return {"h": h, "values": v, "scale": scale}
     g, u = s["g"], s["u"]
-    getattr(X, "xgluq8_" + t)(m, n, g, g.stride(0), u, u.stride(0), q, n, scale)
+    getattr(X, "xsymv_q8glu_" + t)(m, n, g, g.stride(0), u, u.stride(0), q, n, scale)
     read(m, n, q, n, scale, None, m, v, n)
     return {"values": v, "scale": scale}
 
