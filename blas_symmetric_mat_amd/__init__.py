@@ -32,7 +32,12 @@ __all__ = ["xsymv_s", "xsymv_d", "xhemv_c", "xhemv_z", "xsymv_w", "XsymvError",
            "trmv_workspace_bytes", "xsymv_shard_s", "xsymv_shard_d", "xhemv_shard_c",
            "xhemv_shard_z", "xsymv_shard_w", "xsymv_combine_s", "xsymv_combine_d",
            "xhemv_combine_c", "xhemv_combine_z", "xsymv_combine_w", "shard_columns", "shard_plan",
-           "shard_workspace_bytes", "copy_bandwidth", "xsymv_s_noalloc", "STATIC_SCRATCH_BYTES"]
+           "shard_workspace_bytes", "copy_bandwidth", "xsymv_s_noalloc", "STATIC_SCRATCH_BYTES",
+           "xsymv_q8norm_s", "xsymv_q8norm_h", "xsymv_q8norm_b",
+           "xsymv_q8glu_s", "xsymv_q8glu_h", "xsymv_q8glu_b",
+           "xsymv_q8store_s", "xsymv_q8store_h", "xsymv_q8store_b",
+           "xsymv_q8read_s", "xsymv_q8read_h", "xsymv_q8read_b",
+           "xsymv_q8gemm_s", "xsymv_q8gemm_h", "xsymv_q8gemm_b"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libxsymv.so")
 PREC_CODE = {"s": 0, "d": 1, "c": 2, "z": 3, "w": 4}
@@ -204,6 +209,17 @@ def library():
             lib.xgemv_workspace_bytes.argtypes = [ci, cc, ci, ci]
             lib.xgemv_plan.restype = ci
             lib.xgemv_plan.argtypes = [ci, ci, ci, ci, ip, ci, ip, ci]
+            cf = ctypes.c_float
+            for t in "shb":
+                for nm, args in (("norm", [ci, ci, vp, ci, cc, vp, ci, cc, vp, cf, vp, ci, vp, ci,
+                                           vp, vp]),
+                                 ("glu", [ci, ci, vp, ci, vp, ci, vp, ci, vp, vp]),
+                                 ("store", [ci, ci, vp, ci, vp, ci, vp, ci, vp, vp]),
+                                 ("read", [ci, ci, vp, ci, vp, vp, ci, vp, ci, vp]),
+                                 ("gemm", [ci, ci, ci, vp, ci, vp, vp, ci, vp, vp, vp, ci, vp])):
+                    f = getattr(lib, f"xsymv_q8{nm}_{t}")
+                    f.restype = ci
+                    f.argtypes = args
             lib.xsymv_read_bandwidth.restype = ci
             lib.xsymv_read_bandwidth.argtypes = [ctypes.c_size_t, ci, vp, fp, fp]
             lib.xsymv_copy_bandwidth.restype = ci
@@ -457,6 +473,114 @@ def xhemv_combine_z(n, nshards, alpha, P, ldp, beta, y, incy, stream=None):
 def xsymv_combine_w(n, nshards, alpha, P, ldp, beta, y, incy, stream=None):
     """double-double; alpha, beta are (hi, lo) tuples."""
     _cbcall("w", n, nshards, alpha, P, ldp, beta, y, incy, stream)
+
+
+def _q8call(name, *args):
+    rc = getattr(library(), name)(*args)
+    if rc != 0:
+        raise XsymvError(name, rc)
+
+
+def xsymv_q8norm_s(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
+    """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
+    scales; x float32, r and h of letter rtype, w of letter wtype ('s'); r, h may be None."""
+    _q8call("xsymv_q8norm_s", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
+            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+
+
+def xsymv_q8norm_h(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
+    """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
+    scales; x float16, r and h of letter rtype, w of letter wtype ('h' or 's'); r, h may be None."""
+    _q8call("xsymv_q8norm_h", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
+            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+
+
+def xsymv_q8norm_b(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
+    """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
+    scales; x bfloat16, r and h of letter rtype, w of letter wtype ('b' or 's'); r, h may be None."""
+    _q8call("xsymv_q8norm_b", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
+            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+
+
+def xsymv_q8glu_s(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
+    """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u float32."""
+    _q8call("xsymv_q8glu_s", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8glu_h(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
+    """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u float16."""
+    _q8call("xsymv_q8glu_h", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8glu_b(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
+    """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u bfloat16."""
+    _q8call("xsymv_q8glu_b", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8store_s(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
+    """Row i of x (float32) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
+    (slot None: row i; a slot outside the cache leaves the row out)."""
+    _q8call("xsymv_q8store_s", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8store_h(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
+    """Row i of x (float16) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
+    (slot None: row i; a slot outside the cache leaves the row out)."""
+    _q8call("xsymv_q8store_h", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8store_b(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
+    """Row i of x (bfloat16) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
+    (slot None: row i; a slot outside the cache leaves the row out)."""
+    _q8call("xsymv_q8store_b", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
+            _stream(stream))
+
+
+def xsymv_q8read_s(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
+    """out row i (float32) := the values of row slot[i] of a cache of cap rows (slot None: row i;
+    zeros for a slot outside the cache)."""
+    _q8call("xsymv_q8read_s", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
+            _stream(stream))
+
+
+def xsymv_q8read_h(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
+    """out row i (float16) := the values of row slot[i] of a cache of cap rows (slot None: row i;
+    zeros for a slot outside the cache)."""
+    _q8call("xsymv_q8read_h", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
+            _stream(stream))
+
+
+def xsymv_q8read_b(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
+    """out row i (bfloat16) := the values of row slot[i] of a cache of cap rows (slot None: row i;
+    zeros for a slot outside the cache)."""
+    _q8call("xsymv_q8read_b", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
+            _stream(stream))
+
+
+def xsymv_q8gemm_s(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
+    """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], float32; A, W 8-bit codes in
+    rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
+    _q8call("xsymv_q8gemm_s", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
+            _addr(bias), _addr(C), ldc, _stream(stream))
+
+
+def xsymv_q8gemm_h(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
+    """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], float16; A, W 8-bit codes in
+    rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
+    _q8call("xsymv_q8gemm_h", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
+            _addr(bias), _addr(C), ldc, _stream(stream))
+
+
+def xsymv_q8gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
+    """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], bfloat16; A, W 8-bit codes in
+    rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
+    _q8call("xsymv_q8gemm_b", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
+            _addr(bias), _addr(C), ldc, _stream(stream))
 
 
 def shard_columns(n: int, panel: int, nshards: int, shard: int):

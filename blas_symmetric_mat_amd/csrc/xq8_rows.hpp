@@ -1,0 +1,397 @@
+// xq8_rows.hpp -- kernels on rows held in 8 bits: the norm with the
+// residual's addition, the gated activation, and a cache's store and read.
+//
+// A row of n numbers v_j is held as n signed codes and one 32-bit scale:
+//
+//   a = max(max_j |v_j|, 2^-100)
+//   code_j = round_half_even(v_j * (127 / a)),  scale = a / 127
+//   value_j = code_j * scale
+//
+// 2^-100 keeps 127 / a and a / 127 normal numbers for a row of zeros.  The
+// maximum is taken over the magnitudes' bit patterns as unsigned integers,
+// which orders them as numbers and puts infinities and NaN on top: a row that
+// holds one gets a scale that is not finite, codes of zero for its finite
+// elements, and so NaN for every value (as the formula in floating point has
+// it), and no other row is touched.
+//
+// Every kernel is one pass over memory: TPR threads share a row and keep it
+// in registers (J chunks of 8 elements each) between the row's sums and the
+// codes.  What bounds them is HBM; the arithmetic (in 32 bits, the norm's sum
+// of squares in 64) hides behind the loads.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace xsymv {
+
+using q8half = _Float16;
+using q8bf16 = __bf16;
+
+constexpr float Q8_FLOOR = 0x1p-100f;
+constexpr int Q8_CHUNK = 8;  // elements a thread takes at once: 16 bytes of a 16-bit type
+
+// ------------------------------------------------------------------ chunks
+// Chunks are read and written where they lie: gfx950 takes 16-byte global
+// accesses at any address, so odd strides cost partial lines but no other path.
+template <class T>
+__device__ __forceinline__ void q8_load(const T* p, int have, float (&v)[Q8_CHUNK])
+{
+    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK)));
+    if (have >= Q8_CHUNK) {
+        vec t;
+        __builtin_memcpy(&t, p, sizeof(T) * Q8_CHUNK);
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = (float)t[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = e < have ? (float)p[e] : 0.0f;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void q8_store(T* p, int have, const float (&v)[Q8_CHUNK])
+{
+    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK)));
+    if (have >= Q8_CHUNK) {
+        vec t;
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) t[e] = (T)v[e];
+        __builtin_memcpy(p, &t, sizeof(T) * Q8_CHUNK);
+    } else {
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e)
+            if (e < have) p[e] = (T)v[e];
+    }
+}
+
+// Codes of a chunk.  Adding 1.5 * 2^23 to |t| <= 128 leaves t rounded half to
+// even in the low bits, whose last byte is the code in two's complement.
+__device__ __forceinline__ void q8_store_codes(signed char* p, int have, const float (&v)[Q8_CHUNK],
+                                               float inv)
+{
+    unsigned b[Q8_CHUNK];
+#pragma unroll
+    for (int e = 0; e < Q8_CHUNK; ++e) b[e] = __float_as_uint(v[e] * inv + 12582912.0f);
+    if (have >= Q8_CHUNK) {
+        unsigned w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const unsigned lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
+            const unsigned hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000c0cu);
+            w[i] = lo | hi;
+        }
+        __builtin_memcpy(p, w, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e)
+            if (e < have) p[e] = (signed char)b[e];
+    }
+}
+
+// -------------------------------------------------------------- reductions
+// Over the TPR threads of a row: lane exchanges within a wave, then (TPR >
+// 64, the row is the workgroup's) the waves' results through LDS, read by all
+// in the same order.  The LDS words alternate between `par` 0 and 1 from one
+// row to the next, so one barrier per reduction suffices.
+template <int TPR>
+__device__ __forceinline__ unsigned q8_row_max(unsigned v, unsigned (&buf)[2][16], int par)
+{
+#pragma unroll
+    for (int s = (TPR < 64 ? TPR : 64) / 2; s > 0; s >>= 1) {
+        const unsigned o = __shfl_xor(v, s);
+        v = v > o ? v : o;
+    }
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) buf[par][threadIdx.x >> 6] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) {
+            const unsigned o = buf[par][i];
+            v = v > o ? v : o;
+        }
+    }
+    return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ double q8_row_sum(double v, double (&buf)[2][16], int par)
+{
+#pragma unroll
+    for (int s = (TPR < 64 ? TPR : 64) / 2; s > 0; s >>= 1) v += __shfl_xor(v, s);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) buf[par][threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = buf[par][0];
+#pragma unroll
+        for (int i = 1; i < TPR / 64; ++i) v += buf[par][i];
+    }
+    return v;
+}
+
+__device__ __forceinline__ unsigned q8_chunk_max(const float (&v)[Q8_CHUNK], unsigned m)
+{
+#pragma unroll
+    for (int e = 0; e < Q8_CHUNK; ++e) {
+        const unsigned b = __float_as_uint(v[e]) & 0x7fffffffu;
+        m = m > b ? m : b;
+    }
+    return m;
+}
+
+// --------------------------------------------------------------- operators
+// An operator gives: the row's destination (negative: the row is left out),
+// a chunk of it (`first`), and, for the norm, the chunk after the row's sum
+// of squares is known (`second`); `again` is `first` without its side effects.
+
+// h = x + r rounded to R's type (which is what is kept and what is
+// normalised), v = h / sqrt(mean(h^2) + eps) * w.  r may be null (h = x), h
+// may be null (not kept) or r itself: an element is read and written by the
+// same thread.  The sum of squares is taken in 64 bits, which a row of the
+// largest 32-bit numbers cannot overflow, and costs nothing beside the loads.
+template <class T, class R, class W>
+struct Q8Norm {
+    static constexpr bool NORM = true;
+    const T* x;
+    const R* r;
+    R* h;
+    const W* w;
+    long long ldx, ldr, ldh;
+    double eps;
+    int m, n;
+
+    __device__ __forceinline__ long long dest(long long row) const { return row; }
+    __device__ __forceinline__ void sum(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
+    {
+        q8_load(x + row * ldx + c, have, v);
+        if (r != nullptr) {
+            float t[Q8_CHUNK];
+            q8_load(r + row * ldr + c, have, t);
+#pragma unroll
+            for (int e = 0; e < Q8_CHUNK; ++e) v[e] += t[e];
+        }
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = (float)(R)v[e];
+    }
+    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
+                                          double& ss) const
+    {
+        sum(row, c, have, v);
+        if (h != nullptr) q8_store(h + row * ldh + c, have, v);
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
+    }
+    // a row too long for the registers: what was kept is read back (r may
+    // have been overwritten by it)
+    __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
+    {
+        if (h != nullptr)
+            q8_load(h + row * ldh + c, have, v);
+        else
+            sum(row, c, have, v);
+    }
+    __device__ __forceinline__ float factor(double ss) const
+    {
+        return (float)(1.0 / sqrt(ss / n + eps));
+    }
+    __device__ __forceinline__ void second(int c, int have, float (&v)[Q8_CHUNK], float f) const
+    {
+        float t[Q8_CHUNK];
+        q8_load(w + c, have, t);
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = v[e] * f * t[e];
+    }
+};
+
+// v = g / (1 + exp(-g)) * u.  With z = exp(-|g|), which neither overflows nor
+// loses small results, 1 / (1 + exp(-g)) is 1 / (1 + z) for g >= 0 and
+// z / (1 + z) below.  The hardware's 2^t and reciprocal (1 ulp each) serve:
+// the product |g| log2(e) is rounded, so z is off by up to |g| 2^-24, but
+// where |g| is large z is a small part of 1 + z (g > 0) or v is small beside
+// |g u| (g < 0): at most a few 2^-24 of a code's 127 steps.
+template <class T>
+struct Q8Glu {
+    static constexpr bool NORM = false;
+    const T* g;
+    const T* u;
+    long long ldg, ldu;
+    int m, n;
+
+    __device__ __forceinline__ long long dest(long long row) const { return row; }
+    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
+                                          double&) const
+    {
+        float t[Q8_CHUNK];
+        q8_load(g + row * ldg + c, have, v);
+        q8_load(u + row * ldu + c, have, t);
+#pragma unroll
+        for (int e = 0; e < Q8_CHUNK; ++e) {
+            const float z = __builtin_amdgcn_exp2f(-1.44269504f * __builtin_fabsf(v[e]));
+            const float s = (v[e] < 0.0f ? z : 1.0f) * __builtin_amdgcn_rcpf(1.0f + z);
+            v[e] = v[e] * s * t[e];
+        }
+    }
+    __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
+    {
+        double none = 0.0;
+        first(row, c, have, v, none);
+    }
+};
+
+// v = x's row, written to row slot[i] of the cache (i itself without slots);
+// a slot outside [0, cap) leaves the row out.
+template <class T>
+struct Q8Store {
+    static constexpr bool NORM = false;
+    const T* x;
+    const int* slot;
+    long long ldx;
+    int m, n, cap;
+
+    __device__ __forceinline__ long long dest(long long row) const
+    {
+        const int s = slot != nullptr ? slot[row] : row;
+        return s >= 0 && s < cap ? s : -1;
+    }
+    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
+                                          double&) const
+    {
+        q8_load(x + row * ldx + c, have, v);
+    }
+    __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
+    {
+        q8_load(x + row * ldx + c, have, v);
+    }
+};
+
+template <class OP>
+struct Q8RowArgs {
+    OP op;
+    signed char* q;
+    float* scale;
+    long long ldq;
+};
+
+// One row per TPR threads; a workgroup of max(256, TPR) threads.  J chunks
+// of the row in a thread's registers; J = 0: a row longer than 8 chunks of
+// 1024 threads, whose elements are formed again for each of its sums.
+template <class OP, int TPR, int J>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a)
+{
+    constexpr int THREADS = TPR > 256 ? TPR : 256;
+    constexpr int RPB = THREADS / TPR;  // rows per workgroup
+    __shared__ double sbuf[2][16];
+    __shared__ unsigned mbuf[2][16];
+    const OP& op = a.op;
+    const int n = op.n;
+    const int t = threadIdx.x % TPR;
+    int par = 0;
+    for (long long base = (long long)blockIdx.x * RPB; base < op.m;
+         base += (long long)gridDim.x * RPB) {
+        const long long row = base + threadIdx.x / TPR;
+        const long long dst = row < op.m ? op.dest(row) : -1;
+        if (TPR > 64 && dst < 0) continue;  // the whole workgroup's row
+        const int have = dst < 0 ? 0 : n;   // a row left out: its threads hold nothing
+        double ss = 0.0;
+        unsigned mx = 0;
+        if constexpr (J > 0) {
+            float v[J][Q8_CHUNK];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int c = (t + j * TPR) * Q8_CHUNK;
+                if (c < have) {
+                    op.first(row, c, have - c, v[j], ss);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < Q8_CHUNK; ++e) v[j][e] = 0.0f;
+                }
+            }
+            if constexpr (OP::NORM) {
+                const float f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int c = (t + j * TPR) * Q8_CHUNK;
+                    if (c < have) op.second(c, have - c, v[j], f);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) mx = q8_chunk_max(v[j], mx);
+            mx = q8_row_max<TPR>(mx, mbuf, par);
+            par ^= 1;
+            const float top = mx > __float_as_uint(Q8_FLOOR) ? __uint_as_float(mx) : Q8_FLOOR;
+            if (dst < 0) continue;
+            if (t == 0) a.scale[dst] = top / 127.0f;
+            const float inv = 127.0f / top;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int c = (t + j * TPR) * Q8_CHUNK;
+                if (c < n) q8_store_codes(a.q + dst * a.ldq + c, n - c, v[j], inv);
+            }
+        } else {
+            float f = 1.0f;
+            float v[Q8_CHUNK];
+            if constexpr (OP::NORM) {
+                for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK)
+                    op.first(row, (int)c, n - (int)c, v, ss);
+                f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
+            }
+            for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
+                op.again(row, (int)c, n - (int)c, v);
+                if constexpr (OP::NORM) op.second((int)c, n - (int)c, v, f);
+                mx = q8_chunk_max(v, mx);
+            }
+            mx = q8_row_max<TPR>(mx, mbuf, par);
+            par ^= 1;
+            const float top = mx > __float_as_uint(Q8_FLOOR) ? __uint_as_float(mx) : Q8_FLOOR;
+            if (t == 0) a.scale[dst] = top / 127.0f;
+            const float inv = 127.0f / top;
+            for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
+                op.again(row, (int)c, n - (int)c, v);
+                if constexpr (OP::NORM) op.second((int)c, n - (int)c, v, f);
+                q8_store_codes(a.q + dst * a.ldq + c, n - (int)c, v, inv);
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------------- read
+// out_i = code_j * scale of cache row slot[i] (i itself without slots); a
+// slot outside [0, cap) gives a row of zeros.
+template <class T>
+struct Q8ReadArgs {
+    const signed char* q;
+    const float* scale;
+    const int* slot;
+    T* out;
+    long long ldq, ldo;
+    int m, n, cap;
+};
+
+template <class T, int TPR>
+__global__ __launch_bounds__(256) void q8_read(Q8ReadArgs<T> a)
+{
+    constexpr int RPB = 256 / TPR;
+    const int t = threadIdx.x % TPR;
+    for (long long base = (long long)blockIdx.x * RPB; base < a.m;
+         base += (long long)gridDim.x * RPB) {
+        const long long row = base + threadIdx.x / TPR;
+        if (row >= a.m) break;
+        const int s = a.slot != nullptr ? a.slot[row] : (int)row;
+        const bool in = s >= 0 && s < a.cap;
+        const float f = in ? a.scale[s] : 0.0f;
+        for (long long c = (long long)t * Q8_CHUNK; c < a.n; c += TPR * Q8_CHUNK) {
+            const int have = a.n - (int)c;
+            float v[Q8_CHUNK];
+            if (in) {
+                q8_load(a.q + s * a.ldq + c, have, v);
+#pragma unroll
+                for (int e = 0; e < Q8_CHUNK; ++e) v[e] *= f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < Q8_CHUNK; ++e) v[e] = 0.0f;
+            }
+            q8_store(a.out + row * a.ldo + c, have, v);
+        }
+    }
+}
+
+}  // namespace xsymv

@@ -333,6 +333,99 @@ int xtrmv_select_config(int prec, int idx);
 int xtrmv_current_config(int prec, char uplo, char trans, int n);
 size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
 
+/* Operators on rows in 8 bits -- the integer side of a layer that serves a
+ * language model: rows are made by a norm, a gated activation or a cache's
+ * store, and read back or multiplied with rows of weights.  A row of n
+ * numbers v_j is held as n signed codes and one 32-bit scale:
+ *
+ *   a = max(max_j |v_j|, 2^-100)
+ *   code_j = round_half_even(v_j * (127 / a)),  scale = a / 127
+ *   value_j = code_j * scale
+ *
+ * A row that holds an infinity or a NaN gets a scale that is not finite and
+ * reads back as NaN throughout; other rows are not touched by it.
+ *
+ * Matrices are in ROW order, DEVICE pointers: element (i, j) at p[i*ld + j],
+ * ld >= max(1, row length), any alignment; elements past the row length are
+ * neither read nor written.  The letter of a call is the type of its rows:
+ * s float, h IEEE half, b bfloat16 (16-bit words); arithmetic and scales are
+ * in 32 bits, the norm's sum of squares in 64.  Calls are asynchronous on
+ * `stream`, need no workspace (the product apart), can be captured into a
+ * graph, and give the same bytes every time.  m == 0 or n == 0: nothing is
+ * done.  Codes are checked in the order of the arguments before any device work;
+ * pointers are only needed where there are rows.
+ *
+ *   xsymv_q8norm_*:  h = x + r (rounded to r's type), v = h / sqrt(mean(h^2)
+ *   + eps) * w, stored as codes q and scales (one a row).  rtype, wtype: the
+ *   letter of r and h, and of w (n elements): the call's own letter or 's'.
+ *   r NULL: no residual, h = x.  h NULL: not kept.  h may be r itself (with
+ *   ldh == ldr); nothing else may overlap an output.  Codes: -1 m < 0,
+ *   -2 n < 0, -3 x NULL, -4 ldx, -5 rtype, -7 ldr, -8 wtype, -9 w NULL,
+ *   -10 eps < 0 or not finite, -12 ldh, -13 q NULL, -14 ldq, -15 scale NULL.
+ *
+ *   xsymv_q8glu_*:  v = g / (1 + exp(-g)) * u, stored as codes q and scales.
+ *   g and u may be the halves of one matrix's rows.  Codes: -1 m, -2 n,
+ *   -3 g NULL, -4 ldg, -5 u NULL, -6 ldu, -7 q NULL, -8 ldq, -9 scale NULL.
+ *
+ *   xsymv_q8store_*:  row i of x is stored as row slot[i] of a cache of cap
+ *   rows of codes q and scales; a slot outside [0, cap) leaves its row out
+ *   (padding).  Slots that name a row twice leave it undefined.  slot NULL:
+ *   row i is stored as row i (cap >= m), which makes codes of any rows.
+ *   Codes: -1 m, -2 n, -3 x NULL, -4 ldx, -6 cap < 0 (or < m without slots),
+ *   -7 q NULL, -8 ldq, -9 scale NULL.
+ *
+ *   xsymv_q8read_*:  out row i = the values of row slot[i] of the cache, zeros
+ *   for a slot outside [0, cap); slot NULL: row i.  Codes: -1 m, -2 n,
+ *   -3 q NULL, -4 ldq, -5 scale NULL, -7 cap < 0 (or < m without slots),
+ *   -8 out NULL, -9 ldo.
+ *
+ *   xsymv_q8gemm_*:  C[i, j] = (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] +
+ *   bias[j], A m x k and W n x k codes, sa (m) and sw (n) scales, bias n
+ *   floats or NULL, C m x n of the call's type.  The sum is exact (32-bit
+ *   integers, k <= 131071); it, its products with the scales and the sum with
+ *   the bias round once each to 32 bits.  k == 0: C = bias or zeros.  Codes:
+ *   -1 m, -2 n, -3 k < 0 or > 131071, -4 A NULL, -5 lda, -6 sa NULL, -7 W
+ *   NULL, -8 ldw, -9 sw NULL, -11 C NULL, -12 ldc.
+ * All: 1000 + hipError_t. */
+typedef unsigned short xhalf;     /* IEEE half, its 16 bits */
+typedef unsigned short xbfloat16; /* bfloat16, its 16 bits */
+int xsymv_q8norm_s(int m, int n, const float *x, int ldx, char rtype, const void *r,
+                    int ldr, char wtype, const void *w, float eps, void *h, int ldh,
+                    signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8glu_s(int m, int n, const float *g, int ldg, const float *u, int ldu,
+                   signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8store_s(int m, int n, const float *x, int ldx, const int *slot, int cap,
+                     signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8read_s(int m, int n, const signed char *q, int ldq, const float *scale,
+                    const int *slot, int cap, float *out, int ldo, void *stream);
+int xsymv_q8gemm_s(int m, int n, int k, const signed char *a, int lda, const float *sa,
+                    const signed char *w, int ldw, const float *sw, const float *bias,
+                    float *c, int ldc, void *stream);
+int xsymv_q8norm_h(int m, int n, const xhalf *x, int ldx, char rtype, const void *r,
+                    int ldr, char wtype, const void *w, float eps, void *h, int ldh,
+                    signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8glu_h(int m, int n, const xhalf *g, int ldg, const xhalf *u, int ldu,
+                   signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8store_h(int m, int n, const xhalf *x, int ldx, const int *slot, int cap,
+                     signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8read_h(int m, int n, const signed char *q, int ldq, const float *scale,
+                    const int *slot, int cap, xhalf *out, int ldo, void *stream);
+int xsymv_q8gemm_h(int m, int n, int k, const signed char *a, int lda, const float *sa,
+                    const signed char *w, int ldw, const float *sw, const float *bias,
+                    xhalf *c, int ldc, void *stream);
+int xsymv_q8norm_b(int m, int n, const xbfloat16 *x, int ldx, char rtype, const void *r,
+                    int ldr, char wtype, const void *w, float eps, void *h, int ldh,
+                    signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8glu_b(int m, int n, const xbfloat16 *g, int ldg, const xbfloat16 *u, int ldu,
+                   signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8store_b(int m, int n, const xbfloat16 *x, int ldx, const int *slot, int cap,
+                     signed char *q, int ldq, float *scale, void *stream);
+int xsymv_q8read_b(int m, int n, const signed char *q, int ldq, const float *scale,
+                    const int *slot, int cap, xbfloat16 *out, int ldo, void *stream);
+int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const float *sa,
+                    const signed char *w, int ldw, const float *sw, const float *bias,
+                    xbfloat16 *c, int ldc, void *stream);
+
 /* Bytes of device workspace one call of precision `prec` and order n uses
  * with the configuration selected for it now, on the current device (0 for
  * n == 0; -1 cast to size_t for a bad precision code, or when the device
