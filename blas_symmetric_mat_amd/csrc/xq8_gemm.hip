@@ -15,6 +15,20 @@ int stream_launch(const Q8GemmArgs<T>& g, hipStream_t stream)
     return q8_launch(&q8_gemm_stream<T, MT, NT, WK>, (unsigned)blocks, 64 * WK, stream, g);
 }
 
+template <class T, int BM, int BN, int WM, int WN, bool DMA>
+int tile_launch(const Q8GemmArgs<T>& g, hipStream_t stream)
+{
+    const long long tiles = (((long long)g.m + BM - 1) / BM) * (((long long)g.n + BN - 1) / BN);
+    return q8_launch(&q8_gemm_tile<T, BM, BN, WM, WN, DMA>, (unsigned)tiles, 64 * WM * WN, stream,
+                     g);
+}
+
+// Rows at multiples of 16 bytes, and a tile's within 32-bit offsets.
+inline bool rows_aligned(const signed char* p, int ld)
+{
+    return reinterpret_cast<size_t>(p) % 16 == 0 && ld % 16 == 0 && ld <= 1 << 23;
+}
+
 template <class T>
 int gemm_run(int m, int n, int k, const signed char* a, int lda, const float* sa,
              const signed char* w, int ldw, const float* sw, const float* bias, T* c, int ldc,
@@ -36,7 +50,10 @@ int gemm_run(int m, int n, int k, const signed char* a, int lda, const float* sa
     const Q8GemmArgs<T> g{a, w, sa, sw, bias, c, lda, ldw, ldc, m, n, k};
     if (m <= 16) return stream_launch<T, 1, 1, 4>(g, stream);
     if (m <= 32) return stream_launch<T, 2, 1, 4>(g, stream);
-    return stream_launch<T, 4, 2, 4>(g, stream);
+    if (m <= 64) return stream_launch<T, 4, 2, 4>(g, stream);
+    if (rows_aligned(a, lda) && rows_aligned(w, ldw))
+        return tile_launch<T, 256, 256, 2, 4, true>(g, stream);
+    return tile_launch<T, 256, 128, 4, 2, false>(g, stream);
 }
 
 }  // namespace
