@@ -29,8 +29,8 @@ int rows_run(const Q8RowArgs<OP>& a, hipStream_t stream)
     if (chunks <= 128) return rows_launch<OP, 64, 2>(a, stream);
     if (chunks <= 256) return rows_launch<OP, 256, 1>(a, stream);
     if (chunks <= 512) return rows_launch<OP, 256, 2>(a, stream);
-    if (chunks <= 1024) return rows_launch<OP, 256, 4>(a, stream);
-    if (chunks <= 2048) return rows_launch<OP, 512, 4>(a, stream);
+    if (chunks <= 1024) return rows_launch<OP, 512, 2>(a, stream);
+    if (chunks <= 2048) return rows_launch<OP, 1024, 2>(a, stream);
     if (chunks <= 4096) return rows_launch<OP, 1024, 4>(a, stream);
     if (chunks <= 8192) return rows_launch<OP, 1024, 8>(a, stream);
     return rows_launch<OP, 1024, 0>(a, stream);

@@ -33,13 +33,18 @@ constexpr int Q8_CHUNK = 8;  // elements a thread takes at once: 16 bytes of a 1
 // ------------------------------------------------------------------ chunks
 // Chunks are read and written where they lie: gfx950 takes 16-byte global
 // accesses at any address, so odd strides cost partial lines but no other path.
-template <class T>
+// ONCE: the rows are not wanted in the caches after this (a non-temporal
+// access).
+template <bool ONCE = false, class T>
 __device__ __forceinline__ void q8_load(const T* p, int have, float (&v)[Q8_CHUNK])
 {
-    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK)));
+    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK), aligned(sizeof(T))));
     if (have >= Q8_CHUNK) {
         vec t;
-        __builtin_memcpy(&t, p, sizeof(T) * Q8_CHUNK);
+        if constexpr (ONCE)
+            t = __builtin_nontemporal_load((const vec*)p);
+        else
+            t = *(const vec*)p;
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e) v[e] = (float)t[e];
     } else {
@@ -48,15 +53,18 @@ __device__ __forceinline__ void q8_load(const T* p, int have, float (&v)[Q8_CHUN
     }
 }
 
-template <class T>
+template <bool ONCE = false, class T>
 __device__ __forceinline__ void q8_store(T* p, int have, const float (&v)[Q8_CHUNK])
 {
-    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK)));
+    typedef T vec __attribute__((ext_vector_type(Q8_CHUNK), aligned(sizeof(T))));
     if (have >= Q8_CHUNK) {
         vec t;
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e) t[e] = (T)v[e];
-        __builtin_memcpy(p, &t, sizeof(T) * Q8_CHUNK);
+        if constexpr (ONCE)
+            __builtin_nontemporal_store(t, (vec*)p);
+        else
+            *(vec*)p = t;
     } else {
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e)
@@ -221,8 +229,8 @@ struct Q8Glu {
                                           double&) const
     {
         float t[Q8_CHUNK];
-        q8_load(g + row * ldg + c, have, v);
-        q8_load(u + row * ldu + c, have, t);
+        q8_load<true>(g + row * ldg + c, have, v);
+        q8_load<true>(u + row * ldu + c, have, t);
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e) {
             const float z = __builtin_amdgcn_exp2f(-1.44269504f * __builtin_fabsf(v[e]));
@@ -288,9 +296,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
     for (long long base = (long long)blockIdx.x * RPB; base < op.m;
          base += (long long)gridDim.x * RPB) {
         const long long row = base + threadIdx.x / TPR;
-        const long long dst = row < op.m ? op.dest(row) : -1;
-        if (TPR > 64 && dst < 0) continue;  // the whole workgroup's row
-        const int have = dst < 0 ? 0 : n;   // a row left out: its threads hold nothing
+        const bool mine = row < op.m;
+        // (a row left out is formed all the same, so that its loads need not
+        // wait for the slot's)
+        const long long dst = mine ? op.dest(row) : -1;
+        const int have = mine ? n : 0;
         double ss = 0.0;
         unsigned mx = 0;
         if constexpr (J > 0) {
@@ -342,6 +352,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
             mx = q8_row_max<TPR>(mx, mbuf, par);
             par ^= 1;
             const float top = mx > __float_as_uint(Q8_FLOOR) ? __uint_as_float(mx) : Q8_FLOOR;
+            if (dst < 0) continue;
             if (t == 0) a.scale[dst] = top / 127.0f;
             const float inv = 127.0f / top;
             for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
@@ -389,7 +400,7 @@ __global__ __launch_bounds__(256) void q8_read(Q8ReadArgs<T> a)
 #pragma unroll
                 for (int e = 0; e < Q8_CHUNK; ++e) v[e] = 0.0f;
             }
-            q8_store(a.out + row * a.ldo + c, have, v);
+            q8_store<true>(a.out + row * a.ldo + c, have, v);
         }
     }
 }
