@@ -15,11 +15,11 @@ int stream_launch(const Q8GemmArgs<T>& g, hipStream_t stream)
     return q8_launch(&q8_gemm_stream<T, MT, NT, WK>, (unsigned)blocks, 64 * WK, stream, g);
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool DMA>
+template <class T, int BM, int BN, int WM, int WN, int S, int HOW>
 int tile_launch(const Q8GemmArgs<T>& g, hipStream_t stream)
 {
     const long long tiles = (((long long)g.m + BM - 1) / BM) * (((long long)g.n + BN - 1) / BN);
-    return q8_launch(&q8_gemm_tile<T, BM, BN, WM, WN, DMA>, (unsigned)tiles, 64 * WM * WN, stream,
+    return q8_launch(&q8_gemm_tile<T, BM, BN, WM, WN, S, HOW>, (unsigned)tiles, 64 * WM * WN, stream,
                      g);
 }
 
@@ -47,13 +47,13 @@ int gemm_run(int m, int n, int k, const signed char* a, int lda, const float* sa
     if (some && c == nullptr) return -11;
     if (ldc < std::max(1, n)) return -12;
     if (!some) return 0;
-    const Q8GemmArgs<T> g{a, w, sa, sw, bias, c, lda, ldw, ldc, m, n, k};
+    const Q8GemmArgs<T> g{a, w, sa, sw, bias, c, lda, ldw, ldc, m, n, k, nullptr, 1, 1 << 30};
     if (m <= 16) return stream_launch<T, 1, 1, 4>(g, stream);
     if (m <= 32) return stream_launch<T, 2, 1, 4>(g, stream);
     if (m <= 64) return stream_launch<T, 4, 2, 4>(g, stream);
     if (rows_aligned(a, lda) && rows_aligned(w, ldw))
-        return tile_launch<T, 256, 256, 2, 4, true>(g, stream);
-    return tile_launch<T, 256, 128, 4, 2, false>(g, stream);
+        return tile_launch<T, 256, 256, 2, 4, 2, Q8_LINES>(g, stream);
+    return tile_launch<T, 256, 128, 4, 2, 2, Q8_REGS>(g, stream);
 }
 
 }  // namespace

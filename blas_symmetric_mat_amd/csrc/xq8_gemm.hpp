@@ -42,7 +42,14 @@ struct Q8GemmArgs {
     T* c;
     long long lda, ldw, ldc;
     int m, n, k;
+    // k in `splits` shares of `per` steps of 128 bytes, their sums in `part`
+    // (one share: straight to C); the stream kernel takes k whole
+    int* part;
+    int splits, per;
 };
+
+// Row length of the shares' sums.
+__host__ __device__ inline long long q8_part_ld(int n) { return ((long long)n + 3) / 4 * 4; }
 
 // 16 bytes at p, of which `have` (any value) lie within the row; the bytes
 // past it are read from the row's last instead, and zeroed.
@@ -111,6 +118,22 @@ __device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
                     if (c + e < g.n) row[c + e] = t[e];
             }
         }
+    }
+}
+
+// The same results as a share's sums.
+template <class T, int FM, int FN>
+__device__ __forceinline__ void q8_partial(const Q8GemmArgs<T>& g, unsigned share, int i, int j,
+                                           const q8v4 (&sum)[FM][FN])
+{
+    const long long ldp = q8_part_ld(g.n);
+    int* sums = g.part + share * (g.m * ldp);
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+        if (i + 16 * f >= g.m) break;
+#pragma unroll
+        for (int h = 0; h < FN; ++h)
+            if (j + 16 * h < g.n) *(q8v4*)(sums + (i + 16 * f) * ldp + j + 16 * h) = sum[f][h];
     }
 }
 
@@ -196,31 +219,57 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_stream(Q8GemmArgs<T> g)
     }
 }
 
-// ------------------------------------------------------- many rows: tiles
+// ------------------------------------------------------------------- tiles
 // A workgroup of WM x WN waves makes a BM x BN tile of C, 128 bytes of k at a
-// time through LDS, where the tile's rows lie 128 bytes apart with their
-// eight 16-byte pieces permuted by the row (piece c at c ^ (row / 2) % 8), so
-// that the 16 rows a wave reads at once fall on different banks.  Two
-// buffers; one barrier per 128 bytes:
+// time through LDS, in S buffers, with one barrier per 128 bytes:
 //
-//   read the second half of step t     | multiply the first half
+//   multiply the first half of step t, reading the second meanwhile
 //   barrier: step t + 1 has arrived, and nobody reads step t's buffer again
-//   fetch step t + 2 into that buffer, read the first half of step t + 1
-//                                      | multiply the second half of step t
+//   multiply the second half, reading the first half of step t + 1 and
+//   fetching step t + S into the buffer meanwhile
 //
-// so the loads from memory have a whole step to arrive and the reads from LDS
-// half a step, behind the other half's multiplications.
+// so the loads from memory have S - 1 steps to arrive and the reads from LDS
+// half a step.  Loads and reads are issued between the multiplications, a few
+// at a time: issued together they hold up the wave's multiplications until
+// the memory pipeline has taken them all.
 //
-// DMA: the loads go from memory to LDS by themselves (rows at multiples of 16
-// bytes); the wait for them is the one before the barrier.  Otherwise they go
-// through registers, 16 bytes at any address, and are written to LDS before
-// the next barrier.  A k that is no multiple of 128 has its last, partial step
-// taken first, through registers in either case, its bytes past k being zeros.
+// How the rows come to LDS (HOW):
+//
+// Q8_LINES  rows at multiples of 16 bytes.  The loads go from memory to LDS by
+//           themselves, and the wait for them is the one before the barrier.
+//           A row's step is 128 bytes of LDS with its eight 16-byte pieces
+//           permuted (piece c at c ^ (row / 2) % 8), so that the 16 rows a
+//           wave reads at once fall on different banks.
+// Q8_ANY    rows at any stride, the first at a multiple of 16 bytes.  The same
+//           loads take the nine aligned pieces that hold a row's step, 144
+//           bytes of LDS (which spreads 16 rows over the banks as well), and
+//           the reads from LDS start at the byte where the row does.
+// Q8_REGS   anything else: through registers, 16 bytes at any address, written
+//           to LDS before the next barrier; S = 2.
+//
+// The bytes of k that no whole step covers are taken first, through registers
+// and with zeros past k.  With Q8_ANY the ninth piece of a step reaches up to
+// 16 bytes past it, so the last whole step ends 16 bytes or more before k, and
+// the rest, up to 143 bytes, takes one or two such steps.
+enum { Q8_REGS = 0, Q8_LINES = 1, Q8_ANY = 2 };
 
-// Waits for everything this wave has in flight, then for the other waves.
+// Whole steps of 128 bytes and steps in all.
+__host__ __device__ inline int q8_whole(int how, int k)
+{
+    return how != Q8_ANY ? k / 128 : k < 16 ? 0 : (k - 16) / 128;
+}
+__host__ __device__ inline int q8_steps(int how, int k)
+{
+    const int whole = q8_whole(how, k);
+    return whole + (k - whole * 128 + 127) / 128;
+}
+
+// Waits until at most N of this wave's loads are on their way and its reads
+// and writes of LDS are done, then for the other waves.
+template <int N>
 __device__ __forceinline__ void q8_sync()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // 16 bytes of each lane from rsrc's base + voff + soff to LDS address `lds`
@@ -242,151 +291,358 @@ __device__ __forceinline__ q8v4 q8_rsrc(const signed char* p, unsigned bytes)
                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// Work item `id` of `mt` x `nt` tiles: the chip's eight dies take workgroups
-// in turn and have a cache each, so a die gets a run of consecutive tiles,
-// and tiles are numbered in bands of 8 rows of tiles, column by column: the
-// 32 tiles a die works on at a time share 8 blocks of A and 4 of W.
-__device__ __forceinline__ void q8_tile(unsigned id, unsigned mt, unsigned nt, unsigned& ti,
-                                        unsigned& tj)
+// The tile (and share of k) of workgroup blockIdx.x: the chip's eight dies
+// take workgroups in turn and have a cache each, so a die gets a run of
+// consecutive tiles, and the tiles of a share are numbered in bands of 8 rows
+// of tiles, column by column: the 32 tiles a die works on at a time read 8
+// blocks of A and 4 of W.
+__device__ __forceinline__ void q8_tile(unsigned mt, unsigned nt, unsigned& ti, unsigned& tj,
+                                        unsigned& share)
 {
-    const unsigned total = mt * nt, die = id % 8, per = total / 8, more = total % 8;
-    const unsigned k = die * per + (die < more ? die : more) + id / 8;
+    const unsigned die = blockIdx.x % 8, per = gridDim.x / 8, more = gridDim.x % 8;
+    unsigned k = die * per + (die < more ? die : more) + blockIdx.x / 8;
+    share = k / (mt * nt);
+    k -= share * (mt * nt);
     const unsigned band = k / (8 * nt), rows = mt - 8 * band < 8 ? mt - 8 * band : 8;
     const unsigned in = k - band * 8 * nt;
     ti = 8 * band + in % rows;
     tj = in / rows;
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool DMA>
+template <class T, int BM, int BN, int WM, int WN, int S, int HOW>
 __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
 {
-    constexpr int BK = 128, WAVES = WM * WN;
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;    // 16 x 16 results of a wave
-    constexpr int LA = BM / 8 / WAVES, LW = BN / 8 / WAVES;  // 1 KB loads of a wave and step
-    constexpr int BUF = (BM + BN) * BK;
-    static_assert(LA * 8 * WAVES == BM && LW * 8 * WAVES == BN, "whole loads");
-    __shared__ __attribute__((aligned(1024))) signed char lds[2][BUF];
+    constexpr bool DMA = HOW != Q8_REGS;
+    constexpr int BK = 128, WAVES = WM * WN, PITCH = HOW == Q8_ANY ? 144 : 128, CH = PITCH / 16;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 results of a wave
+    constexpr int R = FM + FN;                           // reads of a wave and half step
+    // loads of 64 pieces, a wave each: A's, then W's (the last may reach past
+    // the block's rows), P to a wave (the last ones may be done twice)
+    constexpr int CA = (BM * CH + 63) / 64, CW = (BN * CH + 63) / 64;
+    constexpr int P = (CA + CW + WAVES - 1) / WAVES;
+    constexpr int BUF = (CA + CW) * 1024, OW = CA * 1024;
+    static_assert(DMA ? S >= 2 && (S - 1) * P < 64 : S == 2, "the counter of outstanding loads");
+    __shared__ __attribute__((aligned(1024))) signed char lds[S * BUF];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    unsigned ti, tj;
-    q8_tile(blockIdx.x, (g.m + BM - 1) / BM, (g.n + BN - 1) / BN, ti, tj);
+    unsigned ti, tj, share;
+    q8_tile((g.m + BM - 1) / BM, (g.n + BN - 1) / BN, ti, tj, share);
     const int i0 = ti * BM, j0 = tj * BN;
-    const int steps = (g.k + BK - 1) / BK, part = g.k % BK != 0;
+    // this share's steps: t0 and the `steps` - 1 after it; the first `odd` of
+    // all are the ones with zeros past k
+    const int whole = q8_whole(HOW, g.k), all = q8_steps(HOW, g.k), odd = all - whole;
+    const int t0 = (int)share * g.per;
+    const int steps = all - t0 < g.per ? all - t0 : g.per;
 
-    // loads: 8 rows of 128 bytes each, lane l row l / 8, its piece where the
-    // permutation puts it
-    const int lrow = wave * 8 + (lane >> 3);  // row of load 0; load i: + 8 * WAVES * i
-    const int lpiece = ((lane & 7) ^ ((lrow >> 1) & 7)) * 16;
     const signed char* ga = g.a + i0 * g.lda;
     const signed char* gw = g.w + j0 * g.ldw;
     const int ma = g.m - 1 - i0, mw = g.n - 1 - j0;  // last rows
-    // a tile's rows lie within 32-bit offsets where DMA is chosen
-    typename std::conditional<DMA, unsigned, long long>::type oa[LA], ow[LW];
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-        const int row = lrow + 8 * WAVES * i;
-        oa[i] = (row < ma ? row : ma) * g.lda + lpiece;
-    }
-#pragma unroll
-    for (int i = 0; i < LW; ++i) {
-        const int row = lrow + 8 * WAVES * i;
-        ow[i] = (row < mw ? row : mw) * g.ldw + lpiece;
-    }
-    const q8v4 ra = q8_rsrc(ga, 0xffffffffu), rw = q8_rsrc(gw, 0xffffffffu);
-    const unsigned base = (unsigned)(unsigned long long)(__attribute__((address_space(3))) void*)lds;
-    q8v4 st[DMA ? 1 : LA + LW];
-    int held = -1;  // the step whose bytes wait in st
+    const int sha = HOW == Q8_ANY ? (int)((size_t)ga & 15) : 0;
+    const int shw = HOW == Q8_ANY ? (int)((size_t)gw & 15) : 0;
+    const q8v4 ra = q8_rsrc(ga - sha, 0xffffffffu), rw = q8_rsrc(gw - shw, 0xffffffffu);
 
-    auto put = [&](int t) {  // registers to LDS
+    // a tile's rows lie within 32-bit offsets where the loads need them to
+    typename std::conditional<DMA, unsigned, long long>::type off[P];
+    auto load_id = [&](int p) {
+        const int id = p * WAVES + wave;
+        return (CA + CW) % WAVES == 0 || id < CA + CW ? id : CA + CW - 1;
+    };
+    auto of_w = [&](int p) { return CA % WAVES == 0 ? p >= CA / WAVES : load_id(p) >= CA; };
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const bool w = of_w(p);
+        const int piece = (load_id(p) - (w ? CA : 0)) * 64 + lane;
+        const int r = piece / CH, c = piece % CH, last = w ? mw : ma;
+        const long long o = (r < last ? r : last) * (w ? g.ldw : g.lda);
+        if constexpr (HOW == Q8_ANY)
+            off[p] = (unsigned)((o + (w ? shw : sha)) & ~15ll) + 16 * c;
+        else
+            off[p] = o + 16 * (c ^ ((r >> 1) & 7));
+    }
+    const unsigned base = (unsigned)(unsigned long long)(__attribute__((address_space(3))) void*)lds;
+    q8v4 st[DMA ? 1 : P];
+
+    auto fetch = [&](int t, int p) {  // load p of the share's step t, a whole one
+        const int k0 = (t0 + t - odd) * BK;
+        if constexpr (DMA)
+            q8_fetch(base + (unsigned)(t % S) * BUF + load_id(p) * 1024, off[p], of_w(p) ? rw : ra,
+                     k0);
+        else
+            __builtin_memcpy(&st[p], (of_w(p) ? gw : ga) + off[p] + k0, 16);
+    };
+    auto put = [&](int t) {  // the loads of step t, in registers, to LDS
         if constexpr (!DMA) {
-            if (held < 0) return;
 #pragma unroll
-            for (int i = 0; i < LA; ++i)
-                *(q8v4*)&lds[t & 1][(wave + WAVES * i) * 1024 + lane * 16] = st[i];
-#pragma unroll
-            for (int i = 0; i < LW; ++i)
-                *(q8v4*)&lds[t & 1][BM * BK + (wave + WAVES * i) * 1024 + lane * 16] = st[LA + i];
-            held = -1;
+            for (int p = 0; p < P; ++p)
+                *(q8v4*)&lds[(t % S) * BUF + load_id(p) * 1024 + lane * 16] = st[p];
         }
     };
-    // step t starts at byte (t - part) * BK of k; a partial step is taken first
-    auto fetch = [&](int t) {
-        if (t >= steps) return;
-        const int k0 = (t - part) * BK;
-        if constexpr (DMA) {
-            const unsigned to = base + (t & 1) * BUF + wave * 1024;
-#pragma unroll
-            for (int i = 0; i < LA; ++i) q8_fetch(to + WAVES * 1024 * i, oa[i], ra, k0);
-#pragma unroll
-            for (int i = 0; i < LW; ++i) q8_fetch(to + BM * BK + WAVES * 1024 * i, ow[i], rw, k0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < LA; ++i) __builtin_memcpy(&st[i], ga + oa[i] + k0, 16);
-#pragma unroll
-            for (int i = 0; i < LW; ++i) __builtin_memcpy(&st[LA + i], gw + ow[i] + k0, 16);
-            held = t;
+    auto rest = [&](int t) {  // the share's step t, one of the first `odd`
+        const int k0 = (whole + t0 + t) * BK;
+#pragma unroll 2
+        for (int e = threadIdx.x; e < (BM + BN) * 8; e += 64 * WAVES) {
+            const bool w = e >= BM * 8;
+            const int r = (e >> 3) - (w ? BM : 0), c = e & 7, last = w ? mw : ma;
+            const signed char* row = w ? gw + (r < last ? r : last) * g.ldw
+                                       : ga + (r < last ? r : last) * g.lda;
+            const int at = HOW == Q8_ANY ? 16 * c + (int)((size_t)(w ? gw + r * g.ldw : ga + r * g.lda) & 15)
+                                         : 16 * (c ^ ((r >> 1) & 7));
+            const q8v4 v = q8_load16(row + k0 + 16 * c, g.k - k0 - 16 * c);
+            __builtin_memcpy(&lds[(t % S) * BUF + (w ? OW : 0) + r * PITCH + at], &v, 16);
         }
     };
 
     // reads: lane l takes row l % 16 of a block of 16, piece 4 h + l / 16 of half h
-    const int wm = wave / WN, wn = wave % WN;
-    const int perm = (((lane >> 4) ^ ((lane >> 1) & 7)) * 16) + (lane & 15) * BK;
-    const int fa = wm * FM * 16 * BK, fw = BM * BK + wn * FN * 16 * BK;
+    const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, quad = lane >> 4;
+    const int fa = wm * FM * 16 * PITCH, fw = OW + wn * FN * 16 * PITCH;
+    const int pa = r16 * PITCH + (HOW == Q8_ANY ? quad * 16 + (int)((size_t)(ga + r16 * g.lda) & 15)
+                                                : (quad ^ ((r16 >> 1) & 7)) * 16);
+    const int pw = r16 * PITCH + (HOW == Q8_ANY ? quad * 16 + (int)((size_t)(gw + r16 * g.ldw) & 15)
+                                                : (quad ^ ((r16 >> 1) & 7)) * 16);
     q8v4 xa[2][FM], xw[2][FN], acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
-    auto read = [&](int t, int h) {
-        const signed char* p = &lds[t & 1][perm ^ (h * 64)];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) xw[h][j] = *(const q8v4*)(p + fw + j * 16 * BK);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) xa[h][i] = *(const q8v4*)(p + fa + i * 16 * BK);
+    auto read = [&](int t, int h, int q) {
+        const signed char* p = lds + (t % S) * BUF;
+        const int half = HOW == Q8_ANY ? (q < FN ? pw : pa) + h * 64 : pa ^ (h * 64);
+        q8v4& x = q < FN ? xw[h][q] : xa[h][q - FN];
+        p += half + (q < FN ? fw + q * 16 * PITCH : fa + (q - FN) * 16 * PITCH);
+        if constexpr (HOW == Q8_ANY)
+            __builtin_memcpy(&x, p, 16);
+        else
+            x = *(const q8v4*)p;
     };
-    auto multiply = [&](int h) {
+    auto multiply = [&](int h, int i) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] =
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[h][j], xa[h][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // a step, with another (NEXT) or S others (MORE) after it
+    auto step = [&](int t, auto next, auto more) {
+        constexpr bool NEXT = decltype(next)::value, MORE = decltype(more)::value;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[h][j], xa[h][i], acc[i][j], 0,
-                                                                  0, 0);
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int q = i * R / FM; q < (i + 1) * R / FM; ++q) read(t, 1, q);
+            multiply(0, i);
+        }
+        if constexpr (NEXT) {
+            put(t + 1);
+            if (DMA && (MORE || t + S == steps))
+                q8_sync<DMA ? (S - 2) * P : 0>();
+            else
+                q8_sync<0>();
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            if constexpr (NEXT) {
+#pragma unroll
+                for (int q = i * R / FM; q < (i + 1) * R / FM; ++q) read(t + 1, 0, q);
+            }
+            if constexpr (MORE) {
+#pragma unroll
+                for (int p = i * P / FM; p < (i + 1) * P / FM; ++p) fetch(t + S, p);
+            }
+            multiply(1, i);
+        }
     };
 
     if (steps > 0) {
-        if (part) {
-            const int k0 = g.k / BK * BK, have = g.k - k0 - lpiece;
 #pragma unroll
-            for (int i = 0; i < LA; ++i)
-                *(q8v4*)&lds[0][(wave + WAVES * i) * 1024 + lane * 16] =
-                    q8_load16(ga + oa[i] + k0, have);
+        for (int t = 0; t < S; ++t) {
+            if (t0 + t < odd) {
+                if (t < steps) rest(t);
+            } else if (t < steps) {
 #pragma unroll
-            for (int i = 0; i < LW; ++i)
-                *(q8v4*)&lds[0][BM * BK + (wave + WAVES * i) * 1024 + lane * 16] =
-                    q8_load16(gw + ow[i] + k0, have);
-        } else {
-            fetch(0);
-            put(0);
+                for (int p = 0; p < P; ++p) fetch(t, p);
+                if (t == 0) put(0);
+            }
         }
-        q8_sync();
-        fetch(1);
-        read(0, 0);
-        for (int t = 0; t < steps; ++t) {
-            read(t, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(0);
-            __builtin_amdgcn_sched_barrier(0);
-            put(t + 1);
-            q8_sync();
-            fetch(t + 2);
-            if (t + 1 < steps) read(t + 1, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(1);
-            __builtin_amdgcn_sched_barrier(0);
+        if (DMA && steps >= S)
+            q8_sync<DMA ? (S - 1) * P : 0>();
+        else
+            q8_sync<0>();
+#pragma unroll
+        for (int q = 0; q < R; ++q) read(0, 0, q);
+        int t = 0;
+        for (; t + S < steps; ++t) step(t, std::true_type{}, std::true_type{});
+        for (; t + 1 < steps; ++t) step(t, std::true_type{}, std::false_type{});
+        step(t, std::false_type{}, std::false_type{});
+    }
+    const int ci = i0 + wm * FM * 16 + r16, cj = j0 + wn * FN * 16 + quad * 4;
+    if (g.splits == 1)
+        q8_finish<T, FM, FN>(g, ci, cj, acc);
+    else
+        q8_partial<T, FM, FN>(g, share, ci, cj, acc);
+}
+
+// Adds the shares' sums, whole numbers, and finishes as the tiles do: a
+// thread four neighbouring elements of C.
+template <class T>
+__global__ __launch_bounds__(256) void q8_gemm_join(Q8GemmArgs<T> g)
+{
+    const long long ldp = q8_part_ld(g.n), quads = ldp / 4, total = g.m * quads;
+    for (long long q = blockIdx.x * 256ll + threadIdx.x; q < total; q += gridDim.x * 256ll) {
+        const long long i = q / quads;
+        const int j = (int)(q - i * quads) * 4;
+        q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
+#pragma unroll 4
+        for (int h = 0; h < g.splits; ++h)
+            sum[0][0] += *(const q8v4*)(g.part + h * (g.m * ldp) + i * ldp + j);
+        q8_finish<T, 1, 1>(g, (int)i, j, sum);
+    }
+}
+
+// ------------------------------------------- few rows, aligned: a ring a wave
+// The bytes of W bound the product, so what counts is loads in flight and
+// whole lines.  Every wave owns 16 NT columns of C (rows of W), a share of k
+// and a ring of S buffers in LDS, each one step of 128 bytes of its rows of W
+// and of the 16 MT rows of A (permuted as in the tiles); the loads go to LDS
+// by themselves, 8 whole lines each, S - 1 steps ahead of the step that is
+// multiplied.  No wave waits for another until the sums are added: the waves
+// of a workgroup share its columns and take the steps of k in turn.
+template <int N>
+__device__ __forceinline__ void q8_wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <class T, int MT, int NT, int WK, int S>
+__global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
+{
+    constexpr int BK = 128, LOADS = 2 * (MT + NT), SLOT = 16 * (MT + NT) * BK;
+    static_assert((S - 1) * LOADS < 64, "the counter of outstanding loads");
+    static_assert(S * SLOT >= MT * NT * 1024, "a wave's sums fit its ring");
+    __shared__ __attribute__((aligned(1024))) signed char lds[WK][S * SLOT];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unsigned ti, tj, share;
+    q8_tile((g.m + 16 * MT - 1) / (16 * MT), (g.n + 16 * NT - 1) / (16 * NT), ti, tj, share);
+    const int i0 = (int)ti * 16 * MT, j0 = (int)tj * 16 * NT;
+    // this share's whole steps, t0 and on; a partial one is the first share's
+    const int all = g.k / BK, t0 = (int)share * g.per;
+    const int steps = all - t0 < g.per ? all - t0 : g.per;
+    const int mine = (steps - wave + WK - 1) / WK;  // this wave's steps: wave, wave + WK, ...
+    // rows at a multiple of 4096 bytes lie on the same memory channels, column
+    // by column, so there each workgroup of a die starts at another step
+    const int turn =
+        g.ldw % 4096 == 0 && mine > 0 ? (int)((blockIdx.x / 8) % (unsigned)mine) : 0;
+    const signed char* ga = g.a + i0 * g.lda;
+    const signed char* gw = g.w + j0 * g.ldw;
+    const int ma = g.m - 1 - i0, mw = g.n - 1 - j0;
+
+    unsigned oa[2 * MT], ow[2 * NT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+        oa[i] = (unsigned)(row < ma ? row : ma) * (unsigned)g.lda + 16 * c;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+        const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+        ow[i] = (unsigned)(row < mw ? row : mw) * (unsigned)g.ldw + 16 * c;
+    }
+    const q8v4 ra = q8_rsrc(ga, 0xffffffffu), rw = q8_rsrc(gw, 0xffffffffu);
+    signed char* ring = lds[wave];
+    const unsigned base =
+        (unsigned)(unsigned long long)(__attribute__((address_space(3))) void*)ring;
+    auto fetch = [&](int t) {  // this wave's t-th step
+        int turned = t + turn;
+        turned -= turned >= mine ? mine : 0;
+        const unsigned to = base + (unsigned)(t % S) * SLOT;
+        const unsigned k0 = (unsigned)(t0 + turned * WK + wave) * BK;
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) q8_fetch(to + 1024 * i, ow[i], rw, k0);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) q8_fetch(to + 1024 * (2 * NT + i), oa[i], ra, k0);
+    };
+    for (int t = 0; t < S - 1 && t < mine; ++t) fetch(t);
+
+    q8v4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
+    const int r = lane & 15, piece = lane >> 4;
+    if (g.k % BK != 0 && share == 0 && wave == WK - 1) {
+        // the partial step, straight from memory to the multiplier's layout
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k0 = all * BK + 64 * h + 16 * piece, have = g.k - k0;
+            q8v4 xa[MT], xw[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                xw[j] = q8_load16(gw + (16 * j + r < mw ? 16 * j + r : mw) * g.ldw + k0, have);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                xa[i] = q8_load16(ga + (16 * i + r < ma ? 16 * i + r : ma) * g.lda + k0, have);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[j], xa[i], acc[i][j], 0, 0,
+                                                                      0);
         }
     }
-    q8_finish<T, FM, FN>(g, i0 + wm * FM * 16 + (lane & 15), j0 + wn * FN * 16 + (lane >> 4) * 4, acc);
+
+    const int perm = r * BK + ((piece ^ ((r >> 1) & 7)) * 16);
+    for (int t = 0; t < mine; ++t) {
+        if (t + S - 1 < mine) {
+            fetch(t + S - 1);  // into the buffer of step t - 1, which has been read
+            q8_wait_loads<(S - 1) * LOADS>();
+        } else {
+            q8_wait_loads<0>();
+        }
+        const signed char* p = ring + (t % S) * SLOT;
+        q8v4 xa[2][MT], xw[2][NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                xw[h][j] = *(const q8v4*)(p + (perm ^ (64 * h)) + 16 * BK * j);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                xa[h][i] = *(const q8v4*)(p + (perm ^ (64 * h)) + 16 * BK * (NT + i));
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[h][j], xa[h][i], acc[i][j],
+                                                                      0, 0, 0);
+    }
+    if constexpr (WK > 1) {
+        // the waves' sums, in their rings, which nothing is on its way to
+        q8v4* red = (q8v4*)ring;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) red[(i * NT + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        for (int tile = wave; tile < MT * NT; tile += WK) {
+            q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
+#pragma unroll
+            for (int w = 0; w < WK; ++w) sum[0][0] += ((const q8v4*)lds[w])[tile * 64 + lane];
+            const int ci = i0 + 16 * (tile / NT) + r, cj = j0 + 16 * (tile % NT) + 4 * piece;
+            if (g.splits == 1)
+                q8_finish<T, 1, 1>(g, ci, cj, sum);
+            else
+                q8_partial<T, 1, 1>(g, share, ci, cj, sum);
+        }
+    } else if (g.splits == 1) {
+        q8_finish<T, MT, NT>(g, i0 + r, j0 + 4 * piece, acc);
+    } else {
+        q8_partial<T, MT, NT>(g, share, i0 + r, j0 + 4 * piece, acc);
+    }
 }
 
 }  // namespace xsymv
