@@ -33,7 +33,7 @@ __all__ = ["xsymv_s", "xsymv_d", "xhemv_c", "xhemv_z", "xsymv_w", "XsymvError",
            "xhemv_shard_z", "xsymv_shard_w", "xsymv_combine_s", "xsymv_combine_d",
            "xhemv_combine_c", "xhemv_combine_z", "xsymv_combine_w", "shard_columns", "shard_plan",
            "shard_workspace_bytes", "copy_bandwidth", "xsymv_s_noalloc", "STATIC_SCRATCH_BYTES",
-           "xsymv_q8norm_s", "xsymv_q8norm_h", "xsymv_q8norm_b",
+           "q8gemm_workspace_bytes", "xsymv_q8norm_s", "xsymv_q8norm_h", "xsymv_q8norm_b",
            "xsymv_q8glu_s", "xsymv_q8glu_h", "xsymv_q8glu_b",
            "xsymv_q8store_s", "xsymv_q8store_h", "xsymv_q8store_b",
            "xsymv_q8read_s", "xsymv_q8read_h", "xsymv_q8read_b",
@@ -220,6 +220,8 @@ def library():
                     f = getattr(lib, f"xsymv_q8{nm}_{t}")
                     f.restype = ci
                     f.argtypes = args
+            lib.xsymv_q8gemm_workspace_bytes.restype = ctypes.c_size_t
+            lib.xsymv_q8gemm_workspace_bytes.argtypes = [ci, ci, ci]
             lib.xsymv_read_bandwidth.restype = ci
             lib.xsymv_read_bandwidth.argtypes = [ctypes.c_size_t, ci, vp, fp, fp]
             lib.xsymv_copy_bandwidth.restype = ci
@@ -583,6 +585,11 @@ def xsymv_q8gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
     rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
     _q8call("xsymv_q8gemm_b", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
             _addr(bias), _addr(C), ldc, _stream(stream))
+
+
+def q8gemm_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Device workspace bytes of one 8-bit product at most."""
+    return library().xsymv_q8gemm_workspace_bytes(m, n, k)
 
 
 def shard_columns(n: int, panel: int, nshards: int, shard: int):

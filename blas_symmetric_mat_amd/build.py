@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libxsymv.so")
 UNITS = ["xsymv_host", "xsymv_prec_s", "xsymv_prec_d", "xsymv_prec_c", "xsymv_prec_z",
-         "xsymv_prec_w", "xsymv_static", "xq8_rows", "xq8_gemm"]
+         "xsymv_prec_w", "xsymv_static", "xq8_rows", "xq8_gemm", "xq8_gemm_s", "xq8_gemm_h",
+         "xq8_gemm_b"]
 ARCH = os.environ.get("XSYMV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

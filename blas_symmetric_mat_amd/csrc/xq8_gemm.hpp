@@ -220,49 +220,44 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_stream(Q8GemmArgs<T> g)
 }
 
 // ------------------------------------------------------------------- tiles
-// A workgroup of WM x WN waves makes a BM x BN tile of C, 128 bytes of k at a
-// time through LDS, in S buffers, with one barrier per 128 bytes:
+// A workgroup of WM x WN waves makes a BM x BN tile of C, 128 Q bytes of k at
+// a time through LDS, in S buffers, with one barrier a step:
 //
-//   multiply the first half of step t, reading the second meanwhile
+//   multiply all but the last 64 bytes of step t, reading the next 64 meanwhile
 //   barrier: step t + 1 has arrived, and nobody reads step t's buffer again
-//   multiply the second half, reading the first half of step t + 1 and
-//   fetching step t + S into the buffer meanwhile
+//   multiply the last 64, reading the first 64 of step t + 1 and fetching
+//   step t + S into the buffer meanwhile
 //
 // so the loads from memory have S - 1 steps to arrive and the reads from LDS
-// half a step.  Loads and reads are issued between the multiplications, a few
-// at a time: issued together they hold up the wave's multiplications until
-// the memory pipeline has taken them all.
+// the time of a piece's multiplications.  Loads and reads are issued between
+// the multiplications, a few at a time: issued together they hold up the
+// wave's multiplications until the memory pipeline has taken them all.
 //
 // How the rows come to LDS (HOW):
 //
 // Q8_LINES  rows at multiples of 16 bytes.  The loads go from memory to LDS by
 //           themselves, and the wait for them is the one before the barrier.
-//           A row's step is 128 bytes of LDS with its eight 16-byte pieces
-//           permuted (piece c at c ^ (row / 2) % 8), so that the 16 rows a
-//           wave reads at once fall on different banks.
+//           A row's step is 128 Q bytes of LDS with its 16-byte pieces
+//           permuted by the row, so that the 16 rows a wave reads at once fall
+//           on different banks.
 // Q8_ANY    rows at any stride, the first at a multiple of 16 bytes.  The same
-//           loads take the nine aligned pieces that hold a row's step, 144
-//           bytes of LDS (which spreads 16 rows over the banks as well), and
-//           the reads from LDS start at the byte where the row does.
+//           loads take the 8 Q + 1 aligned pieces that hold a row's step (an
+//           odd number of pieces, which spreads the rows over the banks as
+//           well); the reads take the five words that hold a piece of the row,
+//           and its bytes are shifted out of them before they are multiplied.
+//           (LDS reads 16 bytes at once at any address, but several times
+//           slower.)  Memory delivers 64 bytes at a time, so a row's step that
+//           starts anywhere costs one delivery more: Q = 2 where LDS has room.
 // Q8_REGS   anything else: through registers, 16 bytes at any address, written
 //           to LDS before the next barrier; S = 2.
 //
-// The bytes of k that no whole step covers are taken first, through registers
-// and with zeros past k.  With Q8_ANY the ninth piece of a step reaches up to
-// 16 bytes past it, so the last whole step ends 16 bytes or more before k, and
-// the rest, up to 143 bytes, takes one or two such steps.
+// No load leaves the operands.  Where a step reaches past k, the loads take
+// what lies there, the row's gap or the next row, and the multiplier's first
+// half (A's bytes) is zeroed past k.  In the operand's last row a piece that
+// reaches past its end takes the last whole piece instead; if such a piece
+// still holds the row's last bytes, they are written over it one by one before
+// they are read (patch).
 enum { Q8_REGS = 0, Q8_LINES = 1, Q8_ANY = 2 };
-
-// Whole steps of 128 bytes and steps in all.
-__host__ __device__ inline int q8_whole(int how, int k)
-{
-    return how != Q8_ANY ? k / 128 : k < 16 ? 0 : (k - 16) / 128;
-}
-__host__ __device__ inline int q8_steps(int how, int k)
-{
-    const int whole = q8_whole(how, k);
-    return whole + (k - whole * 128 + 127) / 128;
-}
 
 // Waits until at most N of this wave's loads are on their way and its reads
 // and writes of LDS are done, then for the other waves.
@@ -274,7 +269,7 @@ __device__ __forceinline__ void q8_sync()
 
 // 16 bytes of each lane from rsrc's base + voff + soff to LDS address `lds`
 // plus 16 times the lane.  Nothing is returned; q8_sync waits for it.
-__device__ __forceinline__ void q8_fetch(unsigned lds, unsigned voff, q8v4 rsrc, unsigned soff)
+__device__ __forceinline__ void q8_fetch(unsigned lds, unsigned voff, q8v4 rsrc, unsigned soff = 0)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
@@ -309,13 +304,14 @@ __device__ __forceinline__ void q8_tile(unsigned mt, unsigned nt, unsigned& ti, 
     tj = in / rows;
 }
 
-template <class T, int BM, int BN, int WM, int WN, int S, int HOW>
+template <class T, int BM, int BN, int WM, int WN, int Q, int S, int HOW>
 __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
 {
     constexpr bool DMA = HOW != Q8_REGS;
-    constexpr int BK = 128, WAVES = WM * WN, PITCH = HOW == Q8_ANY ? 144 : 128, CH = PITCH / 16;
+    constexpr int BK = 128 * Q, WAVES = WM * WN, CH = 8 * Q + (HOW == Q8_ANY ? 1 : 0);
+    constexpr int PITCH = 16 * CH, H = 2 * Q;            // bytes of LDS a row, pieces of 64 a step
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 results of a wave
-    constexpr int R = FM + FN;                           // reads of a wave and half step
+    constexpr int R = FM + FN;                           // reads of a wave and 64 bytes
     // loads of 64 pieces, a wave each: A's, then W's (the last may reach past
     // the block's rows), P to a wave (the last ones may be done twice)
     constexpr int CA = (BM * CH + 63) / 64, CW = (BN * CH + 63) / 64;
@@ -329,10 +325,8 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
     unsigned ti, tj, share;
     q8_tile((g.m + BM - 1) / BM, (g.n + BN - 1) / BN, ti, tj, share);
     const int i0 = ti * BM, j0 = tj * BN;
-    // this share's steps: t0 and the `steps` - 1 after it; the first `odd` of
-    // all are the ones with zeros past k
-    const int whole = q8_whole(HOW, g.k), all = q8_steps(HOW, g.k), odd = all - whole;
-    const int t0 = (int)share * g.per;
+    // this share's steps: t0 and the `steps` - 1 after it
+    const int all = (g.k + BK - 1) / BK, t0 = (int)share * g.per;
     const int steps = all - t0 < g.per ? all - t0 : g.per;
 
     const signed char* ga = g.a + i0 * g.lda;
@@ -341,9 +335,15 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
     const int sha = HOW == Q8_ANY ? (int)((size_t)ga & 15) : 0;
     const int shw = HOW == Q8_ANY ? (int)((size_t)gw & 15) : 0;
     const q8v4 ra = q8_rsrc(ga - sha, 0xffffffffu), rw = q8_rsrc(gw - shw, 0xffffffffu);
+    // the operands' ends, from the bases of ra and rw, and their last whole pieces
+    const long long enda = ma * g.lda + sha + g.k, endw = mw * g.ldw + shw + g.k;
+    const unsigned lasta = (unsigned)(enda < 1ll << 32 ? enda - 16 : 0xfffffff0ll) & ~15u;
+    const unsigned lastw = (unsigned)(endw < 1ll << 32 ? endw - 16 : 0xfffffff0ll) & ~15u;
+    auto turned = [](int row) { return Q == 1 ? (row >> 1) & 7 : row & 15; };
 
     // a tile's rows lie within 32-bit offsets where the loads need them to
     typename std::conditional<DMA, unsigned, long long>::type off[P];
+    int in[DMA ? 1 : P];  // the byte of the step a load starts at
     auto load_id = [&](int p) {
         const int id = p * WAVES + wave;
         return (CA + CW) % WAVES == 0 || id < CA + CW ? id : CA + CW - 1;
@@ -358,18 +358,25 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
         if constexpr (HOW == Q8_ANY)
             off[p] = (unsigned)((o + (w ? shw : sha)) & ~15ll) + 16 * c;
         else
-            off[p] = o + 16 * (c ^ ((r >> 1) & 7));
+            off[p] = o + 16 * (c ^ turned(r));
+        if constexpr (!DMA) in[p] = 16 * (c ^ turned(r));
     }
     const unsigned base = (unsigned)(unsigned long long)(__attribute__((address_space(3))) void*)lds;
     q8v4 st[DMA ? 1 : P];
 
-    auto fetch = [&](int t, int p) {  // load p of the share's step t, a whole one
-        const int k0 = (t0 + t - odd) * BK;
-        if constexpr (DMA)
-            q8_fetch(base + (unsigned)(t % S) * BUF + load_id(p) * 1024, off[p], of_w(p) ? rw : ra,
-                     k0);
-        else
-            __builtin_memcpy(&st[p], (of_w(p) ? gw : ga) + off[p] + k0, 16);
+    auto fetch = [&](int t, int p) {  // load p of the share's step t
+        const int k0 = (t0 + t) * BK;
+        if constexpr (DMA) {
+            const unsigned o = off[p] + k0, last = of_w(p) ? lastw : lasta;
+            q8_fetch(base + (unsigned)(t % S) * BUF + load_id(p) * 1024, o < last ? o : last,
+                     of_w(p) ? rw : ra);
+        } else {
+            const signed char* v = (of_w(p) ? gw : ga) + off[p] + k0;
+            if (k0 + BK <= g.k)
+                __builtin_memcpy(&st[p], v, 16);
+            else
+                st[p] = q8_load16(v, g.k - k0 - in[p]);
+        }
     };
     auto put = [&](int t) {  // the loads of step t, in registers, to LDS
         if constexpr (!DMA) {
@@ -378,65 +385,104 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
                 *(q8v4*)&lds[(t % S) * BUF + load_id(p) * 1024 + lane * 16] = st[p];
         }
     };
-    auto rest = [&](int t) {  // the share's step t, one of the first `odd`
-        const int k0 = (whole + t0 + t) * BK;
-#pragma unroll 2
-        for (int e = threadIdx.x; e < (BM + BN) * 8; e += 64 * WAVES) {
-            const bool w = e >= BM * 8;
-            const int r = (e >> 3) - (w ? BM : 0), c = e & 7, last = w ? mw : ma;
-            const signed char* row = w ? gw + (r < last ? r : last) * g.ldw
-                                       : ga + (r < last ? r : last) * g.lda;
-            const int at = HOW == Q8_ANY ? 16 * c + (int)((size_t)(w ? gw + r * g.ldw : ga + r * g.lda) & 15)
-                                         : 16 * (c ^ ((r >> 1) & 7));
-            const q8v4 v = q8_load16(row + k0 + 16 * c, g.k - k0 - 16 * c);
-            __builtin_memcpy(&lds[(t % S) * BUF + (w ? OW : 0) + r * PITCH + at], &v, 16);
+
+    // the last bytes of an operand's last row, where no whole piece holds them:
+    // lanes 0 to 15 those of A, 16 to 31 those of W, if step t covers them (the
+    // last step, or with Q8_ANY the last piece of the one before, which may be
+    // another share's last)
+    const bool frayed = DMA && ((ma < BM && (enda & 15) != 0) || (mw < BN && (endw & 15) != 0)) &&
+                        t0 + steps + 1 >= all;
+    auto patch = [&](int t) {
+        if (wave == 0 && lane < 32) {
+            const bool w = lane >= 16;
+            const int r = w ? mw : ma, e = lane & 15;
+            const long long end = w ? endw : enda, piece = end & ~15ll;
+            const long long row = (r * (w ? g.ldw : g.lda) + (w ? shw : sha)) & ~15ll;
+            const long long c = (piece - row) / 16 - (long long)(t0 + t) * (8 * Q);
+            if (r < (w ? BN : BM) && c >= 0 && c < CH && e < (int)(end - piece)) {
+                const signed char v = ((w ? gw - shw : ga - sha) + piece)[e];
+                const int at = HOW == Q8_ANY ? (int)c : (int)c ^ turned(r);
+                lds[(t % S) * BUF + (w ? OW : 0) + r * PITCH + 16 * at + e] = v;
+            }
         }
+        q8_sync<63>();
     };
 
-    // reads: lane l takes row l % 16 of a block of 16, piece 4 h + l / 16 of half h
+    // reads: lane l takes row l % 16 of a block of 16, 16 bytes l / 16 of 64
+    constexpr int WORDS = HOW == Q8_ANY ? 8 : 4;  // (five of the eight are used)
+    typedef int words __attribute__((ext_vector_type(WORDS)));
     const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, quad = lane >> 4;
     const int fa = wm * FM * 16 * PITCH, fw = OW + wn * FN * 16 * PITCH;
-    const int pa = r16 * PITCH + (HOW == Q8_ANY ? quad * 16 + (int)((size_t)(ga + r16 * g.lda) & 15)
-                                                : (quad ^ ((r16 >> 1) & 7)) * 16);
-    const int pw = r16 * PITCH + (HOW == Q8_ANY ? quad * 16 + (int)((size_t)(gw + r16 * g.ldw) & 15)
-                                                : (quad ^ ((r16 >> 1) & 7)) * 16);
-    q8v4 xa[2][FM], xw[2][FN], acc[FM][FN];
+    // the byte of a piece that a row starts at is the same for rows 16 apart
+    const int sa = HOW == Q8_ANY ? (int)((size_t)(ga + r16 * g.lda) & 15) : 0;
+    const int sw = HOW == Q8_ANY ? (int)((size_t)(gw + r16 * g.ldw) & 15) : 0;
+    const int pl = r16 * PITCH + (HOW == Q8_ANY ? quad : quad ^ turned(r16)) * 16;
+    words xa[2][FM], xw[2][FN];
+    q8v4 acc[FM][FN], bw[FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
     auto read = [&](int t, int h, int q) {
         const signed char* p = lds + (t % S) * BUF;
-        const int half = HOW == Q8_ANY ? (q < FN ? pw : pa) + h * 64 : pa ^ (h * 64);
-        q8v4& x = q < FN ? xw[h][q] : xa[h][q - FN];
-        p += half + (q < FN ? fw + q * 16 * PITCH : fa + (q - FN) * 16 * PITCH);
-        if constexpr (HOW == Q8_ANY)
-            __builtin_memcpy(&x, p, 16);
-        else
-            x = *(const q8v4*)p;
+        words& x = q < FN ? xw[h & 1][q] : xa[h & 1][q - FN];
+        p += q < FN ? fw + q * 16 * PITCH : fa + (q - FN) * 16 * PITCH;
+        if constexpr (HOW == Q8_ANY) {
+            typedef const volatile __attribute__((address_space(3))) int word;
+            word* v = (word*)(p + pl + h * 64 + ((q < FN ? sw : sa) & 12));
+#pragma unroll
+            for (int e = 0; e < 5; ++e) x[e] = v[e];
+        } else {
+            x = *(const words*)(p + (pl ^ (h * 64)));
+        }
     };
-    auto multiply = [&](int h, int i) {
+    auto bytes = [&](const words& x, int shift) {
+        if constexpr (HOW == Q8_ANY) {
+            q8v4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbyte(x[e + 1], x[e], shift);
+            return v;
+        } else {
+            return x;
+        }
+    };
+    auto multiply = [&](int h, int i, int have) {  // `have` bytes of the step before k
+        if (i == 0) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) bw[j] = bytes(xw[h & 1][j], sw & 3);
+        }
+        q8v4 ba = bytes(xa[h & 1][i], sa & 3);
+        if (have < BK) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int b = have - 64 * h - 16 * quad - 4 * e;
+                ba[e] &= b >= 4 ? -1 : b <= 0 ? 0 : (1 << (8 * b)) - 1;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            acc[i][j] =
-                __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[h][j], xa[h][i], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bw[j], ba, acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     // a step, with another (NEXT) or S others (MORE) after it
     auto step = [&](int t, auto next, auto more) {
         constexpr bool NEXT = decltype(next)::value, MORE = decltype(more)::value;
+        const int have = NEXT ? BK : g.k - (t0 + t) * BK;
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
+        for (int h = 0; h < H - 1; ++h)
 #pragma unroll
-            for (int q = i * R / FM; q < (i + 1) * R / FM; ++q) read(t, 1, q);
-            multiply(0, i);
-        }
+            for (int i = 0; i < FM; ++i) {
+#pragma unroll
+                for (int q = i * R / FM; q < (i + 1) * R / FM; ++q) read(t, h + 1, q);
+                multiply(h, i, have);
+            }
         if constexpr (NEXT) {
             put(t + 1);
             if (DMA && (MORE || t + S == steps))
                 q8_sync<DMA ? (S - 2) * P : 0>();
             else
                 q8_sync<0>();
+            if (frayed && t + 3 >= steps) patch(t + 1);
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -448,16 +494,14 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
 #pragma unroll
                 for (int p = i * P / FM; p < (i + 1) * P / FM; ++p) fetch(t + S, p);
             }
-            multiply(1, i);
+            multiply(H - 1, i, have);
         }
     };
 
     if (steps > 0) {
 #pragma unroll
         for (int t = 0; t < S; ++t) {
-            if (t0 + t < odd) {
-                if (t < steps) rest(t);
-            } else if (t < steps) {
+            if (t < steps) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) fetch(t, p);
                 if (t == 0) put(0);
@@ -467,6 +511,7 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
             q8_sync<DMA ? (S - 1) * P : 0>();
         else
             q8_sync<0>();
+        if (frayed && steps <= 2) patch(0);
 #pragma unroll
         for (int q = 0; q < R; ++q) read(0, 0, q);
         int t = 0;

@@ -346,12 +346,15 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  * reads back as NaN throughout; other rows are not touched by it.
  *
  * Matrices are in ROW order, DEVICE pointers: element (i, j) at p[i*ld + j],
- * ld >= max(1, row length), any alignment; elements past the row length are
- * neither read nor written.  The letter of a call is the type of its rows:
+ * ld >= max(1, row length), any alignment.  The gap after a row is never
+ * written; the product may read the gap between two rows (what it holds does
+ * not matter), nothing reads past the last row's end.  The letter of a call is the type of its rows:
  * s float, h IEEE half, b bfloat16 (16-bit words); arithmetic and scales are
  * in 32 bits, the norm's sum of squares in 64.  Calls are asynchronous on
- * `stream`, need no workspace (the product apart), can be captured into a
- * graph, and give the same bytes every time.  m == 0 or n == 0: nothing is
+ * `stream`, can be captured into a graph, and give the same bytes every time.
+ * Only the product uses the stream's workspace (xsymv_q8gemm_workspace_bytes;
+ * 0 where k is not shared out), so it alone has to have run once on a stream,
+ * or have a workspace installed, before it is captured there.  m == 0 or n == 0: nothing is
  * done.  Codes are checked in the order of the arguments before any device work;
  * pointers are only needed where there are rows.
  *
@@ -386,9 +389,14 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  *   the bias round once each to 32 bits.  k == 0: C = bias or zeros.  Codes:
  *   -1 m, -2 n, -3 k < 0 or > 131071, -4 A NULL, -5 lda, -6 sa NULL, -7 W
  *   NULL, -8 ldw, -9 sw NULL, -11 C NULL, -12 ldc.
- * All: 1000 + hipError_t. */
+ *   2000 installed workspace too small.
+ * All: 1000 + hipError_t.
+ *
+ *   xsymv_q8gemm_workspace_bytes: the workspace a product of m x n x k takes
+ *   at most, whatever the operands' alignment (0 for sizes that do nothing). */
 typedef unsigned short xhalf;     /* IEEE half, its 16 bits */
 typedef unsigned short xbfloat16; /* bfloat16, its 16 bits */
+size_t xsymv_q8gemm_workspace_bytes(int m, int n, int k);
 int xsymv_q8norm_s(int m, int n, const float *x, int ldx, char rtype, const void *r,
                     int ldr, char wtype, const void *w, float eps, void *h, int ldh,
                     signed char *q, int ldq, float *scale, void *stream);

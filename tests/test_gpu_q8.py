@@ -338,6 +338,102 @@ def test_gemm_odd(t, m, n, k):
     gemm_case(t, m, n, k, (3, 1, 5), (1, 7, 3), m + n + k + 1, bias=True)
 
 
+@pytest.mark.parametrize("m,n,k", [c for c in GEMM if c[2] >= 16])
+@pytest.mark.parametrize("t", LETTERS)
+def test_gemm_any_stride(t, m, n, k):
+    log(f"gemm {t} {m}x{n}x{k}, the first row at a multiple of 16 bytes, the others anywhere")
+    gemm_case(t, m, n, k, (3 + m % 2, 5, 3), (16, 0, 1), m + n + k + 2, bias=False)
+
+
+# ends of k around the 16-byte pieces and the steps of 128 and 256 bytes, in
+# tiles of every height, with the operands' last rows in and out of a tile
+ENDS = [16, 17, 31, 32, 47, 100, 127, 128, 129, 143, 144, 145, 160, 255, 256, 257, 271, 272, 273,
+        383, 384, 400, 511, 512, 513, 528, 640, 641, 777, 1040]
+
+
+@pytest.mark.parametrize("k", ENDS)
+@pytest.mark.parametrize("m,n", [(1, 1), (2, 67), (16, 128), (20, 33), (33, 130), (70, 64),
+                                 (129, 129), (257, 300), (600, 1100)])
+def test_gemm_ends(m, n, k):
+    log(f"gemm {m}x{n}x{k}: ends")
+    gemm_case("s", m, n, k, (-k % 16, -k % 16 + 16, 0), (0, 0, 0), m + n + k, bias=False)
+    for pad in (1, 2, 4, 8):
+        gemm_case("s", m, n, k, (pad, pad + 6, 0), (0, 16, 0), m + n + k + pad, bias=False)
+    gemm_case("s", m, n, k, (0, 0, 0), (0, 0, 0), m + n + k + 9, bias=False)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 200, 40000), (16, 2048, 28000), (30, 300, 30000),
+                                   (60, 1000, 20000), (130, 2000, 16384), (256, 2048, 9000),
+                                   (300, 4096, 20000), (1024, 8192, 1024), (2048, 4096, 515)])
+@pytest.mark.parametrize("pad", ["lines", "any", "odd"])
+def test_gemm_large(m, n, k, pad):
+    """Sizes at which k is shared out between workgroups, and the largest tiles."""
+    log(f"gemm {m}x{n}x{k} {pad}")
+    pads, offs = {"lines": ((-k % 16, -k % 16, 0), (0, 0, 0)), "any": ((7, 9, 1), (0, 0, 3)),
+                  "odd": ((7, 9, 1), (5, 1, 3))}[pad]
+    gemm_case("b", m, n, k, pads, offs, m + n + k, bias=True)
+
+
+# sizes at which each kernel of the product is the one chosen, k whole and shared out
+KERNELS = [("lines", 5, 33, 300), ("lines", 5, 33, 8200), ("lines", 5, 4100, 300),
+           ("lines", 16, 4100, 16400), ("lines", 40, 33, 2060), ("lines", 100, 33, 2060),
+           ("lines", 100, 8200, 520), ("lines", 2050, 33, 8200), ("lines", 100, 16400, 300),
+           ("lines", 100, 4100, 8200), ("lines", 200, 16400, 300), ("lines", 4100, 33, 16400),
+           ("lines", 260, 30000, 300), ("lines", 130, 4100, 16400),
+           ("any", 5, 16400, 300), ("any", 5, 33, 2060), ("any", 40, 33, 2060),
+           ("any", 100, 33, 1040), ("any", 100, 16400, 300), ("any", 100, 4100, 4110),
+           ("any", 130, 16400, 300), ("any", 4100, 33, 16400), ("any", 260, 16400, 300),
+           ("any", 130, 4100, 8200),
+           ("odd", 5, 16400, 300), ("odd", 5, 33, 2060), ("odd", 40, 33, 1040),
+           ("odd", 200, 16400, 300), ("odd", 130, 2000, 8200)]
+
+
+@pytest.mark.parametrize("how,m,n,k", KERNELS)
+def test_gemm_kernels(how, m, n, k):
+    for end in (0, 4, 11, 12, 13, 28, 84, 85, 99, 100, 101, 115, 116, 211, 212, 213, 228):
+        kk = k // 128 * 128 + end
+        log(f"gemm {how} {m}x{n}x{kk}")
+        pads, offs = {"lines": ((-kk % 16, -kk % 16 + 32, 0), (0, 16, 0)),
+                      "any": ((5, 3, 0), (0, 0, 0)), "odd": ((5, 3, 0), (3, 1, 0))}[how]
+        gemm_case("b", m, n, kk, pads, offs, m + n + kk, bias=False)
+
+
+@pytest.mark.parametrize("t", LETTERS)
+def test_gemm_workspace(t):
+    """A caller's workspace: large enough it is used, too small it is refused
+    before any work; the query covers every alignment."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    m, n, k = 40, 256, 20000
+    need = X.q8gemm_workspace_bytes(m, n, k)
+    assert need > 0 and X.q8gemm_workspace_bytes(1, 1, 16) == 0
+    g = gen(11)
+    a = torch.randint(-127, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones((n,), device="cuda")
+    f = getattr(X, f"xsymv_q8gemm_{t}")
+    want = torch.empty((m, n), device="cuda", dtype=dtype_of(t))
+    f(m, n, k, a, k, one, w, k, one, None, want, n)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty((need,), dtype=torch.uint8, device="cuda")
+    for nbytes in (need, 64):
+        X.set_workspace(ws, nbytes, stream=st)
+        c = torch.full((m, n), math.nan, device="cuda", dtype=dtype_of(t))
+        torch.cuda.synchronize()
+        if nbytes == need:
+            f(m, n, k, a, k, one, w, k, one, None, c, n, stream=st)
+            st.synchronize()
+            assert torch.equal(c, want)
+        else:
+            with pytest.raises(X.XsymvError) as e:
+                f(m, n, k, a, k, one, w, k, one, None, c, n, stream=st)
+            assert e.value.code == 2000
+            st.synchronize()
+            assert bool(c.isnan().all())
+        X.set_workspace(None, stream=st)
+
+
 @pytest.mark.parametrize("t", LETTERS)
 def test_gemm_of_empty_rows(t):
     """k = 0: the bias, or zeros."""
