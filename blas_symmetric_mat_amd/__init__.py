@@ -209,17 +209,6 @@ def library():
             lib.xgemv_workspace_bytes.argtypes = [ci, cc, ci, ci]
             lib.xgemv_plan.restype = ci
             lib.xgemv_plan.argtypes = [ci, ci, ci, ci, ip, ci, ip, ci]
-            cf = ctypes.c_float
-            for t in "shb":
-                for nm, args in (("norm", [ci, ci, vp, ci, cc, vp, ci, cc, vp, cf, vp, ci, vp, ci,
-                                           vp, vp]),
-                                 ("glu", [ci, ci, vp, ci, vp, ci, vp, ci, vp, vp]),
-                                 ("store", [ci, ci, vp, ci, vp, ci, vp, ci, vp, vp]),
-                                 ("read", [ci, ci, vp, ci, vp, vp, ci, vp, ci, vp]),
-                                 ("gemm", [ci, ci, ci, vp, ci, vp, vp, ci, vp, vp, vp, ci, vp])):
-                    f = getattr(lib, f"xsymv_q8{nm}_{t}")
-                    f.restype = ci
-                    f.argtypes = args
             lib.xsymv_q8gemm_workspace_bytes.restype = ctypes.c_size_t
             lib.xsymv_q8gemm_workspace_bytes.argtypes = [ci, ci, ci]
             lib.xsymv_read_bandwidth.restype = ci
@@ -479,112 +468,109 @@ def xsymv_combine_w(n, nshards, alpha, P, ldp, beta, y, incy, stream=None):
     _cbcall("w", n, nshards, alpha, P, ldp, beta, y, incy, stream)
 
 
-def _q8call(name, *args):
-    rc = getattr(library(), name)(*args)
-    if rc != 0:
-        raise XsymvError(name, rc)
+_q8_calls = None
+
+
+def _q8():
+    """The compiled marshalling of the 8-bit row operators (csrc/q8_bind.c)."""
+    global _q8_calls
+    if _q8_calls is None:
+        library()
+        import importlib
+        module = importlib.import_module("blas_symmetric_mat_amd._q8_bind")
+        module.setup(XsymvError, lambda: _stream(None))
+        _q8_calls = module
+    return _q8_calls
 
 
 def xsymv_q8norm_s(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
     scales; x float32, r and h of letter rtype, w of letter wtype ('s'); r, h may be None."""
-    _q8call("xsymv_q8norm_s", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
-            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+    (_q8_calls or _q8()).norm_s(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
+                              stream)
 
 
 def xsymv_q8norm_h(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
     scales; x float16, r and h of letter rtype, w of letter wtype ('h' or 's'); r, h may be None."""
-    _q8call("xsymv_q8norm_h", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
-            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+    (_q8_calls or _q8()).norm_h(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
+                              stream)
 
 
 def xsymv_q8norm_b(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
     scales; x bfloat16, r and h of letter rtype, w of letter wtype ('b' or 's'); r, h may be None."""
-    _q8call("xsymv_q8norm_b", m, n, _addr(x), ldx, _ch(rtype), _addr(r), ldr, _ch(wtype), _addr(w),
-            eps, _addr(h), ldh, _addr(q), ldq, _addr(scale), _stream(stream))
+    (_q8_calls or _q8()).norm_b(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
+                              stream)
 
 
 def xsymv_q8glu_s(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
     """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u float32."""
-    _q8call("xsymv_q8glu_s", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).glu_s(m, n, g, ldg, u, ldu, q, ldq, scale, stream)
 
 
 def xsymv_q8glu_h(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
     """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u float16."""
-    _q8call("xsymv_q8glu_h", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).glu_h(m, n, g, ldg, u, ldu, q, ldq, scale, stream)
 
 
 def xsymv_q8glu_b(m, n, g, ldg, u, ldu, q, ldq, scale, stream=None):
     """v = g / (1 + exp(-g)) * u as rows of 8-bit codes q and scales; g, u bfloat16."""
-    _q8call("xsymv_q8glu_b", m, n, _addr(g), ldg, _addr(u), ldu, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).glu_b(m, n, g, ldg, u, ldu, q, ldq, scale, stream)
 
 
 def xsymv_q8store_s(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
     """Row i of x (float32) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
     (slot None: row i; a slot outside the cache leaves the row out)."""
-    _q8call("xsymv_q8store_s", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).store_s(m, n, x, ldx, slot, cap, q, ldq, scale, stream)
 
 
 def xsymv_q8store_h(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
     """Row i of x (float16) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
     (slot None: row i; a slot outside the cache leaves the row out)."""
-    _q8call("xsymv_q8store_h", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).store_h(m, n, x, ldx, slot, cap, q, ldq, scale, stream)
 
 
 def xsymv_q8store_b(m, n, x, ldx, slot, cap, q, ldq, scale, stream=None):
     """Row i of x (bfloat16) as 8-bit codes and a scale in row slot[i] of a cache of cap rows
     (slot None: row i; a slot outside the cache leaves the row out)."""
-    _q8call("xsymv_q8store_b", m, n, _addr(x), ldx, _addr(slot), cap, _addr(q), ldq, _addr(scale),
-            _stream(stream))
+    (_q8_calls or _q8()).store_b(m, n, x, ldx, slot, cap, q, ldq, scale, stream)
 
 
 def xsymv_q8read_s(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
     """out row i (float32) := the values of row slot[i] of a cache of cap rows (slot None: row i;
     zeros for a slot outside the cache)."""
-    _q8call("xsymv_q8read_s", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
-            _stream(stream))
+    (_q8_calls or _q8()).read_s(m, n, q, ldq, scale, slot, cap, out, ldo, stream)
 
 
 def xsymv_q8read_h(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
     """out row i (float16) := the values of row slot[i] of a cache of cap rows (slot None: row i;
     zeros for a slot outside the cache)."""
-    _q8call("xsymv_q8read_h", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
-            _stream(stream))
+    (_q8_calls or _q8()).read_h(m, n, q, ldq, scale, slot, cap, out, ldo, stream)
 
 
 def xsymv_q8read_b(m, n, q, ldq, scale, slot, cap, out, ldo, stream=None):
     """out row i (bfloat16) := the values of row slot[i] of a cache of cap rows (slot None: row i;
     zeros for a slot outside the cache)."""
-    _q8call("xsymv_q8read_b", m, n, _addr(q), ldq, _addr(scale), _addr(slot), cap, _addr(out), ldo,
-            _stream(stream))
+    (_q8_calls or _q8()).read_b(m, n, q, ldq, scale, slot, cap, out, ldo, stream)
 
 
 def xsymv_q8gemm_s(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
     """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], float32; A, W 8-bit codes in
     rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
-    _q8call("xsymv_q8gemm_s", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
-            _addr(bias), _addr(C), ldc, _stream(stream))
+    (_q8_calls or _q8()).gemm_s(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream)
 
 
 def xsymv_q8gemm_h(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
     """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], float16; A, W 8-bit codes in
     rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
-    _q8call("xsymv_q8gemm_h", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
-            _addr(bias), _addr(C), ldc, _stream(stream))
+    (_q8_calls or _q8()).gemm_h(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream)
 
 
 def xsymv_q8gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
     """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], bfloat16; A, W 8-bit codes in
     rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
-    _q8call("xsymv_q8gemm_b", m, n, k, _addr(A), lda, _addr(sa), _addr(W), ldw, _addr(sw),
-            _addr(bias), _addr(C), ldc, _stream(stream))
+    (_q8_calls or _q8()).gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream)
 
 
 def q8gemm_workspace_bytes(m: int, n: int, k: int) -> int:

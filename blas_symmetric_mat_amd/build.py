@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -21,6 +22,7 @@ UNITS = ["xsymv_host", "xsymv_prec_s", "xsymv_prec_d", "xsymv_prec_c", "xsymv_pr
          "xq8_gemm_b"]
 ARCH = os.environ.get("XSYMV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CC = os.environ.get("CC", "gcc")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-function"]
@@ -36,8 +38,24 @@ def _compile(unit: str, extra: list[str]) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def build_bind() -> str:
+    """The compiled Python side of the 8-bit row operators, linked against the
+    library beside it."""
+    out = os.path.join(HERE, "_q8_bind.so")
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([CC, "-O2", "-Wall", "-shared", "-fPIC",
+                        "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "q8_bind.c"),
+                        "-o", tmp, "-L" + HERE, "-lxsymv", "-Wl,-rpath,$ORIGIN",
+                        "-Wl,--allow-shlib-undefined"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CC} failed on q8_bind:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(jobs: int | None = None, resource_usage: bool = False, verbose: bool = False) -> str:
-    """Compile every unit and link ``libxsymv.so``; returns its path."""
+    """Compile every unit and link ``libxsymv.so``, then the Python side of the
+    8-bit row operators; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Rpass-analysis=kernel-resource-usage"] if resource_usage else []
     jobs = jobs or min(len(UNITS), max(1, min(16, os.cpu_count() or 1)))
@@ -52,6 +70,7 @@ def build(jobs: int | None = None, resource_usage: bool = False, verbose: bool =
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_bind()
     return LIB
 
 

@@ -243,10 +243,11 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_stream(Q8GemmArgs<T> g)
 // Q8_ANY    rows at any stride, the first at a multiple of 16 bytes.  The same
 //           loads take the 8 Q + 1 aligned pieces that hold a row's step (an
 //           odd number of pieces, which spreads the rows over the banks as
-//           well); the reads take the five words that hold a piece of the row,
-//           and its bytes are shifted out of them before they are multiplied.
-//           (LDS reads 16 bytes at once at any address, but several times
-//           slower.)  Memory delivers 64 bytes at a time, so a row's step that
+//           well); the reads take the three words of 8 bytes that hold a piece
+//           of the row, and its bytes are shifted out of them before they are
+//           multiplied.  (LDS reads 16 bytes at once at any address too, but
+//           several times slower, and in words of 4 bytes it takes five reads.)
+//           Memory delivers 64 bytes at a time, so a row's step that
 //           starts anywhere costs one delivery more: Q = 2 where LDS has room.
 // Q8_REGS   anything else: through registers, 16 bytes at any address, written
 //           to LDS before the next barrier; S = 2.
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
     };
 
     // reads: lane l takes row l % 16 of a block of 16, 16 bytes l / 16 of 64
-    constexpr int WORDS = HOW == Q8_ANY ? 8 : 4;  // (five of the eight are used)
+    constexpr int WORDS = HOW == Q8_ANY ? 8 : 4;  // (six of the eight are used)
     typedef int words __attribute__((ext_vector_type(WORDS)));
     const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, quad = lane >> 4;
     const int fa = wm * FM * 16 * PITCH, fw = OW + wn * FN * 16 * PITCH;
@@ -428,19 +429,28 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
         words& x = q < FN ? xw[h & 1][q] : xa[h & 1][q - FN];
         p += q < FN ? fw + q * 16 * PITCH : fa + (q - FN) * 16 * PITCH;
         if constexpr (HOW == Q8_ANY) {
-            typedef const volatile __attribute__((address_space(3))) int word;
-            word* v = (word*)(p + pl + h * 64 + ((q < FN ? sw : sa) & 12));
+            typedef int two __attribute__((ext_vector_type(2)));
+            typedef const volatile __attribute__((address_space(3))) two word;
+            word* v = (word*)(p + pl + h * 64 + ((q < FN ? sw : sa) & 8));
 #pragma unroll
-            for (int e = 0; e < 5; ++e) x[e] = v[e];
+            for (int e = 0; e < 3; ++e) {
+                const two y = v[e];
+                x[2 * e] = y.x;
+                x[2 * e + 1] = y.y;
+            }
         } else {
             x = *(const words*)(p + (pl ^ (h * 64)));
         }
     };
     auto bytes = [&](const words& x, int shift) {
         if constexpr (HOW == Q8_ANY) {
+            const int odd = -(shift >> 2 & 1);  // all bits where it starts in the second half
+            int y[5];
             q8v4 v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbyte(x[e + 1], x[e], shift);
+            for (int e = 0; e < 5; ++e) y[e] = (x[e + 1] & odd) | (x[e] & ~odd);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbyte(y[e + 1], y[e], shift & 3);
             return v;
         } else {
             return x;
@@ -449,9 +459,9 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
     auto multiply = [&](int h, int i, int have) {  // `have` bytes of the step before k
         if (i == 0) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) bw[j] = bytes(xw[h & 1][j], sw & 3);
+            for (int j = 0; j < FN; ++j) bw[j] = bytes(xw[h & 1][j], sw);
         }
-        q8v4 ba = bytes(xa[h & 1][i], sa & 3);
+        q8v4 ba = bytes(xa[h & 1][i], sa);
         if (have < BK) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

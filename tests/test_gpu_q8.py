@@ -379,7 +379,9 @@ KERNELS = [("lines", 5, 33, 300), ("lines", 5, 33, 8200), ("lines", 5, 4100, 300
            ("lines", 16, 4100, 16400), ("lines", 40, 33, 2060), ("lines", 100, 33, 2060),
            ("lines", 100, 8200, 520), ("lines", 2050, 33, 8200), ("lines", 100, 16400, 300),
            ("lines", 100, 4100, 8200), ("lines", 200, 16400, 300), ("lines", 4100, 33, 16400),
-           ("lines", 260, 30000, 300), ("lines", 130, 4100, 16400),
+           ("lines", 260, 30000, 300), ("lines", 130, 4100, 16400), ("lines", 5, 33, 520),
+           ("lines", 5, 500, 8200), ("any", 130, 1000, 16400), ("any", 100, 4100, 16400),
+           ("any", 5, 33, 4110),
            ("any", 5, 16400, 300), ("any", 5, 33, 2060), ("any", 40, 33, 2060),
            ("any", 100, 33, 1040), ("any", 100, 16400, 300), ("any", 100, 4100, 4110),
            ("any", 130, 16400, 300), ("any", 4100, 33, 16400), ("any", 260, 16400, 300),
@@ -623,3 +625,32 @@ def test_refusals_leave_no_trace():
         X.xsymv_q8store_s(4, 8, x, 7, None, 4, q, 8, sc)
     torch.cuda.synchronize()
     assert bool((q == 3).all()) and bool((sc == 2.0).all())
+
+
+def test_layer_of_prompt_and_tokens():
+    """The example layer: a prompt at once and the same tokens one by one give
+    the same bytes (rows do not depend on the rows beside them, the products'
+    sums are exact, and the attention between them runs in 64 bits), and both
+    are what the layer is in 64 bits up to the 8-bit rows' steps."""
+    import torch
+    from blas_symmetric_mat_amd import q8_layer
+    g = gen(21)
+    x = randn((23, 512), g).bfloat16()
+    r = randn((23, 512), g).bfloat16()
+    whole = q8_layer.Q8Layer(d=512, heads=4, f=1100, tokens=64, seed=3)
+    single = q8_layer.Q8Layer(d=512, heads=4, f=1100, tokens=64, seed=3)
+    y, h = whole(x, r)
+    parts = [single(x[i:j], r[i:j]) for i, j in ((0, 7), (7, 8), (8, 9), (9, 20), (20, 23))]
+    torch.cuda.synchronize()
+    assert torch.equal(y, torch.cat([p[0] for p in parts]))
+    assert torch.equal(h, torch.cat([p[1] for p in parts]))
+    for (a, b), (c, d) in zip(whole.kv, single.kv):
+        assert torch.equal(a, c) and torch.equal(b, d)
+    want, want_h = q8_layer.plain(whole, x, r)
+    # A code is off by at most half a step, evenly over it: its variance is
+    # step^2 / 12, and a row's largest of some 500 numbers is about 3.5 times
+    # their size, so a step is 3.5 / 127 and a row is off by 0.8 % of its size;
+    # bfloat16 adds 0.17 % a rounding.  Eight such rows one after the other,
+    # added as independent errors, stay under 2.5 %; the bound is twice that.
+    assert ((y - want).norm() / want.norm()).item() < 0.05
+    assert ((h - want_h).norm() / want_h.norm()).item() < 0.05
