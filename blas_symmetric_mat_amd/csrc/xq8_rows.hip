@@ -16,8 +16,13 @@ int rows_launch(const Q8RowArgs<OP>& a, hipStream_t stream)
     return q8_launch(&q8_rows<OP, TPR, J>, q8_grid(a.op.m, threads / TPR), threads, stream, a);
 }
 
-// Threads per row and chunks per thread by the row's length alone: the
-// smallest of the compiled capacities (TPR * J chunks) that holds the row.
+// Threads per row and chunks per thread by the row's length alone: of the
+// compiled capacities (TPR * J chunks) the smallest that holds the row.  Two
+// or three chunks a thread were the fastest for long rows of every length
+// (norm of 4096 x 8192, bfloat16 with a 32-bit residual: 256 threads of four
+// 80 us, 512 of two 72, 1024 of one 87), the sums' waits being shared by more
+// loads; a capacity that is half empty costs up to 30 % (norm of 3000 x 9000:
+// 1024 threads of two 74 us, 512 of three 56).
 template <class OP>
 int rows_run(const Q8RowArgs<OP>& a, hipStream_t stream)
 {
@@ -26,11 +31,16 @@ int rows_run(const Q8RowArgs<OP>& a, hipStream_t stream)
     if (chunks <= 16) return rows_launch<OP, 16, 1>(a, stream);
     if (chunks <= 32) return rows_launch<OP, 32, 1>(a, stream);
     if (chunks <= 64) return rows_launch<OP, 64, 1>(a, stream);
+    if (chunks <= 96) return rows_launch<OP, 32, 3>(a, stream);
     if (chunks <= 128) return rows_launch<OP, 64, 2>(a, stream);
+    if (chunks <= 192) return rows_launch<OP, 64, 3>(a, stream);
     if (chunks <= 256) return rows_launch<OP, 256, 1>(a, stream);
     if (chunks <= 512) return rows_launch<OP, 256, 2>(a, stream);
+    if (chunks <= 768) return rows_launch<OP, 256, 3>(a, stream);
     if (chunks <= 1024) return rows_launch<OP, 512, 2>(a, stream);
+    if (chunks <= 1536) return rows_launch<OP, 512, 3>(a, stream);
     if (chunks <= 2048) return rows_launch<OP, 1024, 2>(a, stream);
+    if (chunks <= 3072) return rows_launch<OP, 1024, 3>(a, stream);
     if (chunks <= 4096) return rows_launch<OP, 1024, 4>(a, stream);
     if (chunks <= 8192) return rows_launch<OP, 1024, 8>(a, stream);
     return rows_launch<OP, 1024, 0>(a, stream);
@@ -118,7 +128,11 @@ int store_run(int m, int n, const T* x, int ldx, const int* slot, int cap, signe
 template <class T, int TPR>
 int read_launch(const Q8ReadArgs<T>& a, hipStream_t stream)
 {
-    return q8_launch(&q8_read<T, TPR>, q8_grid(a.m, 256 / TPR), 256, stream, a);
+    // some 2^23 workgroups at most, which loop over the rest
+    const long long parts = ((long long)a.n + TPR * Q8_CHUNK - 1) / (TPR * Q8_CHUNK);
+    const unsigned rows = q8_grid(a.m, 256 / TPR);
+    const dim3 grid(rows, (unsigned)std::min(parts, std::max(1ll, (1ll << 16) / rows)));
+    return q8_launch(&q8_read<T, TPR>, grid, 256, stream, a);
 }
 
 template <class T>

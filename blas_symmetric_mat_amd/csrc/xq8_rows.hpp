@@ -98,8 +98,8 @@ __device__ __forceinline__ void q8_store_codes(signed char* p, int have, const f
 
 // -------------------------------------------------------------- reductions
 // Over the TPR threads of a row: lane exchanges within a wave, then (TPR >
-// 64, the row is the workgroup's) the waves' results through LDS, read by all
-// in the same order.  The LDS words alternate between `par` 0 and 1 from one
+// 64) the results of the row's waves through LDS, read by all in the same
+// order.  The LDS words alternate between `par` 0 and 1 from one
 // row to the next, so one barrier per reduction suffices.
 template <int TPR>
 __device__ __forceinline__ unsigned q8_row_max(unsigned v, unsigned (&buf)[2][16], int par)
@@ -112,9 +112,10 @@ __device__ __forceinline__ unsigned q8_row_max(unsigned v, unsigned (&buf)[2][16
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) buf[par][threadIdx.x >> 6] = v;
         __syncthreads();
+        const int first = threadIdx.x / TPR * (TPR / 64);
 #pragma unroll
         for (int i = 0; i < TPR / 64; ++i) {
-            const unsigned o = buf[par][i];
+            const unsigned o = buf[par][first + i];
             v = v > o ? v : o;
         }
     }
@@ -129,9 +130,10 @@ __device__ __forceinline__ double q8_row_sum(double v, double (&buf)[2][16], int
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) buf[par][threadIdx.x >> 6] = v;
         __syncthreads();
-        v = buf[par][0];
+        const int first = threadIdx.x / TPR * (TPR / 64);
+        v = buf[par][first];
 #pragma unroll
-        for (int i = 1; i < TPR / 64; ++i) v += buf[par][i];
+        for (int i = 1; i < TPR / 64; ++i) v += buf[par][first + i];
     }
     return v;
 }
@@ -168,6 +170,7 @@ struct Q8Norm {
     int m, n;
 
     __device__ __forceinline__ long long dest(long long row) const { return row; }
+    __device__ __forceinline__ bool in_place() const { return (const void*)h == (const void*)r; }
     __device__ __forceinline__ void sum(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
     {
         q8_load(x + row * ldx + c, have, v);
@@ -180,13 +183,20 @@ struct Q8Norm {
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e) v[e] = (float)(R)v[e];
     }
-    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
-                                          double& ss) const
+    // (the first `again` elements are another chunk's too, and counted there)
+    __device__ __forceinline__ void first(long long row, int c, int have, int again,
+                                          float (&v)[Q8_CHUNK], double& ss) const
     {
         sum(row, c, have, v);
         if (h != nullptr) q8_store(h + row * ldh + c, have, v);
+        if (again == 0) {
 #pragma unroll
-        for (int e = 0; e < Q8_CHUNK; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
+            for (int e = 0; e < Q8_CHUNK; ++e) ss = __builtin_fma((double)v[e], (double)v[e], ss);
+        } else {
+#pragma unroll
+            for (int e = 1; e < Q8_CHUNK; ++e)
+                if (e >= again) ss = __builtin_fma((double)v[e], (double)v[e], ss);
+        }
     }
     // a row too long for the registers: what was kept is read back (r may
     // have been overwritten by it)
@@ -225,7 +235,8 @@ struct Q8Glu {
     int m, n;
 
     __device__ __forceinline__ long long dest(long long row) const { return row; }
-    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
+    __device__ __forceinline__ bool in_place() const { return false; }
+    __device__ __forceinline__ void first(long long row, int c, int have, int, float (&v)[Q8_CHUNK],
                                           double&) const
     {
         float t[Q8_CHUNK];
@@ -241,7 +252,7 @@ struct Q8Glu {
     __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
     {
         double none = 0.0;
-        first(row, c, have, v, none);
+        first(row, c, have, 0, v, none);
     }
 };
 
@@ -260,7 +271,8 @@ struct Q8Store {
         const int s = slot != nullptr ? slot[row] : row;
         return s >= 0 && s < cap ? s : -1;
     }
-    __device__ __forceinline__ void first(long long row, int c, int have, float (&v)[Q8_CHUNK],
+    __device__ __forceinline__ bool in_place() const { return false; }
+    __device__ __forceinline__ void first(long long row, int c, int have, int, float (&v)[Q8_CHUNK],
                                           double&) const
     {
         q8_load(x + row * ldx + c, have, v);
@@ -270,6 +282,17 @@ struct Q8Store {
         q8_load(x + row * ldx + c, have, v);
     }
 };
+
+// Where chunks start at the latest: a row's last chunk is its last
+// eight elements, some of them the chunk before's as well (their results are
+// the same, whoever stores them), so that it is read and written at once; one
+// element at a time it cost rows of 255 and 1564 elements 40 % more time.
+// Not where an output takes an input's place: there an element belongs to one
+// thread.
+__device__ __forceinline__ int q8_last_column(int n, bool alone)
+{
+    return !alone && n >= Q8_CHUNK ? n - Q8_CHUNK : 0x7fffffff;
+}
 
 template <class OP>
 struct Q8RowArgs {
@@ -282,17 +305,25 @@ struct Q8RowArgs {
 // One row per TPR threads; a workgroup of max(256, TPR) threads.  J chunks
 // of the row in a thread's registers; J = 0: a row longer than 8 chunks of
 // 1024 threads, whose elements are formed again for each of its sums.
+// Two chunks a thread fit 64 registers, which lets a compute unit run two
+// workgroups of 1024 threads: one's loads are on their way while the other
+// waits for its row's sums.
 template <class OP, int TPR, int J>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a)
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 4) void q8_rows(
+    Q8RowArgs<OP> a)
 {
     constexpr int THREADS = TPR > 256 ? TPR : 256;
     constexpr int RPB = THREADS / TPR;  // rows per workgroup
+    // chunks of a thread before the one that can be the row's last (a row takes
+    // the smallest capacity that holds it; the largest one may be half empty)
+    constexpr int LAST = J == 8 ? 4 : J - 1;
     __shared__ double sbuf[2][16];
     __shared__ unsigned mbuf[2][16];
     const OP& op = a.op;
     const int n = op.n;
     const int t = threadIdx.x % TPR;
     int par = 0;
+    const int edge = q8_last_column(n, op.in_place());
     for (long long base = (long long)blockIdx.x * RPB; base < op.m;
          base += (long long)gridDim.x * RPB) {
         const long long row = base + threadIdx.x / TPR;
@@ -307,9 +338,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
             float v[J][Q8_CHUNK];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int c = (t + j * TPR) * Q8_CHUNK;
+                const int c = (t + j * TPR) * Q8_CHUNK, at = j < LAST ? c : min(c, edge);
                 if (c < have) {
-                    op.first(row, c, have - c, v[j], ss);
+                    op.first(row, at, n - at, c - at, v[j], ss);
                 } else {
 #pragma unroll
                     for (int e = 0; e < Q8_CHUNK; ++e) v[j][e] = 0.0f;
@@ -319,8 +350,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
                 const float f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const int c = (t + j * TPR) * Q8_CHUNK;
-                    if (c < have) op.second(c, have - c, v[j], f);
+                    const int c = (t + j * TPR) * Q8_CHUNK, at = j < LAST ? c : min(c, edge);
+                    if (c < have) op.second(at, n - at, v[j], f);
                 }
             }
 #pragma unroll
@@ -333,20 +364,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
             const float inv = 127.0f / top;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const int c = (t + j * TPR) * Q8_CHUNK;
-                if (c < n) q8_store_codes(a.q + dst * a.ldq + c, n - c, v[j], inv);
+                const int c = (t + j * TPR) * Q8_CHUNK, at = j < LAST ? c : min(c, edge);
+                if (c < n) q8_store_codes(a.q + dst * a.ldq + at, n - at, v[j], inv);
             }
         } else {
             float f = 1.0f;
             float v[Q8_CHUNK];
             if constexpr (OP::NORM) {
-                for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK)
-                    op.first(row, (int)c, n - (int)c, v, ss);
+                for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
+                    const int at = min((int)c, edge);
+                    op.first(row, at, n - at, (int)c - at, v, ss);
+                }
                 f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
             }
             for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
-                op.again(row, (int)c, n - (int)c, v);
-                if constexpr (OP::NORM) op.second((int)c, n - (int)c, v, f);
+                const int at = min((int)c, edge);
+                op.again(row, at, n - at, v);
+                if constexpr (OP::NORM) op.second(at, n - at, v, f);
                 mx = q8_chunk_max(v, mx);
             }
             mx = q8_row_max<TPR>(mx, mbuf, par);
@@ -356,9 +390,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void q8_rows(Q8RowArgs<OP> a
             if (t == 0) a.scale[dst] = top / 127.0f;
             const float inv = 127.0f / top;
             for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
-                op.again(row, (int)c, n - (int)c, v);
-                if constexpr (OP::NORM) op.second((int)c, n - (int)c, v, f);
-                q8_store_codes(a.q + dst * a.ldq + c, n - (int)c, v, inv);
+                const int at = min((int)c, edge);
+                op.again(row, at, n - at, v);
+                if constexpr (OP::NORM) op.second(at, n - at, v, f);
+                q8_store_codes(a.q + dst * a.ldq + at, n - at, v, inv);
             }
         }
     }
@@ -377,30 +412,32 @@ struct Q8ReadArgs {
     int m, n, cap;
 };
 
+// TPR threads a row, a chunk each; of a longer row, 256 chunks to a workgroup
+// (blockIdx.y), so that a few long rows are as many loads in flight as many
+// short ones.
 template <class T, int TPR>
 __global__ __launch_bounds__(256) void q8_read(Q8ReadArgs<T> a)
 {
     constexpr int RPB = 256 / TPR;
-    const int t = threadIdx.x % TPR;
-    for (long long base = (long long)blockIdx.x * RPB; base < a.m;
-         base += (long long)gridDim.x * RPB) {
-        const long long row = base + threadIdx.x / TPR;
-        if (row >= a.m) break;
+    const int edge = q8_last_column(a.n, false);
+    const long long first = ((long long)blockIdx.y * TPR + threadIdx.x % TPR) * Q8_CHUNK;
+    for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < a.m;
+         row += (long long)gridDim.x * RPB) {
         const int s = a.slot != nullptr ? a.slot[row] : (int)row;
         const bool in = s >= 0 && s < a.cap;
         const float f = in ? a.scale[s] : 0.0f;
-        for (long long c = (long long)t * Q8_CHUNK; c < a.n; c += TPR * Q8_CHUNK) {
-            const int have = a.n - (int)c;
+        for (long long c = first; c < a.n; c += (long long)gridDim.y * TPR * Q8_CHUNK) {
+            const int at = min((int)c, edge);
             float v[Q8_CHUNK];
             if (in) {
-                q8_load(a.q + s * a.ldq + c, have, v);
+                q8_load(a.q + s * a.ldq + at, a.n - at, v);
 #pragma unroll
                 for (int e = 0; e < Q8_CHUNK; ++e) v[e] *= f;
             } else {
 #pragma unroll
                 for (int e = 0; e < Q8_CHUNK; ++e) v[e] = 0.0f;
             }
-            q8_store<true>(a.out + row * a.ldo + c, have, v);
+            q8_store<true>(a.out + row * a.ldo + at, a.n - at, v);
         }
     }
 }
