@@ -6,17 +6,17 @@ namespace xsymv {
 namespace {
 
 // What a kernel costs, in microseconds, as measured on MI355X over a grid of
-// sizes (m 1 to 4096, n and k 256 to 28672, every number of shares) and
+// sizes (m 1 to 8000, n and k 128 to 28672, every number of shares) and
 // fitted: `launch`, and for every round of workgroups that the chip holds at
 // once `round` plus, for each of the share's steps, `alone` where a compute
-// unit runs one workgroup and `pair` where it runs two; but no less than W's
-// bytes take at `rate` TB/s.  Over that grid the kernel this chooses is 1 %
-// slower on average than the fastest one measured (at worst 1.6 times, at
-// sizes of a few microseconds).  The 64-row tile alone, at its best number of
-// shares, would be 1.07 (m = 65 to 128) to 1.36 times (m > 512) slower, and
-// without shares of k up to 5 times.
+// unit runs one workgroup, `full` where it runs all it can and between them
+// otherwise; but no less than W's bytes take at `rate` TB/s.  Over that grid
+// the kernel this chooses is 1 % slower on average than the fastest one
+// measured (at worst 1.7 times, at sizes of a few microseconds).  The 64-row
+// tile alone, at its best number of shares, would be 1.07 (m = 65 to 128) to
+// 1.36 times (m > 512) slower, and without shares of k up to 5 times.
 struct Cost {
-    float launch, alone, pair, round, rate;
+    float launch, alone, full, round, rate;
 };
 struct Kernel {
     Q8Kernel id;
@@ -29,33 +29,41 @@ struct Kernel {
 
 constexpr int ANY_M = 1 << 30;
 const Kernel LINES[] = {
-    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, {1.86f, 0.49f, 0.49f, 1.45f, 5.54f}},
-    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {3.05f, 0.37f, 1.22f, 0.01f, 5.98f}},
-    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.98f, 0.44f, 0.96f, 0.29f, 5.63f}},
-    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {2.98f, 0.23f, 0.48f, 1.29f, 5.33f}},
-    {Q8_TILE128X64, 128, 64, 8, 256, 1, 1, 65, ANY_M, {1.83f, 0.66f, 0.66f, 2.69f, 5.54f}},
-    {Q8_TILE128, 128, 128, 8, 128, 1, 1, 65, ANY_M, {1.58f, 0.51f, 0.51f, 3.49f, 5.99f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {2.01f, 0.69f, 0.69f, 4.87f, 4.79f}},
-    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {1.32f, 1.21f, 1.21f, 8.06f, 3.91f}},
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, {1.78f, 0.56f, 0.56f, 1.19f, 5.27f}},
+    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {2.99f, 0.37f, 1.16f, 0.48f, 6.44f}},
+    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.27f, 0.33f, 0.98f, 1.57f, 4.87f}},
+    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {2.30f, 0.24f, 0.53f, 1.69f, 5.92f}},
+    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, {2.76f, 0.45f, 1.04f, 0.76f, 4.37f}},
+    {Q8_TILE128X64, 128, 64, 8, 256, 1, 1, 65, ANY_M, {1.78f, 0.64f, 0.64f, 3.06f, 4.81f}},
+    {Q8_TILE128, 128, 128, 8, 128, 1, 1, 65, ANY_M, {1.47f, 0.48f, 0.48f, 4.01f, 5.60f}},
+    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, {2.96f, 0.73f, 1.23f, 1.97f, 4.07f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {1.60f, 0.69f, 0.69f, 5.62f, 4.68f}},
+    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.15f, 1.27f, 1.27f, 4.95f, 3.96f}},
 };
 const Kernel ANY[] = {
-    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.41f, 3.12f, 3.10f, 0.76f, 1.60f}},
-    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {3.59f, 0.46f, 1.01f, 0.24f, 7.99f}},
-    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.25f, 0.75f, 1.32f, 1.88f, 5.54f}},
-    {Q8_TILE64, 64, 64, 4, 256, 1, 2, 17, ANY_M, {3.44f, 0.74f, 1.25f, 1.99f, 5.64f}},
-    {Q8_TILE128, 128, 128, 8, 256, 1, 1, 65, ANY_M, {2.12f, 1.60f, 1.60f, 5.09f, 3.85f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {3.23f, 1.23f, 1.23f, 3.82f, 2.46f}},
-    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.40f, 1.23f, 1.23f, 7.34f, 3.96f}},
+    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.98f, 3.25f, 2.58f, 0.49f, 1.61f}},
+    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {4.15f, 0.47f, 1.05f, 0.14f, 7.60f}},
+    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.39f, 0.74f, 1.37f, 1.80f, 5.59f}},
+    {Q8_TILE64, 64, 64, 4, 256, 1, 2, 17, ANY_M, {3.36f, 0.77f, 1.28f, 2.19f, 5.35f}},
+    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, {2.39f, 0.78f, 1.60f, 1.59f, 3.38f}},
+    {Q8_TILE128, 128, 128, 8, 256, 1, 1, 65, ANY_M, {2.02f, 1.81f, 1.81f, 4.45f, 3.39f}},
+    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, {2.66f, 0.97f, 2.05f, 3.25f, 2.66f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {0.26f, 1.37f, 1.37f, 7.04f, 2.26f}},
+    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.15f, 1.56f, 1.56f, 7.54f, 3.18f}},
 };
 const Kernel REGS[] = {
-    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.31f, 3.84f, 3.82f, 0.01f, 1.91f}},
-    {Q8_TILE16, 16, 64, 4, 128, 1, 4, 1, 16, {2.54f, 0.81f, 0.98f, 0.01f, 3.82f}},
-    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {3.28f, 0.84f, 1.00f, 0.02f, 4.10f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {2.46f, 1.86f, 1.86f, 2.94f, 2.14f}},
+    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.47f, 3.66f, 2.70f, 0.03f, 1.80f}},
+    {Q8_TILE16, 16, 64, 4, 128, 1, 4, 1, 16, {3.16f, 0.67f, 1.62f, 0.01f, 3.78f}},
+    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {2.85f, 0.70f, 0.92f, 0.92f, 3.23f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {1.49f, 1.65f, 1.65f, 4.84f, 1.94f}},
 };
 
 // Adding the shares: a launch, and their sums written and read.
-constexpr float JOIN_LAUNCH = 3.0f, JOIN_MILLION = 1.42f;
+constexpr float JOIN_LAUNCH = 2.9f, JOIN_MILLION = 1.26f;
+// Copying rows to whole lines: a launch, and each byte read and written (what
+// was copied last is still cached when it is read, hence the rate).
+constexpr double COPY_LAUNCH = 2.9, COPY_BYTE = 2.0 / 6.5e6;
+constexpr size_t MAX_COPY = (size_t)1 << 30;
 constexpr int CUS = 256;
 constexpr long long MAX_PART = 1ll << 28;  // bytes of the shares' sums
 
@@ -73,18 +81,22 @@ double cost_of(const Kernel& c, int m, int n, int k, int splits, Q8Plan& p)
         return -1.0;  // a launch's threads are counted in 32 bits
     const int taken = (p.per + c.turn - 1) / c.turn;
     const long long slots = (long long)CUS * c.together, full = groups / slots, rest = groups % slots;
-    double t = (double)full * (taken * (c.together > 1 ? c.cost.pair : c.cost.alone) + c.cost.round);
-    if (rest > 0) t += taken * (rest <= CUS ? c.cost.alone : c.cost.pair) + c.cost.round;
+    double t = (double)full * (taken * (c.together > 1 ? c.cost.full : c.cost.alone) + c.cost.round);
+    if (rest > 0) {
+        const int load = (int)((rest + CUS - 1) / CUS);  // workgroups of the fullest compute unit
+        const float more = c.together > 1 ? (float)(load - 1) / (c.together - 1) : 0.0f;
+        t += taken * (c.cost.alone + (c.cost.full - c.cost.alone) * more) + c.cost.round;
+    }
     t = c.cost.launch + std::max(t, (double)n * k / c.cost.rate * 1e-6);
     if (p.splits > 1) t += JOIN_LAUNCH + JOIN_MILLION * 1e-6 * m * n * p.splits;
     return t;
 }
 
 template <int N>
-Q8Plan cheapest(const Kernel (&list)[N], int m, int n, int k)
+Q8Plan cheapest(const Kernel (&list)[N], int m, int n, int k, double& low)
 {
     Q8Plan best{};
-    double low = -1.0;
+    low = -1.0;
     for (const Kernel& c : list) {
         if (m < c.from || m > c.to) continue;
         for (int splits = 1; splits <= (c.id == Q8_STREAM ? 1 : 16); splits *= 2) {
@@ -113,10 +125,26 @@ Q8Plan q8_plan(int how, int m, int n, int k)
     const unsigned key = ((unsigned)m * 31u + (unsigned)n) * 31u + (unsigned)k * 7u + (unsigned)how;
     Known& e = known[key % 64];
     if (e.m == m && e.n == n && e.k == k && e.how == how && m > 0) return e.plan;
-    Q8Plan p = how == Q8_LINES ? cheapest(LINES, m, n, k)
-               : how == Q8_ANY ? cheapest(ANY, m, n, k)
-                               : cheapest(REGS, m, n, k);
+    double cost = 0.0;
+    Q8Plan p = how == Q8_LINES ? cheapest(LINES, m, n, k, cost)
+               : how == Q8_ANY ? cheapest(ANY, m, n, k, cost)
+                               : cheapest(REGS, m, n, k, cost);
     p.how = how;
+    if (how != Q8_LINES && k >= 16) {
+        // many rows: each is read often, and from whole lines a third faster
+        // (4096 x 28672 x 8192: 1098 us where they lie, 830 with the copy;
+        // 100 x 28672 x 8192: 71 and 142 us)
+        const size_t copy = align_up(((size_t)m + n) * q8_copy_ld(k));
+        double lines = 0.0;
+        Q8Plan c = cheapest(LINES, m, n, k, lines);
+        if (copy <= MAX_COPY && c.groups != 0 &&
+            (p.groups == 0 || lines + COPY_LAUNCH + COPY_BYTE * k * ((double)m + n) < cost)) {
+            p = c;
+            p.how = Q8_LINES;
+            p.ldc = q8_copy_ld(k);
+            p.copy = copy;
+        }
+    }
     e = Known{how, m, n, k, p};
     return p;
 }
@@ -132,6 +160,9 @@ extern "C" size_t xsymv_q8gemm_workspace_bytes(int m, int n, int k)
     for (int rows : {std::min(m, Q8_BLOCK), m % Q8_BLOCK})
         for (int cols : {std::min(n, Q8_BLOCK), n % Q8_BLOCK})
             for (int how : {Q8_REGS, Q8_LINES, Q8_ANY})
-                if (rows > 0 && cols > 0) most = std::max(most, q8_plan(how, rows, cols, k).part);
+                if (rows > 0 && cols > 0) {
+                    const Q8Plan p = q8_plan(how, rows, cols, k);
+                    most = std::max(most, p.copy + p.part);
+                }
     return most;
 }

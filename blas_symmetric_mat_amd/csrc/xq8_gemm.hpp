@@ -68,38 +68,48 @@ __device__ __forceinline__ q8v4 q8_load16(const signed char* p, int have)
     return v;
 }
 
-// A lane's results: rows i + 16 f, four neighbouring columns from j + 16 h on.
-// The scales are loaded ahead of the products (rows and columns past the last
-// take the last's, and are not stored).
+// The scales (and bias) of a lane's results: rows i + 16 f, four neighbouring
+// columns from j + 16 h on.  Rows and columns past the last take the last's,
+// and are not stored.  The ring loads them before its sums (1 x 4096 x 4096
+// 5.8 -> 5.6 us); the tiles after, since the registers they would hold cost
+// them more (128 x 128 at k = 128, odd strides: 20.7 us after, 25.2 before).
 template <class T, int FM, int FN>
-__device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
-                                          const q8v4 (&sum)[FM][FN])
-{
-    typedef T vec __attribute__((ext_vector_type(4)));
+struct Q8Scales {
     float si[FM], sj[FN][4], bj[FN][4];
+
+    __device__ __forceinline__ void load(const Q8GemmArgs<T>& g, int i, int j)
+    {
 #pragma unroll
-    for (int f = 0; f < FM; ++f) si[f] = g.sa[i + 16 * f < g.m ? i + 16 * f : g.m - 1];
-#pragma unroll
-    for (int h = 0; h < FN; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = j + 16 * h + e;
-            sj[h][e] = g.sw[c < g.n ? c : g.n - 1];
-        }
-    if (g.bias != nullptr) {
+        for (int f = 0; f < FM; ++f) si[f] = g.sa[i + 16 * f < g.m ? i + 16 * f : g.m - 1];
 #pragma unroll
         for (int h = 0; h < FN; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int c = j + 16 * h + e;
-                bj[h][e] = g.bias[c < g.n ? c : g.n - 1];
+                sj[h][e] = g.sw[c < g.n ? c : g.n - 1];
             }
-    } else {
+        if (g.bias != nullptr) {
 #pragma unroll
-        for (int h = 0; h < FN; ++h)
+            for (int h = 0; h < FN; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bj[h][e] = -0.0f;  // v + -0 is v
+                for (int e = 0; e < 4; ++e) {
+                    const int c = j + 16 * h + e;
+                    bj[h][e] = g.bias[c < g.n ? c : g.n - 1];
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < FN; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bj[h][e] = -0.0f;  // v + -0 is v
+        }
     }
+};
+
+template <class T, int FM, int FN>
+__device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
+                                          const Q8Scales<T, FM, FN>& s, const q8v4 (&sum)[FM][FN])
+{
+    typedef T vec __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         if (i + 16 * f >= g.m) break;
@@ -109,7 +119,8 @@ __device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
             const int c = j + 16 * h;
             vec t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = (T)((float)sum[f][h][e] * si[f] * sj[h][e] + bj[h][e]);
+            for (int e = 0; e < 4; ++e)
+                t[e] = (T)((float)sum[f][h][e] * s.si[f] * s.sj[h][e] + s.bj[h][e]);
             if (c + 4 <= g.n) {
                 __builtin_memcpy(row + c, &t, sizeof(t));
             } else {
@@ -119,6 +130,15 @@ __device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
             }
         }
     }
+}
+
+template <class T, int FM, int FN>
+__device__ __forceinline__ void q8_finish(const Q8GemmArgs<T>& g, int i, int j,
+                                          const q8v4 (&sum)[FM][FN])
+{
+    Q8Scales<T, FM, FN> s;
+    s.load(g, i, j);
+    q8_finish(g, i, j, s, sum);
 }
 
 // The same results as a share's sums.
@@ -617,6 +637,11 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) q8_fetch(to + 1024 * (2 * NT + i), oa[i], ra, k0);
     };
+    // (the first wave finishes the workgroup's results where there is one tile)
+    Q8Scales<T, 1, 1> scales;
+    constexpr bool EARLY = MT * NT == 1 && WK > 1;
+    if (EARLY && wave == 0 && g.splits == 1)
+        scales.load(g, i0 + (lane & 15), j0 + 4 * (lane >> 4));
     for (int t = 0; t < S - 1 && t < mine; ++t) fetch(t);
 
     q8v4 acc[MT][NT];
@@ -688,15 +713,44 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
 #pragma unroll
             for (int w = 0; w < WK; ++w) sum[0][0] += ((const q8v4*)lds[w])[tile * 64 + lane];
             const int ci = i0 + 16 * (tile / NT) + r, cj = j0 + 16 * (tile % NT) + 4 * piece;
-            if (g.splits == 1)
-                q8_finish<T, 1, 1>(g, ci, cj, sum);
-            else
+            if (g.splits == 1) {
+                if (!EARLY) scales.load(g, ci, cj);
+                q8_finish(g, ci, cj, scales, sum);
+            } else {
                 q8_partial<T, 1, 1>(g, share, ci, cj, sum);
+            }
         }
     } else if (g.splits == 1) {
         q8_finish<T, MT, NT>(g, i0 + r, j0 + 4 * piece, acc);
     } else {
         q8_partial<T, MT, NT>(g, share, i0 + r, j0 + 4 * piece, acc);
+    }
+}
+
+// ------------------------------------------------------------------ copies
+// Rows of A and of W to strides of whole lines, 16 bytes a lane from any
+// address; a row's last 16 bytes are written again by their own lane (k >= 16).
+struct Q8CopyArgs {
+    const signed char* a;
+    const signed char* w;
+    signed char* ca;
+    signed char* cw;
+    long long lda, ldw, ldc;
+    int m, n, k;
+};
+
+static __global__ __launch_bounds__(256) void q8_gemm_copy(Q8CopyArgs g)
+{
+    const long long rows = (long long)g.m + g.n;
+    for (long long r = blockIdx.x * 4ll + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4ll) {
+        const signed char* from = r < g.m ? g.a + r * g.lda : g.w + (r - g.m) * g.ldw;
+        signed char* to = r < g.m ? g.ca + r * g.ldc : g.cw + (r - g.m) * g.ldc;
+        for (int c = (threadIdx.x & 63) * 16; c < g.k; c += 1024) {
+            const int at = c < g.k - 16 ? c : g.k - 16;
+            q8v4 v;
+            __builtin_memcpy(&v, from + at, 16);
+            __builtin_memcpy(to + at, &v, 16);
+        }
     }
 }
 

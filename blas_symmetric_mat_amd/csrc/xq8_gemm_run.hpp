@@ -15,8 +15,10 @@ enum Q8Kernel {
     Q8_TILE16,
     Q8_TILE32,
     Q8_TILE64,
+    Q8_TILE64_SHORT,  // two buffers: more workgroups a compute unit, for few steps
     Q8_TILE128X64,
     Q8_TILE128,
+    Q8_TILE128_SHORT,
     Q8_TILE256X128,
     Q8_TILE256
 };
@@ -26,7 +28,17 @@ struct Q8Plan {
     int how, splits, per;  // how the rows are read; shares of k, steps in each
     unsigned groups;       // workgroups
     size_t part;           // bytes of workspace, for the shares' sums
+    int ldc;               // rows copied to this stride first (0: read where they lie)
+    size_t copy;           // bytes of workspace, for the copies
 };
+
+// Stride of copied rows: whole lines, and not a multiple of 4096 bytes, which
+// would put every row's beginning on the same memory channels.
+inline int q8_copy_ld(int k)
+{
+    const int ld = (k + 127) / 128 * 128;
+    return ld % 4096 == 0 ? ld + 128 : ld;
+}
 
 // The kernel for m x n x k with rows read as `how`.
 Q8Plan q8_plan(int how, int m, int n, int k);
@@ -49,6 +61,7 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
         switch (p.kernel) {
         case Q8_TILE128X64: return &q8_gemm_tile<T, 128, 64, 4, 2, 2, 3, Q8_LINES>;
         case Q8_TILE128: return &q8_gemm_tile<T, 128, 128, 2, 4, 1, 4, Q8_LINES>;
+        case Q8_TILE128_SHORT: return &q8_gemm_tile<T, 128, 128, 2, 4, 1, 2, Q8_LINES>;
         case Q8_TILE256X128: return &q8_gemm_tile<T, 256, 128, 4, 2, 1, 3, Q8_LINES>;
         case Q8_TILE256: return &q8_gemm_tile<T, 256, 256, 2, 4, 1, 2, Q8_LINES>;
         default: break;
@@ -57,12 +70,14 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
         switch (p.kernel) {
         case Q8_TILE16: return &q8_gemm_tile<T, 16, 64, 1, 4, 2, 3, Q8_LINES>;
         case Q8_TILE32: return &q8_gemm_tile<T, 32, 64, 2, 2, 2, 3, Q8_LINES>;
+        case Q8_TILE64_SHORT: return &q8_gemm_tile<T, 64, 64, 2, 2, 1, 2, Q8_LINES>;
         default: return &q8_gemm_tile<T, 64, 64, 2, 2, 1, 4, Q8_LINES>;
         }
     }
     if (p.how == Q8_ANY) {
         switch (p.kernel) {
         case Q8_TILE128: return &q8_gemm_tile<T, 128, 128, 2, 4, 2, 2, Q8_ANY>;
+        case Q8_TILE128_SHORT: return &q8_gemm_tile<T, 128, 128, 2, 4, 1, 2, Q8_ANY>;
         case Q8_TILE256X128: return &q8_gemm_tile<T, 256, 128, 4, 2, 1, 2, Q8_ANY>;
         case Q8_TILE256: return &q8_gemm_tile<T, 256, 256, 2, 4, 1, 2, Q8_ANY>;
         default: break;
@@ -71,6 +86,7 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
         switch (p.kernel) {
         case Q8_TILE16: return &q8_gemm_tile<T, 16, 64, 1, 4, 2, 3, Q8_ANY>;
         case Q8_TILE32: return &q8_gemm_tile<T, 32, 64, 2, 2, 2, 3, Q8_ANY>;
+        case Q8_TILE64_SHORT: return &q8_gemm_tile<T, 64, 64, 2, 2, 1, 2, Q8_ANY>;
         default: return &q8_gemm_tile<T, 64, 64, 2, 2, 2, 2, Q8_ANY>;
         }
     }
@@ -99,25 +115,38 @@ int gemm_block(Q8GemmArgs<T> g, int lda, int ldw, hipStream_t stream)
     const Q8GemmKernel<T> kernel = q8_kernel<T>(p, threads);
     g.splits = p.splits;
     g.per = p.per;
-    if (p.splits == 1) return q8_launch(kernel, p.groups, threads, stream, g);
+    if (p.splits == 1 && p.ldc == 0) return q8_launch(kernel, p.groups, threads, stream, g);
 
     int dev = 0;
     XSYMV_HIP(hipGetDevice(&dev));
     DeviceState* ds = device_state(dev);
     std::lock_guard<std::mutex> lk(device_mutex(ds));
     void* ws = nullptr;
-    const int rc = get_workspace(ds, stream, p.part, &ws);
+    const int rc = get_workspace(ds, stream, p.copy + p.part, &ws);
     if (rc) return rc;
-    g.part = static_cast<int*>(ws);
     TimedCall tc{};
     const int timing = timing_enabled();
     if (timing) {
-        XSYMV_HIP(timed_call_create(tc, timing));
+        XSYMV_HIP(timed_call_create(tc, timing, p.splits > 1));
     }
-    XSYMV_HIP(launch_k(kernel, dim3(p.groups), dim3(threads), stream, g, tc.e0, tc.e1));
-    const long long quads = (long long)g.m * (q8_part_ld(g.n) / 4);
-    XSYMV_HIP(launch_k(&q8_gemm_join<T>, dim3((unsigned)std::min((quads + 255) / 256, 2048ll)),
-                       dim3(256), stream, g, nullptr, tc.e2));
+    hipEvent_t start = tc.e0;  // the call's first kernel
+    if (p.ldc != 0) {
+        signed char* ca = static_cast<signed char*>(ws);
+        const Q8CopyArgs c{g.a, g.w, ca, ca + (size_t)g.m * p.ldc, g.lda, g.ldw, p.ldc, g.m, g.n, g.k};
+        const unsigned groups = (unsigned)std::min(((long long)g.m + g.n + 3) / 4, 1ll << 20);
+        XSYMV_HIP(launch_k(&q8_gemm_copy, dim3(groups), dim3(256), stream, c, start, nullptr));
+        start = nullptr;
+        g.a = c.ca;
+        g.w = c.cw;
+        g.lda = g.ldw = p.ldc;
+    }
+    g.part = reinterpret_cast<int*>(static_cast<char*>(ws) + p.copy);
+    XSYMV_HIP(launch_k(kernel, dim3(p.groups), dim3(threads), stream, g, start, tc.e1));
+    if (p.splits > 1) {
+        const long long quads = (long long)g.m * (q8_part_ld(g.n) / 4);
+        XSYMV_HIP(launch_k(&q8_gemm_join<T>, dim3((unsigned)std::min((quads + 255) / 256, 2048ll)),
+                           dim3(256), stream, g, nullptr, tc.e2));
+    }
     if (timing) timing_push(tc);
     return 0;
 }

@@ -377,17 +377,19 @@ def test_gemm_large(m, n, k, pad):
 # sizes at which each kernel of the product is the one chosen, k whole and shared out
 KERNELS = [("lines", 5, 33, 300), ("lines", 5, 33, 8200), ("lines", 5, 4100, 300),
            ("lines", 16, 4100, 16400), ("lines", 40, 33, 2060), ("lines", 100, 33, 2060),
-           ("lines", 100, 8200, 520), ("lines", 2050, 33, 8200), ("lines", 100, 16400, 300),
+           ("lines", 100, 8200, 780), ("lines", 2050, 33, 8200), ("lines", 100, 16400, 780),
            ("lines", 100, 4100, 8200), ("lines", 200, 16400, 300), ("lines", 4100, 33, 16400),
-           ("lines", 260, 30000, 300), ("lines", 130, 4100, 16400), ("lines", 5, 33, 520),
-           ("lines", 5, 500, 8200), ("any", 130, 1000, 16400), ("any", 100, 4100, 16400),
-           ("any", 5, 33, 4110),
-           ("any", 5, 16400, 300), ("any", 5, 33, 2060), ("any", 40, 33, 2060),
-           ("any", 100, 33, 1040), ("any", 100, 16400, 300), ("any", 100, 4100, 4110),
-           ("any", 130, 16400, 300), ("any", 4100, 33, 16400), ("any", 260, 16400, 300),
-           ("any", 130, 4100, 8200),
-           ("odd", 5, 16400, 300), ("odd", 5, 33, 2060), ("odd", 40, 33, 1040),
-           ("odd", 200, 16400, 300), ("odd", 130, 2000, 8200)]
+           ("lines", 260, 30000, 520), ("lines", 130, 4100, 16400), ("lines", 5, 1000, 8200),
+           ("lines", 40, 16400, 300), ("lines", 200, 16400, 520), ("lines", 130, 8200, 8200),
+           ("any", 5, 16400, 300), ("any", 5, 33, 4110), ("any", 40, 33, 2060),
+           ("any", 100, 33, 300), ("any", 100, 33, 8200), ("any", 100, 16400, 780),
+           ("any", 100, 4100, 4110), ("any", 100, 30000, 2060), ("any", 2050, 130, 8200),
+           ("any", 200, 16400, 300), ("any", 200, 4100, 4110), ("any", 260, 30000, 300),
+           ("any", 100, 4100, 16400), ("any", 600, 1000, 8200), ("any", 1000, 16400, 300),
+           ("any", 1030, 1000, 1040), ("any", 4100, 2000, 300),
+           ("odd", 5, 16400, 300), ("odd", 5, 33, 4110), ("odd", 40, 33, 300),
+           ("odd", 40, 33, 2060), ("odd", 200, 16400, 300), ("odd", 130, 2000, 8200),
+           ("odd", 1030, 500, 8200), ("odd", 2050, 2000, 520)]
 
 
 @pytest.mark.parametrize("how,m,n,k", KERNELS)
