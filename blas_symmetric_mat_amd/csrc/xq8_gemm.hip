@@ -12,8 +12,9 @@ namespace {
 // unit runs one workgroup, `full` where it runs all it can and between them
 // otherwise; but no less than W's bytes take at `rate` TB/s.  Over that grid
 // the kernel this chooses is 1 % slower on average than the fastest one
-// measured (at worst 1.7 times, at sizes of a few microseconds).  The 64-row
-// tile alone, at its best number of shares, would be 1.07 (m = 65 to 128) to
+// measured, 4 % for up to 16 rows at odd strides (at worst 1.7 times, at sizes
+// of a few microseconds).  The ring at odd strides is chosen at 32 of 144 sizes
+// there, 1.19 times faster than the next.  The 64-row tile alone, at its best number of shares, would be 1.07 (m = 65 to 128) to
 // 1.36 times (m > 512) slower, and without shares of k up to 5 times.
 struct Cost {
     float launch, alone, full, round, rate;
@@ -41,6 +42,7 @@ const Kernel LINES[] = {
     {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.15f, 1.27f, 1.27f, 4.95f, 3.96f}},
 };
 const Kernel ANY[] = {
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, {3.39f, 0.50f, 0.50f, 1.34f, 4.14f}},
     {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.98f, 3.25f, 2.58f, 0.49f, 1.61f}},
     {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {4.15f, 0.47f, 1.05f, 0.14f, 7.60f}},
     {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.39f, 0.74f, 1.37f, 1.80f, 5.59f}},

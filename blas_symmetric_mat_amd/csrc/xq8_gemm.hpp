@@ -15,9 +15,16 @@
 // receives four neighbouring elements of a row of C.  Which byte of a step
 // meets which multiplier does not matter as long as both operands agree.
 //
-// Bytes past k are loaded as zeros (in both operands), rows past m or n are
-// the last row again, whose results are not stored: no access leaves the
-// operands.
+// Bytes past k count as zeros, rows past m or n are the last row again, whose
+// results are not stored: no access leaves the operands.
+//
+// Three kinds of kernel make it, each at the sizes where it measured fastest:
+// tiles of 16 to 256 rows of both operands through LDS, whose waves share what
+// is loaded; for at most 16 rows a ring of buffers for each wave, which waits
+// for no other wave; and for the shortest of those rows at odd strides straight
+// loads to registers, which have nothing to set up.  Where there are fewer
+// tiles than the chip holds at once, k is split into shares, whose sums are
+// added by another launch.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -42,7 +49,7 @@ struct Q8GemmArgs {
     T* c;
     long long lda, ldw, ldc;
     int m, n, k;
-    // k in `splits` shares of `per` steps of 128 bytes, their sums in `part`
+    // k in `splits` shares of `per` of the kernel's steps, their sums in `part`
     // (one share: straight to C); the stream kernel takes k whole
     int* part;
     int splits, per;
@@ -157,86 +164,55 @@ __device__ __forceinline__ void q8_partial(const Q8GemmArgs<T>& g, unsigned shar
     }
 }
 
-// Few rows: the bytes of W bound the product, and W is used once per
-// workgroup, so it goes from memory to registers without LDS.  A workgroup of
-// WK waves makes a block of 16 MT rows of C by 16 NT columns; the waves take
-// the 256-byte steps of k in turn and add their sums through LDS.
-template <class T, int MT, int NT, int WK>
-__global__ __launch_bounds__(64 * WK) void q8_gemm_stream(Q8GemmArgs<T> g)
+// ------------------------------------------------ few rows: straight to registers
+// Rows at any address, 16 x 16 results a workgroup: the eight waves take the
+// 256-byte steps of k in turn, load both operands' 16-byte pieces where the
+// multiplier wants them, and add their sums through LDS.  A load brings 64
+// bytes of each of 16 rows, so lines are fetched in halves and long rows take
+// twice as long as with the ring (16 x 1024 x 8192 at odd strides 21.6 us, the
+// ring 8.3); with nothing to set up, short ones are quicker (1 x 1024 x 256
+// 3.2 us, the ring 3.8).
+constexpr int Q8_WAVES = 8;  // of a workgroup of this kernel and the ring
+
+template <class T>
+__global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_stream(Q8GemmArgs<T> g)
 {
     constexpr int U = 4;  // 64-byte steps a wave loads at once
-    __shared__ int red[WK > 1 ? WK : 1][MT * NT][4][64];
+    __shared__ q8v4 red[Q8_WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int mblocks = (g.m + 16 * MT - 1) / (16 * MT);
-    const int i0 = (int)(blockIdx.x % mblocks) * 16 * MT;
-    const int j0 = (int)(blockIdx.x / mblocks) * 16 * NT;
+    const int mblocks = (g.m + 15) / 16;
+    const int i0 = (int)(blockIdx.x % mblocks) * 16, j0 = (int)(blockIdx.x / mblocks) * 16;
     const int r = lane & 15, piece = (lane >> 4) * 16;
-    const signed char* pa[MT];
-    const signed char* pw[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = i0 + 16 * i + r;
-        pa[i] = g.a + (row < g.m ? row : g.m - 1) * g.lda + piece;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int row = j0 + 16 * j + r;
-        pw[j] = g.w + (row < g.n ? row : g.n - 1) * g.ldw + piece;
-    }
-    q8v4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
-
-    for (int k0 = wave * 64 * U; k0 < g.k; k0 += WK * 64 * U) {
-        q8v4 va[U][MT], vw[U][NT];
+    const signed char* pa = g.a + (i0 + r < g.m ? i0 + r : g.m - 1) * g.lda + piece;
+    const signed char* pw = g.w + (j0 + r < g.n ? j0 + r : g.n - 1) * g.ldw + piece;
+    q8v4 acc = {0, 0, 0, 0};
+    for (int k0 = wave * 64 * U; k0 < g.k; k0 += Q8_WAVES * 64 * U) {
+        q8v4 va[U], vw[U];
         if (k0 + 64 * U <= g.k) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) __builtin_memcpy(&vw[u][j], pw[j] + k0 + 64 * u, 16);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) __builtin_memcpy(&va[u][i], pa[i] + k0 + 64 * u, 16);
+                __builtin_memcpy(&vw[u], pw + k0 + 64 * u, 16);
+                __builtin_memcpy(&va[u], pa + k0 + 64 * u, 16);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int have = g.k - k0 - 64 * u - piece;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) vw[u][j] = q8_load16(pw[j] + k0 + 64 * u, have);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) va[u][i] = q8_load16(pa[i] + k0 + 64 * u, have);
+                vw[u] = q8_load16(pw + k0 + 64 * u, have);
+                va[u] = q8_load16(pa + k0 + 64 * u, have);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vw[u][j], va[u][i], acc[i][j],
-                                                                      0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(vw[u], va[u], acc, 0, 0, 0);
     }
-    if constexpr (WK > 1) {
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) red[wave][i * NT + j][e][lane] = acc[i][j][e];
-        __syncthreads();
-        for (int tile = wave; tile < MT * NT; tile += WK) {
-            q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
-#pragma unroll
-            for (int w = 0; w < WK; ++w)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum[0][0][e] += red[w][tile][e][lane];
-            q8_finish<T, 1, 1>(g, i0 + 16 * (tile / NT) + r, j0 + 16 * (tile % NT) + piece / 4, sum);
-        }
-    } else {
-        q8_finish<T, MT, NT>(g, i0 + r, j0 + piece / 4, acc);
-    }
+    for (int w = 0; w < Q8_WAVES; ++w) sum[0][0] += red[w][lane];
+    q8_finish<T, 1, 1>(g, i0 + r, j0 + piece / 4, sum);
 }
 
 // ------------------------------------------------------------------- tiles
@@ -323,6 +299,44 @@ __device__ __forceinline__ void q8_tile(unsigned mt, unsigned nt, unsigned& ti, 
     const unsigned in = k - band * 8 * nt;
     ti = 8 * band + in % rows;
     tj = in / rows;
+}
+
+// 16 bytes of a row in LDS, `at` (plus `k` into the step), as Q8_LINES lays
+// them out; with Q8_ANY the three words of 8 bytes that hold them where the
+// row starts at byte `shift` of its first piece, and then (q8_bytes) the bytes.
+template <int HOW, class V>
+__device__ __forceinline__ void q8_read(V& x, const signed char* p, int at, int k, int shift)
+{
+    if constexpr (HOW == Q8_ANY) {
+        typedef int two __attribute__((ext_vector_type(2)));
+        typedef const volatile __attribute__((address_space(3))) two word;
+        word* v = (word*)(p + at + k + (shift & 8));
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            const two y = v[e];
+            x[2 * e] = y.x;
+            x[2 * e + 1] = y.y;
+        }
+    } else {
+        x = *(const V*)(p + (at ^ k));
+    }
+}
+
+template <int HOW, class V>
+__device__ __forceinline__ q8v4 q8_bytes(const V& x, int shift)
+{
+    if constexpr (HOW == Q8_ANY) {
+        const int odd = -(shift >> 2 & 1);  // all bits where they start in the second half
+        int y[5];
+        q8v4 v;
+#pragma unroll
+        for (int e = 0; e < 5; ++e) y[e] = (x[e + 1] & odd) | (x[e] & ~odd);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbyte(y[e + 1], y[e], shift & 3);
+        return v;
+    } else {
+        return x;
+    }
 }
 
 template <class T, int BM, int BN, int WM, int WN, int Q, int S, int HOW>
@@ -446,42 +460,15 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_gemm_tile(Q8GemmArgs<T> g)
         for (int j = 0; j < FN; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
     auto read = [&](int t, int h, int q) {
         const signed char* p = lds + (t % S) * BUF;
-        words& x = q < FN ? xw[h & 1][q] : xa[h & 1][q - FN];
         p += q < FN ? fw + q * 16 * PITCH : fa + (q - FN) * 16 * PITCH;
-        if constexpr (HOW == Q8_ANY) {
-            typedef int two __attribute__((ext_vector_type(2)));
-            typedef const volatile __attribute__((address_space(3))) two word;
-            word* v = (word*)(p + pl + h * 64 + ((q < FN ? sw : sa) & 8));
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                const two y = v[e];
-                x[2 * e] = y.x;
-                x[2 * e + 1] = y.y;
-            }
-        } else {
-            x = *(const words*)(p + (pl ^ (h * 64)));
-        }
-    };
-    auto bytes = [&](const words& x, int shift) {
-        if constexpr (HOW == Q8_ANY) {
-            const int odd = -(shift >> 2 & 1);  // all bits where it starts in the second half
-            int y[5];
-            q8v4 v;
-#pragma unroll
-            for (int e = 0; e < 5; ++e) y[e] = (x[e + 1] & odd) | (x[e] & ~odd);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbyte(y[e + 1], y[e], shift & 3);
-            return v;
-        } else {
-            return x;
-        }
+        q8_read<HOW>(q < FN ? xw[h & 1][q] : xa[h & 1][q - FN], p, pl, h * 64, q < FN ? sw : sa);
     };
     auto multiply = [&](int h, int i, int have) {  // `have` bytes of the step before k
         if (i == 0) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) bw[j] = bytes(xw[h & 1][j], sw);
+            for (int j = 0; j < FN; ++j) bw[j] = q8_bytes<HOW>(xw[h & 1][j], sw);
         }
-        q8v4 ba = bytes(xa[h & 1][i], sa);
+        q8v4 ba = q8_bytes<HOW>(xa[h & 1][i], sa);
         if (have < BK) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -573,57 +560,66 @@ __global__ __launch_bounds__(256) void q8_gemm_join(Q8GemmArgs<T> g)
     }
 }
 
-// ------------------------------------------- few rows, aligned: a ring a wave
+// ---------------------------------------------------- few rows: a ring a wave
 // The bytes of W bound the product, so what counts is loads in flight and
-// whole lines.  Every wave owns 16 NT columns of C (rows of W), a share of k
-// and a ring of S buffers in LDS, each one step of 128 bytes of its rows of W
-// and of the 16 MT rows of A (permuted as in the tiles); the loads go to LDS
-// by themselves, 8 whole lines each, S - 1 steps ahead of the step that is
-// multiplied.  No wave waits for another until the sums are added: the waves
-// of a workgroup share its columns and take the steps of k in turn.
+// whole lines.  A workgroup makes 16 x 16 results; its waves take the
+// 128-byte steps of the share of k in turn, each with a ring of S buffers in
+// LDS of its own, laid out as in the tiles; the loads go to LDS by themselves
+// (HOW: Q8_LINES or Q8_ANY), S - 1 steps ahead of the step that is multiplied.
+// No wave waits for another until the sums are added.  The end of k goes
+// straight from memory to the multiplier's layout, with zeros past k; with
+// Q8_ANY the whole steps end 16 bytes or more before k, so that the ninth piece
+// of the last one lies within the row.  (16 x 28672 x 8192: 43 us, 5.5 TB/s,
+// where 6.6 is what reading alone reaches; at 16 x 4096 x 8192 12.6 us at odd
+// strides, the tile with shares of k 12.6 to 13.5, at 16 x 1024 x 4096 7.5 and
+// 9.4.)
 template <int N>
 __device__ __forceinline__ void q8_wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <class T, int MT, int NT, int WK, int S>
-__global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
+template <class T, int S, int HOW>
+__global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_ring(Q8GemmArgs<T> g)
 {
-    constexpr int BK = 128, LOADS = 2 * (MT + NT), SLOT = 16 * (MT + NT) * BK;
-    static_assert((S - 1) * LOADS < 64, "the counter of outstanding loads");
-    static_assert(S * SLOT >= MT * NT * 1024, "a wave's sums fit its ring");
-    __shared__ __attribute__((aligned(1024))) signed char lds[WK][S * SLOT];
+    // CB loads of 64 pieces for 16 rows (with Q8_ANY the last one reaches past
+    // them), of W and then of A
+    constexpr int BK = 128, CH = HOW == Q8_ANY ? 9 : 8, CB = (16 * CH + 63) / 64;
+    constexpr int BLOCK = CB * 1024, SLOT = 2 * BLOCK;
+    __shared__ __attribute__((aligned(1024))) signed char lds[Q8_WAVES][S * SLOT];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     unsigned ti, tj, share;
-    q8_tile((g.m + 16 * MT - 1) / (16 * MT), (g.n + 16 * NT - 1) / (16 * NT), ti, tj, share);
-    const int i0 = (int)ti * 16 * MT, j0 = (int)tj * 16 * NT;
-    // this share's whole steps, t0 and on; a partial one is the first share's
-    const int all = g.k / BK, t0 = (int)share * g.per;
+    q8_tile((g.m + 15) / 16, (g.n + 15) / 16, ti, tj, share);
+    const int i0 = (int)ti * 16, j0 = (int)tj * 16;
+    // this share's whole steps, t0 and on; the rest of k is the first share's
+    const int all = HOW == Q8_ANY ? (g.k - 16) / BK : g.k / BK, t0 = (int)share * g.per;
     const int steps = all - t0 < g.per ? all - t0 : g.per;
-    const int mine = (steps - wave + WK - 1) / WK;  // this wave's steps: wave, wave + WK, ...
+    const int mine = (steps - wave + Q8_WAVES - 1) / Q8_WAVES;  // steps wave, wave + 8, ...
     // rows at a multiple of 4096 bytes lie on the same memory channels, column
     // by column, so there each workgroup of a die starts at another step
+    // (16 x 8192 x 28672: 47 -> 41 us; at other strides it costs 2 %)
     const int turn =
         g.ldw % 4096 == 0 && mine > 0 ? (int)((blockIdx.x / 8) % (unsigned)mine) : 0;
     const signed char* ga = g.a + i0 * g.lda;
     const signed char* gw = g.w + j0 * g.ldw;
     const int ma = g.m - 1 - i0, mw = g.n - 1 - j0;
+    const int sha = HOW == Q8_ANY ? (int)((size_t)ga & 15) : 0;
+    const int shw = HOW == Q8_ANY ? (int)((size_t)gw & 15) : 0;
 
-    unsigned oa[2 * MT], ow[2 * NT];
+    unsigned oa[CB], ow[CB];
+    auto offset = [&](int i, int last, long long ld, int sh) {  // load i of an operand's rows
+        const int piece = i * 64 + lane, c = piece % CH, row = piece / CH;
+        const unsigned o = (unsigned)((row < last ? row : last) * ld + sh);
+        return HOW == Q8_ANY ? (o & ~15u) + 16 * c : o + 16 * (c ^ ((row >> 1) & 7));
+    };
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-        const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-        oa[i] = (unsigned)(row < ma ? row : ma) * (unsigned)g.lda + 16 * c;
+    for (int i = 0; i < CB; ++i) {
+        oa[i] = offset(i, ma, g.lda, sha);
+        ow[i] = offset(i, mw, g.ldw, shw);
     }
-#pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
-        const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-        ow[i] = (unsigned)(row < mw ? row : mw) * (unsigned)g.ldw + 16 * c;
-    }
-    const q8v4 ra = q8_rsrc(ga, 0xffffffffu), rw = q8_rsrc(gw, 0xffffffffu);
+    const q8v4 ra = q8_rsrc(ga - sha, 0xffffffffu), rw = q8_rsrc(gw - shw, 0xffffffffu);
     signed char* ring = lds[wave];
     const unsigned base =
         (unsigned)(unsigned long long)(__attribute__((address_space(3))) void*)ring;
@@ -631,100 +627,63 @@ __global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
         int turned = t + turn;
         turned -= turned >= mine ? mine : 0;
         const unsigned to = base + (unsigned)(t % S) * SLOT;
-        const unsigned k0 = (unsigned)(t0 + turned * WK + wave) * BK;
+        const unsigned k0 = (unsigned)(t0 + turned * Q8_WAVES + wave) * BK;
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) q8_fetch(to + 1024 * i, ow[i], rw, k0);
+        for (int i = 0; i < CB; ++i) q8_fetch(to + 1024 * i, ow[i], rw, k0);
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) q8_fetch(to + 1024 * (2 * NT + i), oa[i], ra, k0);
+        for (int i = 0; i < CB; ++i) q8_fetch(to + BLOCK + 1024 * i, oa[i], ra, k0);
     };
-    // (the first wave finishes the workgroup's results where there is one tile)
-    Q8Scales<T, 1, 1> scales;
-    constexpr bool EARLY = MT * NT == 1 && WK > 1;
-    if (EARLY && wave == 0 && g.splits == 1)
-        scales.load(g, i0 + (lane & 15), j0 + 4 * (lane >> 4));
+    const int r = lane & 15, piece = lane >> 4;
+    Q8Scales<T, 1, 1> scales;  // (the first wave finishes the results)
+    if (wave == 0 && g.splits == 1) scales.load(g, i0 + r, j0 + 4 * piece);
     for (int t = 0; t < S - 1 && t < mine; ++t) fetch(t);
 
-    q8v4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
-    const int r = lane & 15, piece = lane >> 4;
-    if (g.k % BK != 0 && share == 0 && wave == WK - 1) {
-        // the partial step, straight from memory to the multiplier's layout
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k0 = all * BK + 64 * h + 16 * piece, have = g.k - k0;
-            q8v4 xa[MT], xw[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                xw[j] = q8_load16(gw + (16 * j + r < mw ? 16 * j + r : mw) * g.ldw + k0, have);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                xa[i] = q8_load16(ga + (16 * i + r < ma ? 16 * i + r : ma) * g.lda + k0, have);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[j], xa[i], acc[i][j], 0, 0,
-                                                                      0);
+    q8v4 acc = {0, 0, 0, 0};
+    if (share == 0 && wave == Q8_WAVES - 1) {
+#pragma unroll 1
+        for (int k0 = all * BK; k0 < g.k; k0 += 64) {
+            const int at = k0 + 16 * piece;
+            const q8v4 xw = q8_load16(gw + (r < mw ? r : mw) * g.ldw + at, g.k - at);
+            const q8v4 xa = q8_load16(ga + (r < ma ? r : ma) * g.lda + at, g.k - at);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw, xa, acc, 0, 0, 0);
         }
     }
 
-    const int perm = r * BK + ((piece ^ ((r >> 1) & 7)) * 16);
+    typedef int words __attribute__((ext_vector_type(HOW == Q8_ANY ? 8 : 4)));
+    const int sa = HOW == Q8_ANY ? (int)((size_t)(ga + r * g.lda) & 15) : 0;
+    const int sw = HOW == Q8_ANY ? (int)((size_t)(gw + r * g.ldw) & 15) : 0;
+    const int pl = r * 16 * CH + (HOW == Q8_ANY ? piece : piece ^ ((r >> 1) & 7)) * 16;
     for (int t = 0; t < mine; ++t) {
         if (t + S - 1 < mine) {
             fetch(t + S - 1);  // into the buffer of step t - 1, which has been read
-            q8_wait_loads<(S - 1) * LOADS>();
+            q8_wait_loads<(S - 1) * 2 * CB>();
         } else {
             q8_wait_loads<0>();
         }
         const signed char* p = ring + (t % S) * SLOT;
-        q8v4 xa[2][MT], xw[2][NT];
+        words xa[2], xw[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                xw[h][j] = *(const q8v4*)(p + (perm ^ (64 * h)) + 16 * BK * j);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                xa[h][i] = *(const q8v4*)(p + (perm ^ (64 * h)) + 16 * BK * (NT + i));
+            q8_read<HOW>(xw[h], p, pl, h * 64, sw);
+            q8_read<HOW>(xa[h], p + BLOCK, pl, h * 64, sa);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[h][j], xa[h][i], acc[i][j],
-                                                                      0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(q8_bytes<HOW>(xw[h], sw),
+                                                        q8_bytes<HOW>(xa[h], sa), acc, 0, 0, 0);
     }
-    if constexpr (WK > 1) {
-        // the waves' sums, in their rings, which nothing is on its way to
-        q8v4* red = (q8v4*)ring;
+    // the waves' sums, in their rings, which nothing is on its way to
+    ((q8v4*)ring)[lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) red[(i * NT + j) * 64 + lane] = acc[i][j];
-        __syncthreads();
-        for (int tile = wave; tile < MT * NT; tile += WK) {
-            q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
-#pragma unroll
-            for (int w = 0; w < WK; ++w) sum[0][0] += ((const q8v4*)lds[w])[tile * 64 + lane];
-            const int ci = i0 + 16 * (tile / NT) + r, cj = j0 + 16 * (tile % NT) + 4 * piece;
-            if (g.splits == 1) {
-                if (!EARLY) scales.load(g, ci, cj);
-                q8_finish(g, ci, cj, scales, sum);
-            } else {
-                q8_partial<T, 1, 1>(g, share, ci, cj, sum);
-            }
-        }
-    } else if (g.splits == 1) {
-        q8_finish<T, MT, NT>(g, i0 + r, j0 + 4 * piece, acc);
-    } else {
-        q8_partial<T, MT, NT>(g, share, i0 + r, j0 + 4 * piece, acc);
-    }
+    for (int w = 0; w < Q8_WAVES; ++w) sum[0][0] += ((const q8v4*)lds[w])[lane];
+    if (g.splits == 1)
+        q8_finish(g, i0 + r, j0 + 4 * piece, scales, sum);
+    else
+        q8_partial<T, 1, 1>(g, share, i0 + r, j0 + 4 * piece, sum);
 }
 
 // ------------------------------------------------------------------ copies

@@ -55,8 +55,9 @@ template <class T>
 Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
 {
     threads = 512;
-    if (p.kernel == Q8_RING) return &q8_gemm_ring<T, 1, 1, 8, 3>;
-    if (p.kernel == Q8_STREAM) return &q8_gemm_stream<T, 1, 1, 8>;
+    if (p.kernel == Q8_RING)
+        return p.how == Q8_LINES ? &q8_gemm_ring<T, 3, Q8_LINES> : &q8_gemm_ring<T, 2, Q8_ANY>;
+    if (p.kernel == Q8_STREAM) return &q8_gemm_stream<T>;
     if (p.how == Q8_LINES) {
         switch (p.kernel) {
         case Q8_TILE128X64: return &q8_gemm_tile<T, 128, 64, 4, 2, 2, 3, Q8_LINES>;

@@ -382,6 +382,8 @@ KERNELS = [("lines", 5, 33, 300), ("lines", 5, 33, 8200), ("lines", 5, 4100, 300
            ("lines", 260, 30000, 520), ("lines", 130, 4100, 16400), ("lines", 5, 1000, 8200),
            ("lines", 40, 16400, 300), ("lines", 200, 16400, 520), ("lines", 130, 8200, 8200),
            ("any", 5, 16400, 300), ("any", 5, 33, 4110), ("any", 40, 33, 2060),
+           ("any", 5, 33, 300), ("any", 16, 130, 2060), ("any", 5, 33, 8200),
+           ("any", 5, 500, 8200),
            ("any", 100, 33, 300), ("any", 100, 33, 8200), ("any", 100, 16400, 780),
            ("any", 100, 4100, 4110), ("any", 100, 30000, 2060), ("any", 2050, 130, 8200),
            ("any", 200, 16400, 300), ("any", 200, 4100, 4110), ("any", 260, 30000, 300),
