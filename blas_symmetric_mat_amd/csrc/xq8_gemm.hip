@@ -13,9 +13,10 @@ namespace {
 // otherwise; but no less than W's bytes take at `rate` TB/s.  Over that grid
 // the kernel this chooses is 1 % slower on average than the fastest one
 // measured, 4 % for up to 16 rows at odd strides (at worst 1.7 times, at sizes
-// of a few microseconds).  The ring at odd strides is chosen at 32 of 144 sizes
-// there, 1.19 times faster than the next.  The 64-row tile alone, at its best number of shares, would be 1.07 (m = 65 to 128) to
-// 1.36 times (m > 512) slower, and without shares of k up to 5 times.
+// of a few microseconds).  The 64-row tile alone, at its best number of shares,
+// would be 1.07 (m = 65 to 128) to 1.36 times (m > 512) slower, and without
+// shares of k up to 5 times.  At odd strides the ring is chosen at 32 of the
+// 144 sizes of up to 16 rows, and 1.19 times faster there than the next.
 struct Cost {
     float launch, alone, full, round, rate;
 };
@@ -25,39 +26,40 @@ struct Kernel {
     int step, turn;     // bytes of k a step; steps that waves take side by side
     int together;       // workgroups a compute unit runs at once
     int from, to;       // rows it is meant for
+    float cut;          // factor of a step where rows cut lines (Q8_LINES)
     Cost cost;
 };
 
 constexpr int ANY_M = 1 << 30;
 const Kernel LINES[] = {
-    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, {1.78f, 0.56f, 0.56f, 1.19f, 5.27f}},
-    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {2.99f, 0.37f, 1.16f, 0.48f, 6.44f}},
-    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.27f, 0.33f, 0.98f, 1.57f, 4.87f}},
-    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {2.30f, 0.24f, 0.53f, 1.69f, 5.92f}},
-    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, {2.76f, 0.45f, 1.04f, 0.76f, 4.37f}},
-    {Q8_TILE128X64, 128, 64, 8, 256, 1, 1, 65, ANY_M, {1.78f, 0.64f, 0.64f, 3.06f, 4.81f}},
-    {Q8_TILE128, 128, 128, 8, 128, 1, 1, 65, ANY_M, {1.47f, 0.48f, 0.48f, 4.01f, 5.60f}},
-    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, {2.96f, 0.73f, 1.23f, 1.97f, 4.07f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {1.60f, 0.69f, 0.69f, 5.62f, 4.68f}},
-    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.15f, 1.27f, 1.27f, 4.95f, 3.96f}},
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, 1.15f, {1.78f, 0.56f, 0.56f, 1.19f, 5.27f}},
+    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, 1.12f, {2.99f, 0.37f, 1.16f, 0.48f, 6.44f}},
+    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, 1.15f, {2.27f, 0.33f, 0.98f, 1.57f, 4.87f}},
+    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, 1.35f, {2.30f, 0.24f, 0.53f, 1.69f, 5.92f}},
+    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, 1.15f, {2.76f, 0.45f, 1.04f, 0.76f, 4.37f}},
+    {Q8_TILE128X64, 128, 64, 8, 256, 1, 1, 65, ANY_M, 1.20f, {1.78f, 0.64f, 0.64f, 3.06f, 4.81f}},
+    {Q8_TILE128, 128, 128, 8, 128, 1, 1, 65, ANY_M, 1.37f, {1.47f, 0.48f, 0.48f, 4.01f, 5.60f}},
+    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, 1.20f, {2.96f, 0.73f, 1.23f, 1.97f, 4.07f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, 1.27f, {1.60f, 0.69f, 0.69f, 5.62f, 4.68f}},
+    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, 1.19f, {4.15f, 1.27f, 1.27f, 4.95f, 3.96f}},
 };
 const Kernel ANY[] = {
-    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, {3.39f, 0.50f, 0.50f, 1.34f, 4.14f}},
-    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.98f, 3.25f, 2.58f, 0.49f, 1.61f}},
-    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, {4.15f, 0.47f, 1.05f, 0.14f, 7.60f}},
-    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, {2.39f, 0.74f, 1.37f, 1.80f, 5.59f}},
-    {Q8_TILE64, 64, 64, 4, 256, 1, 2, 17, ANY_M, {3.36f, 0.77f, 1.28f, 2.19f, 5.35f}},
-    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, {2.39f, 0.78f, 1.60f, 1.59f, 3.38f}},
-    {Q8_TILE128, 128, 128, 8, 256, 1, 1, 65, ANY_M, {2.02f, 1.81f, 1.81f, 4.45f, 3.39f}},
-    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, {2.66f, 0.97f, 2.05f, 3.25f, 2.66f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {0.26f, 1.37f, 1.37f, 7.04f, 2.26f}},
-    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, {4.15f, 1.56f, 1.56f, 7.54f, 3.18f}},
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, 1.0f, {3.39f, 0.50f, 0.50f, 1.34f, 4.14f}},
+    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, 1.0f, {0.98f, 3.25f, 2.58f, 0.49f, 1.61f}},
+    {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, 1.0f, {4.15f, 0.47f, 1.05f, 0.14f, 7.60f}},
+    {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, 1.0f, {2.39f, 0.74f, 1.37f, 1.80f, 5.59f}},
+    {Q8_TILE64, 64, 64, 4, 256, 1, 2, 17, ANY_M, 1.0f, {3.36f, 0.77f, 1.28f, 2.19f, 5.35f}},
+    {Q8_TILE64_SHORT, 64, 64, 4, 128, 1, 4, 17, ANY_M, 1.0f, {2.39f, 0.78f, 1.60f, 1.59f, 3.38f}},
+    {Q8_TILE128, 128, 128, 8, 256, 1, 1, 65, ANY_M, 1.0f, {2.02f, 1.81f, 1.81f, 4.45f, 3.39f}},
+    {Q8_TILE128_SHORT, 128, 128, 8, 128, 1, 2, 65, ANY_M, 1.0f, {2.66f, 0.97f, 2.05f, 3.25f, 2.66f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, 1.0f, {0.26f, 1.37f, 1.37f, 7.04f, 2.26f}},
+    {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, 1.0f, {4.15f, 1.56f, 1.56f, 7.54f, 3.18f}},
 };
 const Kernel REGS[] = {
-    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, {0.47f, 3.66f, 2.70f, 0.03f, 1.80f}},
-    {Q8_TILE16, 16, 64, 4, 128, 1, 4, 1, 16, {3.16f, 0.67f, 1.62f, 0.01f, 3.78f}},
-    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, {2.85f, 0.70f, 0.92f, 0.92f, 3.23f}},
-    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, {1.49f, 1.65f, 1.65f, 4.84f, 1.94f}},
+    {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, 1.0f, {0.47f, 3.66f, 2.70f, 0.03f, 1.80f}},
+    {Q8_TILE16, 16, 64, 4, 128, 1, 4, 1, 16, 1.0f, {3.16f, 0.67f, 1.62f, 0.01f, 3.78f}},
+    {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, 1.0f, {2.85f, 0.70f, 0.92f, 0.92f, 3.23f}},
+    {Q8_TILE256X128, 256, 128, 8, 128, 1, 1, 65, ANY_M, 1.0f, {1.49f, 1.65f, 1.65f, 4.84f, 1.94f}},
 };
 
 // Adding the shares: a launch, and their sums written and read.
@@ -69,7 +71,7 @@ constexpr size_t MAX_COPY = (size_t)1 << 30;
 constexpr int CUS = 256;
 constexpr long long MAX_PART = 1ll << 28;  // bytes of the shares' sums
 
-double cost_of(const Kernel& c, int m, int n, int k, int splits, Q8Plan& p)
+double cost_of(const Kernel& c, bool cut, int m, int n, int k, int splits, Q8Plan& p)
 {
     const int steps = std::max(1, (k + c.step - 1) / c.step);
     p.kernel = c.id;
@@ -81,7 +83,7 @@ double cost_of(const Kernel& c, int m, int n, int k, int splits, Q8Plan& p)
     p.part = p.splits > 1 ? (size_t)p.splits * m * q8_part_ld(n) * sizeof(int) : 0;
     if (groups * c.waves * 64 >= 1ll << 31 || (p.splits > 1 && (long long)p.part > MAX_PART))
         return -1.0;  // a launch's threads are counted in 32 bits
-    const int taken = (p.per + c.turn - 1) / c.turn;
+    const float taken = (float)((p.per + c.turn - 1) / c.turn) * (cut ? c.cut : 1.0f);
     const long long slots = (long long)CUS * c.together, full = groups / slots, rest = groups % slots;
     double t = (double)full * (taken * (c.together > 1 ? c.cost.full : c.cost.alone) + c.cost.round);
     if (rest > 0) {
@@ -95,16 +97,16 @@ double cost_of(const Kernel& c, int m, int n, int k, int splits, Q8Plan& p)
 }
 
 template <int N>
-Q8Plan cheapest(const Kernel (&list)[N], int m, int n, int k, double& low)
+Q8Plan cheapest(const Kernel (&list)[N], bool cut, int m, int n, int k, double& low)
 {
     Q8Plan best{};
     low = -1.0;
     for (const Kernel& c : list) {
         if (m < c.from || m > c.to) continue;
-        for (int splits = 1; splits <= (c.id == Q8_STREAM ? 1 : 16); splits *= 2) {
+        for (int splits = 1; splits <= (c.id == Q8_STREAM ? 1 : 16); ++splits) {
             if (splits > 1 && k / 256 < splits) break;
             Q8Plan p{};
-            const double t = cost_of(c, m, n, k, splits, p);
+            const double t = cost_of(c, cut, m, n, k, splits, p);
             if (t >= 0.0 && (low < 0.0 || t < low)) {
                 low = t;
                 best = p;
@@ -116,29 +118,32 @@ Q8Plan cheapest(const Kernel (&list)[N], int m, int n, int k, double& low)
 
 }  // namespace
 
-Q8Plan q8_plan(int how, int m, int n, int k)
+Q8Plan q8_plan(int how, bool cut, int m, int n, int k)
 {
-    // the last sizes' choices: forty estimates take as long as a third of a launch
+    // the last sizes' choices: some hundred estimates take as long as a launch
     struct Known {
         int how, m, n, k;
+        bool cut;
         Q8Plan plan;
     };
     static thread_local Known known[64] = {};
     const unsigned key = ((unsigned)m * 31u + (unsigned)n) * 31u + (unsigned)k * 7u + (unsigned)how;
     Known& e = known[key % 64];
-    if (e.m == m && e.n == n && e.k == k && e.how == how && m > 0) return e.plan;
+    if (e.m == m && e.n == n && e.k == k && e.how == how && e.cut == cut && m > 0) return e.plan;
     double cost = 0.0;
-    Q8Plan p = how == Q8_LINES ? cheapest(LINES, m, n, k, cost)
-               : how == Q8_ANY ? cheapest(ANY, m, n, k, cost)
-                               : cheapest(REGS, m, n, k, cost);
+    Q8Plan p = how == Q8_LINES ? cheapest(LINES, cut, m, n, k, cost)
+               : how == Q8_ANY ? cheapest(ANY, false, m, n, k, cost)
+                               : cheapest(REGS, false, m, n, k, cost);
     p.how = how;
-    if (how != Q8_LINES && k >= 16) {
+    if ((how != Q8_LINES || cut) && k >= 16) {
         // many rows: each is read often, and from whole lines a third faster
-        // (4096 x 28672 x 8192: 1098 us where they lie, 830 with the copy;
-        // 100 x 28672 x 8192: 71 and 142 us)
+        // than at odd strides (4096 x 28672 x 8192: 1098 us where they lie,
+        // 830 with the copy; 100 x 28672 x 8192: 71 and 142 us), a tenth
+        // faster than where they cut lines (896 and 843; 1024 x 8192 x 4096:
+        // 48 and 50 us)
         const size_t copy = align_up(((size_t)m + n) * q8_copy_ld(k));
         double lines = 0.0;
-        Q8Plan c = cheapest(LINES, m, n, k, lines);
+        Q8Plan c = cheapest(LINES, false, m, n, k, lines);
         if (copy <= MAX_COPY && c.groups != 0 &&
             (p.groups == 0 || lines + COPY_LAUNCH + COPY_BYTE * k * ((double)m + n) < cost)) {
             p = c;
@@ -147,7 +152,7 @@ Q8Plan q8_plan(int how, int m, int n, int k)
             p.copy = copy;
         }
     }
-    e = Known{how, m, n, k, p};
+    e = Known{how, m, n, k, cut, p};
     return p;
 }
 
@@ -162,9 +167,10 @@ extern "C" size_t xsymv_q8gemm_workspace_bytes(int m, int n, int k)
     for (int rows : {std::min(m, Q8_BLOCK), m % Q8_BLOCK})
         for (int cols : {std::min(n, Q8_BLOCK), n % Q8_BLOCK})
             for (int how : {Q8_REGS, Q8_LINES, Q8_ANY})
-                if (rows > 0 && cols > 0) {
-                    const Q8Plan p = q8_plan(how, rows, cols, k);
-                    most = std::max(most, p.copy + p.part);
-                }
+                for (bool cut : {false, true})
+                    if (rows > 0 && cols > 0) {
+                        const Q8Plan p = q8_plan(how, cut, rows, cols, k);
+                        most = std::max(most, p.copy + p.part);
+                    }
     return most;
 }

@@ -40,8 +40,9 @@ inline int q8_copy_ld(int k)
     return ld % 4096 == 0 ? ld + 128 : ld;
 }
 
-// The kernel for m x n x k with rows read as `how`.
-Q8Plan q8_plan(int how, int m, int n, int k);
+// The kernel for m x n x k with rows read as `how`; `cut`: they do not start at
+// multiples of 128 bytes, so that a step's bytes lie on more lines.
+Q8Plan q8_plan(int how, bool cut, int m, int n, int k);
 
 // Rows and columns of one launch at most.
 constexpr int Q8_BLOCK = 1 << 24;
@@ -110,7 +111,10 @@ inline int q8_how(int k, const signed char* a, int lda, const signed char* w, in
 template <class T>
 int gemm_block(Q8GemmArgs<T> g, int lda, int ldw, hipStream_t stream)
 {
-    const Q8Plan p = q8_plan(q8_how(g.k, g.a, lda, g.w, ldw), g.m, g.n, g.k);
+    const int how = q8_how(g.k, g.a, lda, g.w, ldw);
+    const size_t starts = reinterpret_cast<size_t>(g.a) | reinterpret_cast<size_t>(g.w);
+    const bool cut = how == Q8_LINES && (starts | (size_t)(lda | ldw)) % 128 != 0;
+    const Q8Plan p = q8_plan(how, cut, g.m, g.n, g.k);
     if (p.groups == 0) return ERR_HIP + (int)hipErrorInvalidValue;  // more than a launch holds
     int threads = 0;
     const Q8GemmKernel<T> kernel = q8_kernel<T>(p, threads);
