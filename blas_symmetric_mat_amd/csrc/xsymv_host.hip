@@ -40,6 +40,7 @@ struct DeviceState {
     std::map<ShardKey, std::unique_ptr<StripPlan>> shard_plans;
     std::map<std::tuple<int, int, int, int>, std::unique_ptr<StripPlan>> gemv_plans;  // m, n, R, G
     std::map<hipStream_t, Workspace> workspaces;
+    std::vector<void*> captured;  // outgrown workspaces that graphs hold
     // (kernel, threads) -> blocks.  Guarded by its own lock: size queries
     // reach it without `mu`, product calls with `mu` held.
     std::mutex resident_mu;
@@ -583,7 +584,10 @@ int get_workspace(DeviceState* ds, hipStream_t stream, size_t bytes, void** out)
     auto& ws = ds->workspaces[stream];
     if (ws.bytes < bytes) {
         if (!ws.owned) return ERR_WORKSPACE;  // the caller's buffer is too small
-        if (ws.ptr) {
+        if (ws.ptr && ws.captured) {
+            ds->captured.push_back(ws.ptr);
+            ws = Workspace{};
+        } else if (ws.ptr) {
             // the old buffer may still be in use by work queued on this stream
             XSYMV_HIP(hipStreamSynchronize(stream));
             XSYMV_HIP(hipFree(ws.ptr));
@@ -593,6 +597,13 @@ int get_workspace(DeviceState* ds, hipStream_t stream, size_t bytes, void** out)
         const size_t grown = std::max(bytes, (size_t)1 << 20);
         XSYMV_HIP(hipMalloc(&ws.ptr, grown));
         ws.bytes = grown;
+    }
+    // a graph that is being captured keeps the address: a later call that
+    // outgrows the buffer must not free it
+    if (ws.owned && !ws.captured && stream != nullptr) {
+        hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+        ws.captured = hipStreamIsCapturing(stream, &status) == hipSuccess &&
+                      status != hipStreamCaptureStatusNone;
     }
     *out = ws.ptr;
     return 0;
@@ -1022,7 +1033,10 @@ int xsymv_set_workspace(void* dev_ptr, size_t bytes, void* stream)
     if (it != ds->workspaces.end()) {
         // the previous buffer may still be in use by work queued on this stream
         XSYMV_HIP(hipStreamSynchronize(st));
-        if (it->second.owned && it->second.ptr) XSYMV_HIP(hipFree(it->second.ptr));
+        if (it->second.captured)
+            ds->captured.push_back(it->second.ptr);
+        else if (it->second.owned && it->second.ptr)
+            XSYMV_HIP(hipFree(it->second.ptr));
         ds->workspaces.erase(it);
     }
     if (dev_ptr) ds->workspaces[st] = Workspace{dev_ptr, bytes, false};
@@ -1048,6 +1062,8 @@ int xsymv_release(void)
     for (auto& kv : ds->workspaces)
         if (kv.second.owned && kv.second.ptr) note(hipFree(kv.second.ptr));
     ds->workspaces.clear();
+    for (void* p : ds->captured) note(hipFree(p));
+    ds->captured.clear();
     for (auto& kv : ds->plans) {
         Plan* p = kv.second.get();
         note(hipFree(p->d_tiles));

@@ -43,6 +43,7 @@ struct Workspace {
     void* ptr = nullptr;
     size_t bytes = 0;
     bool owned = true;
+    bool captured = false;  // a graph holds its address: freed by xsymv_release only
 };
 constexpr int MERGE_SPLIT = 16;  // waves sharing one 64-row block of the merge
 constexpr int STRIP_CBUF = 256;  // columns a strip workgroup buffers before adding waves

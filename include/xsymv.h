@@ -348,15 +348,13 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  * Matrices are in ROW order, DEVICE pointers: element (i, j) at p[i*ld + j],
  * ld >= max(1, row length), any alignment.  The gap after a row is never
  * written; the product may read the gap between two rows (what it holds does
- * not matter), nothing reads past the last row's end.  The letter of a call is the type of its rows:
- * s float, h IEEE half, b bfloat16 (16-bit words); arithmetic and scales are
- * in 32 bits, the norm's sum of squares in 64.  Calls are asynchronous on
- * `stream`, can be captured into a graph, and give the same bytes every time.
- * Only the product uses the stream's workspace (xsymv_q8gemm_workspace_bytes;
- * 0 where k is not shared out), so it alone has to have run once on a stream,
- * or have a workspace installed, before it is captured there.  m == 0 or n == 0: nothing is
- * done.  Codes are checked in the order of the arguments before any device work;
- * pointers are only needed where there are rows.
+ * not matter), nothing reads past the last row's end.  The letter of a call is
+ * the type of its rows: s float, h IEEE half, b bfloat16 (16-bit words);
+ * arithmetic and scales are in 32 bits, the norm's sum of squares in 64.  Calls
+ * are asynchronous on `stream`, can be captured into a graph, and give the same
+ * bytes every time.  m == 0 or n == 0: nothing is done.  Codes are checked in
+ * the order of the arguments before any device work; pointers are only needed
+ * where there are rows.
  *
  *   xsymv_q8norm_*:  h = x + r (rounded to r's type), v = h / sqrt(mean(h^2)
  *   + eps) * w, stored as codes q and scales (one a row).  rtype, wtype: the
@@ -392,8 +390,16 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  *   2000 installed workspace too small.
  * All: 1000 + hipError_t.
  *
- *   xsymv_q8gemm_workspace_bytes: the workspace a product of m x n x k takes
- *   at most, whatever the operands' alignment (0 for sizes that do nothing). */
+ *   Of these calls only the product uses the stream's workspace: for the sums
+ *   of its shares of k, and where many rows lie at strides that are slow to
+ *   read for a copy of them (up to 1 GiB).  xsymv_q8gemm_workspace_bytes is
+ *   what a product of m x n x k takes at most, whatever the operands' alignment
+ *   (0 where it takes none).  While a stream is captured nothing can be
+ *   allocated, so a product of the same size has to have run on it before, or a
+ *   workspace of that many bytes be installed.  A graph keeps the workspace of
+ *   the stream it was captured on (the library frees such a one in
+ *   xsymv_release only), so its replays must not overlap with products on that
+ *   stream, nor with those of another graph captured there. */
 typedef unsigned short xhalf;     /* IEEE half, its 16 bits */
 typedef unsigned short xbfloat16; /* bfloat16, its 16 bits */
 size_t xsymv_q8gemm_workspace_bytes(int m, int n, int k);

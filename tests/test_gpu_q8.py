@@ -582,6 +582,54 @@ def test_replayed_from_a_graph(t, m, d, f):
                    zip(eager, ("h", "q", "sc", "gu", "q2", "sc2", "y")))
 
 
+def test_graph_keeps_its_workspace():
+    """A captured product whose stream's workspace a later, larger product
+    outgrows, and one whose workspace the caller then replaces: every replay
+    still gives the eager bytes."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    g = gen(21)
+    n, k = 300, 20000
+    w = torch.randint(-127, 128, (2048, k), generator=g, device="cuda", dtype=torch.int8)
+    a = torch.randint(-127, 128, (300, k), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones((2048,), device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    small, large = X.q8gemm_workspace_bytes(40, n, k), X.q8gemm_workspace_bytes(300, 2048, k)
+    assert large > max(small, 1 << 20)
+    c = torch.empty((40, n), device="cuda")
+    big = torch.empty((300, 2048), device="cuda")
+
+    def product(m, cols, out, first=0):
+        X.xsymv_q8gemm_s(m, cols, k, a[first:], k, one, w, k, one, None, out, cols, stream=st)
+
+    product(40, n, c)
+    st.synchronize()
+    want = c.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        product(40, n, c)
+    ws = torch.empty((large,), dtype=torch.uint8, device="cuda")
+    for i in range(4):
+        if i == 1:
+            product(300, 2048, big)
+        if i == 2:
+            X.set_workspace(ws, large, stream=st)
+            product(300, 2048, big)
+        if i == 3:
+            X.set_workspace(None, stream=st)
+            product(20, n, big, first=100)
+        st.synchronize()
+        c.fill_(math.nan)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            graph.replay()
+        st.synchronize()
+        assert torch.equal(c, want)
+    del graph
+    torch.cuda.synchronize()
+
+
 def test_streams_of_their_own():
     """Two streams at once, each with its own buffers, give the bytes of one
     after the other."""
