@@ -569,10 +569,10 @@ __global__ __launch_bounds__(256) void q8_gemm_join(Q8GemmArgs<T> g)
 // No wave waits for another until the sums are added.  The end of k goes
 // straight from memory to the multiplier's layout, with zeros past k; with
 // Q8_ANY the whole steps end 16 bytes or more before k, so that the ninth piece
-// of the last one lies within the row.  (16 x 28672 x 8192: 43 us, 5.5 TB/s,
-// where 6.6 is what reading alone reaches; at 16 x 4096 x 8192 12.6 us at odd
-// strides, the tile with shares of k 12.6 to 13.5, at 16 x 1024 x 4096 7.5 and
-// 9.4.)
+// of the last one lies within the row.  (16 x 4096 x 4096 6.1 us, the 16 x 64
+// tile 10.0; 16 x 8192 x 28672 41 us, 5.7 TB/s, where 6.6 is what reading alone
+// reaches; at odd strides 16 x 1024 x 4096 7.5 us, the tile with 16 shares of k
+// 9.4.  At 28672 columns of 8192 the tile reads W faster: 43 us, the ring 51.)
 template <int N>
 __device__ __forceinline__ void q8_wait_loads()
 {

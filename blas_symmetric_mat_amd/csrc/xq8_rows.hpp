@@ -8,11 +8,11 @@
 //   value_j = code_j * scale
 //
 // 2^-100 keeps 127 / a and a / 127 normal numbers for a row of zeros.  The
-// maximum is taken over the magnitudes' bit patterns as unsigned integers,
-// which orders them as numbers and puts infinities and NaN on top: a row that
-// holds one gets a scale that is not finite, codes of zero for its finite
-// elements, and so NaN for every value (as the formula in floating point has
-// it), and no other row is touched.
+// maximum is the one that a NaN passes through (and, between threads, that of
+// the bit patterns as unsigned integers, which orders them the same way, with
+// infinities and NaN on top): a row that holds an infinity or a NaN gets a
+// scale that is not finite, and so NaN for every value, and no other row is
+// touched.
 //
 // Every kernel is one pass over memory: TPR threads share a row and keep it
 // in registers (J chunks of 8 elements each) between the row's sums and the
@@ -73,13 +73,14 @@ __device__ __forceinline__ void q8_store(T* p, int have, const float (&v)[Q8_CHU
 }
 
 // Codes of a chunk.  Adding 1.5 * 2^23 to |t| <= 128 leaves t rounded half to
-// even in the low bits, whose last byte is the code in two's complement.
+// even in the low bits, whose last byte is the code in two's complement; the
+// product with `inv` is not rounded before.
 __device__ __forceinline__ void q8_store_codes(signed char* p, int have, const float (&v)[Q8_CHUNK],
                                                float inv)
 {
     unsigned b[Q8_CHUNK];
 #pragma unroll
-    for (int e = 0; e < Q8_CHUNK; ++e) b[e] = __float_as_uint(v[e] * inv + 12582912.0f);
+    for (int e = 0; e < Q8_CHUNK; ++e) b[e] = __float_as_uint(__builtin_fmaf(v[e], inv, 12582912.0f));
     if (have >= Q8_CHUNK) {
         unsigned w[2];
 #pragma unroll
@@ -138,14 +139,37 @@ __device__ __forceinline__ double q8_row_sum(double v, double (&buf)[2][16], int
     return v;
 }
 
-__device__ __forceinline__ unsigned q8_chunk_max(const float (&v)[Q8_CHUNK], unsigned m)
+// The larger of m and a chunk's magnitudes, or a NaN (two elements an
+// instruction, where the bit patterns would take four).
+__device__ __forceinline__ float q8_chunk_max(const float (&v)[Q8_CHUNK], float m)
 {
 #pragma unroll
-    for (int e = 0; e < Q8_CHUNK; ++e) {
-        const unsigned b = __float_as_uint(v[e]) & 0x7fffffffu;
-        m = m > b ? m : b;
+    for (int e = 0; e < Q8_CHUNK; e += 2) {
+        const float o = __builtin_elementwise_maximum(__builtin_fabsf(v[e]), __builtin_fabsf(v[e + 1]));
+        m = __builtin_elementwise_maximum(m, o);
     }
     return m;
+}
+
+// a / 127 and 127 / a for 2^-100 <= a, each rounded once: the quotient by a
+// rounded reciprocal is corrected by its exact remainder (Markstein's method),
+// which has been compared with the division for all 2^23 significands and a
+// reciprocal off by one unit either way.  No step leaves the normal numbers
+// (of a / 128 the reciprocal is one for every a).  An infinity or NaN gives NaN.
+// (The divisions were a sixth of a short row's instructions.)
+__device__ __forceinline__ float q8_scale_of(float a)
+{
+    const float q = a * (1.0f / 127.0f);
+    return __builtin_fmaf(__builtin_fmaf(-q, 127.0f, a), 1.0f / 127.0f, q);
+}
+
+__device__ __forceinline__ float q8_inverse_of(float a)
+{
+    const float t = a * 0x1p-7f, c = 127.0f / 128.0f;
+    float y = __builtin_amdgcn_rcpf(t);
+    y = __builtin_fmaf(__builtin_fmaf(-t, y, 1.0f), y, y);
+    const float q = c * y;
+    return __builtin_fmaf(__builtin_fmaf(-q, t, c), y, q);
 }
 
 // --------------------------------------------------------------- operators
@@ -333,7 +357,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 
         const long long dst = mine ? op.dest(row) : -1;
         const int have = mine ? n : 0;
         double ss = 0.0;
-        unsigned mx = 0;
+        float big = 0.0f;
         if constexpr (J > 0) {
             float v[J][Q8_CHUNK];
 #pragma unroll
@@ -355,13 +379,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 
                 }
             }
 #pragma unroll
-            for (int j = 0; j < J; ++j) mx = q8_chunk_max(v[j], mx);
-            mx = q8_row_max<TPR>(mx, mbuf, par);
+            for (int j = 0; j < J; ++j) big = q8_chunk_max(v[j], big);
+            const unsigned mx = q8_row_max<TPR>(__float_as_uint(big) & 0x7fffffffu, mbuf, par);
             par ^= 1;
             const float top = mx > __float_as_uint(Q8_FLOOR) ? __uint_as_float(mx) : Q8_FLOOR;
             if (dst < 0) continue;
-            if (t == 0) a.scale[dst] = top / 127.0f;
-            const float inv = 127.0f / top;
+            if (t == 0) a.scale[dst] = q8_scale_of(top);
+            const float inv = q8_inverse_of(top);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int c = (t + j * TPR) * Q8_CHUNK, at = j < LAST ? c : min(c, edge);
@@ -381,14 +405,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 
                 const int at = min((int)c, edge);
                 op.again(row, at, n - at, v);
                 if constexpr (OP::NORM) op.second(at, n - at, v, f);
-                mx = q8_chunk_max(v, mx);
+                big = q8_chunk_max(v, big);
             }
-            mx = q8_row_max<TPR>(mx, mbuf, par);
+            const unsigned mx = q8_row_max<TPR>(__float_as_uint(big) & 0x7fffffffu, mbuf, par);
             par ^= 1;
             const float top = mx > __float_as_uint(Q8_FLOOR) ? __uint_as_float(mx) : Q8_FLOOR;
             if (dst < 0) continue;
-            if (t == 0) a.scale[dst] = top / 127.0f;
-            const float inv = 127.0f / top;
+            if (t == 0) a.scale[dst] = q8_scale_of(top);
+            const float inv = q8_inverse_of(top);
             for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
                 const int at = min((int)c, edge);
                 op.again(row, at, n - at, v);

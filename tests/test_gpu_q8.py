@@ -6,6 +6,7 @@ code plus what the 32-bit arithmetic before the rounding moves t by; a scale
 and a value by their roundings.  Each bound is derived where it is used."""
 import math
 
+import numpy as np
 import pytest
 
 from tests.gpu_util import log, torch_dev
@@ -628,6 +629,26 @@ def test_graph_keeps_its_workspace():
         assert torch.equal(c, want)
     del graph
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n", [1, 8, 13])
+def test_codes_to_the_bit(n):
+    """Scales and codes are the definition's with one rounding each: a / 127
+    and 127 / a rounded to 32 bits, their exact products with the elements
+    rounded half to even.  Rows of every magnitude down to the floor."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    m = 1 << 17
+    r = np.random.default_rng(n)
+    x = r.uniform(-1.0, 1.0, (m, n)).astype(np.float32)
+    x = np.ldexp(x, r.integers(-110, 127, (m, 1))).astype(np.float32)
+    q = torch.empty((m, n), device="cuda", dtype=torch.int8)
+    s = torch.empty((m,), device="cuda")
+    X.xsymv_q8store_s(m, n, torch.from_numpy(x).cuda(), n, None, m, q, n, s)
+    a = np.maximum(np.abs(x).max(axis=1), np.float32(2.0 ** -100))
+    assert np.array_equal(s.cpu().numpy(), a / np.float32(127.0))
+    inv = (np.float32(127.0) / a).astype(np.float64)[:, None]
+    assert np.array_equal(q.cpu().numpy(), np.rint(x.astype(np.float64) * inv).astype(np.int8))
 
 
 def test_streams_of_their_own():
