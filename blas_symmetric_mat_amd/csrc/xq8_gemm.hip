@@ -137,8 +137,8 @@ Q8Plan q8_plan(int how, bool cut, int m, int n, int k)
     p.how = how;
     if ((how != Q8_LINES || cut) && k >= 16) {
         // many rows: each is read often, and from whole lines a third faster
-        // than at odd strides (4096 x 28672 x 8192: 1098 us where they lie,
-        // 830 with the copy; 100 x 28672 x 8192: 71 and 142 us), a tenth
+        // than at odd strides (4096 x 28672 x 8192: 1124 us where they lie,
+        // 832 with the copy; 100 x 28672 x 8192: 73 and 142 us), a tenth
         // faster than where they cut lines (896 and 843; 1024 x 8192 x 4096:
         // 48 and 50 us)
         const size_t copy = align_up(((size_t)m + n) * q8_copy_ld(k));

@@ -633,9 +633,9 @@ def test_graph_keeps_its_workspace():
 
 @pytest.mark.parametrize("n", [1, 8, 13])
 def test_codes_to_the_bit(n):
-    """Scales and codes are the definition's with one rounding each: a / 127
-    and 127 / a rounded to 32 bits, their exact products with the elements
-    rounded half to even.  Rows of every magnitude down to the floor."""
+    """Scales and codes are the definition's in 32 bits: a / 127, 127 / a and
+    its products with the elements round once each, the products then half to
+    even.  Rows of every magnitude down to the floor."""
     import torch
     import blas_symmetric_mat_amd as X
     m = 1 << 17
@@ -647,8 +647,8 @@ def test_codes_to_the_bit(n):
     X.xsymv_q8store_s(m, n, torch.from_numpy(x).cuda(), n, None, m, q, n, s)
     a = np.maximum(np.abs(x).max(axis=1), np.float32(2.0 ** -100))
     assert np.array_equal(s.cpu().numpy(), a / np.float32(127.0))
-    inv = (np.float32(127.0) / a).astype(np.float64)[:, None]
-    assert np.array_equal(q.cpu().numpy(), np.rint(x.astype(np.float64) * inv).astype(np.int8))
+    inv = (np.float32(127.0) / a)[:, None]
+    assert np.array_equal(q.cpu().numpy(), np.rint(x * inv).astype(np.int8))
 
 
 def test_streams_of_their_own():
