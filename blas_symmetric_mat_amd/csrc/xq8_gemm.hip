@@ -12,11 +12,12 @@ namespace {
 // unit runs one workgroup, `full` where it runs all it can and between them
 // otherwise; but no less than W's bytes take at `rate` TB/s.  Over that grid
 // the kernel this chooses is 1 % slower on average than the fastest one
-// measured, 4 % for up to 16 rows at odd strides (at worst 1.7 times, at sizes
-// of a few microseconds).  The 64-row tile alone, at its best number of shares,
-// would be 1.07 (m = 65 to 128) to 1.36 times (m > 512) slower, and without
-// shares of k up to 5 times.  At odd strides the ring is chosen at 32 of the
-// 144 sizes of up to 16 rows, and 1.19 times faster there than the next.
+// measured, 4 % for up to 16 rows at odd strides (at worst 2 times, at sizes of
+// a few microseconds).  The rings are chosen at 400 of its 1070 sizes of whole
+// lines and 200 of 630 at odd strides, and are 1.16 (up to 16 rows) to 1.37
+// times faster there than the next kernel.  The 64-row tile alone, at its best
+// number of shares, would be 1.07 (m = 65 to 128) to 1.36 times (m > 512)
+// slower than the tiles together, and without shares of k up to 5 times.
 struct Cost {
     float launch, alone, full, round, rate;
 };
@@ -32,7 +33,8 @@ struct Kernel {
 
 constexpr int ANY_M = 1 << 30;
 const Kernel LINES[] = {
-    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, 1.15f, {1.78f, 0.56f, 0.56f, 1.19f, 5.27f}},
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, ANY_M, 1.15f, {2.04f, 0.44f, 0.44f, 1.17f, 5.32f}},
+    {Q8_RING32, 32, 32, 4, 128, 4, 1, 17, ANY_M, 1.25f, {1.97f, 0.34f, 0.34f, 1.34f, 3.21f}},
     {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, 1.12f, {2.99f, 0.37f, 1.16f, 0.48f, 6.44f}},
     {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, 1.15f, {2.27f, 0.33f, 0.98f, 1.57f, 4.87f}},
     {Q8_TILE64, 64, 64, 4, 128, 1, 2, 17, ANY_M, 1.35f, {2.30f, 0.24f, 0.53f, 1.69f, 5.92f}},
@@ -44,7 +46,8 @@ const Kernel LINES[] = {
     {Q8_TILE256, 256, 256, 8, 128, 1, 1, 65, ANY_M, 1.19f, {4.15f, 1.27f, 1.27f, 4.95f, 3.96f}},
 };
 const Kernel ANY[] = {
-    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, 16, 1.0f, {3.39f, 0.50f, 0.50f, 1.34f, 4.14f}},
+    {Q8_RING, 16, 16, 8, 128, 8, 1, 1, ANY_M, 1.0f, {2.38f, 0.61f, 0.61f, 1.73f, 3.69f}},
+    {Q8_RING32, 32, 32, 4, 128, 4, 1, 17, ANY_M, 1.0f, {1.64f, 0.65f, 0.65f, 2.44f, 1.88f}},
     {Q8_STREAM, 16, 16, 8, 256, 8, 4, 1, 16, 1.0f, {0.98f, 3.25f, 2.58f, 0.49f, 1.61f}},
     {Q8_TILE16, 16, 64, 4, 256, 1, 2, 1, 16, 1.0f, {4.15f, 0.47f, 1.05f, 0.14f, 7.60f}},
     {Q8_TILE32, 32, 64, 4, 256, 1, 2, 1, 64, 1.0f, {2.39f, 0.74f, 1.37f, 1.80f, 5.59f}},

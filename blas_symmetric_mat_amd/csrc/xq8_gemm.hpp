@@ -20,8 +20,8 @@
 //
 // Three kinds of kernel make it, each at the sizes where it measured fastest:
 // tiles of 16 to 256 rows of both operands through LDS, whose waves share what
-// is loaded; for at most 16 rows a ring of buffers for each wave, which waits
-// for no other wave; and for the shortest of those rows at odd strides straight
+// is loaded; for few results a ring of buffers for each wave, which waits for
+// no other wave; and for up to 16 of the shortest rows at odd strides straight
 // loads to registers, which have nothing to set up.  Where there are fewer
 // tiles than the chip holds at once, k is split into shares, whose sums are
 // added by another launch.
@@ -172,7 +172,7 @@ __device__ __forceinline__ void q8_partial(const Q8GemmArgs<T>& g, unsigned shar
 // twice as long as with the ring (16 x 1024 x 8192 at odd strides 21.6 us, the
 // ring 8.3); with nothing to set up, short ones are quicker (1 x 1024 x 256
 // 3.2 us, the ring 3.8).
-constexpr int Q8_WAVES = 8;  // of a workgroup of this kernel and the ring
+constexpr int Q8_WAVES = 8;  // of a workgroup
 
 template <class T>
 __global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_stream(Q8GemmArgs<T> g)
@@ -560,43 +560,50 @@ __global__ __launch_bounds__(256) void q8_gemm_join(Q8GemmArgs<T> g)
     }
 }
 
-// ---------------------------------------------------- few rows: a ring a wave
-// The bytes of W bound the product, so what counts is loads in flight and
-// whole lines.  A workgroup makes 16 x 16 results; its waves take the
-// 128-byte steps of the share of k in turn, each with a ring of S buffers in
-// LDS of its own, laid out as in the tiles; the loads go to LDS by themselves
-// (HOW: Q8_LINES or Q8_ANY), S - 1 steps ahead of the step that is multiplied.
-// No wave waits for another until the sums are added.  The end of k goes
-// straight from memory to the multiplier's layout, with zeros past k; with
-// Q8_ANY the whole steps end 16 bytes or more before k, so that the ninth piece
-// of the last one lies within the row.  (16 x 4096 x 4096 6.1 us, the 16 x 64
-// tile 10.0; 16 x 8192 x 28672 41 us, 5.7 TB/s, where 6.6 is what reading alone
-// reaches; at odd strides 16 x 1024 x 4096 7.5 us, the tile with 16 shares of k
-// 9.4.  At 28672 columns of 8192 the tile reads W faster: 43 us, the ring 51.)
+// ------------------------------------------------- few results: a ring a wave
+// Where few rows of A meet W, loads in flight and whole lines count; where
+// there are few results, the time to start, wait and add up.  A workgroup makes
+// 16 F x 16 F results; its WK waves take the 128-byte steps of the share of k
+// in turn, each with a ring of S buffers in LDS of its own, laid out as in the
+// tiles; the loads go to LDS by themselves (HOW: Q8_LINES or Q8_ANY), S - 1
+// steps ahead of the step that is multiplied.  No wave waits for another until
+// the sums are added.  The end of k goes straight from memory to the
+// multiplier's layout, with zeros past k; with Q8_ANY the whole steps end 16
+// bytes or more before k, so that the ninth piece of the last one lies within
+// the row.
+//
+// F = 1, WK = 8 (S = 3, or 2 with Q8_ANY): 16 x 4096 x 4096 6.1 us, the tile of
+// 16 x 64 10.0; 16 x 8192 x 28672 41 us, 5.7 TB/s, where 6.6 is what reading
+// alone reaches; at odd strides 16 x 1024 x 4096 7.5 us, the tile with 16 shares
+// of k 9.4.  (At 28672 columns of 8192 the tile reads W faster: 43 us, the ring
+// 51.)  F = 2, WK = 4: 256 x 1024 x 2048 4.8 us, the 64 x 64 tile with shares
+// 8.4, F = 1 more than one round; at odd strides 6.9 and 10.6.
 template <int N>
 __device__ __forceinline__ void q8_wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <class T, int S, int HOW>
-__global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_ring(Q8GemmArgs<T> g)
+template <class T, int F, int WK, int S, int HOW>
+__global__ __launch_bounds__(64 * WK) void q8_gemm_ring(Q8GemmArgs<T> g)
 {
     // CB loads of 64 pieces for 16 rows (with Q8_ANY the last one reaches past
-    // them), of W and then of A
+    // them), F times of W and then of A
     constexpr int BK = 128, CH = HOW == Q8_ANY ? 9 : 8, CB = (16 * CH + 63) / 64;
-    constexpr int BLOCK = CB * 1024, SLOT = 2 * BLOCK;
-    __shared__ __attribute__((aligned(1024))) signed char lds[Q8_WAVES][S * SLOT];
+    constexpr int BLOCK = CB * 1024, LOADS = 2 * F * CB, SLOT = LOADS * 1024;
+    static_assert((S - 1) * LOADS < 64, "the counter of outstanding loads");
+    static_assert(WK >= F * F, "a wave for each 16 x 16 results");
+    __shared__ __attribute__((aligned(1024))) signed char lds[WK][S * SLOT];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     unsigned ti, tj, share;
-    q8_tile((g.m + 15) / 16, (g.n + 15) / 16, ti, tj, share);
-    const int i0 = (int)ti * 16, j0 = (int)tj * 16;
+    q8_tile((g.m + 16 * F - 1) / (16 * F), (g.n + 16 * F - 1) / (16 * F), ti, tj, share);
+    const int i0 = (int)ti * 16 * F, j0 = (int)tj * 16 * F;
     // this share's whole steps, t0 and on; the rest of k is the first share's
     const int all = HOW == Q8_ANY ? (g.k - 16) / BK : g.k / BK, t0 = (int)share * g.per;
     const int steps = all - t0 < g.per ? all - t0 : g.per;
-    const int mine = (steps - wave + Q8_WAVES - 1) / Q8_WAVES;  // steps wave, wave + 8, ...
+    const int mine = (steps - wave + WK - 1) / WK;  // steps wave, wave + WK, ...
     // rows at a multiple of 4096 bytes lie on the same memory channels, column
     // by column, so there each workgroup of a die starts at another step
     // (16 x 8192 x 28672: 47 -> 41 us; at other strides it costs 2 %)
@@ -608,14 +615,14 @@ __global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_ring(Q8GemmArgs<T> g)
     const int sha = HOW == Q8_ANY ? (int)((size_t)ga & 15) : 0;
     const int shw = HOW == Q8_ANY ? (int)((size_t)gw & 15) : 0;
 
-    unsigned oa[CB], ow[CB];
+    unsigned oa[F * CB], ow[F * CB];
     auto offset = [&](int i, int last, long long ld, int sh) {  // load i of an operand's rows
-        const int piece = i * 64 + lane, c = piece % CH, row = piece / CH;
+        const int piece = i % CB * 64 + lane, c = piece % CH, row = i / CB * 16 + piece / CH;
         const unsigned o = (unsigned)((row < last ? row : last) * ld + sh);
         return HOW == Q8_ANY ? (o & ~15u) + 16 * c : o + 16 * (c ^ ((row >> 1) & 7));
     };
 #pragma unroll
-    for (int i = 0; i < CB; ++i) {
+    for (int i = 0; i < F * CB; ++i) {
         oa[i] = offset(i, ma, g.lda, sha);
         ow[i] = offset(i, mw, g.ldw, shw);
     }
@@ -627,28 +634,48 @@ __global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_ring(Q8GemmArgs<T> g)
         int turned = t + turn;
         turned -= turned >= mine ? mine : 0;
         const unsigned to = base + (unsigned)(t % S) * SLOT;
-        const unsigned k0 = (unsigned)(t0 + turned * Q8_WAVES + wave) * BK;
+        const unsigned k0 = (unsigned)(t0 + turned * WK + wave) * BK;
 #pragma unroll
-        for (int i = 0; i < CB; ++i) q8_fetch(to + 1024 * i, ow[i], rw, k0);
+        for (int i = 0; i < F * CB; ++i) q8_fetch(to + 1024 * i, ow[i], rw, k0);
 #pragma unroll
-        for (int i = 0; i < CB; ++i) q8_fetch(to + BLOCK + 1024 * i, oa[i], ra, k0);
+        for (int i = 0; i < F * CB; ++i) q8_fetch(to + F * BLOCK + 1024 * i, oa[i], ra, k0);
     };
+    // (each of the first F * F waves finishes 16 x 16 of the results)
     const int r = lane & 15, piece = lane >> 4;
-    Q8Scales<T, 1, 1> scales;  // (the first wave finishes the results)
-    if (wave == 0 && g.splits == 1) scales.load(g, i0 + r, j0 + 4 * piece);
+    const int ci = i0 + 16 * (wave / F) + r, cj = j0 + 16 * (wave % F) + 4 * piece;
+    Q8Scales<T, 1, 1> scales;
+    if (wave < F * F && g.splits == 1) scales.load(g, ci, cj);
     for (int t = 0; t < S - 1 && t < mine; ++t) fetch(t);
 
-    q8v4 acc = {0, 0, 0, 0};
-    if (share == 0 && wave == Q8_WAVES - 1) {
+    q8v4 acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = q8v4{0, 0, 0, 0};
+    auto multiply = [&](const q8v4(&xa)[F], const q8v4(&xw)[F]) {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j)
+                acc[i][j] =
+                    __builtin_amdgcn_mfma_i32_16x16x64_i8(xw[j], xa[i], acc[i][j], 0, 0, 0);
+    };
+    if (share == 0 && wave == WK - 1) {
 #pragma unroll 1
         for (int k0 = all * BK; k0 < g.k; k0 += 64) {
             const int at = k0 + 16 * piece;
-            const q8v4 xw = q8_load16(gw + (r < mw ? r : mw) * g.ldw + at, g.k - at);
-            const q8v4 xa = q8_load16(ga + (r < ma ? r : ma) * g.lda + at, g.k - at);
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw, xa, acc, 0, 0, 0);
+            q8v4 xa[F], xw[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int row = 16 * f + r;
+                xw[f] = q8_load16(gw + (row < mw ? row : mw) * g.ldw + at, g.k - at);
+                xa[f] = q8_load16(ga + (row < ma ? row : ma) * g.lda + at, g.k - at);
+            }
+            multiply(xa, xw);
         }
     }
 
+    // the byte of a piece that a row starts at is the same for rows 16 apart
     typedef int words __attribute__((ext_vector_type(HOW == Q8_ANY ? 8 : 4)));
     const int sa = HOW == Q8_ANY ? (int)((size_t)(ga + r * g.lda) & 15) : 0;
     const int sw = HOW == Q8_ANY ? (int)((size_t)(gw + r * g.ldw) & 15) : 0;
@@ -656,34 +683,46 @@ __global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_ring(Q8GemmArgs<T> g)
     for (int t = 0; t < mine; ++t) {
         if (t + S - 1 < mine) {
             fetch(t + S - 1);  // into the buffer of step t - 1, which has been read
-            q8_wait_loads<(S - 1) * 2 * CB>();
+            q8_wait_loads<(S - 1) * LOADS>();
         } else {
             q8_wait_loads<0>();
         }
         const signed char* p = ring + (t % S) * SLOT;
-        words xa[2], xw[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            q8_read<HOW>(xw[h], p, pl, h * 64, sw);
-            q8_read<HOW>(xa[h], p + BLOCK, pl, h * 64, sa);
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        words wa[2][F], ww[2][F];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(q8_bytes<HOW>(xw[h], sw),
-                                                        q8_bytes<HOW>(xa[h], sa), acc, 0, 0, 0);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                q8_read<HOW>(ww[h][f], p + f * BLOCK, pl, h * 64, sw);
+                q8_read<HOW>(wa[h][f], p + (F + f) * BLOCK, pl, h * 64, sa);
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q8v4 xa[F], xw[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                xw[f] = q8_bytes<HOW>(ww[h][f], sw);
+                xa[f] = q8_bytes<HOW>(wa[h][f], sa);
+            }
+            multiply(xa, xw);
+        }
     }
     // the waves' sums, in their rings, which nothing is on its way to
-    ((q8v4*)ring)[lane] = acc;
+    q8v4* sums = (q8v4*)ring;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) sums[(i * F + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    if (wave != 0) return;
+    if (wave >= F * F) return;
     q8v4 sum[1][1] = {{{0, 0, 0, 0}}};
 #pragma unroll
-    for (int w = 0; w < Q8_WAVES; ++w) sum[0][0] += ((const q8v4*)lds[w])[lane];
+    for (int w = 0; w < WK; ++w) sum[0][0] += ((const q8v4*)lds[w])[wave * 64 + lane];
     if (g.splits == 1)
-        q8_finish(g, i0 + r, j0 + 4 * piece, scales, sum);
+        q8_finish(g, ci, cj, scales, sum);
     else
-        q8_partial<T, 1, 1>(g, share, i0 + r, j0 + 4 * piece, sum);
+        q8_partial<T, 1, 1>(g, share, ci, cj, sum);
 }
 
 // ------------------------------------------------------------------ copies

@@ -11,6 +11,7 @@ namespace xsymv {
 
 enum Q8Kernel {
     Q8_RING,
+    Q8_RING32,
     Q8_STREAM,
     Q8_TILE16,
     Q8_TILE32,
@@ -57,7 +58,8 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
 {
     threads = 512;
     if (p.kernel == Q8_RING)
-        return p.how == Q8_LINES ? &q8_gemm_ring<T, 3, Q8_LINES> : &q8_gemm_ring<T, 2, Q8_ANY>;
+        return p.how == Q8_LINES ? &q8_gemm_ring<T, 1, 8, 3, Q8_LINES>
+                                 : &q8_gemm_ring<T, 1, 8, 2, Q8_ANY>;
     if (p.kernel == Q8_STREAM) return &q8_gemm_stream<T>;
     if (p.how == Q8_LINES) {
         switch (p.kernel) {
@@ -70,6 +72,7 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
         }
         threads = 256;
         switch (p.kernel) {
+        case Q8_RING32: return &q8_gemm_ring<T, 2, 4, 3, Q8_LINES>;
         case Q8_TILE16: return &q8_gemm_tile<T, 16, 64, 1, 4, 2, 3, Q8_LINES>;
         case Q8_TILE32: return &q8_gemm_tile<T, 32, 64, 2, 2, 2, 3, Q8_LINES>;
         case Q8_TILE64_SHORT: return &q8_gemm_tile<T, 64, 64, 2, 2, 1, 2, Q8_LINES>;
@@ -86,6 +89,7 @@ Q8GemmKernel<T> q8_kernel(const Q8Plan& p, int& threads)
         }
         threads = 256;
         switch (p.kernel) {
+        case Q8_RING32: return &q8_gemm_ring<T, 2, 4, 2, Q8_ANY>;
         case Q8_TILE16: return &q8_gemm_tile<T, 16, 64, 1, 4, 2, 3, Q8_ANY>;
         case Q8_TILE32: return &q8_gemm_tile<T, 32, 64, 2, 2, 2, 3, Q8_ANY>;
         case Q8_TILE64_SHORT: return &q8_gemm_tile<T, 64, 64, 2, 2, 1, 2, Q8_ANY>;

@@ -390,6 +390,13 @@ KERNELS = [("lines", 5, 33, 300), ("lines", 5, 33, 8200), ("lines", 5, 4100, 300
            ("any", 200, 16400, 300), ("any", 200, 4100, 4110), ("any", 260, 30000, 300),
            ("any", 100, 4100, 16400), ("any", 600, 1000, 8200), ("any", 1000, 16400, 300),
            ("any", 1030, 1000, 1040), ("any", 4100, 2000, 300),
+           ("lines", 130, 500, 300), ("lines", 200, 33, 8200), ("lines", 4100, 33, 300),
+           ("lines", 1030, 33, 16400), ("lines", 130, 2000, 16400), ("lines", 5, 16400, 520),
+           ("lines", 5, 4100, 4110), ("lines", 130, 16400, 8200), ("lines", 257, 1000, 140),
+           ("any", 130, 500, 300), ("any", 100, 130, 8200), ("any", 40, 4100, 300),
+           ("any", 4100, 33, 520), ("any", 1000, 33, 16400), ("any", 4100, 33, 2060),
+           ("any", 4100, 33, 300), ("any", 100, 4100, 8200), ("any", 130, 2000, 2060),
+           ("any", 2050, 500, 8200), ("any", 257, 1000, 140),
            ("odd", 5, 16400, 300), ("odd", 5, 33, 4110), ("odd", 40, 33, 300),
            ("odd", 40, 33, 2060), ("odd", 200, 16400, 300), ("odd", 130, 2000, 8200),
            ("odd", 1030, 500, 8200), ("odd", 2050, 2000, 520)]
