@@ -9,11 +9,20 @@
 namespace xsymv {
 namespace {
 
+// Workgroups for twice the threads that the chip holds at once (256 compute
+// units of 2048), which take the rows in turn: a workgroup for every few rows
+// cost the start of each (store of 65536 x 512 24.7 us, 22.1 so; activation of
+// 4096 x 14336 55.8 and 54.3; norm of 8192 x 4096, bfloat16, 53.7 and 51.4), and
+// with no more than the chip holds a norm's loads wait for its sums (58.5).
+// Norms of one chunk a thread do best with four times as many (200000 x 128:
+// every row its own 42.0 us, twice 40.5, four times 38.9).
 template <class OP, int TPR, int J>
 int rows_launch(const Q8RowArgs<OP>& a, hipStream_t stream)
 {
     constexpr int threads = TPR > 256 ? TPR : 256;
-    return q8_launch(&q8_rows<OP, TPR, J>, q8_grid(a.op.m, threads / TPR), threads, stream, a);
+    constexpr unsigned most = (OP::NORM && J == 1 ? 4 : 2) * (256 * 2048 / threads);
+    const unsigned grid = std::min(q8_grid(a.op.m, threads / TPR), most);
+    return q8_launch(&q8_rows<OP, TPR, J>, grid, threads, stream, a);
 }
 
 // Threads per row and chunks per thread by the row's length alone: of the

@@ -658,6 +658,41 @@ def test_codes_to_the_bit(n):
     assert np.array_equal(q.cpu().numpy(), np.rint(x * inv).astype(np.int8))
 
 
+@pytest.mark.parametrize("m,n", [(70001, 128), (40003, 500), (9001, 2100), (4500, 9000),
+                                 (2300, 16000), (1100, 66000)])
+def test_many_rows_in_turn(m, n):
+    """More rows than workgroups: each takes several in turn, with the bytes
+    of calls on a few rows at a time.  One row in a hundred is not finite."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    log(f"rows in turn {m}x{n}")
+    g = gen(m)
+    x = torch.randn((m, n), generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    x[::100, n // 2] = math.nan
+    w = torch.randn((n,), generator=g, device="cuda").to(torch.bfloat16)
+    u = x.flip(0).contiguous()
+
+    def run(lo, hi):
+        c = hi - lo
+        out = []
+        for f in (lambda q, s: X.xsymv_q8norm_b(c, n, x[lo:hi], n, "b", None, n, "b", w, 1e-5,
+                                                None, n, q, n, s),
+                  lambda q, s: X.xsymv_q8glu_b(c, n, x[lo:hi], n, u[lo:hi], n, q, n, s),
+                  lambda q, s: X.xsymv_q8store_b(c, n, x[lo:hi], n, None, c, q, n, s)):
+            q = torch.empty((c, n), device="cuda", dtype=torch.int8)
+            s = torch.empty((c,), device="cuda")
+            f(q, s)
+            out += [q, s.view(torch.int32)]
+        return out
+
+    full = run(0, m)
+    step = m // 3 if n < 9000 else 300
+    for lo in range(0, m, step):
+        hi = min(lo + step, m)
+        for a, b in zip(full, run(lo, hi)):
+            assert torch.equal(a[lo:hi], b), lo
+
+
 def test_streams_of_their_own():
     """Two streams at once, each with its own buffers, give the bytes of one
     after the other."""
