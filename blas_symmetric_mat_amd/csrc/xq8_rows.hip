@@ -32,27 +32,20 @@ int rows_launch(const Q8RowArgs<OP>& a, hipStream_t stream)
 // 80 us, 512 of two 72, 1024 of one 87), the sums' waits being shared by more
 // loads; a capacity that is half empty costs up to 30 % (norm of 3000 x 9000:
 // 1024 threads of two 74 us, 512 of three 56).
+template <class OP, int TPR, int J, int... NEXT>
+int rows_fit(int chunks, const Q8RowArgs<OP>& a, hipStream_t stream)
+{
+    if constexpr (sizeof...(NEXT) > 0)
+        if (chunks > TPR * J) return rows_fit<OP, NEXT...>(chunks, a, stream);
+    return rows_launch<OP, TPR, J>(a, stream);
+}
+
 template <class OP>
 int rows_run(const Q8RowArgs<OP>& a, hipStream_t stream)
 {
     const int chunks = (int)(((long long)a.op.n + Q8_CHUNK - 1) / Q8_CHUNK);
-    if (chunks <= 8) return rows_launch<OP, 8, 1>(a, stream);
-    if (chunks <= 16) return rows_launch<OP, 16, 1>(a, stream);
-    if (chunks <= 32) return rows_launch<OP, 32, 1>(a, stream);
-    if (chunks <= 64) return rows_launch<OP, 64, 1>(a, stream);
-    if (chunks <= 96) return rows_launch<OP, 32, 3>(a, stream);
-    if (chunks <= 128) return rows_launch<OP, 64, 2>(a, stream);
-    if (chunks <= 192) return rows_launch<OP, 64, 3>(a, stream);
-    if (chunks <= 256) return rows_launch<OP, 256, 1>(a, stream);
-    if (chunks <= 512) return rows_launch<OP, 256, 2>(a, stream);
-    if (chunks <= 768) return rows_launch<OP, 256, 3>(a, stream);
-    if (chunks <= 1024) return rows_launch<OP, 512, 2>(a, stream);
-    if (chunks <= 1536) return rows_launch<OP, 512, 3>(a, stream);
-    if (chunks <= 2048) return rows_launch<OP, 1024, 2>(a, stream);
-    if (chunks <= 3072) return rows_launch<OP, 1024, 3>(a, stream);
-    if (chunks <= 4096) return rows_launch<OP, 1024, 4>(a, stream);
-    if (chunks <= 8192) return rows_launch<OP, 1024, 8>(a, stream);
-    return rows_launch<OP, 1024, 0>(a, stream);
+    return rows_fit<OP, 8, 1, 16, 1, 32, 1, 64, 1, 32, 3, 64, 2, 64, 3, 256, 1, 256, 2, 256, 3, 512,
+                    2, 512, 3, 1024, 2, 1024, 3, 1024, 4, 1024, 8, 1024, 0>(chunks, a, stream);
 }
 
 template <class T, class R, class W>
