@@ -66,17 +66,18 @@ class Q8Layer:
 
     def _slots(self, first, count):
         import torch
-        head = torch.arange(self.heads, dtype=torch.int32, device="cuda")
+        head = torch.arange(self.heads, dtype=torch.int32, device=self.place.device)
         return (self.place[first:first + count, None] * self.heads + head).flatten().contiguous()
 
     def _rows(self, m, n):
         import torch
-        return (torch.empty((m, n), dtype=torch.int8, device="cuda"),
-                torch.empty((m,), dtype=torch.float32, device="cuda"))
+        dev = self.place.device
+        return (torch.empty((m, n), dtype=torch.int8, device=dev),
+                torch.empty((m,), dtype=torch.float32, device=dev))
 
     def _product(self, m, rows, w):
         import torch
-        c = torch.empty((m, w.n), dtype=torch.bfloat16, device="cuda")
+        c = torch.empty((m, w.n), dtype=torch.bfloat16, device=self.place.device)
         X.xsymv_q8gemm_b(m, w.n, w.k, rows[0], w.k, rows[1], w.codes, w.k, w.scale, None, c, w.n)
         return c
 
@@ -88,25 +89,28 @@ class Q8Layer:
 
     def __call__(self, x, r):
         """x, r: the next m tokens' rows and residuals (m x d, bfloat16);
-        returns the layer's output and the new residual."""
+        returns the layer's output and the new residual.  ValueError where the
+        cache has no room for m tokens more: nothing is done then."""
         import torch
         m, d, heads, hd = x.shape[0], self.d, self.heads, self.hd
+        first, seen = self.used, self.used + m
+        if seen > self.tokens:
+            raise ValueError(f"the cache holds {self.tokens} tokens, {first} are there and {m} more "
+                             "do not fit")
         h, rows = self._norm(m, x, r, self.norm1)
         qkv = self._product(m, rows, self.wqkv)
-        first, seen = self.used, self.used + m
-        self.used = seen
         slots, cap = self._slots(first, m), self.tokens * heads
         past, read = self._slots(0, seen), []
         for part, (codes, scale) in enumerate(self.kv, start=1):
             new = qkv[:, part * d:(part + 1) * d].reshape(m * heads, hd)
             X.xsymv_q8store_b(m * heads, hd, new, hd, slots, cap, codes, hd, scale)
-            out = torch.empty((seen * heads, hd), dtype=torch.float32, device="cuda")
+            out = torch.empty((seen * heads, hd), dtype=torch.float32, device=codes.device)
             X.xsymv_q8read_s(seen * heads, hd, codes, hd, scale, past, cap, out, hd)
             read.append(out.view(seen, heads, hd).transpose(0, 1).double())
         q = qkv[:, :d].reshape(m, heads, hd).transpose(0, 1).double()
         score = q @ read[0].transpose(1, 2).contiguous() / math.sqrt(hd)
-        late = (torch.arange(seen, device="cuda")[None, :]
-                > torch.arange(first, seen, device="cuda")[:, None])
+        token = torch.arange(seen, device=score.device)
+        late = token[None, :] > token[first:, None]
         weight = torch.softmax(score.masked_fill(late, -math.inf), dim=-1)
         att = (weight @ read[1].contiguous()).transpose(0, 1).reshape(m, d).bfloat16()
         rows = self._rows(m, d)
@@ -116,7 +120,9 @@ class Q8Layer:
         gu, f = self._product(m, rows, self.wgu), self.f
         rows = self._rows(m, f)
         X.xsymv_q8glu_b(m, f, gu, 2 * f, gu[:, f:], 2 * f, rows[0], f, rows[1])
-        return self._product(m, rows, self.wd), h
+        y = self._product(m, rows, self.wd)
+        self.used = seen
+        return y, h
 
 
 def plain(layer, x, r):
