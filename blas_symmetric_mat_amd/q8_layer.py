@@ -83,16 +83,33 @@ class Q8Layer:
 
     def _norm(self, m, x, r, weight):
         import torch
-        d, h, rows = self.d, torch.empty_like(r), self._rows(m, self.d)
-        X.xsymv_q8norm_b(m, d, x, d, "b", r, d, "b", weight, self.eps, h, d, rows[0], d, rows[1])
+        d, rows = self.d, self._rows(m, self.d)
+        h = torch.empty((m, d), dtype=torch.bfloat16, device=self.place.device)
+        X.xsymv_q8norm_b(m, d, x, self._stride(x), "b", r, self._stride(r), "b", weight, self.eps,
+                         h, d, rows[0], d, rows[1])
         return h, rows
 
+    def _stride(self, t):
+        return t.stride(0) if t.shape[0] > 1 else self.d
+
+    def _check(self, name, t, m):
+        import torch
+        if t.dtype != torch.bfloat16 or t.device != self.place.device:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, not bfloat16 on {self.place.device}")
+        if tuple(t.shape) != (m, self.d):
+            raise ValueError(f"{name} is {tuple(t.shape)}, not {(m, self.d)}")
+        if (self.d > 1 and t.stride(1) != 1) or self._stride(t) < self.d:
+            raise ValueError(f"{name}'s strides are {t.stride()}: rows lie one after the other")
+
     def __call__(self, x, r):
-        """x, r: the next m tokens' rows and residuals (m x d, bfloat16);
-        returns the layer's output and the new residual.  ValueError where the
-        cache has no room for m tokens more: nothing is done then."""
+        """x, r: the next m tokens' rows and residuals (m x d, bfloat16, at any
+        stride of rows); returns the layer's output and the new residual.
+        ValueError, with nothing done, for other tensors and where the cache has
+        no room for m tokens more."""
         import torch
         m, d, heads, hd = x.shape[0], self.d, self.heads, self.hd
+        self._check("x", x, m)
+        self._check("r", r, m)
         first, seen = self.used, self.used + m
         if seen > self.tokens:
             raise ValueError(f"the cache holds {self.tokens} tokens, {first} are there and {m} more "

@@ -81,3 +81,28 @@ def test_a_call_that_fails_takes_no_room(layer, calls, monkeypatch):
     with pytest.raises(X.XsymvError):
         layer(*tokens(2))
     assert layer.used == 0
+
+
+def test_rows_at_a_stride_are_read_there(layer, calls):
+    """x the left half of wider rows, r every second row: the norm is given
+    their strides, and a single row's own length."""
+    wide = torch.zeros((3, 2 * D), dtype=torch.bfloat16)
+    every = torch.zeros((6, D), dtype=torch.bfloat16)[::2]
+    layer(wide[:, :D], every)
+    layer(wide[:1, D:], every[:1].expand(1, D))
+    norms = [a for name, a in calls if name == "xsymv_q8norm_b"]
+    assert [(a[3], a[6], a[11]) for a in norms[0::2]] == [(2 * D, 2 * D, D), (D, D, D)]
+
+
+@pytest.mark.parametrize("which", ["x", "r"])
+def test_other_tensors_are_refused(layer, calls, which):
+    good = torch.zeros((3, D), dtype=torch.bfloat16)
+    for bad in (good.float(), good.half(), good[:, :D - 1], good[:2, None], good.flatten(),
+                torch.zeros((D, 3), dtype=torch.bfloat16).t(), good[:1].expand(3, D),
+                good.to("meta")):
+        x, r = (bad, good) if which == "x" else (good, bad)
+        with pytest.raises(ValueError):
+            layer(x, r)
+    with pytest.raises(ValueError):
+        layer(*((good[:2], good) if which == "x" else (good, good[:2])))
+    assert not calls and layer.used == 0
