@@ -485,21 +485,24 @@ def _q8():
 
 def xsymv_q8norm_s(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
-    scales; x float32, r and h of letter rtype, w of letter wtype ('s'); r, h may be None."""
+    scales; x float32, r and h of letter rtype, w of letter wtype ('s'); r, h may be None,
+    h may be r or x itself."""
     (_q8_calls or _q8()).norm_s(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
                               stream)
 
 
 def xsymv_q8norm_h(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
-    scales; x float16, r and h of letter rtype, w of letter wtype ('h' or 's'); r, h may be None."""
+    scales; x float16, r and h of letter rtype, w of letter wtype ('h' or 's'); r, h may be None,
+    h may be r or x itself."""
     (_q8_calls or _q8()).norm_h(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
                               stream)
 
 
 def xsymv_q8norm_b(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale, stream=None):
     """h := x + r in r's type, v = h / sqrt(mean(h^2) + eps) * w as rows of 8-bit codes q and
-    scales; x bfloat16, r and h of letter rtype, w of letter wtype ('b' or 's'); r, h may be None."""
+    scales; x bfloat16, r and h of letter rtype, w of letter wtype ('b' or 's'); r, h may be None,
+    h may be r or x itself."""
     (_q8_calls or _q8()).norm_b(m, n, x, ldx, rtype, r, ldr, wtype, w, eps, h, ldh, q, ldq, scale,
                               stream)
 

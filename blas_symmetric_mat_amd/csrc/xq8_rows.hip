@@ -78,6 +78,9 @@ int norm_run(int m, int n, const T* x, int ldx, char rtype, const void* r, int l
     if (ldq < std::max(1, n)) return -14;
     if (some && scale == nullptr) return -15;
     if (!some) return 0;
+    // (after the others: it is about two arguments together)
+    if (h == x && rt != 0) return -11;
+    if (h == x && ldh != ldx) return -12;
     if (rt == 0 && wt == 0)
         return norm_typed<T, T, T>(m, n, x, ldx, r, ldr, w, eps, h, ldh, q, ldq, scale, stream);
     if constexpr (!std::is_same<T, float>::value) {

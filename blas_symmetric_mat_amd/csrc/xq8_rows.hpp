@@ -182,8 +182,8 @@ __device__ __forceinline__ float q8_inverse_of(float a)
 
 // h = x + r rounded to R's type (which is what is kept and what is
 // normalised), v = h / sqrt(mean(h^2) + eps) * w.  r may be null (h = x), h
-// may be null (not kept) or r itself: an element is read and written by the
-// same thread.  The sum of squares is taken in 64 bits, which a row of the
+// may be null (not kept), or r or x itself: an element is then read and written
+// by the same thread alone.  The sum of squares is taken in 64 bits, which a row of the
 // largest 32-bit numbers cannot overflow, and costs nothing beside the loads.
 template <class T, class R, class W>
 struct Q8Norm {
@@ -197,7 +197,10 @@ struct Q8Norm {
     int m, n;
 
     __device__ __forceinline__ long long dest(long long row) const { return row; }
-    __device__ __forceinline__ bool in_place() const { return (const void*)h == (const void*)r; }
+    __host__ __device__ __forceinline__ bool in_place() const
+    {
+        return (const void*)h == (const void*)r || (const void*)h == (const void*)x;
+    }
     __device__ __forceinline__ void sum(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
     {
         q8_load(x + row * ldx + c, have, v);
@@ -225,7 +228,7 @@ struct Q8Norm {
                 if (e >= again) ss = __builtin_fma((double)v[e], (double)v[e], ss);
         }
     }
-    // a row too long for the registers: what was kept is read back (r may
+    // a row too long for the registers: what was kept is read back (r or x may
     // have been overwritten by it)
     __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
     {
@@ -316,7 +319,7 @@ struct Q8Store {
 // element at a time it cost rows of 255 and 1564 elements 40 % more time.
 // Not where an output takes an input's place: there an element belongs to one
 // thread.
-__device__ __forceinline__ int q8_last_column(int n, bool alone)
+__host__ __device__ __forceinline__ int q8_last_column(int n, bool alone)
 {
     return !alone && n >= Q8_CHUNK ? n - Q8_CHUNK : 0x7fffffff;
 }

@@ -360,9 +360,11 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  *   + eps) * w, stored as codes q and scales (one a row).  rtype, wtype: the
  *   letter of r and h, and of w (n elements): the call's own letter or 's'.
  *   r NULL: no residual, h = x.  h NULL: not kept.  h may be r itself (with
- *   ldh == ldr); nothing else may overlap an output.  Codes: -1 m < 0,
- *   -2 n < 0, -3 x NULL, -4 ldx, -5 rtype, -7 ldr, -8 wtype, -9 w NULL,
- *   -10 eps < 0 or not finite, -12 ldh, -13 q NULL, -14 ldq, -15 scale NULL.
+ *   ldh == ldr) or x itself (with ldh == ldx, and r of x's type); nothing else
+ *   may overlap an output.  Codes: -1 m < 0, -2 n < 0, -3 x NULL, -4 ldx,
+ *   -5 rtype, -7 ldr, -8 wtype, -9 w NULL, -10 eps < 0 or not finite, -12 ldh,
+ *   -13 q NULL, -14 ldq, -15 scale NULL; then -11 h is x and of another type,
+ *   -12 h is x at another stride.
  *
  *   xsymv_q8glu_*:  v = g / (1 + exp(-g)) * u, stored as codes q and scales.
  *   g and u may be the halves of one matrix's rows.  Codes: -1 m, -2 n,

@@ -103,3 +103,17 @@ def build_abi_caller() -> str:
                    check=True)
     os.replace(tmp, ABI_CALLER)
     return ABI_CALLER
+
+
+def q8_rules() -> dict:
+    """What the row kernels' rules say (q8_rules.cpp), by case."""
+    os.makedirs(_BUILD, exist_ok=True)
+    exe = os.path.join(_BUILD, f"q8_rules.{os.getpid()}")
+    try:
+        subprocess.run(["/opt/rocm/bin/hipcc", "-x", "hip", "--offload-host-only", "-O1",
+                        "-std=c++17", "-o", exe, os.path.join(_HERE, "q8_rules.cpp")], check=True)
+        out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout
+    finally:
+        if os.path.exists(exe):
+            os.remove(exe)
+    return {w[0]: tuple(map(int, w[1:])) for w in map(str.split, out.splitlines())}

@@ -1,0 +1,50 @@
+"""The norm on rows in 8 bits, on the CPU: which of its arguments may be the
+same, and the rule that such rows' elements belong to one thread alone."""
+import pytest
+
+import blas_symmetric_mat_amd as X
+from tests import native
+
+ALONE = 2 ** 31 - 1  # no chunk starts before its own place
+
+
+@pytest.fixture(scope="module")
+def rules():
+    return native.q8_rules()
+
+
+@pytest.mark.parametrize("case", ["h_is_r", "h_is_x", "h_is_x_alone", "all_one"])
+def test_an_output_in_an_inputs_place_is_one_threads(rules, case):
+    """A row's last chunk may not overlap the one before it where h replaces
+    what it is made of: the elements in both would be added twice."""
+    assert rules[case] == (1, ALONE)
+
+
+@pytest.mark.parametrize("case", ["apart", "no_r"])
+def test_last_chunks_overlap_otherwise(rules, case):
+    assert rules[case] == (0, 92)
+
+
+def call(t, **change):
+    # x, r, h, q, w, scale at addresses that nothing follows
+    args = dict(m=3, n=40, x=64, ldx=40, rtype=t, r=4096, ldr=40, wtype=t, w=128, eps=1e-5, h=64,
+                ldh=40, q=192, ldq=40, scale=256)
+    args.update(change)
+    getattr(X, f"xsymv_q8norm_{t}")(*args.values(), stream=0)
+
+
+@pytest.mark.parametrize("t", ["h", "b"])
+@pytest.mark.parametrize("r", [None, 4096])
+def test_h_in_xs_place_of_another_type(t, r):
+    with pytest.raises(X.XsymvError) as e:
+        call(t, rtype="s", r=r)
+    assert e.value.code == -11
+
+
+@pytest.mark.parametrize("t", ["s", "h", "b"])
+def test_h_in_xs_place_at_another_stride(t):
+    for r in (None, 4096):
+        with pytest.raises(X.XsymvError) as e:
+            call(t, r=r, ldh=41)
+        assert e.value.code == -12
+    call(t, m=0, ldh=41)  # nothing to do
