@@ -199,7 +199,8 @@ struct Q8Norm {
     __device__ __forceinline__ long long dest(long long row) const { return row; }
     __host__ __device__ __forceinline__ bool in_place() const
     {
-        return (const void*)h == (const void*)r || (const void*)h == (const void*)x;
+        return h != nullptr &&
+               ((const void*)h == (const void*)r || (const void*)h == (const void*)x);
     }
     __device__ __forceinline__ void sum(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
     {

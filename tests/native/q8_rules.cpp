@@ -28,5 +28,7 @@ int main()
     norm<float>("h_is_x_alone", a, nullptr, a);
     norm<float>("all_one", a, a, a);
     norm<float>("no_r", a, nullptr, c);
+    norm<float>("no_h", a, b, nullptr);
+    norm<float>("neither", a, nullptr, nullptr);
     return 0;
 }
