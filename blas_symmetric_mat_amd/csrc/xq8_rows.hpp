@@ -251,12 +251,16 @@ struct Q8Norm {
     }
 };
 
-// v = g / (1 + exp(-g)) * u.  With z = exp(-|g|), which neither overflows nor
-// loses small results, 1 / (1 + exp(-g)) is 1 / (1 + z) for g >= 0 and
-// z / (1 + z) below.  The hardware's 2^t and reciprocal (1 ulp each) serve:
-// the product |g| log2(e) is rounded, so z is off by up to |g| 2^-24, but
-// where |g| is large z is a small part of 1 + z (g > 0) or v is small beside
-// |g u| (g < 0): at most a few 2^-24 of a code's 127 steps.
+// v = g / (1 + exp(-g)) * u.  With z = exp(-|g|), which does not overflow,
+// 1 / (1 + exp(-g)) is 1 / (1 + z) for g >= 0 and z / (1 + z) below.  z is taken
+// as the square of h = exp(-|g| / 2), and h multiplies g and u below zero: the
+// hardware's 2^t gives zero for results below 2^-126, which z is from g = -87.4
+// on, but a row whose gates are all there has codes all the same (g = -88, u =
+// 60000: 2^-104.6, 5 codes of a row at the floor).  Where h is
+// zero, below g = -174, |g| z |u| < 2^-116 is less than half a code of any row.
+// The hardware's 2^t and reciprocal (1 ulp each) serve: |g| log2(e) is rounded,
+// its constant as well, so v is off by up to (2 |g| + 11) 2^-24 of itself for g
+// < 0, the growing part of it z's alone.
 template <class T>
 struct Q8Glu {
     static constexpr bool NORM = false;
@@ -275,9 +279,9 @@ struct Q8Glu {
         q8_load<true>(u + row * ldu + c, have, t);
 #pragma unroll
         for (int e = 0; e < Q8_CHUNK; ++e) {
-            const float z = __builtin_amdgcn_exp2f(-1.44269504f * __builtin_fabsf(v[e]));
-            const float s = (v[e] < 0.0f ? z : 1.0f) * __builtin_amdgcn_rcpf(1.0f + z);
-            v[e] = v[e] * s * t[e];
+            const float h = __builtin_amdgcn_exp2f(-0.72134752f * __builtin_fabsf(v[e]));
+            const float s = v[e] < 0.0f ? h : 1.0f;
+            v[e] = v[e] * s * __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f)) * (t[e] * s);
         }
     }
     __device__ __forceinline__ void again(long long row, int c, int have, float (&v)[Q8_CHUNK]) const
