@@ -238,16 +238,24 @@ struct Q8Norm {
         else
             sum(row, c, have, v);
     }
-    __device__ __forceinline__ float factor(double ss) const
+    // 1 / sqrt(mean(h^2) + eps) as lift * f: it reaches from 2^-128 (a row of the
+    // largest 32-bit numbers) to 2^165 (one of the smallest, where eps is 0), and
+    // the power of two in front keeps f and h * lift normal numbers.
+    struct Factor {
+        float lift, f;
+    };
+    __device__ __forceinline__ Factor factor(double ss) const
     {
-        return (float)(1.0 / sqrt(ss / n + eps));
+        const double d = 1.0 / sqrt(ss / n + eps);
+        const float lift = d > 0x1p100 ? 0x1p64f : d < 0x1p-100 ? 0x1p-64f : 1.0f;
+        return Factor{lift, (float)(d / lift)};
     }
-    __device__ __forceinline__ void second(int c, int have, float (&v)[Q8_CHUNK], float f) const
+    __device__ __forceinline__ void second(int c, int have, float (&v)[Q8_CHUNK], Factor k) const
     {
         float t[Q8_CHUNK];
         q8_load(w + c, have, t);
 #pragma unroll
-        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = v[e] * f * t[e];
+        for (int e = 0; e < Q8_CHUNK; ++e) v[e] = v[e] * k.lift * k.f * t[e];
     }
 };
 
@@ -264,6 +272,7 @@ struct Q8Norm {
 template <class T>
 struct Q8Glu {
     static constexpr bool NORM = false;
+    struct Factor {};
     const T* g;
     const T* u;
     long long ldg, ldu;
@@ -296,6 +305,7 @@ struct Q8Glu {
 template <class T>
 struct Q8Store {
     static constexpr bool NORM = false;
+    struct Factor {};
     const T* x;
     const int* slot;
     long long ldx;
@@ -382,7 +392,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 
                 }
             }
             if constexpr (OP::NORM) {
-                const float f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
+                const auto f = op.factor(q8_row_sum<TPR>(ss, sbuf, par));
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const int c = (t + j * TPR) * Q8_CHUNK, at = j < LAST ? c : min(c, edge);
@@ -403,7 +413,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, TPR == 1024 && J == 2 ? 8 : 
                 if (c < n) q8_store_codes(a.q + dst * a.ldq + at, n - at, v[j], inv);
             }
         } else {
-            float f = 1.0f;
+            typename OP::Factor f{};
             float v[Q8_CHUNK];
             if constexpr (OP::NORM) {
                 for (long long c = t * Q8_CHUNK; c < n; c += TPR * Q8_CHUNK) {
