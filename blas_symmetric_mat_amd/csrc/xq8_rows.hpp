@@ -157,8 +157,12 @@ __device__ __forceinline__ float q8_chunk_max(const float (&v)[Q8_CHUNK], float 
 // a / 127 and 127 / a for 2^-100 <= a, each rounded once: the quotient by a
 // rounded reciprocal is corrected by its exact remainder (Markstein's method),
 // which has been compared with the division for all 2^23 significands and a
-// reciprocal off by one unit either way.  No step leaves the normal numbers
-// (of a / 128 the reciprocal is one for every a).  An infinity or NaN gives NaN.
+// reciprocal off by one unit either way.  Quotients and reciprocals are normal
+// numbers (of a / 128 the reciprocal is one for every a).  The remainder
+// a - 127 q of a scale can be subnormal for a below 2^-97; it is exact there as
+// well, and then less than the 2^-124 it would take to change q (compared for
+// all significands, the subnormal remainders kept or zero).  An infinity or NaN
+// gives NaN.
 // (The divisions were a sixth of a short row's instructions.)
 __device__ __forceinline__ float q8_scale_of(float a)
 {
