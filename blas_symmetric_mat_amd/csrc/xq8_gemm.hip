@@ -100,13 +100,13 @@ double cost_of(const Kernel& c, bool cut, int m, int n, int k, int splits, Q8Pla
 }
 
 template <int N>
-Q8Plan cheapest(const Kernel (&list)[N], bool cut, int m, int n, int k, double& low)
+Q8Plan cheapest(const Kernel (&list)[N], bool cut, bool whole, int m, int n, int k, double& low)
 {
     Q8Plan best{};
     low = -1.0;
     for (const Kernel& c : list) {
         if (m < c.from || m > c.to) continue;
-        for (int splits = 1; splits <= (c.id == Q8_STREAM ? 1 : 16); ++splits) {
+        for (int splits = 1; splits <= (whole || c.id == Q8_STREAM ? 1 : 16); ++splits) {
             if (splits > 1 && k / 256 < splits) break;
             Q8Plan p{};
             const double t = cost_of(c, cut, m, n, k, splits, p);
@@ -121,24 +121,25 @@ Q8Plan cheapest(const Kernel (&list)[N], bool cut, int m, int n, int k, double& 
 
 }  // namespace
 
-Q8Plan q8_plan(int how, bool cut, int m, int n, int k)
+Q8Plan q8_plan(int how, bool cut, bool whole, int m, int n, int k)
 {
     // the last sizes' choices: some hundred estimates take as long as a launch
     struct Known {
         int how, m, n, k;
-        bool cut;
+        bool cut, whole;
         Q8Plan plan;
     };
     static thread_local Known known[64] = {};
     const unsigned key = ((unsigned)m * 31u + (unsigned)n) * 31u + (unsigned)k * 7u + (unsigned)how;
     Known& e = known[key % 64];
-    if (e.m == m && e.n == n && e.k == k && e.how == how && e.cut == cut && m > 0) return e.plan;
+    if (e.m == m && e.n == n && e.k == k && e.how == how && e.cut == cut && e.whole == whole && m > 0)
+        return e.plan;
     double cost = 0.0;
-    Q8Plan p = how == Q8_LINES ? cheapest(LINES, cut, m, n, k, cost)
-               : how == Q8_ANY ? cheapest(ANY, false, m, n, k, cost)
-                               : cheapest(REGS, false, m, n, k, cost);
+    Q8Plan p = how == Q8_LINES ? cheapest(LINES, cut, whole, m, n, k, cost)
+               : how == Q8_ANY ? cheapest(ANY, false, whole, m, n, k, cost)
+                               : cheapest(REGS, false, whole, m, n, k, cost);
     p.how = how;
-    if ((how != Q8_LINES || cut) && k >= 16) {
+    if ((how != Q8_LINES || cut) && k >= 16 && !whole) {
         // many rows: each is read often, and from whole lines a third faster
         // than at odd strides (4096 x 28672 x 8192: 1124 us where they lie,
         // 832 with the copy; 100 x 28672 x 8192: 73 and 142 us), a tenth
@@ -146,7 +147,7 @@ Q8Plan q8_plan(int how, bool cut, int m, int n, int k)
         // 48 and 50 us)
         const size_t copy = align_up(((size_t)m + n) * q8_copy_ld(k));
         double lines = 0.0;
-        Q8Plan c = cheapest(LINES, false, m, n, k, lines);
+        Q8Plan c = cheapest(LINES, false, false, m, n, k, lines);
         if (copy <= MAX_COPY && c.groups != 0 &&
             (p.groups == 0 || lines + COPY_LAUNCH + COPY_BYTE * k * ((double)m + n) < cost)) {
             p = c;
@@ -155,7 +156,7 @@ Q8Plan q8_plan(int how, bool cut, int m, int n, int k)
             p.copy = copy;
         }
     }
-    e = Known{how, m, n, k, cut, p};
+    e = Known{how, m, n, k, cut, whole, p};
     return p;
 }
 
@@ -172,7 +173,7 @@ extern "C" size_t xsymv_q8gemm_workspace_bytes(int m, int n, int k)
             for (int how : {Q8_REGS, Q8_LINES, Q8_ANY})
                 for (bool cut : {false, true})
                     if (rows > 0 && cols > 0) {
-                        const Q8Plan p = q8_plan(how, cut, rows, cols, k);
+                        const Q8Plan p = q8_plan(how, cut, false, rows, cols, k);
                         most = std::max(most, p.copy + p.part);
                     }
     return most;

@@ -42,8 +42,9 @@ inline int q8_copy_ld(int k)
 }
 
 // The kernel for m x n x k with rows read as `how`; `cut`: they do not start at
-// multiples of 128 bytes, so that a step's bytes lie on more lines.
-Q8Plan q8_plan(int how, bool cut, int m, int n, int k);
+// multiples of 128 bytes, so that a step's bytes lie on more lines; `whole`: of
+// the plans that take no workspace, k in one share and the rows where they lie.
+Q8Plan q8_plan(int how, bool cut, bool whole, int m, int n, int k);
 
 // Rows and columns of one launch at most.
 constexpr int Q8_BLOCK = 1 << 24;
@@ -118,21 +119,39 @@ int gemm_block(Q8GemmArgs<T> g, int lda, int ldw, hipStream_t stream)
     const int how = q8_how(g.k, g.a, lda, g.w, ldw);
     const size_t starts = reinterpret_cast<size_t>(g.a) | reinterpret_cast<size_t>(g.w);
     const bool cut = how == Q8_LINES && (starts | (size_t)(lda | ldw)) % 128 != 0;
-    const Q8Plan p = q8_plan(how, cut, g.m, g.n, g.k);
-    if (p.groups == 0) return ERR_HIP + (int)hipErrorInvalidValue;  // more than a launch holds
+    Q8Plan p = q8_plan(how, cut, false, g.m, g.n, g.k);
+    auto fits = [&] { return p.groups != 0; };  // else more than a launch holds
+    if (!fits()) return ERR_HIP + (int)hipErrorInvalidValue;
     int threads = 0;
-    const Q8GemmKernel<T> kernel = q8_kernel<T>(p, threads);
-    g.splits = p.splits;
-    g.per = p.per;
-    if (p.splits == 1 && p.ldc == 0) return q8_launch(kernel, p.groups, threads, stream, g);
+    auto straight = [&] {  // without a workspace
+        g.splits = 1;
+        g.per = p.per;
+        const Q8GemmKernel<T> kernel = q8_kernel<T>(p, threads);
+        return q8_launch(kernel, p.groups, threads, stream, g);
+    };
+    if (p.copy + p.part == 0) return straight();
 
     int dev = 0;
     XSYMV_HIP(hipGetDevice(&dev));
     DeviceState* ds = device_state(dev);
     std::lock_guard<std::mutex> lk(device_mutex(ds));
     void* ws = nullptr;
-    const int rc = get_workspace(ds, stream, p.copy + p.part, &ws);
+    // Where the workspace cannot be had, because the device has no memory left
+    // or a capture forbids to allocate it, the product is made without: slower,
+    // and to the same bytes.
+    int rc = ERR_HIP + (int)hipErrorOutOfMemory;
+    if (!workspace_barred(ds, stream, p.copy + p.part)) {
+        rc = get_workspace(ds, stream, p.copy + p.part, &ws);
+        if (rc == ERR_HIP + (int)hipErrorOutOfMemory) (void)hipGetLastError();  // dealt with
+    }
+    if (rc == ERR_HIP + (int)hipErrorOutOfMemory) {
+        p = q8_plan(how, cut, true, g.m, g.n, g.k);
+        return fits() ? straight() : rc;
+    }
     if (rc) return rc;
+    g.splits = p.splits;
+    g.per = p.per;
+    const Q8GemmKernel<T> kernel = q8_kernel<T>(p, threads);
     TimedCall tc{};
     const int timing = timing_enabled();
     if (timing) {

@@ -579,6 +579,20 @@ int get_strip_plan(DeviceState* ds, int dev, bool upper, int n, int R, int G, in
     return 0;
 }
 
+static bool is_captured(hipStream_t stream)
+{
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    return stream != nullptr && hipStreamIsCapturing(stream, &status) == hipSuccess &&
+           status != hipStreamCaptureStatusNone;
+}
+
+bool workspace_barred(DeviceState* ds, hipStream_t stream, size_t bytes)
+{
+    const auto it = ds->workspaces.find(stream);
+    if (it != ds->workspaces.end() && (!it->second.owned || it->second.bytes >= bytes)) return false;
+    return is_captured(stream);
+}
+
 int get_workspace(DeviceState* ds, hipStream_t stream, size_t bytes, void** out)
 {
     auto& ws = ds->workspaces[stream];
@@ -600,11 +614,7 @@ int get_workspace(DeviceState* ds, hipStream_t stream, size_t bytes, void** out)
     }
     // a graph that is being captured keeps the address: a later call that
     // outgrows the buffer must not free it
-    if (ws.owned && !ws.captured && stream != nullptr) {
-        hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-        ws.captured = hipStreamIsCapturing(stream, &status) == hipSuccess &&
-                      status != hipStreamCaptureStatusNone;
-    }
+    if (ws.owned && !ws.captured) ws.captured = is_captured(stream);
     *out = ws.ptr;
     return 0;
 }

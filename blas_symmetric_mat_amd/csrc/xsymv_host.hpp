@@ -203,6 +203,9 @@ int resident_blocks(const void* kernel, int threads, int* out);
 int get_plan(DeviceState* ds, int dev, bool upper, int n, int NB, int R, hipStream_t stream,
              const Plan** out);
 int get_workspace(DeviceState* ds, hipStream_t stream, size_t bytes, void** out);
+// Whether the stream is being captured while its workspace (the library's own)
+// holds less than `bytes`: growing it would end the capture.
+bool workspace_barred(DeviceState* ds, hipStream_t stream, size_t bytes);
 std::mutex& device_mutex(DeviceState* ds);
 
 inline size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }

@@ -396,10 +396,13 @@ size_t xtrmv_workspace_bytes(int prec, char uplo, char trans, int n);
  *   of its shares of k, and where many rows lie at strides that are slow to
  *   read for a copy of them (up to 1 GiB).  xsymv_q8gemm_workspace_bytes is
  *   what a product of m x n x k takes at most, whatever the operands' alignment
- *   (0 where it takes none).  While a stream is captured nothing can be
- *   allocated, so a product of the same size has to have run on it before, or a
- *   workspace of that many bytes be installed.  A graph keeps the workspace of
- *   the stream it was captured on (the library frees such a one in
+ *   (0 where it takes none).  A call that outgrows the stream's workspace waits
+ *   for the stream's earlier work while it is replaced.  Where it cannot grow,
+ *   for want of device memory or because the stream is being captured, the
+ *   product is made without: the same bytes, in up to several times the time.
+ *   For a graph of the usual speed, run a product of the same size on the
+ *   stream before, or install a workspace of that many bytes.  A graph keeps the
+ *   workspace of the stream it was captured on (the library frees such a one in
  *   xsymv_release only), so its replays must not overlap with products on that
  *   stream, nor with those of another graph captured there. */
 typedef unsigned short xhalf;     /* IEEE half, its 16 bits */

@@ -117,3 +117,43 @@ def q8_rules() -> dict:
         if os.path.exists(exe):
             os.remove(exe)
     return {w[0]: tuple(map(int, w[1:])) for w in map(str.split, out.splitlines())}
+
+
+def build_q8_host() -> str:
+    """Compile the product's host side on a stand-in for the HIP runtime
+    (q8_host.cpp); libxsymv must be built.  The caller removes it."""
+    os.makedirs(_BUILD, exist_ok=True)
+    lib_dir = os.path.join(os.path.dirname(os.path.dirname(_HERE)), "blas_symmetric_mat_amd")
+    exe = os.path.join(_BUILD, f"q8_host.{os.getpid()}")
+    subprocess.run(["/opt/rocm/bin/hipcc", "-O1", "-std=c++17", "-o", exe,
+                    os.path.join(_HERE, "q8_host.cpp"), "-L", lib_dir, "-lxsymv",
+                    "-Wl,-rpath," + lib_dir, "-ldl"], check=True)
+    return exe
+
+
+class Q8Host:
+    """A run of that program: `ask` gives one command, `many` a list of them;
+    an answer is its words."""
+
+    def __init__(self, exe):
+        self.run = subprocess.Popen([exe], stdin=subprocess.PIPE, stdout=subprocess.PIPE,
+                                    text=True)
+
+    def ask(self, *words):
+        return self.many([words])[0]
+
+    def many(self, commands):
+        out = []
+        for i in range(0, len(commands), 100):  # as many as the pipes hold
+            part = commands[i:i + 100]
+            self.run.stdin.write("".join(" ".join(map(str, c)) + "\n" for c in part))
+            self.run.stdin.flush()
+            lines = [self.run.stdout.readline() for _ in part]
+            assert all(lines), "the program ended"
+            out += [line.split() for line in lines]
+        return out
+
+    def close(self):
+        self.run.stdin.close()
+        self.run.wait(timeout=30)
+        self.run.stdout.close()
