@@ -1,11 +1,17 @@
 """The 8-bit product's host side, without a GPU: what it does where a stream's
-workspace cannot be had, on a stand-in for the HIP runtime that writes kernels
-down and counts device memory (tests/native/q8_host.cpp)."""
+workspace cannot be had, and which kernels it chooses, on a stand-in for the HIP
+runtime that writes kernels down and counts device memory
+(tests/native/q8_host.cpp)."""
+import collections
+import math
 import os
+import random
 
 import pytest
 
 from tests import native
+from tests.test_gpu_q8 import KERNELS
+from tests.test_gpu_q8_gemm import ENDS, MORE, operands
 
 MiB = 1 << 20
 
@@ -106,3 +112,43 @@ def test_what_a_graph_holds_is_not_freed(host):
     assert held - MiB == 256 * 8192 * 4 * 4  # both buffers
     assert host.ask("release") == ["0"]
     assert product(host, ("b", 1, 16, 16, 4096, 16, 4096, 16))[1] == 0
+
+
+def chosen(host, sizes):
+    """The kernel of each product (how, m, n, k), bfloat16, and whether k is
+    shared out."""
+    calls = []
+    for how, m, n, k in sizes:
+        pads, offs = operands(how, k)
+        calls.append(("gemm", "b", m, n, k, 4096 + offs[0], k + pads[0], 8192 + offs[1], k + pads[1]))
+    out = []
+    for size, words in zip(sizes, host.many(calls)):
+        assert words[0] == "0", size
+        kernels = [w.split(":")[0] for w in words[2:]]
+        product, = [w for w, kind in zip(kernels, kinds(kernels)) if kind == "product"]
+        out.append((product, "join" in kinds(kernels)))
+    return out
+
+
+def test_every_kernel_is_tested(host):
+    """Sizes over the whole range choose no kernel, whole or with k shared out,
+    that the sizes of the GPU tests of kernels do not choose at a dozen ends of
+    k or more."""
+    tested = collections.Counter(chosen(host, [(how, m, n, k // 128 * 128 + end)
+                                               for how, m, n, k in KERNELS + MORE for end in ENDS]))
+    rng = random.Random(3)
+
+    def log(low, high):
+        return int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))
+
+    reached = collections.Counter()
+    for how in ("lines", "any", "odd"):
+        sizes = []
+        while len(sizes) < 20000:
+            m, n, k = log(1, 8192), log(1, 32768), log(1, 32768)
+            if m * n * k <= 1 << 40:
+                sizes.append((how, m, n, k))
+        reached.update(chosen(host, sizes))
+    missing = {k: (n, tested[k]) for k, n in reached.items() if tested[k] < 12}
+    assert not missing
+    assert len(reached) > 30
