@@ -15,6 +15,7 @@ raises ``ImportError``.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -470,15 +471,64 @@ def xsymv_combine_w(n, nshards, alpha, P, ldp, beta, y, incy, stream=None):
 
 _q8_calls = None
 
+# arguments of the 8-bit row operators before the stream: i number, p address,
+# c type letter, f real number
+_Q8_ARGS = {"norm": "iipicpicpfpipip", "glu": "iipipipip", "store": "iipipipip",
+            "read": "iipippipi", "gemm": "iiipippipppi"}
+
+
+def _q8_int(v):
+    v = operator.index(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise OverflowError("an argument is outside the C int range")
+    return v
+
+
+def _q8_letter(v):
+    if not isinstance(v, (str, bytes)):
+        raise TypeError("a type letter is a string")
+    return (v.encode() if isinstance(v, str) else v)[:1] or b"\0"
+
+
+class _Q8Ctypes:
+    """The 8-bit row operators' calls through ctypes, under the names of the
+    compiled module, where that has not been built."""
+
+    _KIND = {"i": (ctypes.c_int, _q8_int), "p": (ctypes.c_void_p, _addr),
+             "c": (ctypes.c_char, _q8_letter), "f": (ctypes.c_float, float)}
+
+    def __init__(self):
+        for op, kinds in _Q8_ARGS.items():
+            for t in "shb":
+                setattr(self, f"{op}_{t}", self._entry(f"xsymv_q8{op}_{t}", kinds))
+
+    def _entry(self, name, kinds):
+        f = getattr(library(), name)
+        f.restype = ctypes.c_int
+        f.argtypes = [self._KIND[c][0] for c in kinds] + [ctypes.c_void_p]
+        convert = [self._KIND[c][1] for c in kinds]
+
+        def call(*args):
+            if len(args) != len(convert) + 1:
+                raise TypeError(f"{name} takes {len(convert)} arguments and a stream")
+            rc = f(*[c(a) for c, a in zip(convert, args)], _stream(args[-1]))
+            if rc != 0:
+                raise XsymvError(name, rc)
+        return call
+
 
 def _q8():
-    """The compiled marshalling of the 8-bit row operators (csrc/q8_bind.c)."""
+    """The marshalling of the 8-bit row operators: compiled (csrc/q8_bind.c),
+    through ctypes where it has not been."""
     global _q8_calls
     if _q8_calls is None:
         library()
-        import importlib
-        module = importlib.import_module("blas_symmetric_mat_amd._q8_bind")
-        module.setup(XsymvError, lambda: _stream(None))
+        try:
+            from . import _q8_bind as module
+        except ImportError:
+            module = _Q8Ctypes()
+        else:
+            module.setup(XsymvError, lambda: _stream(None))
         _q8_calls = module
     return _q8_calls
 

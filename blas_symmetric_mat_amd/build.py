@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -22,7 +23,8 @@ UNITS = ["xsymv_host", "xsymv_prec_s", "xsymv_prec_d", "xsymv_prec_c", "xsymv_pr
          "xq8_gemm_b"]
 ARCH = os.environ.get("XSYMV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-CC = os.environ.get("CC", "gcc")
+# any C compiler does for the Python side: the one asked for, gcc, or hipcc's own clang
+CC = os.environ.get("CC") or shutil.which("gcc") or os.path.join(os.path.dirname(HIPCC), "amdclang")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-function"]
@@ -38,13 +40,22 @@ def _compile(unit: str, extra: list[str]) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def build_bind() -> str:
+def build_bind() -> str | None:
     """The compiled Python side of the 8-bit row operators, linked against the
-    library beside it."""
-    out = os.path.join(HERE, "_q8_bind.so")
+    library beside it; the file is this interpreter's (its name says which).
+    Without a C compiler or Python's headers there is none, and the calls are
+    marshalled by ctypes (1 us more each)."""
+    out = os.path.join(HERE, "_q8_bind" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+    include = sysconfig.get_paths()["include"]
+    if shutil.which(CC) is None or not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write(f"no {CC} or no Python.h in {include}: the 8-bit row operators are called "
+                         "through ctypes\n")
+        if os.path.exists(out):
+            os.remove(out)  # an older library's
+        return None
     tmp = out + f".tmp{os.getpid()}"
-    r = subprocess.run([CC, "-O2", "-Wall", "-shared", "-fPIC",
-                        "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "q8_bind.c"),
+    r = subprocess.run([CC, "-O2", "-Wall", "-shared", "-fPIC", "-I" + include,
+                        os.path.join(CSRC, "q8_bind.c"),
                         "-o", tmp, "-L" + HERE, "-lxsymv", "-Wl,-rpath,$ORIGIN",
                         "-Wl,--allow-shlib-undefined"], capture_output=True, text=True)
     if r.returncode != 0:
@@ -55,7 +66,7 @@ def build_bind() -> str:
 
 def build(jobs: int | None = None, resource_usage: bool = False, verbose: bool = False) -> str:
     """Compile every unit and link ``libxsymv.so``, then the Python side of the
-    8-bit row operators; returns the library's path."""
+    8-bit row operators where it can be; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Rpass-analysis=kernel-resource-usage"] if resource_usage else []
     jobs = jobs or min(len(UNITS), max(1, min(16, os.cpu_count() or 1)))
