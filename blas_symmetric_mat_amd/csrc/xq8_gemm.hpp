@@ -231,9 +231,10 @@ __global__ __launch_bounds__(64 * Q8_WAVES) void q8_gemm_stream(Q8GemmArgs<T> g)
 //
 // What bounds a full compute unit is LDS, at 128 bytes a cycle: a step of 128
 // bytes of k takes 1024 cycles of reads and writes and 512 of multiplications
-// in a 128 x 128 tile of eight waves (0.48 us measured, 1010 cycles), 1408 and
-// 1024 in 256 x 128 (0.69 us), 2048 and 2048 in 256 x 256 (1.27 us, at the
-// clock of 1.9 GHz that the multiplications leave).  The loads could bring
+// in a 128 x 128 tile of eight waves, 1408 and 1024 in 256 x 128, 2048 and 2048
+// in 256 x 256.  The steps that fit best over many sizes are 0.48, 0.69 and 1.27
+// us; the last is 1.6 in 4096 x 28672 x 8192 (740 us, 448 steps one after the
+// other), where the multiplications leave a clock of 1.9 GHz.  The loads could bring
 // twice the bytes (125 GB/s a compute unit from the die's cache).  Four waves
 // of larger parts read less but wait more: 2048 x 8192 x 8192 by 128 x 128
 // tiles of four waves 196 us, of eight 163, by 256 x 128 of eight 131.

@@ -133,7 +133,7 @@ int store_run(int m, int n, const T* x, int ldx, const int* slot, int cap, signe
 template <class T, int TPR>
 int read_launch(const Q8ReadArgs<T>& a, hipStream_t stream)
 {
-    // some 2^23 workgroups at most, which loop over the rest
+    // 2^20 workgroups at most, which loop over the rest
     const long long parts = ((long long)a.n + TPR * Q8_CHUNK - 1) / (TPR * Q8_CHUNK);
     const unsigned rows = q8_grid(a.m, 256 / TPR);
     const dim3 grid(rows, (unsigned)std::min(parts, std::max(1ll, (1ll << 16) / rows)));

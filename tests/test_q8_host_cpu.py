@@ -3,12 +3,15 @@ workspace cannot be had, and which kernels it chooses, on a stand-in for the HIP
 runtime that writes kernels down and counts device memory
 (tests/native/q8_host.cpp)."""
 import collections
+import json
 import math
 import os
 import random
+import re
 
 import pytest
 
+import blas_symmetric_mat_amd as X
 from tests import native
 from tests.test_gpu_q8 import KERNELS
 from tests.test_gpu_q8_gemm import ENDS, MORE, operands
@@ -152,3 +155,48 @@ def test_every_kernel_is_tested(host):
     missing = {k: (n, tested[k]) for k, n in reached.items() if tested[k] < 12}
     assert not missing
     assert len(reached) > 30
+
+
+def named(kernel, groups, m, n):
+    """A launched kernel's name in the record, and its shares of k."""
+    a = [int(v) for v in re.findall(r"Li(\d+)E", kernel)]
+    if "stream" in kernel:
+        name, tile = "stream", (16, 16)
+    elif "ring" in kernel:
+        name, tile = ("ring", "ring32")[a[0] - 1], (16 * a[0], 16 * a[0])
+    else:
+        bm, bn, _, _, q, buffers, how = a
+        tile = bm, bn
+        name = {(16, 64): "tile16", (32, 64): "tile32", (64, 64): "tile64", (128, 64): "tile128x64",
+                (128, 128): "tile128", (256, 128): "tile256x128", (256, 256): "tile256"}[tile]
+        if name in ("tile64", "tile128") and (q, buffers) == (1, 2) and how != 0:
+            name += "_short"
+    return name, groups // (-(-m // tile[0]) * -(-n // tile[1]))
+
+
+@pytest.mark.parametrize("how,over", [("lines", 1.02), ("any", 1.03), ("odd", 1.02)])
+def test_choices_against_the_record(host, how, over):
+    """Over the sizes of the committed measurements the kernel and the shares
+    of k that the cost model chooses are hardly slower on average than the
+    fastest that was measured (products whose rows are copied first apart)."""
+    path = os.path.join(os.path.dirname(X.__file__), "tuned", "mi355x_q8gemm.json")
+    with open(path) as f:
+        record = json.load(f)
+    names, rows = record["kernels"], record[how]
+    pad_a, pad_w, start = {"lines": (0, 0, 0), "any": (3, 5, 0), "odd": (3, 5, 1)}[how]
+    calls = [("gemm", "b", m, n, k, 4096 + start, k + pad_a, 8192 + start, k + pad_w)
+             for m, n, k, *_ in rows]
+    ratios, unmeasured, copied = [], 0, 0
+    for (m, n, k, *times), words in zip(rows, host.many(calls)):
+        kernel, groups, _ = words[2].split(":")
+        if kernel == "?":
+            copied += 1
+            continue
+        measured = {(names[i], s): us for i, s, us in zip(times[::3], times[1::3], times[2::3])}
+        us = measured.get(named(kernel, int(groups), m, n))
+        if us is None:  # not measured, or slower than the record keeps
+            unmeasured += 1
+        else:
+            ratios.append(us / min(measured.values()))
+    assert math.exp(sum(map(math.log, ratios)) / len(ratios)) <= over
+    assert unmeasured <= 0.1 * len(rows) and copied <= 0.4 * len(rows)
