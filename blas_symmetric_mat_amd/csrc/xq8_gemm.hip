@@ -7,7 +7,8 @@ namespace {
 
 // What ranks the kernels: a model of a call's time fitted to measurements on
 // MI355X over a grid of sizes (m 1 to 8000, n and k 128 to 28672, every number
-// of shares; tuned/mi355x_q8gemm.json holds them).  `launch`, and for every
+// of shares; tuned/mi355x_q8gemm.json holds what is within 1.5 times of each
+// size's fastest).  `launch`, and for every
 // round of workgroups that the chip holds at once `round` plus, for each of the
 // share's steps, `alone` where a compute unit runs one workgroup, `full` where
 // it runs all it can and between them otherwise; but no less than W's bytes take
@@ -18,8 +19,8 @@ namespace {
 // not in it (8000 x 8192 x 1024 in 256 x 256 tiles 94 us, estimated 65).  The
 // choice is 1 % slower on average than the fastest kernel measured (2 % for up
 // to 16 rows, 4 % where those lie at odd strides; at worst 2 times, at sizes of
-// a few microseconds).  The rings are chosen at 400 of the grid's 1070 sizes of whole lines and 200 of 630
-// at odd strides, and are 1.16 (up to 16 rows) to 1.37 times faster there than
+// a few microseconds).  The rings are chosen at 400 of the grid's 1070 sizes of
+// whole lines and 200 of 630 at odd strides, and are 1.16 (up to 16 rows) to 1.37 times faster there than
 // the next kernel.  The 64-row tile alone, at its best number of shares, would
 // be 1.07 (m = 65 to 128) to 1.36 times (m > 512) slower than the tiles together,
 // and without shares of k up to 5 times.

@@ -270,6 +270,7 @@ struct Q8Norm {
 // on, but a row whose gates are all there has codes all the same (g = -88, u =
 // 60000: 2^-104.6, 5 codes of a row at the floor).  Where h is
 // zero, below g = -174, |g| z |u| < 2^-116 is less than half a code of any row.
+// (z by itself: 4096 x 14336 52.4 us, so 53.1.)
 // The hardware's 2^t and reciprocal (1 ulp each) serve: |g| log2(e) is rounded,
 // its constant as well, so v is off by up to (2 |g| + 11) 2^-24 of itself for g
 // < 0, the growing part of it z's alone.
