@@ -38,7 +38,11 @@ __all__ = ["xsymv_s", "xsymv_d", "xhemv_c", "xhemv_z", "xsymv_w", "XsymvError",
            "xsymv_q8glu_s", "xsymv_q8glu_h", "xsymv_q8glu_b",
            "xsymv_q8store_s", "xsymv_q8store_h", "xsymv_q8store_b",
            "xsymv_q8read_s", "xsymv_q8read_h", "xsymv_q8read_b",
-           "xsymv_q8gemm_s", "xsymv_q8gemm_h", "xsymv_q8gemm_b"]
+           "xsymv_q8gemm_s", "xsymv_q8gemm_h", "xsymv_q8gemm_b",
+           "xsymv_q8attn_s", "xsymv_q8attn_h", "xsymv_q8attn_b", "q8attn_workspace_bytes",
+           "xsymv_q8pages_grow", "xsymv_q8pages_slots", "xsymv_q8pages_fork",
+           "xsymv_q8pages_free", "xsymv_q8pages_compact", "xsymv_q8pages_copy",
+           "xsymv_logp_s", "xsymv_logp_h", "xsymv_logp_b", "logp_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libxsymv.so")
 PREC_CODE = {"s": 0, "d": 1, "c": 2, "z": 3, "w": 4}
@@ -212,6 +216,10 @@ def library():
             lib.xgemv_plan.argtypes = [ci, ci, ci, ci, ip, ci, ip, ci]
             lib.xsymv_q8gemm_workspace_bytes.restype = ctypes.c_size_t
             lib.xsymv_q8gemm_workspace_bytes.argtypes = [ci, ci, ci]
+            lib.xsymv_q8attn_workspace_bytes.restype = ctypes.c_size_t
+            lib.xsymv_q8attn_workspace_bytes.argtypes = [ci] * 6
+            lib.xsymv_logp_workspace_bytes.restype = ctypes.c_size_t
+            lib.xsymv_logp_workspace_bytes.argtypes = [ci, ci, ci]
             lib.xsymv_read_bandwidth.restype = ci
             lib.xsymv_read_bandwidth.argtypes = [ctypes.c_size_t, ci, vp, fp, fp]
             lib.xsymv_copy_bandwidth.restype = ci
@@ -474,7 +482,12 @@ _q8_calls = None
 # arguments of the 8-bit row operators before the stream: i number, p address,
 # c type letter, f real number
 _Q8_ARGS = {"norm": "iipicpicpfpipip", "glu": "iipipipip", "store": "iipipipip",
-            "read": "iipippipi", "gemm": "iiipippipppi"}
+            "read": "iipippipi", "gemm": "iiipippipppi",
+            "attn": "iiiipiipppiipppippipiifpip"}
+# of the calls on a cache's pages, and of the log probabilities
+_PAGES_ARGS = {"grow": "ippippiiipp", "slots": "iipippiiip", "fork": "ippippiiippp",
+               "free": "ipippiiip", "compact": "ipipiippppp", "copy": "ippiiipippipii"}
+_LOGP_ARGS = "iipippppippi"
 
 
 def _q8_int(v):
@@ -501,6 +514,10 @@ class _Q8Ctypes:
         for op, kinds in _Q8_ARGS.items():
             for t in "shb":
                 setattr(self, f"{op}_{t}", self._entry(f"xsymv_q8{op}_{t}", kinds))
+        for op, kinds in _PAGES_ARGS.items():
+            setattr(self, f"pages_{op}", self._entry(f"xsymv_q8pages_{op}", kinds))
+        for t in "shb":
+            setattr(self, f"logp_{t}", self._entry(f"xsymv_logp_{t}", _LOGP_ARGS))
 
     def _entry(self, name, kinds):
         f = getattr(library(), name)
@@ -624,6 +641,99 @@ def xsymv_q8gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream=None):
     """C[i, j] := (sum_l A[i, l] * W[j, l]) * sa[i] * sw[j] + bias[j], bfloat16; A, W 8-bit codes in
     rows, the sum exact (k <= 131071); sa, sw, bias float32, bias may be None."""
     (_q8_calls or _q8()).gemm_b(m, n, k, A, lda, sa, W, ldw, sw, bias, C, ldc, stream)
+
+
+def xsymv_q8attn_s(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first, shared,
+                   k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream=None):
+    """out := softmax(scale * q K^T) V, float32, for the last rows of `seqs` sequences, whose keys and
+    values lie in a cache of 8-bit rows in pages (table, seqs x ldt; len); start None: a row each.
+    The first shared[g] tokens of sequences first[g] to first[g + 1] are the same pages."""
+    (_q8_calls or _q8()).attn_s(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first,
+                                shared, k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream)
+
+
+def xsymv_q8attn_h(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first, shared,
+                   k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream=None):
+    """out := softmax(scale * q K^T) V, float16, for the last rows of `seqs` sequences, whose keys and
+    values lie in a cache of 8-bit rows in pages (table, seqs x ldt; len); start None: a row each.
+    The first shared[g] tokens of sequences first[g] to first[g + 1] are the same pages."""
+    (_q8_calls or _q8()).attn_h(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first,
+                                shared, k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream)
+
+
+def xsymv_q8attn_b(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first, shared,
+                   k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream=None):
+    """out := softmax(scale * q K^T) V, bfloat16, for the last rows of `seqs` sequences, whose keys and
+    values lie in a cache of 8-bit rows in pages (table, seqs x ldt; len); start None: a row each.
+    The first shared[g] tokens of sequences first[g] to first[g + 1] are the same pages."""
+    (_q8_calls or _q8()).attn_b(rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt, groups, first,
+                                shared, k, ldk, ks, v, ldv, vs, pages, ps, scale, out, ldo, lse, stream)
+
+
+def xsymv_q8pages_grow(n, seq, add, seqs, len, table, ldt, pages, ps, refs, got, stream=None):
+    """Sequence seq[i] gets add[i] tokens more: free pages, the lowest first, enter its row of the
+    table; got[i] = add[i], or 0 where that cannot be."""
+    (_q8_calls or _q8()).pages_grow(n, seq, add, seqs, len, table, ldt, pages, ps, refs, got, stream)
+
+
+def xsymv_q8pages_slots(rows, kvheads, start, seqs, len, table, ldt, pages, ps, slot, stream=None):
+    """slot[r * kvheads + h] = the cache's row of row r's token and head h, -1 where there is none
+    (for xsymv_q8store_*)."""
+    (_q8_calls or _q8()).pages_slots(rows, kvheads, start, seqs, len, table, ldt, pages, ps, slot, stream)
+
+
+def xsymv_q8pages_fork(n, parent, child, seqs, len, table, ldt, pages, ps, refs, src, dst, stream=None):
+    """Sequence child[i] becomes a copy of parent[i]: whole pages are held by both, a last one that is
+    not full is to be copied from page src[i] to dst[i] (xsymv_q8pages_copy)."""
+    (_q8_calls or _q8()).pages_fork(n, parent, child, seqs, len, table, ldt, pages, ps, refs, src, dst, stream)
+
+
+def xsymv_q8pages_free(n, seq, seqs, len, table, ldt, pages, ps, refs, stream=None):
+    """Sequence seq[i] gives its pages back and is empty."""
+    (_q8_calls or _q8()).pages_free(n, seq, seqs, len, table, ldt, pages, ps, refs, stream)
+
+
+def xsymv_q8pages_compact(seqs, table, ldt, out, ldo, pages, refs, rout, src, dst, live, stream=None):
+    """The pages that are held are to move together: from page src[k] to dst[k] (xsymv_q8pages_copy);
+    out, rout: the table and the counts as they are then, live: how many pages."""
+    (_q8_calls or _q8()).pages_compact(seqs, table, ldt, out, ldo, pages, refs, rout, src, dst, live, stream)
+
+
+def xsymv_q8pages_copy(n, src, dst, pages, rows, hd, k, ldk, ks, v, ldv, vs, layers=1, stride=0, stream=None):
+    """Page src[i] copied to page dst[i] (rows of hd codes and their scales, keys and values), in each
+    of `layers` caches that lie `stride` rows apart; numbers that are no pages are passed over."""
+    (_q8_calls or _q8()).pages_copy(n, src, dst, pages, rows, hd, k, ldk, ks, v, ldv, vs, layers, stride, stream)
+
+
+def xsymv_logp_s(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream=None):
+    """Log probability of token[i] in row i of the float32 logits x, the row's entropy and log-sum, and
+    its `top` most likely tokens (ties to the lowest index) with their log probabilities; token,
+    entropy, lse and value may be None."""
+    (_q8_calls or _q8()).logp_s(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream)
+
+
+def xsymv_logp_h(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream=None):
+    """Log probability of token[i] in row i of the float16 logits x, the row's entropy and log-sum, and
+    its `top` most likely tokens (ties to the lowest index) with their log probabilities; token,
+    entropy, lse and value may be None."""
+    (_q8_calls or _q8()).logp_h(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream)
+
+
+def xsymv_logp_b(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream=None):
+    """Log probability of token[i] in row i of the bfloat16 logits x, the row's entropy and log-sum, and
+    its `top` most likely tokens (ties to the lowest index) with their log probabilities; token,
+    entropy, lse and value may be None."""
+    (_q8_calls or _q8()).logp_b(m, n, x, ldx, token, logp, entropy, lse, top, index, value, ldt, stream)
+
+
+def q8attn_workspace_bytes(rows: int, heads: int, kvheads: int, hd: int, seqs: int, groups: int) -> int:
+    """Bytes of workspace an attention of these sizes takes at most."""
+    return library().xsymv_q8attn_workspace_bytes(rows, heads, kvheads, hd, seqs, groups)
+
+
+def logp_workspace_bytes(m: int, n: int, top: int) -> int:
+    """Bytes of workspace the log probabilities of m rows of n logits take."""
+    return library().xsymv_logp_workspace_bytes(m, n, top)
 
 
 def q8gemm_workspace_bytes(m: int, n: int, k: int) -> int:

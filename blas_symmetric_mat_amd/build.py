@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libxsymv.so")
 UNITS = ["xsymv_host", "xsymv_prec_s", "xsymv_prec_d", "xsymv_prec_c", "xsymv_prec_z",
          "xsymv_prec_w", "xsymv_static", "xq8_rows", "xq8_gemm", "xq8_gemm_s", "xq8_gemm_h",
-         "xq8_gemm_b"]
+         "xq8_gemm_b", "xq8_pages", "xq8_attn", "xq8_attn_s", "xq8_attn_h", "xq8_attn_b", "xlogp"]
 ARCH = os.environ.get("XSYMV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # any C compiler does for the Python side: the one asked for, gcc, or hipcc's own clang

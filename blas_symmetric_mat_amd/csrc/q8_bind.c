@@ -1,4 +1,5 @@
-/* q8_bind.c -- the Python side of the operators on rows in 8 bits.
+/* q8_bind.c -- the Python side of the operators on rows in 8 bits, of the
+ * attention and the pages of a cache of such rows, and of log probabilities.
  *
  * A serving loop makes these calls with a row or a few, where a kernel takes
  * 3 to 6 microseconds and the call's own cost shows: marshalling a dozen
@@ -206,6 +207,124 @@ OPERATORS(s, float)
 OPERATORS(h, xhalf)
 OPERATORS(b, xbfloat16)
 
+/* Attention over a cache's pages, and log probabilities. */
+#define SEQUENCE_OPERATORS(L)                                                                     \
+    static PyObject *attn_##L(PyObject *self, PyObject *const *a, Py_ssize_t n)                   \
+    {                                                                                             \
+        int ok = 1;                                                                               \
+        if (!counted("xsymv_q8attn_" #L, n, 27)) return NULL;                                     \
+        const int rows = NUM(0), heads = NUM(1), kvheads = NUM(2), hd = NUM(3);                   \
+        const void *q = PTR(4);                                                                   \
+        const int ldq = NUM(5), seqs = NUM(6);                                                    \
+        const void *start = PTR(7), *len = PTR(8), *table = PTR(9);                               \
+        const int ldt = NUM(10), groups = NUM(11);                                                \
+        const void *first = PTR(12), *shared = PTR(13), *k = PTR(14);                             \
+        const int ldk = NUM(15);                                                                  \
+        const void *ks = PTR(16), *v = PTR(17);                                                   \
+        const int ldv = NUM(18);                                                                  \
+        const void *vs = PTR(19);                                                                 \
+        const int pages = NUM(20), ps = NUM(21);                                                  \
+        const float scale = real(a[22], &ok);                                                     \
+        void *out = PTR(23);                                                                      \
+        const int ldo = NUM(24);                                                                  \
+        void *lse = PTR(25), *st = stream_of(a[26], &ok);                                         \
+        CALL(xsymv_q8attn_##L, (rows, heads, kvheads, hd, q, ldq, seqs, start, len, table, ldt,   \
+                                groups, first, shared, k, ldk, ks, v, ldv, vs, pages, ps, scale,  \
+                                out, ldo, lse, st));                                              \
+    }                                                                                             \
+    static PyObject *logp_##L(PyObject *self, PyObject *const *a, Py_ssize_t n)                   \
+    {                                                                                             \
+        int ok = 1;                                                                               \
+        if (!counted("xsymv_logp_" #L, n, 13)) return NULL;                                       \
+        const int m = NUM(0), cols = NUM(1);                                                      \
+        const void *x = PTR(2);                                                                   \
+        const int ldx = NUM(3);                                                                   \
+        const void *token = PTR(4);                                                               \
+        void *logp = PTR(5), *entropy = PTR(6), *lse = PTR(7);                                    \
+        const int top = NUM(8);                                                                   \
+        void *index = PTR(9), *value = PTR(10);                                                   \
+        const int ldt = NUM(11);                                                                  \
+        void *st = stream_of(a[12], &ok);                                                         \
+        CALL(xsymv_logp_##L, (m, cols, x, ldx, token, logp, entropy, lse, top, index, value, ldt, \
+                              st));                                                               \
+    }
+
+SEQUENCE_OPERATORS(s)
+SEQUENCE_OPERATORS(h)
+SEQUENCE_OPERATORS(b)
+
+/* Pages of a cache. */
+#define PAGES(NAME, COUNT)                                                                \
+    static PyObject *pages_##NAME(PyObject *self, PyObject *const *a, Py_ssize_t n)       \
+    {                                                                                     \
+        int ok = 1;                                                                       \
+        if (!counted("xsymv_q8pages_" #NAME, n, COUNT)) return NULL;
+
+PAGES(grow, 12)
+        const int m = NUM(0);
+        const void *seq = PTR(1), *add = PTR(2);
+        const int seqs = NUM(3);
+        void *len = PTR(4), *table = PTR(5);
+        const int ldt = NUM(6), pages = NUM(7), ps = NUM(8);
+        void *refs = PTR(9), *got = PTR(10), *st = stream_of(a[11], &ok);
+        CALL(xsymv_q8pages_grow, (m, seq, add, seqs, len, table, ldt, pages, ps, refs, got, st));
+    }
+
+PAGES(slots, 11)
+        const int rows = NUM(0), kvheads = NUM(1);
+        const void *start = PTR(2);
+        const int seqs = NUM(3);
+        const void *len = PTR(4), *table = PTR(5);
+        const int ldt = NUM(6), pages = NUM(7), ps = NUM(8);
+        void *slot = PTR(9), *st = stream_of(a[10], &ok);
+        CALL(xsymv_q8pages_slots, (rows, kvheads, start, seqs, len, table, ldt, pages, ps, slot, st));
+    }
+
+PAGES(fork, 13)
+        const int m = NUM(0);
+        const void *parent = PTR(1), *child = PTR(2);
+        const int seqs = NUM(3);
+        void *len = PTR(4), *table = PTR(5);
+        const int ldt = NUM(6), pages = NUM(7), ps = NUM(8);
+        void *refs = PTR(9), *src = PTR(10), *dst = PTR(11), *st = stream_of(a[12], &ok);
+        CALL(xsymv_q8pages_fork, (m, parent, child, seqs, len, table, ldt, pages, ps, refs, src, dst, st));
+    }
+
+PAGES(free, 10)
+        const int m = NUM(0);
+        const void *seq = PTR(1);
+        const int seqs = NUM(2);
+        void *len = PTR(3), *table = PTR(4);
+        const int ldt = NUM(5), pages = NUM(6), ps = NUM(7);
+        void *refs = PTR(8), *st = stream_of(a[9], &ok);
+        CALL(xsymv_q8pages_free, (m, seq, seqs, len, table, ldt, pages, ps, refs, st));
+    }
+
+PAGES(compact, 12)
+        const int seqs = NUM(0);
+        const void *table = PTR(1);
+        const int ldt = NUM(2);
+        void *out = PTR(3);
+        const int ldo = NUM(4), pages = NUM(5);
+        const void *refs = PTR(6);
+        void *rout = PTR(7), *src = PTR(8), *dst = PTR(9), *live = PTR(10), *st = stream_of(a[11], &ok);
+        CALL(xsymv_q8pages_compact, (seqs, table, ldt, out, ldo, pages, refs, rout, src, dst, live, st));
+    }
+
+PAGES(copy, 15)
+        const int m = NUM(0);
+        const void *src = PTR(1), *dst = PTR(2);
+        const int pages = NUM(3), rows = NUM(4), hd = NUM(5);
+        void *k = PTR(6);
+        const int ldk = NUM(7);
+        void *ks = PTR(8), *v = PTR(9);
+        const int ldv = NUM(10);
+        void *vs = PTR(11);
+        const int layers = NUM(12), stride = NUM(13);
+        void *st = stream_of(a[14], &ok);
+        CALL(xsymv_q8pages_copy, (m, src, dst, pages, rows, hd, k, ldk, ks, v, ldv, vs, layers, stride, st));
+    }
+
 static PyObject *setup(PyObject *self, PyObject *args)
 {
     PyObject *e, *c;
@@ -224,11 +343,16 @@ static PyObject *setup(PyObject *self, PyObject *args)
     {"glu_" #L, (PyCFunction)(void *)glu_##L, METH_FASTCALL, 0},     \
     {"store_" #L, (PyCFunction)(void *)store_##L, METH_FASTCALL, 0}, \
     {"read_" #L, (PyCFunction)(void *)read_##L, METH_FASTCALL, 0},   \
-    {"gemm_" #L, (PyCFunction)(void *)gemm_##L, METH_FASTCALL, 0}
+    {"gemm_" #L, (PyCFunction)(void *)gemm_##L, METH_FASTCALL, 0},   \
+    {"attn_" #L, (PyCFunction)(void *)attn_##L, METH_FASTCALL, 0},   \
+    {"logp_" #L, (PyCFunction)(void *)logp_##L, METH_FASTCALL, 0}
+#define PAGES_ENTRY(NAME) {"pages_" #NAME, (PyCFunction)(void *)pages_##NAME, METH_FASTCALL, 0}
 
 static PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, "setup(error class, function giving the current stream)"},
     ENTRIES(s), ENTRIES(h), ENTRIES(b),
+    PAGES_ENTRY(grow), PAGES_ENTRY(slots), PAGES_ENTRY(fork), PAGES_ENTRY(free), PAGES_ENTRY(compact),
+    PAGES_ENTRY(copy),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8_bind", NULL, -1, methods};

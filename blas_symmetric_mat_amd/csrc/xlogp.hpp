@@ -1,0 +1,309 @@
+// xlogp.hpp -- log probabilities of a row of logits: of a given token, the
+// entropy, and the most likely tokens.
+//
+//   lse = log sum_j e^(x_j),  logp = x[token] - lse,
+//   entropy = -sum_j p_j log p_j = log l - s / l,  l = sum_j e^(x_j - c),  s = sum_j e^(x_j - c) (x_j - c)
+//
+// for any c; one pass keeps c near the largest logit so far.  A row's largest
+// `top` logits are found in the same pass: each thread remembers the largest of
+// its own and where, the top-th largest of these bounds the row's top-th logit
+// from below, and only the few threads that hold one above it read theirs again.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "xq8_rows.hpp"
+
+namespace xsymv {
+
+constexpr int LP_THREADS = 256;
+constexpr int LP_TOP = 128;     // alternatives of one row at most
+constexpr int LP_CAP = 1024;    // candidates ranked at once
+constexpr int LP_PARTS = 64;    // workgroups that share a row at most
+constexpr int LP_LISTS = 2048;  // alternatives of all parts of a row at most
+
+typedef unsigned long long lp_key;
+
+// What a row is reduced to: c, l and s above, s in units of log 2.
+struct LpSums {
+    float c, l, s;
+};
+
+template <class T>
+struct LpArgs {
+    const T* x;
+    const int* token;
+    float *logp, *entropy, *lse;
+    int* index;
+    float* value;
+    int m, n, ldx, top, ldt;
+    int parts, each;  // workgroups that share a row, logits of one (a multiple of 8)
+    LpSums* sums;     // where there are several: of row i's part p at i * parts + p
+    lp_key* keys;     // top keys of each, the largest first, 0 behind the last
+};
+
+// Order of the logits as whole numbers: the larger value first, the lower index
+// of equal ones (and -0 equals 0).  0 stands below every logit.
+__device__ __forceinline__ lp_key lp_order(float v, unsigned index)
+{
+    const unsigned b = __float_as_uint(v + 0.0f);
+    // (a NaN above all: every stretch of a row has its share of the order)
+    const unsigned u = v != v ? 0xffffffffu : b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
+    return (lp_key)u << 32 | (0xffffffffu - index);
+}
+__device__ __forceinline__ float lp_value(lp_key k)
+{
+    const unsigned u = (unsigned)(k >> 32);
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ int lp_index(lp_key k) { return (int)(0xffffffffu - (unsigned)k); }
+
+constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
+constexpr float LP_LOWEST = -3.4028234663852886e38f;
+
+// Sums for another reference c.  The difference is bounded, so that nothing (l =
+// s = 0) stays nothing.
+__device__ __forceinline__ void lp_move(LpSums& a, float c)
+{
+    const float d = fmaxf((a.c - c) * LP_LOG2E, -1e5f), f = __builtin_amdgcn_exp2f(d);
+    a.s = f * (a.s + a.l * d);
+    a.l *= f;
+    a.c = c;
+}
+__device__ __forceinline__ void lp_add(LpSums& a, LpSums b)
+{
+    const float c = fmaxf(a.c, b.c);
+    lp_move(a, c);
+    lp_move(b, c);
+    a.l += b.l;
+    a.s += b.s;
+}
+
+// Eight logits, -infinity behind a row's last.
+template <class T>
+__device__ __forceinline__ void lp_load(const T* x, int have, float (&v)[8])
+{
+    q8_load(x, have, v);
+    if (have < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= have) v[e] = -INFINITY;
+    }
+}
+
+// -infinity as a finite number whose power is zero too; a NaN passes.
+__device__ __forceinline__ float lp_above(float z) { return __builtin_elementwise_maximum(z, -1e30f); }
+
+// Adds eight logits.  c follows where one is more than 20 above it (e^20 times
+// the number of logits is far below the largest float).
+__device__ __forceinline__ float lp_take(LpSums& a, const float (&v)[8])
+{
+    float most = v[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) most = fmaxf(most, v[e]);
+    if (most > a.c + 20.0f || (a.c == LP_LOWEST && most > a.c)) lp_move(a, most);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // the difference first: c itself has power 1, and masks of the type's lowest
+        // value, times log2(e), would be no numbers
+        const float z = lp_above((v[e] - a.c) * LP_LOG2E), p = __builtin_amdgcn_exp2f(z);
+        a.l += p;
+        a.s = __builtin_fmaf(p, z, a.s);
+    }
+    return most;
+}
+
+// What a row's sums give: log probabilities are (x - c) - log_l, so that they
+// keep their bits where c is large.
+struct LpRow {
+    float c, log_l;
+    bool none;  // nothing but -infinity
+    __device__ float of(float x) const { return none ? -INFINITY : (x - c) - log_l; }
+};
+
+template <class T>
+__device__ __forceinline__ LpRow lp_finish(const LpArgs<T>& a, int row, LpSums t, bool write)
+{
+    const float log_l = logf(t.l);
+    const LpRow r{t.c, log_l, t.l == 0.0f};
+    if (write) {
+        if (a.token != nullptr) {
+            const int k = a.token[row];
+            a.logp[row] = (unsigned)k < (unsigned)a.n ? r.of((float)a.x[(size_t)row * a.ldx + k]) : 0.0f;
+        }
+        if (a.entropy != nullptr) a.entropy[row] = r.none ? 0.0f : log_l - t.s / t.l * LP_LN2;
+        if (a.lse != nullptr) a.lse[row] = r.none ? -INFINITY : t.c + log_l;
+    }
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void lp_alternative(const LpArgs<T>& a, int row, int rank, lp_key k, const LpRow& r)
+{
+    const size_t at = (size_t)row * a.ldt + rank;
+    a.index[at] = lp_index(k);
+    if (a.value != nullptr) a.value[at] = r.of(lp_value(k));
+}
+
+template <class T, bool TOP>
+__global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
+{
+    __shared__ LpSums of_wave[LP_THREADS / 64];
+    __shared__ lp_key bound[TOP ? LP_THREADS : 1], found[TOP ? LP_CAP : 1], least;
+    __shared__ int chosen[TOP ? LP_THREADS : 1], chosen_n, found_n;
+    const int t = threadIdx.x;
+    const long long all = (long long)a.m * a.parts;
+    for (long long item = blockIdx.x; item < all; item += gridDim.x) {
+        const int row = (int)(item / a.parts), part = (int)(item % a.parts);
+        const int from = part * a.each, have = min(a.n - from, a.each), vecs = (have + 7) / 8;
+        const T* x = a.x + (size_t)row * a.ldx + from;
+        LpSums sum{LP_LOWEST, 0.0f, 0.0f};
+        float best = -INFINITY;
+        int best_at = t;
+        constexpr int U = 4;  // loads in flight
+        for (int v = t; v < vecs; v += LP_THREADS * U) {
+            float e[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * LP_THREADS < vecs) {
+                    const int at = (v + u * LP_THREADS) * 8;
+                    lp_load(x + at, have - at, e[u]);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * LP_THREADS < vecs) {
+                    const float most = lp_take(sum, e[u]);
+                    if (TOP && most > best) {
+                        best = most;
+                        best_at = v + u * LP_THREADS;
+                    }
+                }
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const LpSums o{__shfl_xor(sum.c, d, 64), __shfl_xor(sum.l, d, 64), __shfl_xor(sum.s, d, 64)};
+            lp_add(sum, o);
+        }
+        __syncthreads();  // the row before is done with LDS
+        if ((t & 63) == 0) of_wave[t >> 6] = sum;
+        if (TOP) {
+            // of all its logits that equal `best`, a thread's have this index at most
+            bound[t] = t < vecs ? lp_order(best, from + best_at * 8 + 7) : 0;
+            if (t == 0) {
+                least = 0;
+                chosen_n = 0;
+            }
+        }
+        __syncthreads();
+        sum = of_wave[0];
+        for (int w = 1; w < LP_THREADS / 64; ++w) lp_add(sum, of_wave[w]);
+        LpRow of{};
+        if (a.parts == 1)
+            of = lp_finish(a, row, sum, t == 0);
+        else if (t == 0)
+            a.sums[item] = sum;
+        if constexpr (TOP) {
+            int rank = 0;
+            for (int o = 0; o < LP_THREADS; ++o) rank += bound[o] > bound[t];
+            if (rank == a.top - 1 && bound[t] != 0) least = bound[t];
+            __syncthreads();
+            // threads that hold a logit at or above `least`
+            if (t < vecs && lp_order(best, from + best_at * 8) >= least)
+                chosen[atomicAdd(&chosen_n, 1)] = t;
+            __syncthreads();
+            const int turns = (vecs + LP_THREADS - 1) / LP_THREADS, pairs = chosen_n * turns;
+            // their logits at or above `low`: counted, and kept as far as there is room
+            auto gather = [&](lp_key low) {
+                __syncthreads();
+                if (t == 0) found_n = 0;
+                __syncthreads();
+                for (int p = t; p < pairs; p += LP_THREADS) {
+                    const int at = (chosen[p % chosen_n] + p / chosen_n * LP_THREADS) * 8;
+                    if (at >= have) continue;
+                    float e[8];
+                    lp_load(x + at, have - at, e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const lp_key k = lp_order(e[i], from + at + i);
+                        if (at + i < have && k >= low) {
+                            const int place = atomicAdd(&found_n, 1);
+                            if (place < LP_CAP) found[place] = k;
+                        }
+                    }
+                }
+                __syncthreads();
+                return found_n;
+            };
+            lp_key low = least, high = ~0ull, under = low;
+            int count = gather(low);
+            const int want = min(a.top, have);
+            // Too many only where a row's large logits lie on few threads (all in one
+            // stretch, or in ascending order): the bound between is halved until they fit,
+            // 64 times at most, as the keys differ.
+            for (int i = 0; i < 64 && (count > LP_CAP || count < want); ++i) {
+                if (count > LP_CAP)
+                    under = low;
+                else
+                    high = low;
+                low = under + (high - under) / 2;
+                count = gather(low);
+            }
+            count = min(count, LP_CAP);
+            for (int i = t; i < count; i += LP_THREADS) {
+                const lp_key k = found[i];
+                int before = 0;
+                for (int o = 0; o < count; ++o) before += found[o] > k;
+                if (before < a.top) {
+                    if (a.parts == 1)
+                        lp_alternative(a, row, before, k, of);
+                    else
+                        a.keys[item * a.top + before] = k;
+                }
+            }
+            if (a.parts > 1)
+                for (int i = count + t; i < a.top; i += LP_THREADS) a.keys[item * a.top + i] = 0;
+        }
+    }
+}
+
+// A row from its parts.
+template <class T>
+__global__ __launch_bounds__(LP_THREADS) void logp_join(LpArgs<T> a)
+{
+    __shared__ lp_key keys[LP_LISTS];
+    const int t = threadIdx.x, lists = a.parts * a.top;
+    for (int row = blockIdx.x; row < a.m; row += gridDim.x) {
+        const size_t first = (size_t)row * a.parts;
+        __syncthreads();
+        for (int i = t; i < lists; i += LP_THREADS) keys[i] = a.keys[first * a.top + i];
+        const int lane = t & 63;
+        LpSums sum{LP_LOWEST, 0.0f, 0.0f};
+        if (lane < a.parts) sum = a.sums[first + lane];
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const LpSums o{__shfl_xor(sum.c, d, 64), __shfl_xor(sum.l, d, 64), __shfl_xor(sum.s, d, 64)};
+            lp_add(sum, o);
+        }
+        const LpRow of = lp_finish(a, row, sum, t == 0);
+        __syncthreads();
+        for (int i = t; i < lists; i += LP_THREADS) {
+            const lp_key k = keys[i];
+            if (k == 0) continue;
+            int before = 0;  // larger ones: of every sorted list, those before the first below k
+            for (int p = 0; p < a.parts && before < a.top; ++p) {
+                int lo = 0, hi = a.top;
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (keys[p * a.top + mid] > k)
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                before += lo;
+            }
+            if (before < a.top) lp_alternative(a, row, before, k, of);
+        }
+    }
+}
+
+}  // namespace xsymv

@@ -4,6 +4,7 @@
 #include "xsymv_host.hpp"
 #include "xq8_rows.hpp"
 
+#include <mutex>
 #include <new>
 
 namespace xsymv {
@@ -37,6 +38,38 @@ int q8_launch(void (*k)(A), dim3 grid, unsigned threads, hipStream_t stream, con
     XSYMV_HIP(launch_k(k, grid, dim3(threads), stream, a, tc.e0, tc.e1));
     if (timing) timing_push(tc);
     return 0;
+}
+
+// A call that wants `bytes` of the stream's workspace and can do without: run(ws,
+// events) with a null ws where none is wanted, where device memory is used up or
+// where a capture forbids to allocate it.  `second`: it launches a second kernel.
+template <class F>
+int q8_with_workspace(size_t bytes, bool second, hipStream_t stream, F&& run)
+{
+    TimedCall tc{};
+    const int timing = timing_enabled();
+    void* ws = nullptr;
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    std::unique_lock<std::mutex> lk;
+    if (bytes > 0) {
+        XSYMV_HIP(hipGetDevice(&dev));
+        ds = device_state(dev);
+        lk = std::unique_lock<std::mutex>(device_mutex(ds));
+        if (!workspace_barred(ds, stream, bytes)) {
+            const int rc = get_workspace(ds, stream, bytes, &ws);
+            if (rc == ERR_HIP + (int)hipErrorOutOfMemory) {
+                (void)hipGetLastError();  // dealt with
+                ws = nullptr;
+            } else if (rc) {
+                return rc;
+            }
+        }
+    }
+    if (timing) XSYMV_HIP(timed_call_create(tc, timing, second && ws != nullptr));
+    const int rc = run(ws, tc);
+    if (rc == 0 && timing) timing_push(tc);
+    return rc;
 }
 
 // No exception leaves a C entry point.

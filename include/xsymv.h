@@ -445,6 +445,154 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
                     const signed char *w, int ldw, const float *sw, const float *bias,
                     xbfloat16 *c, int ldc, void *stream);
 
+/* Several answers to one prompt -- attention, pages and log probabilities for
+ * sequences that are served together from one cache of 8-bit rows.
+ *
+ * A cache of `pages` pages of `ps` tokens for `kvheads` heads is two matrices of
+ * rows as above (codes and one scale a row), the keys and the values: token t of
+ * a sequence lies in page p = table[t / ps] of the sequence's row of the table,
+ * and its row for head h is
+ *
+ *   row = (p * kvheads + h) * ps + t % ps        (pages * kvheads * ps < 2^31)
+ *
+ * DEVICE arrays of int: table (seqs rows of ldt entries), len (tokens of each
+ * sequence), refs (for each page the sequences that hold it; 0: a free page).  A
+ * len below zero counts as zero, one above ldt * ps as that.  Where a call takes
+ * `start` (seqs + 1 ascending numbers), rows start[i] to start[i + 1] - 1 of its
+ * matrices are the last tokens of sequence i, of which a sequence may have none;
+ * start NULL: row i is the last token of sequence i.  Rows outside start[0] to
+ * start[seqs] are left as they are.  All calls are asynchronous on `stream`, can
+ * be captured into a graph (the arrays are read when it is replayed), and give
+ * the same bytes every time.  Codes are checked in the order of the arguments
+ * before any device work; what device arrays hold cannot be refused: numbers of
+ * pages and sequences that do not exist are passed over as said below, and no
+ * number in them makes a call read or write outside its arrays.  The matrices of
+ * a call may not overlap where it does not say so.
+ *
+ *   xsymv_q8attn_*:  for each row r and head h < heads, with the keys k_t and
+ *   values v_t of head h * kvheads / heads (kvheads divides heads),
+ *
+ *     out = sum_t e^(s_t - lse) v_t,  s_t = scale * (q . k_t),  lse = log sum_t e^(s_t)
+ *
+ *   over the tokens t <= len - (the sequence's rows) + (the row's place among
+ *   them, from 0): a row sees the tokens up to its own.  Head h of row r is at
+ *   q[r * ldq + h * hd] and out[r * ldo + h * hd], and at lse[r * heads + h] (lse
+ *   NULL: not kept).  Tokens whose page is outside [0, pages) are passed over; a
+ *   row that sees none gets zeros and -infinity.  hd <= 256.
+ *   Sequences first[g] to first[g + 1] - 1 (groups + 1 ascending numbers from 0
+ *   to seqs) have their first shared[g] tokens in common: their rows of the table
+ *   name the same pages there, and these are read once for all of them where that
+ *   takes less time.  groups == 0: nothing is shared.  Products of 16 bits
+ *   (letters h and b) or 22 (s), sums in 32.  Uses the stream's workspace, up to
+ *   xsymv_q8attn_workspace_bytes; where it cannot be had (as for the product
+ *   above) the call is made without, in up to many times the time.
+ *   Codes: -1 rows < 0, -2 heads < 1 or not a multiple of kvheads (or heads * hd
+ *   over 2^31 - 1), -3 kvheads < 1, -4 hd < 1 or > 256, -5 q NULL, -6 ldq, -7
+ *   seqs < 0, or not rows without start, -9 len NULL, -10 table NULL, -11 ldt <
+ *   0, -12 groups < 0, -13 first NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd,
+ *   -17 ks NULL, -18 v NULL, -19 ldv < hd, -20 vs NULL, -21 pages < 0 or too many
+ *   rows, -22 ps < 1, -23 scale not finite, -24 out NULL, -25 ldo, 2000 installed
+ *   workspace too small.
+ *
+ *   xsymv_q8pages_grow:  sequence seq[i] gets add[i] tokens more (n of them, in
+ *   order; n <= 8192): free pages, the lowest first, are entered in its row of
+ *   the table, their refs set to one, and its len raised; got[i] = add[i].
+ *   A sequence that does not exist, that is listed before, whose tokens would not
+ *   fit its row of the table, or for which not enough free pages are left behind
+ *   those before it in the list, stays as it is: got[i] = 0.  Codes: -1 n < 0 or >
+ *   8192, -2 seq NULL, -3 add NULL, -4 seqs < 0, -5 len NULL, -6 table NULL, -7
+ *   ldt < 0, -8 pages < 0, -9 ps < 1, -10 refs NULL, -11 got NULL.
+ *
+ *   xsymv_q8pages_slots:  slot[r * kvheads + h] = the cache's row of row r's token
+ *   and head h, for xsymv_q8store_*; -1 where there is none.  Codes: -1 rows < 0,
+ *   -2 kvheads < 1, -4 seqs < 0, or not rows without start, -5 len NULL, -6 table
+ *   NULL, -7 ldt < 0, -8 pages < 0 or too many rows, -9 ps < 1, -10 slot NULL.
+ *
+ *   xsymv_q8pages_fork:  sequence child[i], which is empty (len 0), becomes a copy
+ *   of parent[i] as that was before the call (n <= 8192): it holds the parent's
+ *   whole pages too (their refs are raised) and a page of its own, the lowest
+ *   free one, for a last page that is not full: src[i] = the parent's, dst[i] =
+ *   the new one, for xsymv_q8pages_copy; both -1 where the last page is full.
+ *   Both -2, and nothing done, where one of them does not exist, the child is not
+ *   empty or listed before, or no free page is left.  Codes: -1 n < 0 or > 8192,
+ *   -2 parent NULL, -3 child NULL, -4 seqs < 0, -5 len NULL, -6 table NULL, -7
+ *   ldt < 0, -8 pages < 0, -9 ps < 1, -10 refs NULL, -11 src NULL, -12 dst NULL.
+ *
+ *   xsymv_q8pages_free:  sequence seq[i] gives its pages back: their refs are
+ *   lowered, its entries become -1 and its len 0.  Sequences that do not exist are
+ *   passed over; one that is listed twice is freed once.  Codes: -1 n < 0, -2 seq
+ *   NULL, -3 seqs < 0, -4 len NULL, -5 table NULL, -6 ldt < 0, -7 pages < 0, -8
+ *   ps < 1, -9 refs NULL.
+ *
+ *   xsymv_q8pages_compact:  with live[0] = the number of pages whose refs are not
+ *   0, the live pages from place live[0] on are to move to the free places before
+ *   it, the k-th of them (ascending) to the k-th place: src and dst list them for
+ *   xsymv_q8pages_copy (pages / 2 entries each, -1 behind the last), out and rout
+ *   are the table and refs as they are then (they may be table, with ldo == ldt,
+ *   and refs); entries that name no live page become -1.  Codes: -1 seqs < 0, -2
+ *   table NULL, -3 ldt < 0, -4 out NULL, -5 ldo < ldt, or not ldt where out is
+ *   table, -6 pages < 0, -7 refs NULL, -8 rout NULL, -9 src NULL, -10 dst NULL,
+ *   -11 live NULL.
+ *
+ *   xsymv_q8pages_copy:  page src[i] is copied to page dst[i], `rows` rows (kvheads
+ *   * ps) of hd codes and their scales, of the keys and of the values (v NULL: of
+ *   k alone), in each of `layers` caches of which one lies `stride` rows behind the
+ *   other in the same matrices.  Pairs with a number outside [0, pages) are passed
+ *   over.  A page that is the dst of two pairs, or of one and the src of another,
+ *   is left undefined.  Codes: -1 n < 0, -2 src NULL, -3 dst NULL, -4 pages < 0, or
+ *   pages * rows over 2^31 - 1, -5 rows < 0, -6 hd < 0, -7 k NULL, -8 ldk < hd, -9
+ *   ks NULL, -11 ldv < hd, -12 vs NULL, -13 layers < 0, -14 stride < pages * rows
+ *   with more than one layer.
+ *
+ *   xsymv_logp_*:  of m rows of n logits, log probabilities with lse = log sum_j
+ *   e^(x_j): logp[i] = x[token[i]] - lse (0 for a token outside [0, n)), entropy[i]
+ *   = -sum_j p_j log p_j, lse[i]; and the `top` largest logits, the larger first
+ *   and the lower index first of equal ones: index[i * ldt + r], value[i * ldt + r]
+ *   = x - lse.  token (with logp), entropy, lse and value may be NULL; index only
+ *   with top == 0.  Tokens of logit -infinity have no part in the entropy.  A row
+ *   of these alone: lse, logp and value -infinity, entropy 0.  A row that holds a
+ *   NaN or +infinity: NaN, and indexes of which only is said that they differ.
+ *   Uses the stream's workspace, up to xsymv_logp_workspace_bytes, as xsymv_q8attn_*
+ *   does.  Codes: -1 m < 0, -2 n < 0, -3 x NULL, -4 ldx, -6 logp NULL with token,
+ *   -9 top < 0, > n or > 128, -10 index NULL, -12 ldt < top, 2000.
+ * All: 1000 + hipError_t. */
+size_t xsymv_q8attn_workspace_bytes(int rows, int heads, int kvheads, int hd, int seqs, int groups);
+size_t xsymv_logp_workspace_bytes(int m, int n, int top);
+int xsymv_q8attn_s(int rows, int heads, int kvheads, int hd, const float *q, int ldq, int seqs,
+                   const int *start, const int *len, const int *table, int ldt, int groups,
+                   const int *first, const int *shared, const signed char *k, int ldk,
+                   const float *ks, const signed char *v, int ldv, const float *vs, int pages,
+                   int ps, float scale, float *out, int ldo, float *lse, void *stream);
+int xsymv_logp_s(int m, int n, const float *x, int ldx, const int *token, float *logp, float *entropy,
+                 float *lse, int top, int *index, float *value, int ldt, void *stream);
+int xsymv_q8attn_h(int rows, int heads, int kvheads, int hd, const xhalf *q, int ldq, int seqs,
+                   const int *start, const int *len, const int *table, int ldt, int groups,
+                   const int *first, const int *shared, const signed char *k, int ldk,
+                   const float *ks, const signed char *v, int ldv, const float *vs, int pages,
+                   int ps, float scale, xhalf *out, int ldo, float *lse, void *stream);
+int xsymv_logp_h(int m, int n, const xhalf *x, int ldx, const int *token, float *logp, float *entropy,
+                 float *lse, int top, int *index, float *value, int ldt, void *stream);
+int xsymv_q8attn_b(int rows, int heads, int kvheads, int hd, const xbfloat16 *q, int ldq, int seqs,
+                   const int *start, const int *len, const int *table, int ldt, int groups,
+                   const int *first, const int *shared, const signed char *k, int ldk,
+                   const float *ks, const signed char *v, int ldv, const float *vs, int pages,
+                   int ps, float scale, xbfloat16 *out, int ldo, float *lse, void *stream);
+int xsymv_logp_b(int m, int n, const xbfloat16 *x, int ldx, const int *token, float *logp, float *entropy,
+                 float *lse, int top, int *index, float *value, int ldt, void *stream);
+int xsymv_q8pages_grow(int n, const int *seq, const int *add, int seqs, int *len, int *table, int ldt,
+                       int pages, int ps, int *refs, int *got, void *stream);
+int xsymv_q8pages_slots(int rows, int kvheads, const int *start, int seqs, const int *len,
+                        const int *table, int ldt, int pages, int ps, int *slot, void *stream);
+int xsymv_q8pages_fork(int n, const int *parent, const int *child, int seqs, int *len, int *table,
+                       int ldt, int pages, int ps, int *refs, int *src, int *dst, void *stream);
+int xsymv_q8pages_free(int n, const int *seq, int seqs, int *len, int *table, int ldt, int pages,
+                       int ps, int *refs, void *stream);
+int xsymv_q8pages_compact(int seqs, const int *table, int ldt, int *out, int ldo, int pages,
+                          const int *refs, int *rout, int *src, int *dst, int *live, void *stream);
+int xsymv_q8pages_copy(int n, const int *src, const int *dst, int pages, int rows, int hd,
+                       signed char *k, int ldk, float *ks, signed char *v, int ldv, float *vs,
+                       int layers, int stride, void *stream);
+
 /* Bytes of device workspace one call of precision `prec` and order n uses
  * with the configuration selected for it now, on the current device (0 for
  * n == 0; -1 cast to size_t for a bad precision code, or when the device

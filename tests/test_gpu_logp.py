@@ -1,0 +1,216 @@
+"""Log probabilities, entropy and alternatives against their definition in 64 bits.
+
+Bounds, with u = 2^-24: a power e^z (z = x - c, c within 20 of the row's largest logit where it counts)
+is off by 3 u |z| (its argument's rounding in units of log 2, and the constant's on x) plus 2 u; sums of n
+add n u relative to the sum; log l is off by that, relative errors becoming absolute; results round once more.
+"""
+import math
+
+import pytest
+
+from tests.test_gpu_q8 import LETTERS, U, Rows, dtype_of, gen
+
+pytestmark = pytest.mark.gpu
+
+
+def logits(m, n, t, seed=0, spread=3.0, pad=0, off=0):
+    import torch
+    return Rows(m, n, dtype_of(t), pad, off, data=torch.randn((m, n), generator=gen(seed), device="cuda") * spread)
+
+
+def call(x, t, token, top, ldt=None, stream=None, skip=()):
+    """logp, entropy, lse, index, value of rows x; what is in `skip` is not asked for."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    ldt = top if ldt is None else ldt
+    f = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
+    out = {"logp": f(x.m), "entropy": f(x.m), "lse": f(x.m),
+           "index": torch.full((x.m, ldt), -7, dtype=torch.int32, device="cuda"), "value": f(x.m, ldt)}
+    give = {k: None if k in skip else v for k, v in out.items()}
+    getattr(X, "xsymv_logp_" + t)(x.m, x.n, x.t, x.ld, token, give["logp"], give["entropy"], give["lse"], top,
+                                  give["index"], give["value"], ldt, stream=stream)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(x, token, got, top):
+    """Against 64 bits, row by row in one go; the alternatives exactly."""
+    import torch
+    v = x.t.double()
+    n = x.n
+    m = v.amax(1)
+    z = v - m[:, None]
+    e = z.exp()
+    l = e.sum(1)
+    lse = m + l.log()
+    size = torch.where(e > 0, z, 0.0).abs()
+    rel = (3 * U * size + 2 * U)
+    # the reference may lie up to 20 below the largest, and is itself up to |m| + 20 in size
+    err_l = (e * rel).sum(1) / l + n * U + 6 * U * (m.abs() + 25)
+    tol = err_l + 4 * U * lse.abs() + 4 * U
+    assert bool(((got["lse"].double() - lse).abs() <= tol).all())
+    if token is not None:
+        ok = (token >= 0) & (token < n)
+        want = torch.where(ok, v.gather(1, token.long().clamp(0, n - 1)[:, None])[:, 0] - lse, 0.0)
+        same = got["logp"].double() == want
+        assert bool((same | ((got["logp"].double() - want).abs() <= tol + 2 * U * want.abs())).all())
+    p = e / l[:, None]
+    ent = l.log() - torch.where(e > 0, p * z, 0.0).sum(1)
+    # s / l: each term off by e's error and n roundings of sums of terms up to z in size (taken from the reference)
+    err_e = tol + (p * (size + 25) * (2 * rel + 2 * n * U)).sum(1) + err_l * (l.log() + 25)
+    assert bool(((got["entropy"].double() - ent).abs() <= err_e).all())
+    if top:
+        val, idx = torch.sort(x.t, dim=1, descending=True, stable=True)
+        assert torch.equal(got["index"][:, :top].long(), idx[:, :top])
+        want = val[:, :top].double() - lse[:, None]
+        some = want > -math.inf
+        assert bool((got["value"][:, :top][~some] == -math.inf).all())
+        off = (got["value"][:, :top].double() - want).abs() <= tol[:, None] + 2 * U * want.abs()
+        assert bool(off[some].all())
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m,n", [(1, 1), (3, 7), (2, 8), (1, 255), (5, 256), (2, 2047), (3, 2049), (1, 4097),
+                                 (1, 32000), (37, 50021), (300, 1003), (1500, 2500), (1, 262147), (9, 131072)])
+def test_sizes(t, m, n):
+    """Rows alone and many, lengths around a load's, a workgroup's and a part's ends, odd strides."""
+    import torch
+    for pad, off in ((0, 0), (3, 1)):
+        x = logits(m, n, t, seed=n, pad=pad, off=off)
+        token = torch.randint(0, n, (m,), generator=gen(m), device="cuda").to(torch.int32)
+        for top in sorted({min(n, k) for k in (0, 1, 5, 20, 128)}):
+            check(x, token, call(x, t, token, top, ldt=top + 2), top)
+        assert x.intact()
+
+
+@pytest.mark.parametrize("t", LETTERS)
+def test_order(t):
+    """Rows in ascending and descending order, equal throughout, of few values, with all large logits in
+    one stretch, in one thread's places: the alternatives are the largest, the lowest index first."""
+    import torch
+    for n in (3000, 40000, 100001):
+        up = torch.linspace(-8, 8, n, device="cuda")
+        few = torch.randint(0, 3, (n,), generator=gen(n), device="cuda").float()
+        block = torch.where((torch.arange(n, device="cuda") - n // 2).abs() < 900, 5.0 + up, up / 16)
+        comb = torch.where(torch.arange(n, device="cuda") % 2048 < 8, 9.0 + up / 8, up / 16)
+        zeros = torch.where(torch.arange(n, device="cuda") % 3 == 0, -0.0, 0.0)
+        rows = torch.stack([up, up.flip(0), torch.zeros_like(up), few, block, comb, comb.flip(0), zeros])
+        for many in (1, 200):  # parts of a row, and whole rows
+            x = Rows(8 * many, n, dtype_of(t), data=rows.repeat(many, 1))
+            for top in (1, 7, 128):
+                check(x, None, call(x, t, None, top, skip=("logp",)), top)
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m", [1, 700])
+def test_masks(t, m):
+    """Tokens of logit -infinity or the type's lowest value, rows of nothing else, single ones left."""
+    import torch
+    n = 5003
+    lowest = torch.finfo(dtype_of(t)).min
+    for mask in (-math.inf, lowest):
+        x = logits(m, n, t, seed=3)
+        x.t[torch.rand((m, n), generator=gen(1), device="cuda") < 0.9] = mask
+        x.t[:, 17] = 1.0
+        token = torch.full((m,), 17, dtype=torch.int32, device="cuda")
+        check(x, token, call(x, t, token, 20), 20)
+        x.t.fill_(mask)
+        x.t[:, n - 1] = -2.5
+        token.fill_(n - 1)
+        got = call(x, t, token, 3)
+        assert bool((got["logp"] == 0).all()) and bool((got["entropy"] == 0).all())
+        assert got["index"].tolist() == [[n - 1, 0, 1]] * m
+    x.t.fill_(lowest)
+    got = call(x, t, token, 3)
+    assert bool(((got["logp"] + math.log(n)).abs() <= (n + 40) * U).all())
+    assert bool(((got["entropy"] - math.log(n)).abs() <= (n + 40) * U).all())
+    x.t.fill_(-math.inf)
+    got = call(x, t, token, 3)
+    assert bool((got["lse"] == -math.inf).all()) and bool((got["logp"] == -math.inf).all())
+    assert bool((got["entropy"] == 0).all()) and bool((got["value"] == -math.inf).all())
+    assert got["index"].tolist() == [[0, 1, 2]] * m
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m", [1, 600])
+def test_rows_that_are_no_numbers(t, m):
+    """A NaN or +infinity makes its row's numbers NaN, no other's, and the indexes still differ."""
+    import torch
+    n = 9000
+    x = logits(m + 3, n, t, seed=5)
+    token = torch.full((m + 3,), 100, dtype=torch.int32, device="cuda")
+    clean = call(x, t, token, 16)
+    x.t[0, 4321], x.t[1, 77] = float("nan"), math.inf
+    x.t[2] = float("nan")
+    got = call(x, t, token, 16)
+    for k in ("logp", "entropy", "lse", "value"):
+        assert bool(got[k][:3].isnan().all())
+        assert torch.equal(got[k][3:], clean[k][3:])
+    assert torch.equal(got["index"][3:], clean["index"][3:])
+    for r in range(3):
+        i = got["index"][r].tolist()
+        assert len(set(i)) == 16 and all(0 <= v < n for v in i)
+
+
+def test_what_is_asked_for():
+    """Each output alone; tokens outside the row; entries beyond top stay."""
+    import torch
+    x = logits(5, 3001, "b", seed=1)
+    token = torch.tensor([-1, 3001, 0, 3000, 1 << 30], dtype=torch.int32, device="cuda")
+    whole = call(x, "b", token, 4, ldt=6)
+    check(x, token, whole, 4)
+    assert bool((whole["index"][:, 4:] == -7).all()) and bool((whole["value"][:, 4:] == 7).all())
+    for keep in ("logp", "entropy", "lse"):
+        got = call(x, "b", token if keep == "logp" else None, 0,
+                   skip=[k for k in ("logp", "entropy", "lse", "index", "value") if k != keep])
+        assert torch.equal(got[keep], whole[keep])
+    got = call(x, "b", None, 4, ldt=6, skip=("logp", "entropy", "lse", "value"))
+    assert torch.equal(got["index"], whole["index"])
+
+
+@pytest.mark.parametrize("m", [1, 30])
+def test_a_captured_call(m):
+    """Without a workspace (rows whole) and with one (rows in parts): the same alternatives, numbers within
+    the bound, replay after replay."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    x = logits(m, 70001, "h", seed=2)
+    token = torch.zeros((m,), dtype=torch.int32, device="cuda")
+    out = {"logp": torch.empty((m,), device="cuda"), "entropy": torch.empty((m,), device="cuda"),
+           "lse": torch.empty((m,), device="cuda"), "index": torch.empty((m, 9), dtype=torch.int32, device="cuda"),
+           "value": torch.empty((m, 9), device="cuda")}
+
+    def run():
+        X.xsymv_logp_h(m, x.n, x.t, x.ld, token, out["logp"], out["entropy"], out["lse"], 9, out["index"],
+                       out["value"], 9)
+
+    assert X.logp_workspace_bytes(m, x.n, 9) > 0
+    for warm in (False, True):
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if warm:
+            with torch.cuda.stream(side):
+                run()
+            torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+        for seed in (3, 4, 5):
+            x.t.copy_(torch.randn((m, x.n), generator=gen(seed), device="cuda"))
+            graph.replay()
+            torch.cuda.synchronize()
+            check(x, token, out, 9)
+        del graph
+
+
+def test_many_rows_and_long_offsets():
+    """Rows whose elements lie beyond 2^31."""
+    import torch
+    m, n, ld = 40, 1000, 1 << 26
+    buf = torch.zeros((m * ld,), dtype=torch.bfloat16, device="cuda")
+    x = Rows(1, 1, torch.bfloat16)
+    x.m, x.n, x.ld = m, n, ld
+    x.t = torch.as_strided(buf, (m, n), (ld, 1), 0)
+    x.t.copy_(torch.randn((m, n), generator=gen(1), device="cuda"))
+    token = torch.arange(m, device="cuda").to(torch.int32)
+    check(x, token, call(x, "b", token, 10), 10)
