@@ -2,87 +2,915 @@
 //
 //   s_t = scale * ks_t * sum_d q_d kc_td,  m = max_t s_t,  l = sum_t e^(s_t - m)
 //   out = sum_t e^(s_t - m) vs_t vc_t / l,  lse = m + log l
+//
+// Codes are whole numbers up to 127, which half precision holds exactly: both
+// products run on the 16 x 16 x 32 half-precision matrix instructions with sums
+// in 32 bits, the keys' scales applied to the scores, the values' scales to the
+// weights.  q is brought to half precision by a power of two a row (bfloat16 loses
+// nothing by it; float is two numbers, 22 bits); weights e^(s - m) vs are rounded
+// to 11 bits (float: two numbers again).
+//
+// The score product is taken transposed (tokens are the instruction's rows, rows of
+// q its columns), so that each lane's results are scores of one row of q, and are,
+// rounded, the operand of the second product as they stand: nothing crosses lanes
+// between the two.  Of the running maximum only what is needed is done: a row's
+// reference m follows a score that is more than a factor of two above it, which
+// after a few tokens is rare, and sums stay in the lanes until the end.
+//
+// Work is cut into jobs: a block of rows of q (those of one sequence, or of a group
+// that shares tokens) with one head's keys over the tokens they see.  All jobs lie
+// in one line of costs, of which each workgroup takes an equal piece, so that
+// lengths may differ as they like: a piece may begin and end inside a job, whose
+// parts q8_attn_join adds (xq8_attn_plan.hpp has the arithmetic).  Each workgroup sums
+// the costs itself, which takes less than a launch.
+//
+//   narrow jobs (up to 16 rows of q: single tokens): each wave takes 32 tokens of
+//     128, codes come from memory to the registers that the instruction reads them
+//     from, and the waves' results are added in LDS.  Bound by the cache's bytes.
+//   wide jobs (up to 128 rows: a group's tokens, prompts): each wave has 16 or 32
+//     rows and every token; the waves make operands of 16 tokens each and share
+//     them through LDS, so that codes are converted once for 128 rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
-#include "xq8_cache.hpp"
+#include "xq8_attn_plan.hpp"
 #include "xq8_rows.hpp"
 
 namespace xsymv {
 
-constexpr int AT_HD = 256;  // widest head
+typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
+typedef float at_f2 __attribute__((ext_vector_type(2)));
+typedef float at_f4 __attribute__((ext_vector_type(4)));
+typedef int at_i4 __attribute__((ext_vector_type(4)));
 
 template <class T>
 struct AttnArgs {
+    AtPlan p;
     const T* q;
     T* out;
     float* lse;
-    const int *start, *len, *table, *first, *shared;
     const signed char *k, *v;
     const float *ks, *vs;
-    float scale;
-    int rows, heads, kvheads, hd, ldq, seqs, ldt, groups, ldk, ldv, pages, ps, ldo;
+    float scale;  // times log2(e): scores are kept in units of log 2
+    int ldq, ldk, ldv, ldo;
+    float* slabs;  // parts of jobs (see AtPlan)
 };
 
-// One workgroup a row and head.
-template <class T>
-__global__ __launch_bounds__(256) void q8_attn_simple(AttnArgs<T> a)
+constexpr float AT_LN2 = 0.6931471805599453f;
+constexpr float AT_LOWEST = -3.4028234663852886e38f;
+// Weights are at most 2 (the reference follows beyond that) times 1 (the values'
+// scale over the largest so far), times this: half precision's range is used down
+// to 2^-39 of the largest.
+constexpr float AT_UP = 16384.0f, AT_DOWN = 1.0f / 16384.0f;
+
+// Codes of one dword, as half-precision numbers: with the sign's bit turned over a
+// code is c + 128, which under the exponent byte 0x64 stands for 1024 + c + 128.
+__device__ __forceinline__ int at_turn(int x) { return x ^ (int)0x80808080; }
+__device__ __forceinline__ at_h2 at_codes(int bits)
 {
-    __shared__ float q[AT_HD], p[256], of_wave[4];
-    __shared__ int at[256];
-    const int t = threadIdx.x;
-    for (long long item = blockIdx.x; item < (long long)a.rows * a.heads; item += gridDim.x) {
-        const int r = (int)(item / a.heads), h = (int)(item % a.heads), g = h / (a.heads / a.kvheads);
-        const int s = pg_sequence(a.start, a.seqs, r);
-        if (s < 0) continue;
-        const long long room = (long long)a.ldt * a.ps;
-        const int behind = a.start ? a.start[s + 1] - 1 - r : 0;
-        const long long seen = min((long long)a.len[s], room) - behind;
-        const int* row = a.table + (size_t)s * a.ldt;
+    at_h2 h;
+    __builtin_memcpy(&h, &bits, 4);
+    return h - (at_h2){1152.0f, 1152.0f};
+}
+// Bytes 0, 1 (or 2, 3) of a turned dword.
+__device__ __forceinline__ at_h2 at_low(int x)
+{
+    return at_codes(__builtin_amdgcn_perm(0x64646464, x, 0x04010400));
+}
+__device__ __forceinline__ at_h2 at_high(int x)
+{
+    return at_codes(__builtin_amdgcn_perm(0x64646464, x, 0x04030402));
+}
+// Byte B of two turned dwords.
+template <int B>
+__device__ __forceinline__ at_h2 at_pair(int x, int y)
+{
+    constexpr unsigned sel = 0x0c000c00u | (unsigned)B | (unsigned)(4 + B) << 16;
+    return at_codes(__builtin_amdgcn_perm(y, x, sel) | 0x64006400);
+}
+// Eight codes of a row, turned.
+__device__ __forceinline__ at_h8 at_eight(int x, int y)
+{
+    const at_h2 a = at_low(x), b = at_high(x), c = at_low(y), d = at_high(y);
+    return (at_h8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Where a lane's pieces of a row lie.  Keys: HD / 64 pieces of 16 codes, of which
+// a row's last is its last sixteen codes (q holds zeros where two pieces overlap).
+// Values: HD / 16 codes, the last ones again (results that two lanes hold are the
+// same numbers).  Rows of fewer than 16 codes are read code by code.
+template <int HD>
+struct AtLanes {
+    static constexpr int NK = HD / 64, CB = HD / 16;
+    int n, g;          // lane % 16, lane / 16
+    int koff[NK];      // of the keys' pieces
+    int voff;          // of the values' piece
+    bool small;
+    __device__ AtLanes(int hd)
+    {
+        const int lane = threadIdx.x & 63;
+        n = lane & 15;
+        g = lane >> 4;
+        small = hd < 16;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int at = j * 64 + g * 16;
+            koff[j] = at >= hd || small ? 0 : min(at, hd - 16);
+        }
+        voff = at_value(n, hd);
+    }
+    // first code of lane x's piece of the values
+    static __device__ int at_value(int x, int hd) { return hd < 16 ? x * CB : min(x * CB, hd - CB); }
+    // q's index that belongs to code e of piece j, -1 where q counts as zero
+    __device__ int q_index(int j, int e, int hd) const
+    {
+        const int at = j * 64 + g * 16, d = koff[j] + e;
+        return small ? (j == 0 && g == 0 && e < hd ? e : -1) : at < hd && d >= at ? d : -1;
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void at_bytes(const signed char* p, int have, int (&x)[N])
+{
+#pragma unroll
+    for (int w = 0; w < N; ++w) {
+        unsigned v = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (w * 4 + b < have) v |= (unsigned)(unsigned char)p[w * 4 + b] << (8 * b);
+        x[w] = (int)v;
+    }
+}
+template <int N>
+__device__ __forceinline__ void at_load(const signed char* p, int (&x)[N])
+{
+    typedef int vec __attribute__((ext_vector_type(N), aligned(1)));
+    const vec v = *(const vec*)p;
+#pragma unroll
+    for (int w = 0; w < N; ++w) x[w] = v[w];
+}
+template <>
+__device__ __forceinline__ void at_load<1>(const signed char* p, int (&x)[1])
+{
+    typedef int one __attribute__((aligned(1)));
+    x[0] = *(const one*)p;
+}
+
+// A lane's keys of one token, turned, and its values of one token.
+template <int HD>
+__device__ __forceinline__ void at_keys(const signed char* row, const AtLanes<HD>& a, int hd,
+                                        int (&x)[AtLanes<HD>::NK][4])
+{
+#pragma unroll
+    for (int j = 0; j < AtLanes<HD>::NK; ++j) {
+        if (a.small)
+            at_bytes(row, j == 0 && a.g == 0 ? hd : 0, x[j]);
+        else
+            at_load(row + a.koff[j], x[j]);
+    }
+}
+template <int HD>
+__device__ __forceinline__ void at_values(const signed char* row, const AtLanes<HD>& a, int hd,
+                                          int (&x)[AtLanes<HD>::CB / 4])
+{
+    if (a.small)
+        at_bytes(row + a.voff, hd - a.voff, x);
+    else
+        at_load(row + a.voff, x);
+}
+
+// A tile of 16 rows of q as the score product's operand, for lane (n, g): row n's
+// numbers that belong to its codes.  SPLIT: as the sum of two.
+template <class T, int HD>
+struct AtQuery {
+    static constexpr int NF = HD / 32;
+    static constexpr bool SPLIT = std::is_same<T, float>::value;
+    at_h8 hi[NF], lo[SPLIT ? NF : 1];
+    float unit;  // score = sum of products * key's scale * unit
+    __device__ void load(const T* row, bool some, const AtLanes<HD>& a, int hd, float scale)
+    {
+        float v[NF][8], most = 0.0f;
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = a.q_index(f / 2, (f & 1) * 8 + e, hd);
+                v[f][e] = some && d >= 0 ? (float)row[d] : 0.0f;
+                most = __builtin_elementwise_maximum(most, __builtin_fabsf(v[f][e]));
+            }
+        most = __builtin_elementwise_maximum(most, __shfl_xor(most, 16, 64));
+        most = __builtin_elementwise_maximum(most, __shfl_xor(most, 32, 64));
+        float up = 1.0f, down = 1.0f;
+        if (!std::is_same<T, q8half>::value && most > 0.0f && most < INFINITY) {
+            // the largest between 2^14 and 2^15
+            const int e = min(max(14 + 127 - (int)(__float_as_uint(most) >> 23), -126), 126);
+            up = __uint_as_float((unsigned)(127 + e) << 23);
+            down = __uint_as_float((unsigned)(127 - e) << 23);
+        }
+        unit = scale * down;
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = v[f][e] * up;
+                hi[f][e] = (_Float16)x;
+                if constexpr (SPLIT) lo[f][e] = (_Float16)(x - (float)hi[f][e]);
+            }
+    }
+};
+
+// Results so far of 16 rows of q, in the lanes of their columns: l, the sum of the
+// weights e^(s - m) of a lane's tokens, and out in units of `unit` / 2^14.
+template <int HD>
+struct AtRows {
+    static constexpr int CB = HD / 16;
+    float m, l;
+    at_f4 o[CB];  // o[jd][i]: row n's code voff(4 g + i) + jd
+    __device__ void clear()
+    {
+        m = AT_LOWEST;
+        l = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CB; ++j) o[j] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ void times(float f)
+    {
+#pragma unroll
+        for (int j = 0; j < CB; ++j) o[j] *= f;
+    }
+    __device__ void whole()  // l of all the row's tokens
+    {
+        l += __shfl_xor(l, 16, 64);
+        l += __shfl_xor(l, 32, 64);
+    }
+};
+
+// Scores of one lane to weights.  x: N scores of row n in units of log 2; on
+// return e^(s - m).
+template <int N, int HD>
+__device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N])
+{
+    float most = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
+    if (__ballot(most > r.m + 1.0f) != 0) {
+        most = fmaxf(most, __shfl_xor(most, 16, 64));
+        most = fmaxf(most, __shfl_xor(most, 32, 64));
+        const float to = fmaxf(most, r.m), f = __builtin_amdgcn_exp2f(r.m - to);
+        r.m = to;
+        r.l *= f;
+        r.times(f);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(x[i] - r.m);
+        r.l += x[i];
+    }
+}
+
+// The largest values' scale so far, as a power of two, for a wave.  Scales that are
+// not finite do not count: their weights are not finite in their own rows.
+struct AtUnit {
+    float unit = 0x1p-100f;
+    // raised to hold `v` (any lane's); the factor for what was summed in the old one
+    __device__ bool raise(float v, float& f)
+    {
+        v = fabsf(v);
+        const bool more = v > unit && v < INFINITY;
+        if (__ballot(more) == 0) return false;
+        float most = more ? v : unit;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
+        // the next power of two (the largest ones: 2^127)
+        const unsigned e = min((__float_as_uint(most) >> 23) + 1, 254u);
+        const float to = __uint_as_float(__builtin_amdgcn_readfirstlane(e << 23));
+        f = unit / to;
+        unit = to;
+        return true;
+    }
+    __device__ float up() const { return AT_UP / unit; }
+};
+
+template <class H8>
+__device__ __forceinline__ at_f4 at_product(H8 a, H8 b, at_f4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Eight weights as the second product's operand.
+__device__ __forceinline__ at_h8 at_round(const float (&w)[8])
+{
+    at_h8 h;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const at_h2 p = __builtin_convertvector((at_f2){w[i], w[i + 1]}, at_h2);
+        h[i] = p[0];
+        h[i + 1] = p[1];
+    }
+    return h;
+}
+__device__ __forceinline__ at_h8 at_rest(const float (&w)[8], at_h8 h)
+{
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = w[i] - (float)h[i];
+    return at_round(r);
+}
+
+// Values of eight tokens as operands of the second product: code B of dword W.
+template <int W, int B, int N>
+__device__ __forceinline__ at_h8 at_column(const int (&v)[8][N])
+{
+    const at_h2 a = at_pair<B>(v[0][W], v[1][W]), b = at_pair<B>(v[2][W], v[3][W]);
+    const at_h2 c = at_pair<B>(v[4][W], v[5][W]), d = at_pair<B>(v[6][W], v[7][W]);
+    return (at_h8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A row's results to out and lse.
+template <class T>
+__device__ __forceinline__ void at_lse(const AttnArgs<T>& a, size_t row, int head, float m, float l)
+{
+    if (a.lse != nullptr) a.lse[row * a.p.heads + head] = l == 0.0f ? -INFINITY : m * AT_LN2 + logf(l);
+}
+
+// ------------------------------------------------------------------- narrow
+// Rows of the cache, and scales, of a wave's 32 tokens.
+struct AtTokens {
+    int row[32];
+    float ks[32], vs[32];
+};
+
+template <class T, int HD>
+struct AtNarrow {
+    static constexpr int NK = HD / 64, CB = HD / 16, NV = CB / 4, STEP = 32;
+    static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
+    struct Lds {
+        AtTokens tokens[4][2];
+        float m[4][16], l[4][16], f[4][16];
+        float o[4][16][HD + 4];
+    };
+    struct Codes {  // of one step
+        int k[2][NK][4], v[8][NV];
+        float ks, vs;
+        unsigned long long ok;  // tokens (bits 0 to 31) that are there
+    };
+
+    const AttnArgs<T>& a;
+    const AtJob& job;
+    const AtLanes<HD>& at;
+    Lds& lds;
+    const int* pages;  // the sequence's row of the table
+    int lane, wave, limit, least;
+    AtQuery<T, HD> q;
+    AtRows<HD> r;
+    AtUnit unit;
+
+    __device__ int page_of(int t) const
+    {
+        return lane < STEP && t < job.end ? pages[t / a.p.ps] : -1;
+    }
+    // rows of the step's tokens to LDS, and their codes and scales on their way
+    __device__ void fetch(Codes& c, AtTokens& tok, int base, int page)
+    {
+        const int t = base + lane;
+        int row = -1;
+        if (lane < STEP && t < job.end && (unsigned)page < (unsigned)a.p.pages)
+            row = (page * a.p.kvheads + job.head) * a.p.ps + t % a.p.ps;
+        c.ok = __ballot(row >= 0);
+        c.ks = c.vs = 0.0f;
+        if (row >= 0) {
+            c.ks = a.ks[row];
+            c.vs = a.vs[row];
+        }
+        if (lane < STEP) tok.row[lane] = max(row, 0);
+        at_wave_sync();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            at_keys<HD>(a.k + (size_t)tok.row[16 * i + at.n] * a.ldk, at, a.p.hd, c.k[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            at_values<HD>(a.v + (size_t)tok.row[i / 4 * 16 + 4 * at.g + i % 4] * a.ldv, at, a.p.hd, c.v[i]);
+    }
+    __device__ void compute(Codes& c, AtTokens& tok, int base)
+    {
+        float f;
+        if (unit.raise(c.vs, f)) r.times(f);
+        if (lane < STEP) {
+            tok.ks[lane] = c.ks;
+            tok.vs[lane] = c.vs * unit.up();
+        }
+        at_wave_sync();
+        float x[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            at_f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const at_h8 k = at_eight(at_turn(c.k[i][j][2 * half]), at_turn(c.k[i][j][2 * half + 1]));
+                    s = at_product(k, q.hi[2 * j + half], s);
+                    if constexpr (SPLIT) s = at_product(k, q.lo[2 * j + half], s);
+                }
+            const at_f4 ks = *(const at_f4*)&tok.ks[16 * i + 4 * at.g];
+            const at_f4 vs = *(const at_f4*)&tok.vs[16 * i + 4 * at.g];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[4 * i + e] = s[e] * ks[e] * q.unit;
+                w[4 * i + e] = vs[e];
+            }
+        }
+        const bool all = (unsigned)c.ok == ~0u && base + STEP <= least;
+        unsigned mask = 0xff;
+        if (!all) {  // (scales behind the sequence or of a page that is none are zeros)
+            mask = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = i / 4 * 16 + 4 * at.g + i % 4;
+                if (base + t < limit && (c.ok >> t & 1)) mask |= 1u << i;
+                if (!(mask >> i & 1)) x[i] = -INFINITY;
+            }
+        }
+        at_weigh(r, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= x[i];
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(mask >> i & 1)) w[i] = 0.0f;
+        }
+        const at_h8 p = at_round(w);
+        at_h8 rest;
+        if constexpr (SPLIT) rest = at_rest(w, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int d = 0; d < NV; ++d) c.v[i][d] = at_turn(c.v[i][d]);
+        auto add = [&](int j, at_h8 v) {
+            r.o[j] = at_product(v, p, r.o[j]);
+            if constexpr (SPLIT) r.o[j] = at_product(v, rest, r.o[j]);
+        };
+        at_each<NV>([&](auto W) {
+            constexpr int d = decltype(W)::value;
+            add(4 * d + 0, at_column<d, 0>(c.v));
+            add(4 * d + 1, at_column<d, 1>(c.v));
+            add(4 * d + 2, at_column<d, 2>(c.v));
+            add(4 * d + 3, at_column<d, 3>(c.v));
+        });
+    }
+    // Tokens from `from` to `to` of the job: tiles of 128, 32 of each for a wave.
+    __device__ void tokens(int from, int to)
+    {
+        r.clear();
+        const int first = from + wave * STEP;
+        const int count = first < to ? (to - first + AT_TILE - 1) / AT_TILE : 0;
+        if (count == 0) return;
+        Codes c[2];
+        int page = page_of(first + lane);
+        fetch(c[0], lds.tokens[wave][0], first, page);
+        page = page_of(first + AT_TILE + lane);
+        auto step = [&](Codes& now, Codes& next, AtTokens& tn, AtTokens& tx, int s) {
+            const int base = first + s * AT_TILE;
+            if (s + 1 < count) {
+                fetch(next, tx, base + AT_TILE, page);
+                page = page_of(base + 2 * AT_TILE + lane);
+            }
+            compute(now, tn, base);
+        };
+        for (int s = 0; s < count; s += 2) {
+            step(c[0], c[1], lds.tokens[wave][0], lds.tokens[wave][1], s);
+            if (s + 1 < count) step(c[1], c[0], lds.tokens[wave][1], lds.tokens[wave][0], s + 1);
+        }
+    }
+    // The waves' results together, to out or to the job's part.
+    __device__ void finish(float* slab)
+    {
+        r.whole();
+        if (lane < 16) {
+            lds.m[wave][lane] = r.m;
+            lds.l[wave][lane] = r.l;
+        }
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds.o[wave][at.n][(4 * at.g + i) * CB + j] = r.o[j][i];
         __syncthreads();
-        if (t < a.hd) q[t] = (float)a.q[(size_t)r * a.ldq + (size_t)h * a.hd + t];
-        float m = -INFINITY, l = 0.0f, o = 0.0f;
-        for (long long base = 0; base < seen; base += 256) {
-            __syncthreads();
-            const long long tok = base + t;
-            float x = -INFINITY, vs = 0.0f;
-            at[t] = -1;
-            if (tok < seen) {
-                const int page = row[tok / a.ps];
-                if ((unsigned)page < (unsigned)a.pages) {
-                    const int c = (page * a.kvheads + g) * a.ps + (int)(tok % a.ps);
-                    at[t] = c;
-                    const signed char* k = a.k + (size_t)c * a.ldk;
-                    float dot = 0.0f;
-                    for (int d = 0; d < a.hd; ++d) dot = __builtin_fmaf(q[d], (float)k[d], dot);
-                    x = dot * a.ks[c] * a.scale;
-                    vs = a.vs[c];
+        float m = lds.m[0][at.n], l = 0.0f;
+        for (int w = 1; w < 4; ++w) m = fmaxf(m, lds.m[w][at.n]);
+        for (int w = 0; w < 4; ++w) l += lds.l[w][at.n] * __builtin_amdgcn_exp2f(lds.m[w][at.n] - m);
+        if (lane < 16) {
+            // each wave its own factor
+            const float f = __builtin_amdgcn_exp2f(r.m - m) * (unit.unit * AT_DOWN);
+            lds.f[wave][lane] = slab != nullptr ? f : l == 0.0f ? 0.0f : f / l;
+            if (wave == 0 && lane < job.rows) {
+                if (slab != nullptr) {
+                    slab[2 * lane] = m;
+                    slab[2 * lane + 1] = l;
+                } else {
+                    size_t row;
+                    const int head = job.place(a.p, lane, row);
+                    at_lse(a, row, head, m, l);
                 }
             }
-            float most = x;
-            for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-            if ((t & 63) == 0) of_wave[t / 64] = most;
-            __syncthreads();
-            most = fmaxf(fmaxf(of_wave[0], of_wave[1]), fmaxf(of_wave[2], of_wave[3]));
-            most = fmaxf(m, most);
-            const float keep = most == -INFINITY ? 1.0f : expf(m - most);
-            const float e = at[t] < 0 ? 0.0f : expf(x - (most == -INFINITY ? 0.0f : most));
-            m = most;
-            float sum = e;
-            for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-            __syncthreads();
-            if ((t & 63) == 0) of_wave[t / 64] = sum;
-            p[t] = e * vs;
-            __syncthreads();
-            l = l * keep + of_wave[0] + of_wave[1] + of_wave[2] + of_wave[3];
-            o *= keep;
-            if (t < a.hd)
-                for (int j = 0; j < 256; ++j)
-                    if (at[j] >= 0) o = __builtin_fmaf(p[j], (float)a.v[(size_t)at[j] * a.ldv + t], o);
         }
-        if (t < a.hd) a.out[(size_t)r * a.ldo + (size_t)h * a.hd + t] = (T)(l == 0.0f ? 0.0f : o / l);
-        if (t == 0 && a.lse) a.lse[item] = l == 0.0f ? -INFINITY : m + logf(l);
+        __syncthreads();
+        const int hd = a.p.hd;
+        for (int i = threadIdx.x; i < 16 * CB * 16; i += 256) {
+            const int n = i / (16 * CB), piece = i / CB % 16, j = i % CB;
+            const int d = AtLanes<HD>::at_value(piece, hd) + j;
+            // (a code that two pieces hold is written by the lower one)
+            if (n >= job.rows || d >= hd || d < piece * CB) continue;
+            float o = 0.0f;
+            for (int w = 0; w < 4; ++w) {
+                const float f = lds.f[w][n];
+                // (nothing times what is no number: of a wave without a token)
+                o += lds.l[w][n] == 0.0f ? 0.0f : f * lds.o[w][n][piece * CB + j];
+            }
+            if (slab != nullptr) {
+                slab[2 * AT_NARROW + (size_t)n * hd + d] = o;
+            } else {
+                size_t row;
+                const int head = job.place(a.p, n, row);
+                a.out[row * a.ldo + (size_t)head * hd + d] = (T)o;
+            }
+        }
+        __syncthreads();
+    }
+    __device__ void run(int from, int to, float* slab)
+    {
+        size_t row = 0;
+        const bool some = at.n < job.rows;
+        const int head = job.place(a.p, some ? at.n : 0, row);
+        q.load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
+        limit = some ? job.limit(a.p, at.n) : 0x7fffffff;
+        least = at_least(limit);
+        tokens(from, to);
+        finish(slab);
+    }
+};
+
+// --------------------------------------------------------------------- wide
+template <class T, int HD>
+struct AtWide {
+    static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4, STEP = 64;
+    static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
+    struct Step {
+        at_h8 k[4][NF][64];     // keys of 16 tokens each, as the lanes read them
+        at_h8 v[2][CB][64];     // values of 32 tokens each
+        float ks[64], vs[64];
+        unsigned short ok[4];   // tokens that are there
+    };
+    struct Lds {
+        Step step[2];
+    };
+    struct Codes {  // a wave's 16 tokens of one step
+        int k[NK][4], v[4][NV];
+        float ks, vs;
+        int ok;
+    };
+
+    const AttnArgs<T>& a;
+    const AtJob& job;
+    const AtLanes<HD>& at;
+    Lds& lds;
+    const int* pages;
+    int lane, wave;
+    int tiles;       // tiles of 16 rows of a wave: 1 or 2
+    int first;       // the wave's first row
+    AtQuery<T, HD> q[2];
+    AtRows<HD> r[2];
+    AtUnit unit;
+    int limit[2], least, most;
+
+    __device__ int page_of(int t) const { return t < job.end ? pages[t / a.p.ps] : -1; }
+
+    __device__ void fetch(Codes& c, int base, int page)
+    {
+        const int t = base + wave * 16 + at.n;
+        int row = -1;
+        if (t < job.end && (unsigned)page < (unsigned)a.p.pages)
+            row = (page * a.p.kvheads + job.head) * a.p.ps + t % a.p.ps;
+        c.ok = row >= 0;
+        c.ks = c.vs = 0.0f;
+        if (row >= 0) {
+            c.ks = a.ks[row];
+            c.vs = a.vs[row];
+        }
+        row = max(row, 0);
+        at_keys<HD>(a.k + (size_t)row * a.ldk, at, a.p.hd, c.k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            at_values<HD>(a.v + (size_t)__shfl(row, 4 * at.g + i, 64) * a.ldv, at, a.p.hd, c.v[i]);
+    }
+    __device__ void share(Codes& c, Step& s)
+    {
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                s.k[wave][2 * j + half][lane] = at_eight(at_turn(c.k[j][2 * half]), at_turn(c.k[j][2 * half + 1]));
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < NV; ++d) c.v[i][d] = at_turn(c.v[i][d]);
+        auto put = [&](int j, at_h2 x, at_h2 y) {
+            h4* to = reinterpret_cast<h4*>(&s.v[wave >> 1][j][lane]) + (wave & 1);
+            *to = (h4){x[0], x[1], y[0], y[1]};
+        };
+        at_each<NV>([&](auto W) {
+            constexpr int d = decltype(W)::value;
+            put(4 * d + 0, at_pair<0>(c.v[0][d], c.v[1][d]), at_pair<0>(c.v[2][d], c.v[3][d]));
+            put(4 * d + 1, at_pair<1>(c.v[0][d], c.v[1][d]), at_pair<1>(c.v[2][d], c.v[3][d]));
+            put(4 * d + 2, at_pair<2>(c.v[0][d], c.v[1][d]), at_pair<2>(c.v[2][d], c.v[3][d]));
+            put(4 * d + 3, at_pair<3>(c.v[0][d], c.v[1][d]), at_pair<3>(c.v[2][d], c.v[3][d]));
+        });
+        const unsigned long long ok = __ballot(c.ok);
+        if (lane < 16) {
+            s.ks[wave * 16 + lane] = c.ks;
+            s.vs[wave * 16 + lane] = c.vs;
+        }
+        if (lane == 0) s.ok[wave] = (unsigned short)ok;
+    }
+    template <int TILES>
+    __device__ void compute(const Step& s, int base)
+    {
+        float x[TILES][16];
+        at_f4 vs[4];
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+            at_f4 acc[TILES];
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) acc[i] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const at_h8 k = s.k[sub][f][lane];
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    acc[i] = at_product(k, q[i].hi[f], acc[i]);
+                    if constexpr (SPLIT) acc[i] = at_product(k, q[i].lo[f], acc[i]);
+                }
+            }
+            const at_f4 ks = *(const at_f4*)&s.ks[16 * sub + 4 * at.g];
+            vs[sub] = *(const at_f4*)&s.vs[16 * sub + 4 * at.g];
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e] * q[i].unit;
+        }
+        float v = 0.0f, f;
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v = fabsf(vs[sub][e]) < INFINITY ? fmaxf(v, fabsf(vs[sub][e])) : v;
+        if (unit.raise(v, f))
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) r[i].times(f);
+        const float up = unit.up();
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
+        unsigned long long ok;
+        __builtin_memcpy(&ok, s.ok, 8);
+        const bool all = ok == ~0ull && base + STEP <= least;
+        unsigned mask[TILES];
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                mask[i] = 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = e / 4 * 16 + 4 * at.g + e % 4;
+                    if (base + t < limit[i] && (ok >> t & 1)) mask[i] |= 1u << e;
+                    if (!(mask[i] >> e & 1)) x[i][e] = -INFINITY;
+                }
+            }
+        }
+        at_h8 p[TILES][2], rest[TILES][SPLIT ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            at_weigh(r[i], x[i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = x[i][8 * h + e] * vs[2 * h + e / 4][e % 4];
+                if (!all) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!(mask[i] >> (8 * h + e) & 1)) w[e] = 0.0f;
+                }
+                p[i][h] = at_round(w);
+                if constexpr (SPLIT) rest[i][h] = at_rest(w, p[i][h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+                const at_h8 c = s.v[h][j][lane];
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
+                    if constexpr (SPLIT) r[i].o[j] = at_product(c, rest[i][h], r[i].o[j]);
+                }
+            }
+    }
+    __device__ void finish(float* slab)
+    {
+        const int hd = a.p.hd;
+        for (int i = 0; i < tiles; ++i) {
+            AtRows<HD>& t = i == 0 ? r[0] : r[1];
+            t.whole();
+            const int n = first + 16 * i + at.n;
+            if (n >= job.rows) continue;
+            float f = unit.unit * AT_DOWN;
+            if (t.l == 0.0f) f = 0.0f;
+            if (slab != nullptr) {
+                float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
+                const int m = n % AT_NARROW;
+                if (at.g == 0) {
+                    part[2 * m] = t.m;
+                    part[2 * m + 1] = t.l;
+                }
+                write(t, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
+            } else {
+                size_t row;
+                const int head = job.place(a.p, n, row);
+                if (at.g == 0) at_lse(a, row, head, t.m, t.l);
+                write(t, a.out + row * a.ldo + (size_t)head * hd, t.l == 0.0f ? 0.0f : f / t.l, hd);
+            }
+        }
+    }
+    template <class O>
+    __device__ void write(const AtRows<HD>& t, O* to, float f, int hd)
+    {
+        typedef O vec __attribute__((ext_vector_type(CB), aligned(sizeof(O))));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = AtLanes<HD>::at_value(4 * at.g + i, hd);
+            vec v;
+#pragma unroll
+            for (int j = 0; j < CB; ++j) v[j] = (O)(t.o[j][i] * f);
+            if (hd >= 16)
+                *(vec*)(to + d) = v;
+            else
+#pragma unroll
+                for (int j = 0; j < CB; ++j)
+                    if (d + j < hd) to[d + j] = v[j];
+        }
+    }
+    __device__ void run(int from, int to, float* slab)
+    {
+        // few rows are dealt 16 to a wave, so that all waves have some
+        tiles = job.rows > 64 ? 2 : 1;
+        first = wave * 16 * tiles;
+        least = 0x7fffffff;
+        most = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int n = first + 16 * i + at.n;
+            const bool some = i < tiles && n < job.rows;
+            size_t row = 0;
+            const int head = job.place(a.p, some ? n : 0, row);
+            q[i].load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
+            limit[i] = some ? job.limit(a.p, n) : 0x7fffffff;
+            least = min(least, at_least(limit[i]));
+            most = max(most, at_most(some ? limit[i] : 0));
+            r[i].clear();
+        }
+        Codes c;
+        const int mine = wave * 16 + at.n;
+        if (from < to) {
+            fetch(c, from, page_of(from + mine));
+            int page = page_of(from + STEP + mine), p = 0;
+            for (int base = from; base < to; base += STEP, p ^= 1) {
+                share(c, lds.step[p]);
+                __syncthreads();
+                if (base + STEP < to) {
+                    fetch(c, base + STEP, page);
+                    page = page_of(base + 2 * STEP + mine);
+                }
+                if (base < most) {
+                    if (tiles == 2)
+                        compute<2>(lds.step[p], base);
+                    else
+                        compute<1>(lds.step[p], base);
+                }
+            }
+        }
+        finish(slab);
+        __syncthreads();
+    }
+};
+
+// Workgroups a compute unit has room for: wide heads and float's two numbers take
+// the registers of two.
+template <class T, int HD>
+constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
+
+template <class T, int HD>
+__global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T> a)
+{
+    __shared__ AtScan scan;
+    __shared__ union {
+        typename AtNarrow<T, HD>::Lds narrow;
+        typename AtWide<T, HD>::Lds wide;
+    } lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const AtLanes<HD> at(a.p.hd);
+    AtCursor cursor(a.p, scan);
+    AtJob job;
+    int from, to;
+    long long slab;
+    while (cursor.next(a.p, job, from, to, slab)) {
+        float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
+        const int* pages = a.p.table + (size_t)job.table * a.p.ldt;
+        if (job.wide) {
+            AtWide<T, HD> w{a, job, at, lds.wide, pages, lane, wave};
+            w.run(from, to, part);
+        } else {
+            AtNarrow<T, HD> w{a, job, at, lds.narrow, pages, lane, wave};
+            w.run(from, to, part);
+        }
+    }
+}
+
+// Adds the parts of each row's jobs.  A workgroup has a few rows' heads of one
+// head's keys, of which it looks at all at once for those with something to add;
+// parts go to its waves in turn.
+template <class T>
+struct AttnJoinArgs {
+    AttnArgs<T> a;
+    int per;  // rows' heads of keys of a workgroup, 64 at most
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void q8_attn_join(AttnJoinArgs<T> j_)
+{
+    const AttnArgs<T>& a = j_.a;
+    const int per = j_.per;
+    __shared__ float sums[4][AT_HD + 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd, share = a.p.share;
+    const long long all = (long long)a.p.rows * a.p.kvheads, first = (long long)blockIdx.x * per;
+    AtParts parts[2];
+    unsigned long long todo = __ballot(
+        lane < per && first + lane < all &&
+        at_parts(a.p, (int)((first + lane) / a.p.kvheads), (int)((first + lane) % a.p.kvheads), parts));
+    for (; todo != 0; todo &= todo - 1) {
+        const long long item = first + __ffsll(todo) - 1;
+        const int row = (int)(item / a.p.kvheads), kv = (int)(item % a.p.kvheads);
+        at_parts(a.p, row, kv, parts);
+        for (int h = 0; h < share; ++h) {
+            if (!parts[1].of.joined && parts[1].count(h) == 1) continue;
+            float m = AT_LOWEST, l = 0.0f, o[AT_HD / 64] = {};
+            for (int j = 0; j < 2; ++j) {
+                const AtParts& p = parts[j];
+                const int count = p.count(h);
+                for (int i = wave; i < count; i += 4) {
+                    const int n = p.row(h) % AT_NARROW;
+                    const long long at = p.slab(h, i);
+                    if (at < 0) continue;
+                    const float* s = a.slabs + at * at_slab(hd);
+                    const float pm = s[2 * n], pl = s[2 * n + 1];
+                    float v[AT_HD / 64];
+#pragma unroll
+                    for (int e = 0; e < AT_HD / 64; ++e)
+                        v[e] = lane + 64 * e < hd ? s[2 * AT_NARROW + (size_t)n * hd + lane + 64 * e] : 0.0f;
+                    if (pl == 0.0f) continue;
+                    const float to = fmaxf(m, pm);
+                    const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
+                    m = to;
+                    l = l * f + pl * g;
+#pragma unroll
+                    for (int e = 0; e < AT_HD / 64; ++e) o[e] = o[e] * f + v[e] * g;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < AT_HD / 64; ++e)
+                if (lane + 64 * e < hd) sums[wave][lane + 64 * e] = o[e];
+            if (lane == 0) {
+                sums[wave][AT_HD] = m;
+                sums[wave][AT_HD + 1] = l;
+            }
+            __syncthreads();
+            float most = sums[0][AT_HD], total = 0.0f;
+            for (int w = 1; w < 4; ++w) most = fmaxf(most, sums[w][AT_HD]);
+            float f[4];
+            for (int w = 0; w < 4; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(sums[w][AT_HD] - most);
+                total += sums[w][AT_HD + 1] * f[w];
+            }
+            const int head = kv * share + h;
+            for (int d = threadIdx.x; d < hd; d += 256) {
+                float v = 0.0f;
+                for (int w = 0; w < 4; ++w) v += sums[w][d] * f[w];
+                a.out[(size_t)row * a.ldo + (size_t)head * hd + d] = (T)(total == 0.0f ? 0.0f : v / total);
+            }
+            if (threadIdx.x == 0) at_lse(a, (size_t)row, head, most, total);
+        }
     }
 }
 
