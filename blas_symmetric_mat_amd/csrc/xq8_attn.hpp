@@ -100,49 +100,29 @@ __device__ __forceinline__ at_h8 at_eight(int x, int y)
 // Where a lane's pieces of a row lie.  Keys: HD / 64 pieces of 16 codes, of which
 // a row's last is its last sixteen codes (q holds zeros where two pieces overlap).
 // Values: HD / 16 codes, the last ones again (results that two lanes hold are the
-// same numbers).  Rows of fewer than 16 codes are read code by code.
+// same numbers).
 template <int HD>
 struct AtLanes {
     static constexpr int NK = HD / 64, CB = HD / 16;
     int n, g;          // lane % 16, lane / 16
     int koff[NK];      // of the keys' pieces
     int voff;          // of the values' piece
-    bool small;
     __device__ AtLanes(int hd)
     {
         const int lane = threadIdx.x & 63;
         n = lane & 15;
         g = lane >> 4;
-        small = hd < 16;
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
             const int at = j * 64 + g * 16;
-            koff[j] = at >= hd || small ? 0 : min(at, hd - 16);
+            koff[j] = at >= hd ? 0 : min(at, hd - 16);
         }
         voff = at_value(n, hd);
     }
     // first code of lane x's piece of the values
-    static __device__ int at_value(int x, int hd) { return hd < 16 ? x * CB : min(x * CB, hd - CB); }
-    // q's index that belongs to code e of piece j, -1 where q counts as zero
-    __device__ int q_index(int j, int e, int hd) const
-    {
-        const int at = j * 64 + g * 16, d = koff[j] + e;
-        return small ? (j == 0 && g == 0 && e < hd ? e : -1) : at < hd && d >= at ? d : -1;
-    }
+    static __device__ __forceinline__ int at_value(int x, int hd) { return min(x * CB, hd - CB); }
 };
 
-template <int N>
-__device__ __forceinline__ void at_bytes(const signed char* p, int have, int (&x)[N])
-{
-#pragma unroll
-    for (int w = 0; w < N; ++w) {
-        unsigned v = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            if (w * 4 + b < have) v |= (unsigned)(unsigned char)p[w * 4 + b] << (8 * b);
-        x[w] = (int)v;
-    }
-}
 template <int N>
 __device__ __forceinline__ void at_load(const signed char* p, int (&x)[N])
 {
@@ -158,27 +138,19 @@ __device__ __forceinline__ void at_load<1>(const signed char* p, int (&x)[1])
     x[0] = *(const one*)p;
 }
 
-// A lane's keys of one token, turned, and its values of one token.
+// A lane's keys of one token, and its values of one.
 template <int HD>
-__device__ __forceinline__ void at_keys(const signed char* row, const AtLanes<HD>& a, int hd,
+__device__ __forceinline__ void at_keys(const signed char* row, const AtLanes<HD>& a,
                                         int (&x)[AtLanes<HD>::NK][4])
 {
 #pragma unroll
-    for (int j = 0; j < AtLanes<HD>::NK; ++j) {
-        if (a.small)
-            at_bytes(row, j == 0 && a.g == 0 ? hd : 0, x[j]);
-        else
-            at_load(row + a.koff[j], x[j]);
-    }
+    for (int j = 0; j < AtLanes<HD>::NK; ++j) at_load(row + a.koff[j], x[j]);
 }
 template <int HD>
-__device__ __forceinline__ void at_values(const signed char* row, const AtLanes<HD>& a, int hd,
+__device__ __forceinline__ void at_values(const signed char* row, const AtLanes<HD>& a,
                                           int (&x)[AtLanes<HD>::CB / 4])
 {
-    if (a.small)
-        at_bytes(row + a.voff, hd - a.voff, x);
-    else
-        at_load(row + a.voff, x);
+    at_load(row + a.voff, x);
 }
 
 // A tile of 16 rows of q as the score product's operand, for lane (n, g): row n's
@@ -189,17 +161,19 @@ struct AtQuery {
     static constexpr bool SPLIT = std::is_same<T, float>::value;
     at_h8 hi[NF], lo[SPLIT ? NF : 1];
     float unit;  // score = sum of products * key's scale * unit
-    __device__ void load(const T* row, bool some, const AtLanes<HD>& a, int hd, float scale)
+    __device__ __forceinline__ void load(const T* row, bool some, const AtLanes<HD>& a, int hd, float scale)
     {
         float v[NF][8], most = 0.0f;
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int f = 0; f < NF; ++f) {
+            const int from = a.koff[f / 2] + (f & 1) * 8, at = f / 2 * 64 + a.g * 16;
+            q8_load(row + from, some && at < hd ? 8 : 0, v[f]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int d = a.q_index(f / 2, (f & 1) * 8 + e, hd);
-                v[f][e] = some && d >= 0 ? (float)row[d] : 0.0f;
+                if (from + e < at) v[f][e] = 0.0f;
                 most = __builtin_elementwise_maximum(most, __builtin_fabsf(v[f][e]));
             }
+        }
         most = __builtin_elementwise_maximum(most, __shfl_xor(most, 16, 64));
         most = __builtin_elementwise_maximum(most, __shfl_xor(most, 32, 64));
         float up = 1.0f, down = 1.0f;
@@ -228,19 +202,19 @@ struct AtRows {
     static constexpr int CB = HD / 16;
     float m, l;
     at_f4 o[CB];  // o[jd][i]: row n's code voff(4 g + i) + jd
-    __device__ void clear()
+    __device__ __forceinline__ void clear()
     {
         m = AT_LOWEST;
         l = 0.0f;
 #pragma unroll
         for (int j = 0; j < CB; ++j) o[j] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
     }
-    __device__ void times(float f)
+    __device__ __forceinline__ void times(float f)
     {
 #pragma unroll
         for (int j = 0; j < CB; ++j) o[j] *= f;
     }
-    __device__ void whole()  // l of all the row's tokens
+    __device__ __forceinline__ void whole()  // l of all the row's tokens
     {
         l += __shfl_xor(l, 16, 64);
         l += __shfl_xor(l, 32, 64);
@@ -275,7 +249,7 @@ __device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N])
 struct AtUnit {
     float unit = 0x1p-100f;
     // raised to hold `v` (any lane's); the factor for what was summed in the old one
-    __device__ bool raise(float v, float& f)
+    __device__ __forceinline__ bool raise(float v, float& f)
     {
         v = fabsf(v);
         const bool more = v > unit && v < INFINITY;
@@ -290,7 +264,7 @@ struct AtUnit {
         unit = to;
         return true;
     }
-    __device__ float up() const { return AT_UP / unit; }
+    __device__ __forceinline__ float up() const { return AT_UP / unit; }
 };
 
 template <class H8>
@@ -367,12 +341,12 @@ struct AtNarrow {
     AtRows<HD> r;
     AtUnit unit;
 
-    __device__ int page_of(int t) const
+    __device__ __forceinline__ int page_of(int t) const
     {
         return lane < STEP && t < job.end ? pages[t / a.p.ps] : -1;
     }
     // rows of the step's tokens to LDS, and their codes and scales on their way
-    __device__ void fetch(Codes& c, AtTokens& tok, int base, int page)
+    __device__ __forceinline__ void fetch(Codes& c, AtTokens& tok, int base, int page)
     {
         const int t = base + lane;
         int row = -1;
@@ -388,12 +362,12 @@ struct AtNarrow {
         at_wave_sync();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            at_keys<HD>(a.k + (size_t)tok.row[16 * i + at.n] * a.ldk, at, a.p.hd, c.k[i]);
+            at_keys<HD>(a.k + (size_t)tok.row[16 * i + at.n] * a.ldk, at, c.k[i]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            at_values<HD>(a.v + (size_t)tok.row[i / 4 * 16 + 4 * at.g + i % 4] * a.ldv, at, a.p.hd, c.v[i]);
+            at_values<HD>(a.v + (size_t)tok.row[i / 4 * 16 + 4 * at.g + i % 4] * a.ldv, at, c.v[i]);
     }
-    __device__ void compute(Codes& c, AtTokens& tok, int base)
+    __device__ __forceinline__ void compute(Codes& c, AtTokens& tok, int base)
     {
         float f;
         if (unit.raise(c.vs, f)) r.times(f);
@@ -461,7 +435,7 @@ struct AtNarrow {
         });
     }
     // Tokens from `from` to `to` of the job: tiles of 128, 32 of each for a wave.
-    __device__ void tokens(int from, int to)
+    __device__ __forceinline__ void tokens(int from, int to)
     {
         r.clear();
         const int first = from + wave * STEP;
@@ -485,7 +459,7 @@ struct AtNarrow {
         }
     }
     // The waves' results together, to out or to the job's part.
-    __device__ void finish(float* slab)
+    __device__ __forceinline__ void finish(float* slab)
     {
         r.whole();
         if (lane < 16) {
@@ -521,7 +495,7 @@ struct AtNarrow {
             const int n = i / (16 * CB), piece = i / CB % 16, j = i % CB;
             const int d = AtLanes<HD>::at_value(piece, hd) + j;
             // (a code that two pieces hold is written by the lower one)
-            if (n >= job.rows || d >= hd || d < piece * CB) continue;
+            if (n >= job.rows || d < piece * CB) continue;
             float o = 0.0f;
             for (int w = 0; w < 4; ++w) {
                 const float f = lds.f[w][n];
@@ -538,7 +512,7 @@ struct AtNarrow {
         }
         __syncthreads();
     }
-    __device__ void run(int from, int to, float* slab)
+    __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         size_t row = 0;
         const bool some = at.n < job.rows;
@@ -584,9 +558,9 @@ struct AtWide {
     AtUnit unit;
     int limit[2], least, most;
 
-    __device__ int page_of(int t) const { return t < job.end ? pages[t / a.p.ps] : -1; }
+    __device__ __forceinline__ int page_of(int t) const { return t < job.end ? pages[t / a.p.ps] : -1; }
 
-    __device__ void fetch(Codes& c, int base, int page)
+    __device__ __forceinline__ void fetch(Codes& c, int base, int page)
     {
         const int t = base + wave * 16 + at.n;
         int row = -1;
@@ -599,12 +573,12 @@ struct AtWide {
             c.vs = a.vs[row];
         }
         row = max(row, 0);
-        at_keys<HD>(a.k + (size_t)row * a.ldk, at, a.p.hd, c.k);
+        at_keys<HD>(a.k + (size_t)row * a.ldk, at, c.k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            at_values<HD>(a.v + (size_t)__shfl(row, 4 * at.g + i, 64) * a.ldv, at, a.p.hd, c.v[i]);
+            at_values<HD>(a.v + (size_t)__shfl(row, 4 * at.g + i, 64) * a.ldv, at, c.v[i]);
     }
-    __device__ void share(Codes& c, Step& s)
+    __device__ __forceinline__ void share(Codes& c, Step& s)
     {
 #pragma unroll
         for (int j = 0; j < NK; ++j)
@@ -635,7 +609,7 @@ struct AtWide {
         if (lane == 0) s.ok[wave] = (unsigned short)ok;
     }
     template <int TILES>
-    __device__ void compute(const Step& s, int base)
+    __device__ __forceinline__ void compute(const Step& s, int base)
     {
         float x[TILES][16];
         at_f4 vs[4];
@@ -659,6 +633,7 @@ struct AtWide {
             for (int i = 0; i < TILES; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e] * q[i].unit;
+            __builtin_amdgcn_sched_barrier(0);  // (operands of one step in registers, not of all)
         }
         float v = 0.0f, f;
 #pragma unroll
@@ -715,36 +690,37 @@ struct AtWide {
                     r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
                     if constexpr (SPLIT) r[i].o[j] = at_product(c, rest[i][h], r[i].o[j]);
                 }
+                if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
     }
-    __device__ void finish(float* slab)
+    __device__ __forceinline__ void finish(float* slab)
     {
-        const int hd = a.p.hd;
-        for (int i = 0; i < tiles; ++i) {
-            AtRows<HD>& t = i == 0 ? r[0] : r[1];
-            t.whole();
-            const int n = first + 16 * i + at.n;
-            if (n >= job.rows) continue;
-            float f = unit.unit * AT_DOWN;
-            if (t.l == 0.0f) f = 0.0f;
-            if (slab != nullptr) {
-                float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
-                const int m = n % AT_NARROW;
-                if (at.g == 0) {
-                    part[2 * m] = t.m;
-                    part[2 * m + 1] = t.l;
-                }
-                write(t, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
-            } else {
-                size_t row;
-                const int head = job.place(a.p, n, row);
-                if (at.g == 0) at_lse(a, row, head, t.m, t.l);
-                write(t, a.out + row * a.ldo + (size_t)head * hd, t.l == 0.0f ? 0.0f : f / t.l, hd);
+        one(r[0], 0, slab);
+        if (tiles == 2) one(r[1], 1, slab);
+    }
+    __device__ __forceinline__ void one(AtRows<HD>& t, int i, float* slab)
+    {
+        const int hd = a.p.hd, n = first + 16 * i + at.n;
+        t.whole();
+        if (n >= job.rows) return;
+        const float f = t.l == 0.0f ? 0.0f : unit.unit * AT_DOWN;
+        if (slab != nullptr) {
+            float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
+            const int m = n % AT_NARROW;
+            if (at.g == 0) {
+                part[2 * m] = t.m;
+                part[2 * m + 1] = t.l;
             }
+            write(t, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
+        } else {
+            size_t row;
+            const int head = job.place(a.p, n, row);
+            if (at.g == 0) at_lse(a, row, head, t.m, t.l);
+            write(t, a.out + row * a.ldo + (size_t)head * hd, t.l == 0.0f ? 0.0f : f / t.l, hd);
         }
     }
     template <class O>
-    __device__ void write(const AtRows<HD>& t, O* to, float f, int hd)
+    __device__ __forceinline__ void write(const AtRows<HD>& t, O* to, float f, int hd)
     {
         typedef O vec __attribute__((ext_vector_type(CB), aligned(sizeof(O))));
 #pragma unroll
@@ -753,15 +729,10 @@ struct AtWide {
             vec v;
 #pragma unroll
             for (int j = 0; j < CB; ++j) v[j] = (O)(t.o[j][i] * f);
-            if (hd >= 16)
-                *(vec*)(to + d) = v;
-            else
-#pragma unroll
-                for (int j = 0; j < CB; ++j)
-                    if (d + j < hd) to[d + j] = v[j];
+            *(vec*)(to + d) = v;
         }
     }
-    __device__ void run(int from, int to, float* slab)
+    __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         // few rows are dealt 16 to a wave, so that all waves have some
         tiles = job.rows > 64 ? 2 : 1;

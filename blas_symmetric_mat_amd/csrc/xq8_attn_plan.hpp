@@ -21,7 +21,7 @@
 
 namespace xsymv {
 
-constexpr int AT_HD = 256;     // widest head
+constexpr int AT_LOW = 16, AT_HD = 256;  // least and widest head
 constexpr int AT_NARROW = 16;  // rows of a narrow job, and of a slab
 constexpr int AT_WIDE = 128;   // rows of a wide job
 constexpr int AT_TILE = 128;   // tokens of a tile
@@ -33,7 +33,7 @@ constexpr int AT_LEAST = AT_TILE * AT_WEIGHT;
 
 // Floats of a slab, the results of 16 rows in a part of a job: m and l of each,
 // then their out, not yet divided by l.
-__host__ __device__ inline size_t at_slab(int hd) { return (size_t)AT_NARROW * (2 + hd); }
+__host__ __device__ __forceinline__ size_t at_slab(int hd) { return (size_t)AT_NARROW * (2 + hd); }
 
 struct AtPlan {
     const int *start, *len, *table, *first, *shared;
@@ -46,13 +46,13 @@ struct AtPlan {
     long long* quota;
     long long *cost_at, *slab_at;
 
-    __device__ int entries() const { return groups + seqs; }
-    __device__ int length(int s) const
+    __device__ __forceinline__ int entries() const { return groups + seqs; }
+    __device__ __forceinline__ int length(int s) const
     {
         const long long room = min((long long)ldt * ps, 0x7fffff00ll);
         return (int)min((long long)max(len[s], 0), room);
     }
-    __device__ int row_of(int s) const { return start != nullptr ? min(max(start[s], 0), rows) : s; }
+    __device__ __forceinline__ int row_of(int s) const { return start != nullptr ? min(max(start[s], 0), rows) : s; }
 };
 
 struct AtEntry {
@@ -64,27 +64,27 @@ struct AtEntry {
     bool wide, group, joined;
     long long cost;  // of one head
 
-    __device__ int block_slabs() const { return wide ? AT_WIDE / AT_NARROW : 1; }
-    __device__ long long slabs() const { return joined ? (long long)blocks * block_slabs() : 0; }
+    __device__ __forceinline__ int block_slabs() const { return wide ? AT_WIDE / AT_NARROW : 1; }
+    __device__ __forceinline__ long long slabs() const { return joined ? (long long)blocks * block_slabs() : 0; }
     // costs of the blocks before block b
-    __device__ long long before_block(const AtPlan& p, long long b) const
+    __device__ __forceinline__ long long before_block(const AtPlan& p, long long b) const
     {
         if (p.whole) return b;
         if (!wide || group) return b * (AT_OVER + (long long)(t1 - t0) * (wide ? AT_WEIGHT : 1));
         const int step = (AT_WIDE + p.share - 1) / p.share;  // rows of q a block
         return b * (AT_OVER + (long long)AT_WEIGHT * max(before - t0, 0)) + AT_WEIGHT * step * (b * (b + 1) / 2);
     }
-    __device__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
+    __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
     // end of the tokens that block b sees
-    __device__ int end(const AtPlan& p, int b) const
+    __device__ __forceinline__ int end(const AtPlan& p, int b) const
     {
         if (group) return t1;
         const long long last = min((long long)(b + 1) * block_rows(), (long long)rows) - 1;
         return (int)min(max(before + last / p.share + 1, (long long)t0), (long long)t1);
     }
-    __device__ int tiles(const AtPlan& p, int b) const { return max(1, (end(p, b) - t0 + AT_TILE - 1) / AT_TILE); }
-    __device__ int tile_cost() const { return AT_TILE * (wide ? AT_WEIGHT : 1); }
-    __device__ void shape(const AtPlan& p)
+    __device__ __forceinline__ int tiles(const AtPlan& p, int b) const { return max(1, (end(p, b) - t0 + AT_TILE - 1) / AT_TILE); }
+    __device__ __forceinline__ int tile_cost() const { return AT_TILE * (wide ? AT_WEIGHT : 1); }
+    __device__ __forceinline__ void shape(const AtPlan& p)
     {
         wide = rows > AT_NARROW;
         blocks = (rows + block_rows() - 1) / block_rows();
@@ -97,7 +97,7 @@ struct AtEntry {
 struct AtGroup {
     int s0, s1, row0, rows, tokens;
     bool pays;
-    __device__ AtGroup(const AtPlan& p, int g)
+    __device__ __forceinline__ AtGroup(const AtPlan& p, int g)
     {
         s0 = min(max(p.first[g], 0), p.seqs);
         s1 = min(max(p.first[g + 1], s0), p.seqs);
@@ -112,14 +112,14 @@ struct AtGroup {
             pays = work(all) < count * work(one);
         }
     }
-    static __device__ long long work(long long rows)
+    static __device__ __forceinline__ long long work(long long rows)
     {
         return rows <= AT_NARROW ? 1 : (rows + AT_WIDE - 1) / AT_WIDE * AT_WEIGHT;
     }
 };
 
 // The group that sequence s reads its first tokens with, -1: none.
-__device__ inline int at_group(const AtPlan& p, int s, int& tokens)
+__device__ __forceinline__ int at_group(const AtPlan& p, int s, int& tokens)
 {
     tokens = 0;
     if (p.whole || p.groups == 0) return -1;
@@ -138,7 +138,7 @@ __device__ inline int at_group(const AtPlan& p, int s, int& tokens)
     return lo;
 }
 
-__device__ inline AtEntry at_entry(const AtPlan& p, int e)
+__device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
 {
     AtEntry x{};
     if (e < p.groups) {
@@ -171,14 +171,14 @@ struct AtJob {
     int head, rows, rho0, row0, end, before, table;
     bool wide, group;
     // row n's row and head of q
-    __device__ int place(const AtPlan& p, int n, size_t& row) const
+    __device__ __forceinline__ int place(const AtPlan& p, int n, size_t& row) const
     {
         const int rho = rho0 + n;
         row = (size_t)row0 + rho / p.share;
         return head * p.share + rho % p.share;
     }
     // tokens that row n sees
-    __device__ int limit(const AtPlan& p, int n) const
+    __device__ __forceinline__ int limit(const AtPlan& p, int n) const
     {
         const int at = (rho0 + n) / p.share;
         if (!group) return before + at + 1;
@@ -230,7 +230,7 @@ __device__ __forceinline__ long long at_uniform(long long v)
 }
 
 // An entry that all lanes have alike.
-__device__ inline AtEntry at_uniform(const AtEntry& x)
+__device__ __forceinline__ AtEntry at_uniform(const AtEntry& x)
 {
     AtEntry u;
     u.row0 = __builtin_amdgcn_readfirstlane(x.row0);
@@ -254,7 +254,7 @@ struct AtCursor {
     int worker, entry;
     AtEntry of;
 
-    __device__ AtCursor(const AtPlan& p, AtScan& scan)
+    __device__ __forceinline__ AtCursor(const AtPlan& p, AtScan& scan)
     {
         // workgroups of one die, which takes every eighth, have pieces side by side
         const int per = p.grid / 8;
@@ -331,7 +331,7 @@ struct AtCursor {
         settle(p);
     }
     // to the entry that holds pos
-    __device__ void settle(const AtPlan& p)
+    __device__ __forceinline__ void settle(const AtPlan& p)
     {
         while (entry + 1 < p.entries() && pos >= base + of.cost * p.kvheads) {
             base += of.cost * p.kvheads;
@@ -341,7 +341,7 @@ struct AtCursor {
     }
     // The next job with tiles in the piece: its tokens from `from` to `to`, and the
     // slab for its results (-1: they are whole, and go to out).
-    __device__ bool next(const AtPlan& p, AtJob& job, int& from, int& to, long long& part)
+    __device__ __forceinline__ bool next(const AtPlan& p, AtJob& job, int& from, int& to, long long& part)
     {
         while (pos < end) {
             settle(p);
@@ -400,7 +400,7 @@ struct AtParts {
     int kv, rho;  // rho: the entry's row of the first head
     bool some;
 
-    __device__ void set(const AtPlan& p, int e, int row, int head)
+    __device__ __forceinline__ void set(const AtPlan& p, int e, int row, int head)
     {
         plan = &p;
         of = at_entry(p, e);
@@ -411,17 +411,17 @@ struct AtParts {
         rho = (row - of.row0) * p.share;
         some = row >= of.row0 && rho < of.rows;
     }
-    __device__ int block(int h) const { return (rho + h) / of.block_rows(); }
-    __device__ int row(int h) const { return (rho + h) % of.block_rows(); }
+    __device__ __forceinline__ int block(int h) const { return (rho + h) / of.block_rows(); }
+    __device__ __forceinline__ int row(int h) const { return (rho + h) % of.block_rows(); }
     // the workgroups that the job's first and last tiles are taken by
-    __device__ void workers(int h, int& w0, int& w1) const
+    __device__ __forceinline__ void workers(int h, int& w0, int& w1) const
     {
         const int b = block(h);
         const long long at = base + kv * of.cost + of.before_block(*plan, b);
         w0 = (int)(at / quota);
         w1 = (int)((at + (long long)(of.tiles(*plan, b) - 1) * of.tile_cost()) / quota);
     }
-    __device__ int count(int h) const
+    __device__ __forceinline__ int count(int h) const
     {
         if (!some) return 0;
         int w0, w1;
@@ -429,7 +429,7 @@ struct AtParts {
         return w1 - w0 + 1;
     }
     // slab of part i of head h's job, -1: there is none
-    __device__ long long slab(int h, int i) const
+    __device__ __forceinline__ long long slab(int h, int i) const
     {
         int w0, w1;
         workers(h, w0, w1);
@@ -442,7 +442,7 @@ struct AtParts {
 
 // A row's parts: of its group's tokens, and of its own; false where the row has
 // none that are to be added.
-__device__ inline bool at_parts(const AtPlan& p, int row, int kv, AtParts (&parts)[2])
+__device__ __forceinline__ bool at_parts(const AtPlan& p, int row, int kv, AtParts (&parts)[2])
 {
     const int s = pg_sequence(p.start, p.seqs, row);
     if (s < 0) return false;

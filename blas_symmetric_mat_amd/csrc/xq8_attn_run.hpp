@@ -86,7 +86,7 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     if (rows < 0) return -1;
     if (heads < 1 || (kvheads >= 1 && heads % kvheads != 0)) return -2;
     if (kvheads < 1) return -3;
-    if (hd < 1 || hd > AT_HD) return -4;
+    if (hd < AT_LOW || hd > AT_HD) return -4;
     const long long wide = (long long)heads * hd;
     if (wide > 0x7fffffffll) return -2;
     const bool some = rows > 0 && (seqs > 0 || start == nullptr);

@@ -11,15 +11,15 @@ struct PgCache {
     int* refs;
     int seqs, ldt, pages, ps;
     // tokens of sequence s, as far as its row of the table can hold them
-    __device__ int length(int s) const
+    __device__ __forceinline__ int length(int s) const
     {
         const long long room = (long long)ldt * ps;
         const int n = __hip_atomic_load(&len[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         return n < 0 ? 0 : n > room ? (int)room : n;
     }
-    __device__ int* row(int s) const { return table + (size_t)s * ldt; }
-    __device__ bool is_page(int p) const { return (unsigned)p < (unsigned)pages; }
-    __device__ bool is_seq(int s) const { return (unsigned)s < (unsigned)seqs; }
+    __device__ __forceinline__ int* row(int s) const { return table + (size_t)s * ldt; }
+    __device__ __forceinline__ bool is_page(int p) const { return (unsigned)p < (unsigned)pages; }
+    __device__ __forceinline__ bool is_seq(int s) const { return (unsigned)s < (unsigned)seqs; }
 };
 
 // Sequence of row r of the calls that take `start`, -1 for none: the last one

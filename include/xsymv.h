@@ -478,7 +478,7 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   them, from 0): a row sees the tokens up to its own.  Head h of row r is at
  *   q[r * ldq + h * hd] and out[r * ldo + h * hd], and at lse[r * heads + h] (lse
  *   NULL: not kept).  Tokens whose page is outside [0, pages) are passed over; a
- *   row that sees none gets zeros and -infinity.  hd <= 256.
+ *   row that sees none gets zeros and -infinity.  16 <= hd <= 256.
  *   Sequences first[g] to first[g + 1] - 1 (groups + 1 ascending numbers from 0
  *   to seqs) have their first shared[g] tokens in common: their rows of the table
  *   name the same pages there, and these are read once for all of them where that
@@ -486,8 +486,8 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   (letters h and b) or 22 (s), sums in 32.  Uses the stream's workspace, up to
  *   xsymv_q8attn_workspace_bytes; where it cannot be had (as for the product
  *   above) the call is made without, in up to many times the time.
- *   Codes: -1 rows < 0, -2 heads < 1 or not a multiple of kvheads (or heads * hd
- *   over 2^31 - 1), -3 kvheads < 1, -4 hd < 1 or > 256, -5 q NULL, -6 ldq, -7
+ *   Codes: -1 rows < 0 (or rows * heads over 2^31 - 1), -2 heads < 1 or not a
+ *   multiple of kvheads (or heads * hd over 2^31 - 1), -3 kvheads < 1, -4 hd < 16 or > 256, -5 q NULL, -6 ldq, -7
  *   seqs < 0, or not rows without start, -9 len NULL, -10 table NULL, -11 ldt <
  *   0, -12 groups < 0, -13 first NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd,
  *   -17 ks NULL, -18 v NULL, -19 ldv < hd, -20 vs NULL, -21 pages < 0 or too many

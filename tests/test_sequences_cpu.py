@@ -22,7 +22,7 @@ GOOD = {
 BIG = 2147483647
 BAD = {
     "attn": [("rows", -1, -1), ("heads", 0, -2), ("heads", 7, -2), ("heads", 1 << 26, -2), ("kvheads", 0, -3),
-             ("hd", 0, -4), ("hd", 257, -4), ("q", None, -5), ("ldq", 511, -6), ("seqs", -1, -7), ("seqs", 2, -7),
+             ("hd", 15, -4), ("hd", 257, -4), ("rows", 1 << 29, -1), ("q", None, -5), ("ldq", 511, -6), ("seqs", -1, -7), ("seqs", 2, -7),
              ("len", None, -9), ("table", None, -10), ("ldt", -1, -11), ("groups", -1, -12), ("first", None, -13),
              ("shared", None, -14), ("k", None, -15), ("ldk", 63, -16), ("ks", None, -17), ("v", None, -18),
              ("ldv", 63, -19), ("vs", None, -20), ("pages", -1, -21), ("pages", BIG // 30, -21), ("ps", 0, -22),
