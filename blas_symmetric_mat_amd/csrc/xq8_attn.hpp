@@ -18,18 +18,18 @@
 // after a few tokens is rare, and sums stay in the lanes until the end.
 //
 // Work is cut into jobs: a block of rows of q (those of one sequence, or of a group
-// that shares tokens) with one head's keys over the tokens they see.  All jobs lie
-// in one line of costs, of which each workgroup takes an equal piece, so that
-// lengths may differ as they like: a piece may begin and end inside a job, whose
-// parts q8_attn_join adds (xq8_attn_plan.hpp has the arithmetic).  Each workgroup sums
-// the costs itself, which takes less than a launch.
+// that shares tokens) with one head's keys over the tokens they see.  Every worker
+// takes an equal piece of the jobs' costs, so that lengths may differ as they like:
+// a piece may begin and end inside a job, whose parts q8_attn_join adds
+// (xq8_attn_plan.hpp).  Each workgroup sums the costs itself, which takes less than a
+// launch.
 //
-//   narrow jobs (up to 16 rows of q: single tokens): each wave takes 32 tokens of
-//     128, codes come from memory to the registers that the instruction reads them
-//     from, and the waves' results are added in LDS.  Bound by the cache's bytes.
-//   wide jobs (up to 128 rows: a group's tokens, prompts): each wave has 16 or 32
-//     rows and every token; the waves make operands of 16 tokens each and share
-//     them through LDS, so that codes are converted once for 128 rows.
+//   narrow jobs (up to 16 rows of q: single tokens): a wave takes 32 tokens at a
+//     time, whose codes come from memory to the registers that the instruction reads
+//     them from.  Waves work by themselves.  Bound by the cache's bytes.
+//   wide jobs (up to 128 rows: a group's tokens, prompts): each wave of a workgroup
+//     has 16 or 32 rows and every token; the waves make operands of 16 tokens each
+//     and share them through LDS, so that codes are converted once for 128 rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -56,6 +56,7 @@ struct AttnArgs {
     float scale;  // times log2(e): scores are kept in units of log 2
     int ldq, ldk, ldv, ldo;
     float* slabs;  // parts of jobs (see AtPlan)
+    int per;       // of the join: rows and heads that a wave looks at
 };
 
 constexpr float AT_LN2 = 0.6931471805599453f;
@@ -309,6 +310,46 @@ __device__ __forceinline__ void at_lse(const AttnArgs<T>& a, size_t row, int hea
     if (a.lse != nullptr) a.lse[row * a.p.heads + head] = l == 0.0f ? -INFINITY : m * AT_LN2 + logf(l);
 }
 
+// One lane's codes of a row of results, times f.
+template <int HD, class O>
+__device__ __forceinline__ void at_write(const AtRows<HD>& r, const AtLanes<HD>& at, O* to, float f, int hd)
+{
+    constexpr int CB = HD / 16;
+    typedef O vec __attribute__((ext_vector_type(CB), aligned(sizeof(O))));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        vec v;
+#pragma unroll
+        for (int j = 0; j < CB; ++j) v[j] = (O)(r.o[j][i] * f);
+        *(vec*)(to + AtLanes<HD>::at_value(4 * at.g + i, hd)) = v;
+    }
+}
+
+// A tile of 16 rows, of which the lanes' is the job's row n, to out or to its part.
+template <class T, int HD>
+__device__ __forceinline__ void at_finish(const AttnArgs<T>& a, const AtJob& job, const AtLanes<HD>& at,
+                                          AtRows<HD>& r, const AtUnit& unit, int n, float* slab)
+{
+    const int hd = a.p.hd;
+    r.whole();
+    if (n >= job.rows) return;
+    const float f = r.l == 0.0f ? 0.0f : unit.unit * AT_DOWN;
+    if (slab != nullptr) {
+        float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
+        const int m = n % AT_NARROW;
+        if (at.g == 0) {
+            part[2 * m] = r.m;
+            part[2 * m + 1] = r.l;
+        }
+        at_write(r, at, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
+    } else {
+        size_t row;
+        const int head = job.place(a.p, n, row);
+        if (at.g == 0) at_lse(a, row, head, r.m, r.l);
+        at_write(r, at, a.out + row * a.ldo + (size_t)head * hd, r.l == 0.0f ? 0.0f : f / r.l, hd);
+    }
+}
+
 // ------------------------------------------------------------------- narrow
 // Rows of the cache, and scales, of a wave's 32 tokens.
 struct AtTokens {
@@ -318,12 +359,10 @@ struct AtTokens {
 
 template <class T, int HD>
 struct AtNarrow {
-    static constexpr int NK = HD / 64, CB = HD / 16, NV = CB / 4, STEP = 32;
+    static constexpr int NK = HD / 64, CB = HD / 16, NV = CB / 4, STEP = AT_TILE[0];
     static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
     struct Lds {
         AtTokens tokens[4][2];
-        float m[4][16], l[4][16], f[4][16];
-        float o[4][16][HD + 4];
     };
     struct Codes {  // of one step
         int k[2][NK][4], v[8][NV];
@@ -334,16 +373,16 @@ struct AtNarrow {
     const AttnArgs<T>& a;
     const AtJob& job;
     const AtLanes<HD>& at;
-    Lds& lds;
+    AtTokens (&lds)[2];
     const int* pages;  // the sequence's row of the table
-    int lane, wave, limit, least;
+    int lane, limit, least;
     AtQuery<T, HD> q;
     AtRows<HD> r;
     AtUnit unit;
 
     __device__ __forceinline__ int page_of(int t) const
     {
-        return lane < STEP && t < job.end ? pages[t / a.p.ps] : -1;
+        return lane < STEP && t < job.end ? pages[a.p.by_page.of(t)] : -1;
     }
     // rows of the step's tokens to LDS, and their codes and scales on their way
     __device__ __forceinline__ void fetch(Codes& c, AtTokens& tok, int base, int page)
@@ -351,7 +390,7 @@ struct AtNarrow {
         const int t = base + lane;
         int row = -1;
         if (lane < STEP && t < job.end && (unsigned)page < (unsigned)a.p.pages)
-            row = (page * a.p.kvheads + job.head) * a.p.ps + t % a.p.ps;
+            row = (page * a.p.kvheads + job.head) * a.p.ps + t - a.p.by_page.of(t) * a.p.ps;
         c.ok = __ballot(row >= 0);
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
@@ -434,101 +473,43 @@ struct AtNarrow {
             add(4 * d + 3, at_column<d, 3>(c.v));
         });
     }
-    // Tokens from `from` to `to` of the job: tiles of 128, 32 of each for a wave.
-    __device__ __forceinline__ void tokens(int from, int to)
+    // The job's tokens from `from` to `to`.
+    __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         r.clear();
-        const int first = from + wave * STEP;
-        const int count = first < to ? (to - first + AT_TILE - 1) / AT_TILE : 0;
-        if (count == 0) return;
+        const int count = (to - from + STEP - 1) / STEP;
         Codes c[2];
-        int page = page_of(first + lane);
-        fetch(c[0], lds.tokens[wave][0], first, page);
-        page = page_of(first + AT_TILE + lane);
+        int page = page_of(from + lane);
+        size_t row = 0;
+        const bool some = at.n < job.rows;
+        const int head = job.place(a.p, some ? at.n : 0, row);
+        if (count > 0) {
+            fetch(c[0], lds[0], from, page);
+            page = page_of(from + STEP + lane);
+        }
+        q.load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
+        limit = some ? job.limit(a.p, at.n) : 0x7fffffff;
+        least = at_least(limit);
         auto step = [&](Codes& now, Codes& next, AtTokens& tn, AtTokens& tx, int s) {
-            const int base = first + s * AT_TILE;
+            const int base = from + s * STEP;
             if (s + 1 < count) {
-                fetch(next, tx, base + AT_TILE, page);
-                page = page_of(base + 2 * AT_TILE + lane);
+                fetch(next, tx, base + STEP, page);
+                page = page_of(base + 2 * STEP + lane);
             }
             compute(now, tn, base);
         };
         for (int s = 0; s < count; s += 2) {
-            step(c[0], c[1], lds.tokens[wave][0], lds.tokens[wave][1], s);
-            if (s + 1 < count) step(c[1], c[0], lds.tokens[wave][1], lds.tokens[wave][0], s + 1);
+            step(c[0], c[1], lds[0], lds[1], s);
+            if (s + 1 < count) step(c[1], c[0], lds[1], lds[0], s + 1);
         }
-    }
-    // The waves' results together, to out or to the job's part.
-    __device__ __forceinline__ void finish(float* slab)
-    {
-        r.whole();
-        if (lane < 16) {
-            lds.m[wave][lane] = r.m;
-            lds.l[wave][lane] = r.l;
-        }
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lds.o[wave][at.n][(4 * at.g + i) * CB + j] = r.o[j][i];
-        __syncthreads();
-        float m = lds.m[0][at.n], l = 0.0f;
-        for (int w = 1; w < 4; ++w) m = fmaxf(m, lds.m[w][at.n]);
-        for (int w = 0; w < 4; ++w) l += lds.l[w][at.n] * __builtin_amdgcn_exp2f(lds.m[w][at.n] - m);
-        if (lane < 16) {
-            // each wave its own factor
-            const float f = __builtin_amdgcn_exp2f(r.m - m) * (unit.unit * AT_DOWN);
-            lds.f[wave][lane] = slab != nullptr ? f : l == 0.0f ? 0.0f : f / l;
-            if (wave == 0 && lane < job.rows) {
-                if (slab != nullptr) {
-                    slab[2 * lane] = m;
-                    slab[2 * lane + 1] = l;
-                } else {
-                    size_t row;
-                    const int head = job.place(a.p, lane, row);
-                    at_lse(a, row, head, m, l);
-                }
-            }
-        }
-        __syncthreads();
-        const int hd = a.p.hd;
-        for (int i = threadIdx.x; i < 16 * CB * 16; i += 256) {
-            const int n = i / (16 * CB), piece = i / CB % 16, j = i % CB;
-            const int d = AtLanes<HD>::at_value(piece, hd) + j;
-            // (a code that two pieces hold is written by the lower one)
-            if (n >= job.rows || d < piece * CB) continue;
-            float o = 0.0f;
-            for (int w = 0; w < 4; ++w) {
-                const float f = lds.f[w][n];
-                // (nothing times what is no number: of a wave without a token)
-                o += lds.l[w][n] == 0.0f ? 0.0f : f * lds.o[w][n][piece * CB + j];
-            }
-            if (slab != nullptr) {
-                slab[2 * AT_NARROW + (size_t)n * hd + d] = o;
-            } else {
-                size_t row;
-                const int head = job.place(a.p, n, row);
-                a.out[row * a.ldo + (size_t)head * hd + d] = (T)o;
-            }
-        }
-        __syncthreads();
-    }
-    __device__ __forceinline__ void run(int from, int to, float* slab)
-    {
-        size_t row = 0;
-        const bool some = at.n < job.rows;
-        const int head = job.place(a.p, some ? at.n : 0, row);
-        q.load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
-        limit = some ? job.limit(a.p, at.n) : 0x7fffffff;
-        least = at_least(limit);
-        tokens(from, to);
-        finish(slab);
+        at_finish(a, job, at, r, unit, at.n, slab);
     }
 };
 
 // --------------------------------------------------------------------- wide
 template <class T, int HD>
 struct AtWide {
-    static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4, STEP = 64;
+    static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4, STEP = AT_TILE[1];
     static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
     struct Step {
         at_h8 k[4][NF][64];     // keys of 16 tokens each, as the lanes read them
@@ -558,14 +539,14 @@ struct AtWide {
     AtUnit unit;
     int limit[2], least, most;
 
-    __device__ __forceinline__ int page_of(int t) const { return t < job.end ? pages[t / a.p.ps] : -1; }
+    __device__ __forceinline__ int page_of(int t) const { return t < job.end ? pages[a.p.by_page.of(t)] : -1; }
 
     __device__ __forceinline__ void fetch(Codes& c, int base, int page)
     {
         const int t = base + wave * 16 + at.n;
         int row = -1;
         if (t < job.end && (unsigned)page < (unsigned)a.p.pages)
-            row = (page * a.p.kvheads + job.head) * a.p.ps + t % a.p.ps;
+            row = (page * a.p.kvheads + job.head) * a.p.ps + t - a.p.by_page.of(t) * a.p.ps;
         c.ok = row >= 0;
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
@@ -693,45 +674,6 @@ struct AtWide {
                 if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
     }
-    __device__ __forceinline__ void finish(float* slab)
-    {
-        one(r[0], 0, slab);
-        if (tiles == 2) one(r[1], 1, slab);
-    }
-    __device__ __forceinline__ void one(AtRows<HD>& t, int i, float* slab)
-    {
-        const int hd = a.p.hd, n = first + 16 * i + at.n;
-        t.whole();
-        if (n >= job.rows) return;
-        const float f = t.l == 0.0f ? 0.0f : unit.unit * AT_DOWN;
-        if (slab != nullptr) {
-            float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
-            const int m = n % AT_NARROW;
-            if (at.g == 0) {
-                part[2 * m] = t.m;
-                part[2 * m + 1] = t.l;
-            }
-            write(t, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
-        } else {
-            size_t row;
-            const int head = job.place(a.p, n, row);
-            if (at.g == 0) at_lse(a, row, head, t.m, t.l);
-            write(t, a.out + row * a.ldo + (size_t)head * hd, t.l == 0.0f ? 0.0f : f / t.l, hd);
-        }
-    }
-    template <class O>
-    __device__ __forceinline__ void write(const AtRows<HD>& t, O* to, float f, int hd)
-    {
-        typedef O vec __attribute__((ext_vector_type(CB), aligned(sizeof(O))));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = AtLanes<HD>::at_value(4 * at.g + i, hd);
-            vec v;
-#pragma unroll
-            for (int j = 0; j < CB; ++j) v[j] = (O)(t.o[j][i] * f);
-            *(vec*)(to + d) = v;
-        }
-    }
     __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         // few rows are dealt 16 to a wave, so that all waves have some
@@ -771,7 +713,8 @@ struct AtWide {
                 }
             }
         }
-        finish(slab);
+        at_finish(a, job, at, r[0], unit, first + at.n, slab);
+        if (tiles == 2) at_finish(a, job, at, r[1], unit, first + 16 + at.n, slab);
         __syncthreads();
     }
 };
@@ -781,107 +724,124 @@ struct AtWide {
 template <class T, int HD>
 constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
 
-template <class T, int HD>
+template <class T, int HD, bool MIXED>
 __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T> a)
 {
-    __shared__ AtScan scan;
-    __shared__ union {
+    struct Narrow {
+        typename AtNarrow<T, HD>::Lds narrow;
+    };
+    union Both {
         typename AtNarrow<T, HD>::Lds narrow;
         typename AtWide<T, HD>::Lds wide;
-    } lds;
+    };
+    __shared__ AtScan scan;
+    __shared__ typename std::conditional<MIXED, Both, Narrow>::type lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AtLanes<HD> at(a.p.hd);
-    AtCursor cursor(a.p, scan);
+    // workgroups of one die, which takes every eighth, have pieces side by side
+    const int per = a.p.grid / 8, b = (int)blockIdx.x;
+    const int worker = a.p.grid % 8 == 0 ? b % 8 * per + b / 8 : b;
+    at_scan<MIXED>(a.p, scan);
     AtJob job;
     int from, to;
     long long slab;
-    while (cursor.next(a.p, job, from, to, slab)) {
-        float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
-        const int* pages = a.p.table + (size_t)job.table * a.p.ldt;
-        if (job.wide) {
-            AtWide<T, HD> w{a, job, at, lds.wide, pages, lane, wave};
-            w.run(from, to, part);
-        } else {
-            AtNarrow<T, HD> w{a, job, at, lds.narrow, pages, lane, wave};
+    if constexpr (MIXED) {
+        AtCursor<MIXED, true> cursor(a.p, scan, worker, a.p.grid);
+        while (cursor.next(a.p, job, from, to, slab)) {
+            float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
+            AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
             w.run(from, to, part);
         }
     }
+    AtCursor<MIXED, false> cursor(a.p, scan, worker * 4 + wave, a.p.grid * 4);
+    while (cursor.next(a.p, job, from, to, slab)) {
+        float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
+        AtNarrow<T, HD> w{a, job, at, lds.narrow.tokens[wave], a.p.table + (size_t)job.table * a.p.ldt, lane};
+        w.run(from, to, part);
+    }
 }
 
-// Adds the parts of each row's jobs.  A workgroup has a few rows' heads of one
-// head's keys, of which it looks at all at once for those with something to add;
-// parts go to its waves in turn.
-template <class T>
-struct AttnJoinArgs {
-    AttnArgs<T> a;
-    int per;  // rows' heads of keys of a workgroup, 64 at most
-};
-
-template <class T>
-__global__ __launch_bounds__(256) void q8_attn_join(AttnJoinArgs<T> j_)
+// Adds the parts of rows' results.  A wave looks at `per` rows and heads at once for
+// those that have parts; WAVES waves share the parts of each.
+template <class T, int WAVES>
+__global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
 {
-    const AttnArgs<T>& a = j_.a;
-    const int per = j_.per;
-    __shared__ float sums[4][AT_HD + 2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd, share = a.p.share;
-    const long long all = (long long)a.p.rows * a.p.kvheads, first = (long long)blockIdx.x * per;
-    AtParts parts[2];
-    unsigned long long todo = __ballot(
-        lane < per && first + lane < all &&
-        at_parts(a.p, (int)((first + lane) / a.p.kvheads), (int)((first + lane) % a.p.kvheads), parts));
-    for (; todo != 0; todo &= todo - 1) {
-        const long long item = first + __ffsll(todo) - 1;
-        const int row = (int)(item / a.p.kvheads), kv = (int)(item % a.p.kvheads);
-        at_parts(a.p, row, kv, parts);
-        for (int h = 0; h < share; ++h) {
-            if (!parts[1].of.joined && parts[1].count(h) == 1) continue;
-            float m = AT_LOWEST, l = 0.0f, o[AT_HD / 64] = {};
-            for (int j = 0; j < 2; ++j) {
-                const AtParts& p = parts[j];
-                const int count = p.count(h);
-                for (int i = wave; i < count; i += 4) {
-                    const int n = p.row(h) % AT_NARROW;
-                    const long long at = p.slab(h, i);
-                    if (at < 0) continue;
-                    const float* s = a.slabs + at * at_slab(hd);
-                    const float pm = s[2 * n], pl = s[2 * n + 1];
-                    float v[AT_HD / 64];
+    constexpr int NE = AT_HD / 64, U = 4;
+    __shared__ float sums[WAVES > 1 ? 4 : 1][AT_HD + 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd, mine = WAVES > 1 ? wave : 0;
+    const long long all = (long long)a.p.rows * a.p.heads;
+    const long long first = ((long long)blockIdx.x * (4 / WAVES) + (WAVES > 1 ? 0 : wave)) * a.per, at = first + lane;
+    int2 own{0, 0}, shared{0, 0};
+    if (lane < a.per && at < all) {
+        own = a.p.own[at];
+        if (a.p.groups > 0) shared = a.p.shared_parts[at];
+        if (a.p.start != nullptr) {
+            // rows outside the sequences hold what an earlier call left there
+            const long long row = at / a.p.heads;
+            if (row < a.p.start[0] || row >= a.p.start[a.p.seqs]) own.y = 0;
+        }
+    }
+    if (!(own.y >> 24 & 1)) shared.y = 0;
+    for (unsigned long long todo = __ballot(own.y != 0); todo != 0; todo &= todo - 1) {
+        const int from = __builtin_ctzll(todo);
+        const size_t item = first + from, row = item / a.p.heads;
+        const int head = (int)(item % a.p.heads);
+        float m = AT_LOWEST, l = 0.0f, o[NE] = {};
+        auto add = [&](int2 where) {
+            const int count = where.y & 0xffff, n = where.y >> 16 & 15;
+            const long long last = a.p.slabs - 1;
+            auto slab = [&](int i) { return a.slabs + min(max(at_part(where, i), 0ll), last) * at_slab(hd); };
+            for (int base = mine; base < count; base += WAVES * U) {
+                float pm[U], pl[U], v[U][NE];
 #pragma unroll
-                    for (int e = 0; e < AT_HD / 64; ++e)
-                        v[e] = lane + 64 * e < hd ? s[2 * AT_NARROW + (size_t)n * hd + lane + 64 * e] : 0.0f;
-                    if (pl == 0.0f) continue;
-                    const float to = fmaxf(m, pm);
-                    const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
+                for (int u = 0; u < U; ++u) {
+                    const int i = base + u * WAVES;
+                    const float* s = slab(min(i, count - 1));
+                    pm[u] = i < count ? s[2 * n] : AT_LOWEST;
+                    pl[u] = i < count ? s[2 * n + 1] : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < NE; ++e)
+                        v[u][e] = lane + 64 * e < hd ? s[2 * AT_NARROW + (size_t)n * hd + lane + 64 * e] : 0.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float to = fmaxf(m, pm[u]);
+                    const float f = __builtin_amdgcn_exp2f(m - to);
+                    // (a part without tokens, or none: what its place holds does not count)
+                    const float g = pl[u] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm[u] - to);
                     m = to;
-                    l = l * f + pl * g;
+                    l = l * f + pl[u] * g;
 #pragma unroll
-                    for (int e = 0; e < AT_HD / 64; ++e) o[e] = o[e] * f + v[e] * g;
+                    for (int e = 0; e < NE; ++e) o[e] = o[e] * f + (pl[u] == 0.0f ? 0.0f : v[u][e] * g);
                 }
             }
+        };
+        add(make_int2(at_lane(own.x, from), at_lane(own.y, from)));
+        add(make_int2(at_lane(shared.x, from), at_lane(shared.y, from)));
+        if constexpr (WAVES > 1) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < AT_HD / 64; ++e)
-                if (lane + 64 * e < hd) sums[wave][lane + 64 * e] = o[e];
+            for (int e = 0; e < NE; ++e) sums[wave][lane + 64 * e] = o[e];
             if (lane == 0) {
                 sums[wave][AT_HD] = m;
                 sums[wave][AT_HD + 1] = l;
             }
             __syncthreads();
-            float most = sums[0][AT_HD], total = 0.0f;
-            for (int w = 1; w < 4; ++w) most = fmaxf(most, sums[w][AT_HD]);
-            float f[4];
-            for (int w = 0; w < 4; ++w) {
-                f[w] = __builtin_amdgcn_exp2f(sums[w][AT_HD] - most);
-                total += sums[w][AT_HD + 1] * f[w];
+            if (wave != 0) continue;
+            for (int w = 1; w < WAVES; ++w) {
+                const float pm = sums[w][AT_HD], to = fmaxf(m, pm);
+                const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
+                m = to;
+                l = l * f + sums[w][AT_HD + 1] * g;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) o[e] = o[e] * f + sums[w][lane + 64 * e] * g;
             }
-            const int head = kv * share + h;
-            for (int d = threadIdx.x; d < hd; d += 256) {
-                float v = 0.0f;
-                for (int w = 0; w < 4; ++w) v += sums[w][d] * f[w];
-                a.out[(size_t)row * a.ldo + (size_t)head * hd + d] = (T)(total == 0.0f ? 0.0f : v / total);
-            }
-            if (threadIdx.x == 0) at_lse(a, (size_t)row, head, most, total);
         }
+        T* out = a.out + row * a.ldo + (size_t)head * hd;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (lane + 64 * e < hd) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
+        if (lane == 0) at_lse(a, row, head, m, l);
     }
 }
 

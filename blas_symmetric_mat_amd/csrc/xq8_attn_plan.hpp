@@ -7,12 +7,16 @@
 // the `share` heads of q that read the same keys; blocks are of 16 rows where an
 // entry has no more (narrow), else of 128 (wide).
 //
-// Jobs lie one after the other in a line of costs (entries, heads, blocks), of
-// which every workgroup takes AtPlan's quota.  A job's tiles of 128 tokens lie in
-// its costs from the start; a tile is taken by the workgroup in whose piece it
-// begins.  Costs need not be exact, only the same wherever they are computed: the
-// kernel's workgroups and the join each do that from the arrays on the device, so
-// that a captured call follows them.
+// There are two lines of jobs, one after the other by entry, head and block, each
+// with a cost in tokens: wide jobs, of which every workgroup takes an equal piece,
+// and narrow ones, of which every wave does.  A job's tiles (32 tokens of a narrow
+// job, 64 of a wide one) lie in its costs from the start; a tile is taken by the
+// worker in whose piece it begins.  Costs need not be exact, only the same for all
+// workers, which compute them from the arrays on the device, so that a captured call
+// follows what these hold.
+//
+// Who takes a job's first tile writes down, for each of its rows, where the parts of
+// its results are; the join reads that.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,38 +26,65 @@
 namespace xsymv {
 
 constexpr int AT_LOW = 16, AT_HD = 256;  // least and widest head
-constexpr int AT_NARROW = 16;  // rows of a narrow job, and of a slab
-constexpr int AT_WIDE = 128;   // rows of a wide job
-constexpr int AT_TILE = 128;   // tokens of a tile
-// Costs in tokens of a narrow job: those of a wide one, and of a job besides.
-constexpr int AT_WEIGHT = 2, AT_OVER = 64;
-// A workgroup's piece is a wide tile at least, so that each has one of every job
-// that it is in the middle of.
-constexpr int AT_LEAST = AT_TILE * AT_WEIGHT;
+constexpr int AT_NARROW = 16;            // rows of a narrow job, and of a slab
+constexpr int AT_WIDE = 128;             // rows of a wide job
+constexpr int AT_SLABS = AT_WIDE / AT_NARROW;
+constexpr int AT_TILE[2] = {32, 64};  // tokens of a narrow and of a wide tile
+constexpr int AT_OVER = 48;           // cost of a job besides its tokens
+// A piece is two tiles at least: so that each worker has one of every job that it is
+// in the middle of, and for the join's sake.
+constexpr int AT_LEAST[2] = {64, 128};
 
 // Floats of a slab, the results of 16 rows in a part of a job: m and l of each,
 // then their out, not yet divided by l.
-__host__ __device__ __forceinline__ size_t at_slab(int hd) { return (size_t)AT_NARROW * (2 + hd); }
+__host__ __device__ inline size_t at_slab(int hd) { return (size_t)AT_NARROW * (2 + hd); }
+
+// Quotients of numbers below 2^31 by one that the host knows.
+struct AtDivisor {
+    unsigned d, mul, shift;
+    AtDivisor(int by = 1)
+    {
+        d = (unsigned)by;
+        shift = 0;
+        while (((unsigned long long)1 << shift) < d) ++shift;
+        mul = (unsigned)((((unsigned long long)1 << 32) * (((unsigned long long)1 << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const
+    {
+        return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+    }
+};
 
 struct AtPlan {
     const int *start, *len, *table, *first, *shared;
     int rows, heads, kvheads, share, hd, seqs, ldt, groups, pages, ps;
-    int grid;    // workgroups
-    int whole;   // no job is cut, nothing is shared: no workspace
-    int blocks;  // slabs of a part of a cut job: 8, or 1 where no job is wide
-    long long slabs;  // of the workspace; what starts that do not ascend would have beyond is left out
-    // workspace: the quota, and where each entry's costs and whole parts begin
-    long long* quota;
-    long long *cost_at, *slab_at;
+    AtDivisor by_share, by_page;
+    int grid;   // workgroups
+    int whole;  // no job is cut, nothing is shared: no workspace
+    // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
+    // narrow ones', two a wave; of whole parts) and, for each row and head, where its
+    // own parts and its group's are.
+    long long slabs, narrow_at, whole_at;
+    int2 *own, *shared_parts;
 
     __device__ __forceinline__ int entries() const { return groups + seqs; }
-    __device__ __forceinline__ int length(int s) const
+    __device__ __forceinline__ int room() const { return (int)min((long long)ldt * ps, 0x7fffff00ll); }
+    __device__ __forceinline__ int length(int s) const { return min(max(len[s], 0), room()); }
+    __device__ __forceinline__ int row_of(int s) const
     {
-        const long long room = min((long long)ldt * ps, 0x7fffff00ll);
-        return (int)min((long long)max(len[s], 0), room);
+        return start != nullptr ? min(max(start[s], 0), rows) : s;
     }
-    __device__ __forceinline__ int row_of(int s) const { return start != nullptr ? min(max(start[s], 0), rows) : s; }
 };
+
+// Floor of a / b for 0 <= a < 2^62, b > 0 and a quotient that an int holds: a
+// division in 32-bit floating point, put right.
+__device__ __forceinline__ int at_quotient(long long a, long long b)
+{
+    int q = (int)fminf((float)a / (float)b, 2.1e9f);
+    while ((long long)q * b > a) --q;
+    while ((long long)(q + 1) * b <= a) ++q;
+    return q;
+}
 
 struct AtEntry {
     int row0, rows;  // the first row of q; rows of the entry
@@ -61,34 +92,26 @@ struct AtEntry {
     int before;      // tokens before the first row's own (a sequence's)
     int table;       // the row of the table that is read
     int blocks;
-    bool wide, group, joined;
+    int wide, group, joined;
     long long cost;  // of one head
 
-    __device__ __forceinline__ int block_slabs() const { return wide ? AT_WIDE / AT_NARROW : 1; }
+    __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
+    __device__ __forceinline__ int block_slabs() const { return wide ? AT_SLABS : 1; }
     __device__ __forceinline__ long long slabs() const { return joined ? (long long)blocks * block_slabs() : 0; }
     // costs of the blocks before block b
-    __device__ __forceinline__ long long before_block(const AtPlan& p, long long b) const
+    __device__ __forceinline__ long long before_block(const AtPlan& p, int b) const
     {
         if (p.whole) return b;
-        if (!wide || group) return b * (AT_OVER + (long long)(t1 - t0) * (wide ? AT_WEIGHT : 1));
-        const int step = (AT_WIDE + p.share - 1) / p.share;  // rows of q a block
-        return b * (AT_OVER + (long long)AT_WEIGHT * max(before - t0, 0)) + AT_WEIGHT * step * (b * (b + 1) / 2);
+        if (!wide || group) return (long long)b * (AT_OVER + t1 - t0);
+        const int step = p.by_share.of(AT_WIDE + p.share - 1);  // rows of q a block
+        return (long long)b * (AT_OVER + max(before - t0, 0)) + step * ((long long)b * (b + 1) / 2);
     }
-    __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
     // end of the tokens that block b sees
     __device__ __forceinline__ int end(const AtPlan& p, int b) const
     {
         if (group) return t1;
-        const long long last = min((long long)(b + 1) * block_rows(), (long long)rows) - 1;
-        return (int)min(max(before + last / p.share + 1, (long long)t0), (long long)t1);
-    }
-    __device__ __forceinline__ int tiles(const AtPlan& p, int b) const { return max(1, (end(p, b) - t0 + AT_TILE - 1) / AT_TILE); }
-    __device__ __forceinline__ int tile_cost() const { return AT_TILE * (wide ? AT_WEIGHT : 1); }
-    __device__ __forceinline__ void shape(const AtPlan& p)
-    {
-        wide = rows > AT_NARROW;
-        blocks = (rows + block_rows() - 1) / block_rows();
-        cost = blocks == 0 ? 0 : before_block(p, blocks);
+        const int last = (int)min((long long)(b + 1) * block_rows(), (long long)rows) - 1;
+        return min(max(before + p.by_share.of(last) + 1, t0), t1);
     }
 };
 
@@ -101,28 +124,27 @@ struct AtGroup {
     {
         s0 = min(max(p.first[g], 0), p.seqs);
         s1 = min(max(p.first[g + 1], s0), p.seqs);
-        const long long room = min((long long)p.ldt * p.ps, 0x7fffff00ll);
-        tokens = (int)min((long long)max(p.shared[g], 0), room);
+        tokens = min(max(p.shared[g], 0), p.room());
         row0 = p.row_of(s0);
         rows = max(p.row_of(s1) - row0, 0);
         const int count = s1 - s0;
         pays = false;
         if (tokens > 0 && count > 1 && rows > 0) {
-            const long long one = ((long long)rows + count - 1) / count * p.share, all = (long long)rows * p.share;
-            pays = work(all) < count * work(one);
+            const long long one = (long long)((rows + count - 1) / count) * p.share;
+            pays = work((long long)rows * p.share) < count * work(one);
         }
     }
+    // a wide tile of tokens takes about as long as two narrow ones
     static __device__ __forceinline__ long long work(long long rows)
     {
-        return rows <= AT_NARROW ? 1 : (rows + AT_WIDE - 1) / AT_WIDE * AT_WEIGHT;
+        return rows <= AT_NARROW ? 1 : (rows + AT_WIDE - 1) / AT_WIDE * 2;
     }
 };
 
-// The group that sequence s reads its first tokens with, -1: none.
-__device__ __forceinline__ int at_group(const AtPlan& p, int s, int& tokens)
+// The tokens that sequence s reads with its group, 0: none.
+__device__ __forceinline__ int at_shared(const AtPlan& p, int s)
 {
-    tokens = 0;
-    if (p.whole || p.groups == 0) return -1;
+    if (p.whole || p.groups == 0) return 0;
     int lo = 0, hi = p.groups;  // the last group that begins at or before s
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
@@ -131,18 +153,18 @@ __device__ __forceinline__ int at_group(const AtPlan& p, int s, int& tokens)
         else
             hi = mid;
     }
-    if (lo >= p.groups) return -1;
+    if (lo >= p.groups) return 0;
     const AtGroup g(p, lo);
-    if (!g.pays || s < g.s0 || s >= g.s1) return -1;
-    tokens = g.tokens;
-    return lo;
+    return g.pays && s >= g.s0 && s < g.s1 ? g.tokens : 0;
 }
 
+// MIXED: the call has groups, several rows a sequence or many heads that share keys.
+template <bool MIXED>
 __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
 {
     AtEntry x{};
-    if (e < p.groups) {
-        x.group = x.joined = true;
+    if (MIXED && e < p.groups) {
+        x.group = x.joined = 1;
         if (!p.whole) {
             const AtGroup g(p, e);
             if (g.pays) {
@@ -152,35 +174,42 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
                 x.table = g.s0;
             }
         }
-    } else {
+    } else if (MIXED) {
         const int s = e - p.groups, from = p.row_of(s), count = max(p.row_of(s + 1) - from, 0);
         const int len = p.length(s);
         x.row0 = from;
         x.rows = count * p.share;
-        x.joined = at_group(p, s, x.t0) >= 0;
+        x.t0 = at_shared(p, s);
+        x.joined = x.t0 > 0;
         x.t1 = max(len, x.t0);
         x.before = len - count;
         x.table = s;
+    } else {
+        x.row0 = x.table = e;
+        x.rows = p.share;
+        x.t1 = p.length(e);
+        x.before = x.t1 - 1;
     }
-    x.shape(p);
+    x.wide = MIXED && x.rows > AT_NARROW;
+    x.blocks = x.wide ? (x.rows + AT_WIDE - 1) / AT_WIDE : x.rows > 0;
+    x.cost = x.blocks == 0 ? 0 : x.before_block(p, x.blocks);
     return x;
 }
 
 // A piece of work: rows of an entry, a head of keys.
 struct AtJob {
-    int head, rows, rho0, row0, end, before, table;
-    bool wide, group;
+    int head, rows, rho0, row0, end, before, table, group;
     // row n's row and head of q
     __device__ __forceinline__ int place(const AtPlan& p, int n, size_t& row) const
     {
-        const int rho = rho0 + n;
-        row = (size_t)row0 + rho / p.share;
-        return head * p.share + rho % p.share;
+        const int rho = rho0 + n, at = p.by_share.of(rho);
+        row = (size_t)row0 + at;
+        return head * p.share + rho - at * p.share;
     }
     // tokens that row n sees
     __device__ __forceinline__ int limit(const AtPlan& p, int n) const
     {
-        const int at = (rho0 + n) / p.share;
+        const int at = p.by_share.of(rho0 + n);
         if (!group) return before + at + 1;
         const int row = row0 + at, s = pg_sequence(p.start, p.seqs, row);
         if (s < 0) return 0;
@@ -189,7 +218,7 @@ struct AtJob {
 };
 
 struct AtScan {
-    long long cost[257], slab[257], wave_cost[4], wave_slab[4];
+    long long cost[2][257], slab[257], wave[3][4];
 };
 
 // Least and largest of a number that lanes n, n + 16, ... have alike.
@@ -223,240 +252,210 @@ __device__ __forceinline__ void at_each(F&& f)
         at_each<N, I + 1>(f);
     }
 }
-__device__ __forceinline__ long long at_uniform(long long v)
+// Lane `from`'s number, the same for all.
+__device__ __forceinline__ int at_lane(int v, int from) { return __builtin_amdgcn_readlane(v, from); }
+__device__ __forceinline__ long long at_lane(long long v, int from)
 {
-    const int lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    const int lo = __builtin_amdgcn_readlane((int)v, from), hi = __builtin_amdgcn_readlane((int)(v >> 32), from);
     return (long long)hi << 32 | (unsigned)lo;
 }
-
-// An entry that all lanes have alike.
-__device__ __forceinline__ AtEntry at_uniform(const AtEntry& x)
+// Sums of the lanes up to and with this one.
+__device__ __forceinline__ long long at_sums(long long v, int lane)
 {
-    AtEntry u;
-    u.row0 = __builtin_amdgcn_readfirstlane(x.row0);
-    u.rows = __builtin_amdgcn_readfirstlane(x.rows);
-    u.t0 = __builtin_amdgcn_readfirstlane(x.t0);
-    u.t1 = __builtin_amdgcn_readfirstlane(x.t1);
-    u.before = __builtin_amdgcn_readfirstlane(x.before);
-    u.table = __builtin_amdgcn_readfirstlane(x.table);
-    u.blocks = __builtin_amdgcn_readfirstlane(x.blocks);
-    u.wide = __builtin_amdgcn_readfirstlane(x.wide);
-    u.group = __builtin_amdgcn_readfirstlane(x.group);
-    u.joined = __builtin_amdgcn_readfirstlane(x.joined);
-    u.cost = at_uniform(x.cost);
-    return u;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long long o = __shfl_up(v, d, 64);
+        v += lane >= d ? o : 0;
+    }
+    return v;
 }
 
-// A workgroup's way through its piece of the line.
+// The lines' costs, by the whole workgroup: 256 stretches of entries.
+template <bool MIXED>
+__device__ __forceinline__ void at_scan(const AtPlan& p, AtScan& scan)
+{
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int entries = p.entries(), chunk = (entries + 255) / 256;
+    long long v[3] = {0, 0, 0};  // narrow, wide, slabs
+    for (int e = t * chunk; e < min((t + 1) * chunk, entries); ++e) {
+        const AtEntry x = at_entry<MIXED>(p, e);
+        const long long cost = x.cost * p.kvheads;
+        v[0] += x.wide ? 0 : cost;
+        if (MIXED) {
+            v[1] += x.wide ? cost : 0;
+            v[2] += x.slabs() * p.kvheads;
+        }
+    }
+    constexpr int N = MIXED ? 3 : 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = at_sums(v[i], lane);
+        if (lane == 63) scan.wave[i][wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        for (int w = 0; w < wave; ++w) v[i] += scan.wave[i][w];
+    scan.cost[0][t + 1] = v[0];
+    if (MIXED) {
+        scan.cost[1][t + 1] = v[1];
+        scan.slab[t + 1] = v[2];
+    }
+    if (t == 0) scan.cost[0][0] = scan.cost[1][0] = scan.slab[0] = 0;
+    __syncthreads();
+}
+
+// A worker's way through its piece of a line: a wave's (narrow jobs) or a
+// workgroup's (wide ones).
+template <bool MIXED, bool WIDE>
 struct AtCursor {
+    static constexpr int TILE = AT_TILE[WIDE];
     long long pos, end, quota;
     long long base, slab;  // where the entry's costs, and its whole parts, begin
     int worker, entry;
     AtEntry of;
 
-    __device__ __forceinline__ AtCursor(const AtPlan& p, AtScan& scan)
+    __device__ __forceinline__ AtCursor(const AtPlan& p, const AtScan& scan, int worker_, int workers)
     {
-        // workgroups of one die, which takes every eighth, have pieces side by side
-        const int per = p.grid / 8;
-        worker = p.grid % 8 == 0 ? (int)(blockIdx.x % 8) * per + (int)blockIdx.x / 8 : (int)blockIdx.x;
-        const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-        const int entries = p.entries(), chunk = (entries + 255) / 256;
-        long long cost = 0;
-        long long slabs = 0;
-        for (int e = t * chunk; e < min((t + 1) * chunk, entries); ++e) {
-            const AtEntry x = at_entry(p, e);
-            cost += x.cost * p.kvheads;
-            slabs += x.slabs() * p.kvheads;
-        }
-        long long c = cost;
-        long long s = slabs;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const long long oc = __shfl_up(c, d, 64);
-            const long long os = __shfl_up(s, d, 64);
-            if (lane >= d) {
-                c += oc;
-                s += os;
-            }
-        }
-        if (lane == 63) {
-            scan.wave_cost[wave] = c;
-            scan.wave_slab[wave] = s;
-        }
-        __syncthreads();
-        for (int w = 0; w < wave; ++w) {
-            c += scan.wave_cost[w];
-            s += scan.wave_slab[w];
-        }
-        scan.cost[t + 1] = c;
-        scan.slab[t + 1] = s;
-        if (t == 0) {
-            scan.cost[0] = 0;
-            scan.slab[0] = 0;
-        }
-        __syncthreads();
-        const long long total = at_uniform(scan.cost[256]);
-        quota = (total + p.grid - 1) / p.grid;
-        if (!p.whole) {
-            quota = max(quota, (long long)AT_LEAST);
-            if (blockIdx.x == 0) {  // for the join
-                if (t == 0) p.quota[0] = quota;
-                long long at = c - cost;
-                long long sl = s - slabs;
-                for (int e = t * chunk; e < min((t + 1) * chunk, entries); ++e) {
-                    const AtEntry x = at_entry(p, e);
-                    p.cost_at[e] = at;
-                    p.slab_at[e] = sl;
-                    at += x.cost * p.kvheads;
-                    sl += x.slabs() * p.kvheads;
-                }
-            }
-        }
+        worker = worker_;
+        const int lane = threadIdx.x & 63;
+        const long long total = at_lane(scan.cost[WIDE][256], 0);
+        // a little more than total / workers, which need not be exact
+        quota = (long long)((float)total / (float)workers * 1.000001f) + 1;
+        if (!p.whole) quota = max(quota, (long long)AT_LEAST[WIDE]);
         pos = worker * quota;
         end = min(pos + quota, total);
+        of.cost = 0;
+        base = slab = 0;
+        entry = 0;
         if (pos >= end) return;
-        int lo = 0, hi = 255;  // the last chunk that begins at or before pos
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (scan.cost[mid] <= pos)
-                lo = mid;
-            else
-                hi = mid - 1;
+        // the last stretch that begins at or before pos: of 256, four to a lane
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned long long at = __ballot(scan.cost[WIDE][64 * i + lane] <= pos);
+            if (at != 0) last = 64 * i + 63 - __builtin_clzll(at);
         }
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        base = at_uniform(scan.cost[lo]);
-        slab = at_uniform(scan.slab[lo]);
-        entry = lo * chunk;
-        of = at_uniform(at_entry(p, entry));
-        settle(p);
+        const int chunk = (p.entries() + 255) / 256;
+        base = at_lane(scan.cost[WIDE][last], 0);
+        if (MIXED) slab = at_lane(scan.slab[last], 0);
+        entry = last * chunk;
     }
-    // to the entry that holds pos
-    __device__ __forceinline__ void settle(const AtPlan& p)
+    // To the entry that holds pos; each lane looks at one.
+    __device__ __forceinline__ bool settle(const AtPlan& p)
     {
-        while (entry + 1 < p.entries() && pos >= base + of.cost * p.kvheads) {
-            base += of.cost * p.kvheads;
-            slab += of.slabs() * p.kvheads;
-            of = at_uniform(at_entry(p, ++entry));
+        const int lane = threadIdx.x & 63, entries = p.entries();
+        for (; entry < entries; entry += 64) {
+            AtEntry x{};
+            if (entry + lane < entries) x = at_entry<MIXED>(p, entry + lane);
+            const long long cost = x.wide == (int)WIDE ? x.cost * p.kvheads : 0;
+            const long long sums = at_sums(cost, lane);
+            long long slabs = 0, part = 0;
+            if (MIXED) {
+                part = x.slabs() * p.kvheads;
+                slabs = at_sums(part, lane);
+            }
+            const unsigned long long found = __ballot(base + sums > pos);
+            if (found == 0) {
+                base += at_lane(sums, 63);
+                slab += at_lane(slabs, 63);
+                continue;
+            }
+            const int at = __builtin_ctzll(found);
+            base += at_lane(sums - cost, at);
+            slab += at_lane(slabs - part, at);
+            entry += at;
+            of.row0 = at_lane(x.row0, at);
+            of.rows = at_lane(x.rows, at);
+            of.t0 = at_lane(x.t0, at);
+            of.t1 = at_lane(x.t1, at);
+            of.before = at_lane(x.before, at);
+            of.table = at_lane(x.table, at);
+            of.blocks = at_lane(x.blocks, at);
+            of.wide = WIDE;
+            of.group = at_lane(x.group, at);
+            of.joined = at_lane(x.joined, at);
+            of.cost = at_lane(x.cost, at);
+            return true;
         }
+        return false;
     }
     // The next job with tiles in the piece: its tokens from `from` to `to`, and the
     // slab for its results (-1: they are whole, and go to out).
     __device__ __forceinline__ bool next(const AtPlan& p, AtJob& job, int& from, int& to, long long& part)
     {
         while (pos < end) {
-            settle(p);
-            if (of.cost <= 0) return false;
-            const long long in = pos - base, head = in / of.cost, rest = in - head * of.cost;
-            if (head >= p.kvheads) return false;
-            int lo = 0, hi = of.blocks - 1;  // the last block that begins at or before it
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (of.before_block(p, mid) <= rest)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+            if (of.cost == 0) {
+                if (!settle(p)) return false;
+            } else if (pos >= base + of.cost * p.kvheads) {
+                of.cost = 0;
+                continue;
             }
-            const int b = lo, tiles = of.tiles(p, b), weight = of.tile_cost();
+            const int head = at_quotient(pos - base, of.cost);
+            const long long rest = pos - base - head * of.cost;
+            int b = 0;  // the last block that begins at or before it
+            if (WIDE)
+                for (int hi = of.blocks - 1; b < hi;) {
+                    const int mid = (b + hi + 1) / 2;
+                    if (of.before_block(p, mid) <= rest)
+                        b = mid;
+                    else
+                        hi = mid - 1;
+                }
             const long long c0 = of.before_block(p, b), c1 = of.before_block(p, b + 1);
             const long long x = rest - c0, y = min(x + end - pos, c1 - c0);
-            pos += y - x;
+            job.end = of.end(p, b);
+            const int tiles = max(1, (job.end - of.t0 + TILE - 1) / TILE);
             int t0 = 0, t1 = tiles;
             if (!p.whole) {
-                t0 = (int)min((x + weight - 1) / weight, (long long)tiles);
-                t1 = (int)min((y + weight - 1) / weight, (long long)tiles);
+                t0 = (int)min((x + TILE - 1) / TILE, (long long)tiles);
+                t1 = (int)min((y + TILE - 1) / TILE, (long long)tiles);
             }
+            pos += y - x;
             if (t0 >= t1) continue;
-            job.head = (int)head;
+            job.head = head;
             job.rho0 = b * of.block_rows();
             job.rows = min(of.rows - job.rho0, of.block_rows());
             job.row0 = of.row0;
-            job.end = of.end(p, b);
             job.before = of.before;
             job.table = of.table;
-            job.wide = of.wide;
             job.group = of.group;
-            from = of.t0 + t0 * AT_TILE;
-            to = min(of.t0 + t1 * AT_TILE, job.end);
+            from = of.t0 + t0 * TILE;
+            to = min(of.t0 + t1 * TILE, job.end);
             part = -1;
-            if (!p.whole) {
-                if (t0 > 0 || t1 < tiles)
-                    part = (2ll * worker + (t0 == 0)) * p.blocks;
-                else if (of.joined)
-                    part = 2ll * p.grid * p.blocks + slab + head * of.slabs() + (long long)b * of.block_slabs();
-                if (part + of.block_slabs() > p.slabs) continue;
-            }
+            if (p.whole) return true;
+            if (t0 > 0 || t1 < tiles)
+                part = WIDE ? (2ll * worker + (t0 == 0)) * AT_SLABS : p.narrow_at + 2ll * worker + (t0 == 0);
+            else if (of.joined)
+                part = p.whole_at + slab + head * of.slabs() + (long long)b * of.block_slabs();
+            if (part + of.block_slabs() > p.slabs) continue;  // (starts that do not ascend)
+            if (t0 == 0) note(p, job, part, t1 < tiles ? c0 + (long long)(tiles - 1) * TILE - rest - (y - x) : -1);
             return true;
         }
         return false;
     }
-};
-
-// Where the results of a row of q lie, for one head of keys and one of its entries.
-struct AtParts {
-    const AtPlan* plan;
-    AtEntry of;
-    long long base, quota;
-    long long slab0;
-    int kv, rho;  // rho: the entry's row of the first head
-    bool some;
-
-    __device__ __forceinline__ void set(const AtPlan& p, int e, int row, int head)
+    // For the join: where the parts of the job's rows are.  behind: how far behind the
+    // piece the last tile begins, -1 where the job is whole.
+    __device__ __forceinline__ void note(const AtPlan& p, const AtJob& job, long long part, long long behind)
     {
-        plan = &p;
-        of = at_entry(p, e);
-        base = p.cost_at[e];
-        slab0 = p.slab_at[e];
-        quota = p.quota[0];
-        kv = head;
-        rho = (row - of.row0) * p.share;
-        some = row >= of.row0 && rho < of.rows;
-    }
-    __device__ __forceinline__ int block(int h) const { return (rho + h) / of.block_rows(); }
-    __device__ __forceinline__ int row(int h) const { return (rho + h) % of.block_rows(); }
-    // the workgroups that the job's first and last tiles are taken by
-    __device__ __forceinline__ void workers(int h, int& w0, int& w1) const
-    {
-        const int b = block(h);
-        const long long at = base + kv * of.cost + of.before_block(*plan, b);
-        w0 = (int)(at / quota);
-        w1 = (int)((at + (long long)(of.tiles(*plan, b) - 1) * of.tile_cost()) / quota);
-    }
-    __device__ __forceinline__ int count(int h) const
-    {
-        if (!some) return 0;
-        int w0, w1;
-        workers(h, w0, w1);
-        return w1 - w0 + 1;
-    }
-    // slab of part i of head h's job, -1: there is none
-    __device__ __forceinline__ long long slab(int h, int i) const
-    {
-        int w0, w1;
-        workers(h, w0, w1);
-        const long long at = w0 == w1 ? 2ll * plan->grid * plan->blocks + slab0 + kv * of.slabs() +
-                                            (long long)block(h) * of.block_slabs()
-                                      : (2ll * (w0 + i) + (i == 0)) * plan->blocks;
-        return at + of.block_slabs() > plan->slabs ? -1 : at + row(h) / AT_NARROW;
+        const int count = behind >= 0 ? 2 + at_quotient(behind, quota) : of.joined;
+        const int n = WIDE ? threadIdx.x : threadIdx.x & 63;
+        if (n < job.rows) {
+            size_t row;
+            const int head = job.place(p, n, row);
+            // the number of parts, the row in its slab, whether shared parts are to be added
+            const int what = count == 0 ? 0 : count | (n % AT_NARROW) << 16 | of.joined << 24 | (int)WIDE << 25;
+            (job.group ? p.shared_parts : p.own)[row * p.heads + head] =
+                make_int2(part < 0 ? 0 : (int)(part + n / AT_NARROW), what);
+        }
     }
 };
 
-// A row's parts: of its group's tokens, and of its own; false where the row has
-// none that are to be added.
-__device__ __forceinline__ bool at_parts(const AtPlan& p, int row, int kv, AtParts (&parts)[2])
+// Slab of part i of a row: the first one's, then one of each of the next workers.
+__device__ __forceinline__ long long at_part(int2 where, int i)
 {
-    const int s = pg_sequence(p.start, p.seqs, row);
-    if (s < 0) return false;
-    parts[1].set(p, p.groups + s, row, kv);
-    parts[0].some = false;
-    int tokens;
-    const int g = at_group(p, s, tokens);
-    if (g >= 0) {
-        parts[0].set(p, g, row, kv);
-        return true;
-    }
-    for (int h = 0; h < p.share; h += parts[1].of.block_rows())
-        if (parts[1].count(h) > 1) return true;
-    return parts[1].count(p.share - 1) > 1;
+    const int step = where.y >> 25 & 1 ? AT_SLABS : 1;
+    return where.x + (i == 0 ? 0ll : (2ll * i - 1) * step);
 }
 
 }  // namespace xsymv

@@ -12,69 +12,80 @@ namespace xsymv {
 // Workgroups at most: what two a compute unit are.
 constexpr int AT_GRID = 512;
 
-// Slabs of a part of a cut job: no job is wide where rows are single tokens' and
-// few heads share keys.
-inline int attn_blocks(int heads, int kvheads, int groups, bool single)
+// A call of single tokens with nothing in common and few heads that share keys has
+// narrow jobs alone.
+inline bool attn_mixed(int heads, int kvheads, int groups, bool single)
 {
-    return single && groups == 0 && heads / kvheads <= AT_NARROW ? 1 : AT_WIDE / AT_NARROW;
+    return !single || groups > 0 || heads / kvheads > AT_NARROW;
 }
 
-// Workspace: the quota, the entries' places in the line, parts of cut jobs (two a
-// workgroup), and where groups share tokens the whole parts.
+// Workspace: where the rows' parts are, and their slabs: of cut jobs (two a worker),
+// and where groups share tokens of whole ones.
 struct AttnSpace {
-    size_t costs, slabs, parts, count, bytes;
+    size_t shared, parts, narrow, whole, slabs, bytes;
     AttnSpace(int rows, int heads, int kvheads, int hd, int seqs, int groups, bool single)
     {
-        const size_t entries = (size_t)groups + seqs, share = heads / kvheads;
-        costs = align_up(sizeof(long long));
-        slabs = costs + align_up(entries * sizeof(long long));
-        parts = slabs + align_up(entries * sizeof(long long));
-        constexpr size_t wide = AT_WIDE / AT_NARROW;
-        count = 2 * (size_t)AT_GRID * attn_blocks(heads, kvheads, groups, single);
+        const size_t share = heads / kvheads, table = align_up((size_t)rows * heads * sizeof(int2));
+        shared = table;
+        parts = groups > 0 ? 2 * table : table;
+        narrow = attn_mixed(heads, kvheads, groups, single) ? 2 * (size_t)AT_GRID * AT_SLABS : 0;
+        whole = narrow + 2 * 4 * (size_t)AT_GRID;
+        slabs = whole;
         if (groups > 0) {
             const size_t blocks = (size_t)rows * share / AT_WIDE;
-            const size_t own = single ? seqs * (share <= AT_NARROW ? 1 : (share + AT_WIDE - 1) / AT_WIDE * wide)
-                                      : (blocks + seqs) * wide;
-            count += kvheads * (own + (blocks + groups) * wide);
+            const size_t own = single ? seqs * (share <= AT_NARROW ? 1 : (share + AT_WIDE - 1) / AT_WIDE * AT_SLABS)
+                                      : (blocks + seqs) * AT_SLABS;
+            slabs += kvheads * (own + (blocks + groups) * AT_SLABS);
         }
-        bytes = parts + count * at_slab(hd) * sizeof(float);
+        bytes = parts + slabs * at_slab(hd) * sizeof(float);
     }
 };
 
-template <class T, int HD>
+template <class T, int HD, bool MIXED>
 int attn_launch(AttnArgs<T> a, hipStream_t stream)
 {
     AtPlan& p = a.p;
-    const bool single = p.start == nullptr;
-    // Sequences of a tile at most are whole as they are: one launch.
-    const bool cut = p.groups > 0 || (long long)p.ldt * p.ps > AT_TILE;
-    const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, single);
+    // Sequences of a piece at most are whole as they are: one launch.
+    const bool cut = p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST[0];
+    const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, p.start == nullptr);
     int resident = 0;
-    const int rc = resident_blocks(reinterpret_cast<const void*>(&q8_attn<T, HD>), 256, &resident);
+    const int rc = resident_blocks(reinterpret_cast<const void*>(&q8_attn<T, HD, MIXED>), 256, &resident);
     if (rc) return rc;
     return q8_with_workspace(cut ? space.bytes : 0, true, stream, [&](void* ws, const TimedCall& tc) -> int {
         p.whole = ws == nullptr;
-        p.blocks = attn_blocks(p.heads, p.kvheads, p.groups, single);
-        // no more than there can be tiles
-        const long long blocks = (long long)p.rows * p.share / AT_WIDE + 1ll * p.seqs;
-        const long long tiles = p.whole ? 1 : ((long long)p.ldt * p.ps + AT_TILE - 1) / AT_TILE;
-        p.grid = (int)std::min((long long)std::min(resident, AT_GRID), std::max(1ll, blocks * p.kvheads * tiles));
+        // no more than there can be pieces
+        const long long jobs = ((long long)p.rows * p.share / AT_WIDE + p.seqs) * p.kvheads;
+        const long long tiles = p.whole ? 1 : ((long long)p.ldt * p.ps + AT_LEAST[0] - 1) / AT_LEAST[0];
+        const long long most = MIXED ? jobs * tiles + p.groups : (jobs * tiles + 3) / 4;
+        p.grid = (int)std::min((long long)std::min(resident, AT_GRID), std::max(1ll, most));
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
-            p.quota = reinterpret_cast<long long*>(at);
-            p.cost_at = reinterpret_cast<long long*>(at + space.costs);
-            p.slab_at = reinterpret_cast<long long*>(at + space.slabs);
-            p.slabs = (long long)space.count;
+            p.own = reinterpret_cast<int2*>(at);
+            p.shared_parts = reinterpret_cast<int2*>(at + space.shared);
+            p.slabs = (long long)space.slabs;
+            p.narrow_at = (long long)space.narrow;
+            p.whole_at = (long long)space.whole;
             a.slabs = reinterpret_cast<float*>(at + space.parts);
         }
-        XSYMV_HIP(launch_k(&q8_attn<T, HD>, dim3(p.grid), dim3(256), stream, a, tc.e0, tc.e1));
+        XSYMV_HIP(launch_k(&q8_attn<T, HD, MIXED>, dim3(p.grid), dim3(256), stream, a, tc.e0, tc.e1));
         if (p.whole) return 0;
-        const long long all = (long long)p.rows * p.kvheads;
-        AttnJoinArgs<T> j{a, (int)std::min(std::max(all / 2048, 1ll), 64ll)};
-        XSYMV_HIP(launch_k(&q8_attn_join<T>, dim3((unsigned)((all + j.per - 1) / j.per)), dim3(256), stream, j,
-                           nullptr, tc.e2));
+        // Four waves for a row and head where there are few, else one for several.
+        const long long all = (long long)p.rows * p.heads;
+        const bool few = all <= 4096;
+        a.per = few ? 1 : (int)std::min(std::max(all / 8192, 1ll), 64ll);
+        const long long each = few ? 1 : 4 * a.per;
+        XSYMV_HIP(launch_k(few ? &q8_attn_join<T, 4> : &q8_attn_join<T, 1>, dim3((unsigned)((all + each - 1) / each)),
+                           dim3(256), stream, a, nullptr, tc.e2));
         return 0;
     });
+}
+
+template <class T, int HD>
+int attn_width(const AttnArgs<T>& a, hipStream_t stream)
+{
+    const AtPlan& p = a.p;
+    return attn_mixed(p.heads, p.kvheads, p.groups, p.start == nullptr) ? attn_launch<T, HD, true>(a, stream)
+                                                                        : attn_launch<T, HD, false>(a, stream);
 }
 
 template <class T>
@@ -115,12 +126,40 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     if (ldo < wide) return -25;
     if (!some) return 0;
     if ((long long)rows * heads > 0x7fffffffll) return -1;
-    const AtPlan p{start, len,  table, tokens ? first : nullptr, shared, rows, heads, kvheads, heads / kvheads,
-                   hd,    seqs, pages > 0 ? ldt : 0, tokens ? groups : 0, pages, ps};
-    const AttnArgs<T> a{p, q, out, lse, k, v, ks, vs, scale * 1.4426950408889634f, ldq, ldk, ldv, ldo, nullptr};
-    if (hd <= 64) return attn_launch<T, 64>(a, stream);
-    if (hd <= 128) return attn_launch<T, 128>(a, stream);
-    return attn_launch<T, 256>(a, stream);
+    AttnArgs<T> a{};
+    AtPlan& p = a.p;
+    p.start = start;
+    p.len = len;
+    p.table = table;
+    p.first = first;
+    p.shared = shared;
+    p.rows = rows;
+    p.heads = heads;
+    p.kvheads = kvheads;
+    p.share = heads / kvheads;
+    p.hd = hd;
+    p.seqs = seqs;
+    p.ldt = tokens ? ldt : 0;
+    p.groups = tokens ? groups : 0;
+    p.pages = pages;
+    p.ps = ps;
+    p.by_share = AtDivisor(p.share);
+    p.by_page = AtDivisor(ps);
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.k = k;
+    a.v = v;
+    a.ks = ks;
+    a.vs = vs;
+    a.scale = scale * 1.4426950408889634f;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.ldo = ldo;
+    if (hd <= 64) return attn_width<T, 64>(a, stream);
+    if (hd <= 128) return attn_width<T, 128>(a, stream);
+    return attn_width<T, 256>(a, stream);
 }
 
 }  // namespace xsymv
