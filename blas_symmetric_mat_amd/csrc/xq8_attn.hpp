@@ -245,6 +245,15 @@ __device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N])
     }
 }
 
+// Which of 64 tokens a row sees: those that are there (`ok`) and lie before `limit`;
+// bit 0 is a lane's first token, 4 g.  (A weight of zero is not multiplied with its
+// token's scale, which may be no number.)
+__device__ __forceinline__ unsigned long long at_seen(unsigned long long ok, int limit, int g)
+{
+    const int n = min(max(limit, 0), 64);
+    return (n == 64 ? ok : ok & ((1ull << n) - 1)) >> (4 * g);
+}
+
 // The largest values' scale so far, as a power of two, for a wave.  Scales that are
 // not finite do not count: their weights are not finite in their own rows.
 struct AtUnit {
@@ -435,24 +444,17 @@ struct AtNarrow {
                 w[4 * i + e] = vs[e];
             }
         }
-        const bool all = (unsigned)c.ok == ~0u && base + STEP <= least;
-        unsigned mask = 0xff;
-        if (!all) {  // (scales behind the sequence or of a page that is none are zeros)
-            mask = 0;
+        if ((unsigned)c.ok == ~0u && base + STEP <= least) {
+            at_weigh(r, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = i / 4 * 16 + 4 * at.g + i % 4;
-                if (base + t < limit && (c.ok >> t & 1)) mask |= 1u << i;
-                if (!(mask >> i & 1)) x[i] = -INFINITY;
-            }
-        }
-        at_weigh(r, x);
+            for (int i = 0; i < 8; ++i) w[i] *= x[i];
+        } else {
+            const unsigned mask = (unsigned)at_seen(c.ok, limit - base, at.g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] *= x[i];
-        if (!all) {
+            for (int i = 0; i < 8; ++i) x[i] = mask >> (i / 4 * 16 + i % 4) & 1 ? x[i] : -INFINITY;
+            at_weigh(r, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!(mask >> i & 1)) w[i] = 0.0f;
+            for (int i = 0; i < 8; ++i) w[i] = x[i] == 0.0f ? 0.0f : x[i] * w[i];
         }
         const at_h8 p = at_round(w);
         at_h8 rest;
@@ -630,22 +632,14 @@ struct AtWide {
         unsigned long long ok;
         __builtin_memcpy(&ok, s.ok, 8);
         const bool all = ok == ~0ull && base + STEP <= least;
-        unsigned mask[TILES];
-        if (!all) {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                mask[i] = 0;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int t = e / 4 * 16 + 4 * at.g + e % 4;
-                    if (base + t < limit[i] && (ok >> t & 1)) mask[i] |= 1u << e;
-                    if (!(mask[i] >> e & 1)) x[i][e] = -INFINITY;
-                }
-            }
-        }
         at_h8 p[TILES][2], rest[TILES][SPLIT ? 2 : 1];
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
+            if (!all) {
+                const unsigned long long mask = at_seen(ok, limit[i] - base, at.g);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[i][e] = mask >> (e / 4 * 16 + e % 4) & 1 ? x[i][e] : -INFINITY;
+            }
             at_weigh(r[i], x[i]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -654,8 +648,7 @@ struct AtWide {
                 for (int e = 0; e < 8; ++e) w[e] = x[i][8 * h + e] * vs[2 * h + e / 4][e % 4];
                 if (!all) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!(mask[i] >> (8 * h + e) & 1)) w[e] = 0.0f;
+                    for (int e = 0; e < 8; ++e) w[e] = x[i][8 * h + e] == 0.0f ? 0.0f : w[e];
                 }
                 p[i][h] = at_round(w);
                 if constexpr (SPLIT) rest[i][h] = at_rest(w, p[i][h]);
@@ -734,28 +727,36 @@ __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T>
         typename AtNarrow<T, HD>::Lds narrow;
         typename AtWide<T, HD>::Lds wide;
     };
-    __shared__ AtScan scan;
+    __shared__ AtScan<MIXED> scan;
     __shared__ typename std::conditional<MIXED, Both, Narrow>::type lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AtLanes<HD> at(a.p.hd);
-    // workgroups of one die, which takes every eighth, have pieces side by side
-    const int per = a.p.grid / 8, b = (int)blockIdx.x;
-    const int worker = a.p.grid % 8 == 0 ? b % 8 * per + b / 8 : b;
-    at_scan<MIXED>(a.p, scan);
+    // Workgroups b, b + 8, ... are of one die: they have pieces side by side.
+    int b = (int)blockIdx.x;
     AtJob job;
-    int from, to;
-    long long slab;
+    int from, to, slab;
     if constexpr (MIXED) {
-        AtCursor<MIXED, true> cursor(a.p, scan, worker, a.p.grid);
-        while (cursor.next(a.p, job, from, to, slab)) {
-            float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
-            AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
-            w.run(from, to, part);
+        // Every other one takes wide jobs: where there are both, a compute unit runs one
+        // that waits for memory beside one that computes.
+        const bool wide = b / 8 % 2 == 0;
+        b = b / 16 * 8 + b % 8;
+        if (wide) {
+            const int worker = a.p.grid % 8 == 0 ? b % 8 * (a.p.grid / 8) + b / 8 : b;
+            const AtLines<true> lines(a.p, scan);
+            AtCursor<true, true> cursor(a.p, scan, lines, worker, a.p.grid);
+            while (cursor.next(a.p, job, from, to, slab)) {
+                float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
+                AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
+                w.run(from, to, part);
+            }
+            return;
         }
     }
-    AtCursor<MIXED, false> cursor(a.p, scan, worker * 4 + wave, a.p.grid * 4);
+    const int worker = a.p.grid % 8 == 0 ? b % 8 * (a.p.grid / 8) + b / 8 : b;
+    const AtLines<MIXED> lines(a.p, scan);
+    AtCursor<MIXED, false> cursor(a.p, scan, lines, worker * 4 + wave, a.p.grid * 4);
     while (cursor.next(a.p, job, from, to, slab)) {
-        float* part = slab < 0 ? nullptr : a.slabs + slab * at_slab(a.p.hd);
+        float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
         AtNarrow<T, HD> w{a, job, at, lds.narrow.tokens[wave], a.p.table + (size_t)job.table * a.p.ldt, lane};
         w.run(from, to, part);
     }

@@ -7,13 +7,14 @@
 // the `share` heads of q that read the same keys; blocks are of 16 rows where an
 // entry has no more (narrow), else of 128 (wide).
 //
-// There are two lines of jobs, one after the other by entry, head and block, each
-// with a cost in tokens: wide jobs, of which every workgroup takes an equal piece,
-// and narrow ones, of which every wave does.  A job's tiles (32 tokens of a narrow
-// job, 64 of a wide one) lie in its costs from the start; a tile is taken by the
-// worker in whose piece it begins.  Costs need not be exact, only the same for all
-// workers, which compute them from the arrays on the device, so that a captured call
-// follows what these hold.
+// There are two lines of jobs, one after the other by entry, head and block: wide
+// jobs, of which every workgroup takes an equal piece, and narrow ones, of which
+// every wave does.  Lines are counted in tiles (32 tokens of a narrow job, 64 of a
+// wide one): a job's tiles come first in its stretch of the line, then some that
+// stand for what a job takes besides.  Stretches may be longer than need be, but have
+// to be the same for all workers, which compute them from the arrays on the device,
+// so that a captured call follows what these hold.  A single sequence's step waits for
+// this: it is some hundred instructions, with sums over lanes (64 entries at a time).
 //
 // Who takes a job's first tile writes down, for each of its rows, where the parts of
 // its results are; the join reads that.
@@ -30,10 +31,11 @@ constexpr int AT_NARROW = 16;            // rows of a narrow job, and of a slab
 constexpr int AT_WIDE = 128;             // rows of a wide job
 constexpr int AT_SLABS = AT_WIDE / AT_NARROW;
 constexpr int AT_TILE[2] = {32, 64};  // tokens of a narrow and of a wide tile
-constexpr int AT_OVER = 48;           // cost of a job besides its tokens
-// A piece is two tiles at least: so that each worker has one of every job that it is
-// in the middle of, and for the join's sake.
-constexpr int AT_LEAST[2] = {64, 128};
+constexpr int AT_OVER = 2;            // tiles that a job takes besides its own
+// A piece is two tiles at least, for the join's sake.
+constexpr int AT_LEAST = 2;
+// Entries of a call at most: windows of 64, of which LDS holds the sums.
+constexpr int AT_WINDOWS = 1024, AT_ENTRIES = 64 * AT_WINDOWS;
 
 // Floats of a slab, the results of 16 rows in a part of a job: m and l of each,
 // then their out, not yet divided by l.
@@ -59,12 +61,12 @@ struct AtPlan {
     const int *start, *len, *table, *first, *shared;
     int rows, heads, kvheads, share, hd, seqs, ldt, groups, pages, ps;
     AtDivisor by_share, by_page;
-    int grid;   // workgroups
+    int grid;   // workgroups of each kind
     int whole;  // no job is cut, nothing is shared: no workspace
     // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
     // narrow ones', two a wave; of whole parts) and, for each row and head, where its
     // own parts and its group's are.
-    long long slabs, narrow_at, whole_at;
+    int slabs, narrow_at, whole_at;
     int2 *own, *shared_parts;
 
     __device__ __forceinline__ int entries() const { return groups + seqs; }
@@ -76,11 +78,11 @@ struct AtPlan {
     }
 };
 
-// Floor of a / b for 0 <= a < 2^62, b > 0 and a quotient that an int holds: a
-// division in 32-bit floating point, put right.
-__device__ __forceinline__ int at_quotient(long long a, long long b)
+// Floor of a / b for a >= 0, b > 0: a division in floating point, put right.
+__device__ __forceinline__ int at_quotient(int a, int b)
 {
-    int q = (int)fminf((float)a / (float)b, 2.1e9f);
+    int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b));
+    q = min(q, a);
     while ((long long)q * b > a) --q;
     while ((long long)(q + 1) * b <= a) ++q;
     return q;
@@ -91,20 +93,24 @@ struct AtEntry {
     int t0, t1;      // tokens
     int before;      // tokens before the first row's own (a sequence's)
     int table;       // the row of the table that is read
-    int blocks;
     int wide, group, joined;
-    long long cost;  // of one head
+    int cost;  // tiles of one head
 
     __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
     __device__ __forceinline__ int block_slabs() const { return wide ? AT_SLABS : 1; }
-    __device__ __forceinline__ long long slabs() const { return joined ? (long long)blocks * block_slabs() : 0; }
-    // costs of the blocks before block b
-    __device__ __forceinline__ long long before_block(const AtPlan& p, int b) const
+    __device__ __forceinline__ int blocks() const { return wide ? (rows + AT_WIDE - 1) / AT_WIDE : rows > 0; }
+    __device__ __forceinline__ int slabs() const { return joined ? blocks() * block_slabs() : 0; }
+    // length of the blocks before block b
+    __device__ __forceinline__ int before_block(const AtPlan& p, int b) const
     {
         if (p.whole) return b;
-        if (!wide || group) return (long long)b * (AT_OVER + t1 - t0);
-        const int step = p.by_share.of(AT_WIDE + p.share - 1);  // rows of q a block
-        return (long long)b * (AT_OVER + max(before - t0, 0)) + step * ((long long)b * (b + 1) / 2);
+        const int tile = wide ? AT_TILE[1] : AT_TILE[0];
+        if (!wide || group) return b * (AT_OVER + (t1 - t0 + tile - 1) / tile);
+        // block b sees up to step * (b + 1) tokens more than what lies before the
+        // rows; the sums of these are rounded down, for which one tile makes up
+        const int step = p.by_share.of(AT_WIDE + p.share - 1);
+        return b * (AT_OVER + 1 + (max(before - t0, 0) + tile - 1) / tile) +
+               (int)((long long)b * (b + 1) / 2 * step / tile);
     }
     // end of the tokens that block b sees
     __device__ __forceinline__ int end(const AtPlan& p, int b) const
@@ -145,7 +151,7 @@ struct AtGroup {
 __device__ __forceinline__ int at_shared(const AtPlan& p, int s)
 {
     if (p.whole || p.groups == 0) return 0;
-    int lo = 0, hi = p.groups;  // the last group that begins at or before s
+    int lo = 0, hi = p.groups > 1 ? p.groups : 0;  // the last group that begins at or before s
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         if (p.first[mid + 1] <= s)
@@ -191,8 +197,7 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
         x.before = x.t1 - 1;
     }
     x.wide = MIXED && x.rows > AT_NARROW;
-    x.blocks = x.wide ? (x.rows + AT_WIDE - 1) / AT_WIDE : x.rows > 0;
-    x.cost = x.blocks == 0 ? 0 : x.before_block(p, x.blocks);
+    x.cost = x.before_block(p, x.blocks());
     return x;
 }
 
@@ -217,8 +222,10 @@ struct AtJob {
     }
 };
 
+// Sums of 64 entries each: narrow tiles, wide tiles, slabs.
+template <bool MIXED>
 struct AtScan {
-    long long cost[2][257], slab[257], wave[3][4];
+    int sums[MIXED ? 3 : 1][AT_WINDOWS];
 };
 
 // Least and largest of a number that lanes n, n + 16, ... have alike.
@@ -254,168 +261,184 @@ __device__ __forceinline__ void at_each(F&& f)
 }
 // Lane `from`'s number, the same for all.
 __device__ __forceinline__ int at_lane(int v, int from) { return __builtin_amdgcn_readlane(v, from); }
-__device__ __forceinline__ long long at_lane(long long v, int from)
-{
-    const int lo = __builtin_amdgcn_readlane((int)v, from), hi = __builtin_amdgcn_readlane((int)(v >> 32), from);
-    return (long long)hi << 32 | (unsigned)lo;
-}
 // Sums of the lanes up to and with this one.
-__device__ __forceinline__ long long at_sums(long long v, int lane)
+__device__ __forceinline__ int at_sums(int v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const long long o = __shfl_up(v, d, 64);
-        v += lane >= d ? o : 0;
-    }
+    // within rows of 16 lanes, then the last lanes of the rows before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // from 1, 2, 4, 8 lanes before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);  // lane 15 to row 1, 47 to row 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);  // lane 31 to rows 2 and 3
     return v;
 }
 
-// The lines' costs, by the whole workgroup: 256 stretches of entries.
+// 64 entries, one a lane, and their sums up to and with the lane's.
 template <bool MIXED>
-__device__ __forceinline__ void at_scan(const AtPlan& p, AtScan& scan)
-{
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int entries = p.entries(), chunk = (entries + 255) / 256;
-    long long v[3] = {0, 0, 0};  // narrow, wide, slabs
-    for (int e = t * chunk; e < min((t + 1) * chunk, entries); ++e) {
-        const AtEntry x = at_entry<MIXED>(p, e);
-        const long long cost = x.cost * p.kvheads;
-        v[0] += x.wide ? 0 : cost;
-        if (MIXED) {
-            v[1] += x.wide ? cost : 0;
-            v[2] += x.slabs() * p.kvheads;
+struct AtWindow {
+    static constexpr int N = MIXED ? 3 : 1;
+    AtEntry x;
+    int own[N], sums[N];  // narrow tiles, wide tiles, slabs
+    __device__ __forceinline__ void load(const AtPlan& p, int window)
+    {
+        const int e = window * 64 + (threadIdx.x & 63);
+        x = AtEntry{};
+        if (e < p.entries()) x = at_entry<MIXED>(p, e);
+        const int cost = x.cost * p.kvheads;
+        own[0] = x.wide ? 0 : cost;
+        if constexpr (MIXED) {
+            own[1] = x.wide ? cost : 0;
+            own[2] = x.slabs() * p.kvheads;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) sums[i] = at_sums(own[i]);
+    }
+    __device__ __forceinline__ int all(int i) const { return at_lane(sums[i], 63); }
+};
+
+// The whole lines: their lengths, and with more than 64 entries the windows' sums.
+template <bool MIXED>
+struct AtLines {
+    AtWindow<MIXED> w;
+    int total[2], windows;
+    __device__ __forceinline__ AtLines(const AtPlan& p, AtScan<MIXED>& scan)
+    {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        windows = (p.entries() + 63) / 64;
+        total[1] = 0;
+        if (windows <= 1) {
+            w.load(p, 0);
+            total[0] = w.all(0);
+            if constexpr (MIXED) total[1] = w.all(1);
+            return;
+        }
+        for (int i = wave; i < windows; i += 4) {
+            w.load(p, i);
+            if (lane == 63)
+#pragma unroll
+                for (int j = 0; j < AtWindow<MIXED>::N; ++j) scan.sums[j][i] = w.sums[j];
+        }
+        __syncthreads();
+        total[0] = 0;
+        for (int i = 0; i < windows; i += 64) {
+            const bool some = i + lane < windows;
+            total[0] += at_lane(at_sums(some ? scan.sums[0][i + lane] : 0), 63);
+            if constexpr (MIXED) total[1] += at_lane(at_sums(some ? scan.sums[1][i + lane] : 0), 63);
         }
     }
-    constexpr int N = MIXED ? 3 : 1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = at_sums(v[i], lane);
-        if (lane == 63) scan.wave[i][wave] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        for (int w = 0; w < wave; ++w) v[i] += scan.wave[i][w];
-    scan.cost[0][t + 1] = v[0];
-    if (MIXED) {
-        scan.cost[1][t + 1] = v[1];
-        scan.slab[t + 1] = v[2];
-    }
-    if (t == 0) scan.cost[0][0] = scan.cost[1][0] = scan.slab[0] = 0;
-    __syncthreads();
-}
+};
 
 // A worker's way through its piece of a line: a wave's (narrow jobs) or a
 // workgroup's (wide ones).
 template <bool MIXED, bool WIDE>
 struct AtCursor {
     static constexpr int TILE = AT_TILE[WIDE];
-    long long pos, end, quota;
-    long long base, slab;  // where the entry's costs, and its whole parts, begin
-    int worker, entry;
+    int pos, end, quota;
+    int base, slab;  // where the window's tiles, and its whole parts, begin
+    int worker, window, windows;
+    int first, parts;  // the same of the entry
     AtEntry of;
 
-    __device__ __forceinline__ AtCursor(const AtPlan& p, const AtScan& scan, int worker_, int workers)
+    __device__ __forceinline__ AtCursor(const AtPlan& p, const AtScan<MIXED>& scan, const AtLines<MIXED>& lines,
+                                        int worker_, int workers)
     {
+        AtWindow<MIXED> w = lines.w;
         worker = worker_;
-        const int lane = threadIdx.x & 63;
-        const long long total = at_lane(scan.cost[WIDE][256], 0);
+        const int lane = threadIdx.x & 63, total = lines.total[WIDE];
         // a little more than total / workers, which need not be exact
-        quota = (long long)((float)total / (float)workers * 1.000001f) + 1;
-        if (!p.whole) quota = max(quota, (long long)AT_LEAST[WIDE]);
-        pos = worker * quota;
-        end = min(pos + quota, total);
-        of.cost = 0;
-        base = slab = 0;
-        entry = 0;
+        quota = (int)((float)total * __builtin_amdgcn_rcpf((float)workers) * 1.00001f) + 1;
+        if (!p.whole) quota = max(quota, AT_LEAST);
+        const long long at = (long long)worker * quota;
+        pos = (int)min(at, (long long)total);
+        end = (int)min(at + quota, (long long)total);
+        base = slab = window = 0;
+        windows = lines.windows;
         if (pos >= end) return;
-        // the last stretch that begins at or before pos: of 256, four to a lane
-        int last = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned long long at = __ballot(scan.cost[WIDE][64 * i + lane] <= pos);
-            if (at != 0) last = 64 * i + 63 - __builtin_clzll(at);
-        }
-        const int chunk = (p.entries() + 255) / 256;
-        base = at_lane(scan.cost[WIDE][last], 0);
-        if (MIXED) slab = at_lane(scan.slab[last], 0);
-        entry = last * chunk;
-    }
-    // To the entry that holds pos; each lane looks at one.
-    __device__ __forceinline__ bool settle(const AtPlan& p)
-    {
-        const int lane = threadIdx.x & 63, entries = p.entries();
-        for (; entry < entries; entry += 64) {
-            AtEntry x{};
-            if (entry + lane < entries) x = at_entry<MIXED>(p, entry + lane);
-            const long long cost = x.wide == (int)WIDE ? x.cost * p.kvheads : 0;
-            const long long sums = at_sums(cost, lane);
-            long long slabs = 0, part = 0;
-            if (MIXED) {
-                part = x.slabs() * p.kvheads;
-                slabs = at_sums(part, lane);
-            }
-            const unsigned long long found = __ballot(base + sums > pos);
-            if (found == 0) {
+        if (windows > 1) {
+            for (int i = 0; i < windows; i += 64) {
+                const bool some = i + lane < windows;
+                const int v = some ? scan.sums[WIDE][i + lane] : 0, sums = at_sums(v);
+                int part = 0, slabs = 0;
+                if constexpr (MIXED) {
+                    part = some ? scan.sums[2][i + lane] : 0;
+                    slabs = at_sums(part);
+                }
+                const unsigned long long found = __ballot(base + sums > pos);
+                if (found != 0) {
+                    const int in = __builtin_ctzll(found);
+                    window = i + in;
+                    base += at_lane(sums - v, in);
+                    slab += at_lane(slabs - part, in);
+                    break;
+                }
                 base += at_lane(sums, 63);
                 slab += at_lane(slabs, 63);
-                continue;
             }
-            const int at = __builtin_ctzll(found);
-            base += at_lane(sums - cost, at);
-            slab += at_lane(slabs - part, at);
-            entry += at;
-            of.row0 = at_lane(x.row0, at);
-            of.rows = at_lane(x.rows, at);
-            of.t0 = at_lane(x.t0, at);
-            of.t1 = at_lane(x.t1, at);
-            of.before = at_lane(x.before, at);
-            of.table = at_lane(x.table, at);
-            of.blocks = at_lane(x.blocks, at);
-            of.wide = WIDE;
-            of.group = at_lane(x.group, at);
-            of.joined = at_lane(x.joined, at);
-            of.cost = at_lane(x.cost, at);
-            return true;
+            w.load(p, window);
+        }
+        if (!find(w)) end = pos;
+    }
+    // The window's entry that holds pos.
+    __device__ __forceinline__ bool find(const AtWindow<MIXED>& w)
+    {
+        const unsigned long long found = __ballot(base + w.sums[WIDE] > pos);
+        if (found == 0) return false;
+        const int at = __builtin_ctzll(found);
+        first = base + at_lane(w.sums[WIDE] - w.own[WIDE], at);
+        parts = 0;
+        if constexpr (MIXED) parts = slab + at_lane(w.sums[2] - w.own[2], at);
+        of.row0 = at_lane(w.x.row0, at);
+        of.rows = at_lane(w.x.rows, at);
+        of.t0 = at_lane(w.x.t0, at);
+        of.t1 = at_lane(w.x.t1, at);
+        of.before = at_lane(w.x.before, at);
+        of.table = at_lane(w.x.table, at);
+        of.wide = WIDE;
+        of.group = MIXED ? at_lane(w.x.group, at) : 0;
+        of.joined = MIXED ? at_lane(w.x.joined, at) : 0;
+        of.cost = at_lane(w.x.cost, at);
+        return of.cost > 0;
+    }
+    // To the entry that holds pos, in this window or one behind it.  (Read again rather
+    // than kept in registers while jobs run.)
+    __device__ __forceinline__ bool settle(const AtPlan& p)
+    {
+        for (; window < windows; ++window) {
+            AtWindow<MIXED> w;
+            w.load(p, window);
+            if (find(w)) return true;
+            base += w.all(WIDE);
+            if constexpr (MIXED) slab += w.all(2);
         }
         return false;
     }
     // The next job with tiles in the piece: its tokens from `from` to `to`, and the
     // slab for its results (-1: they are whole, and go to out).
-    __device__ __forceinline__ bool next(const AtPlan& p, AtJob& job, int& from, int& to, long long& part)
+    __device__ __forceinline__ bool next(const AtPlan& p, AtJob& job, int& from, int& to, int& part)
     {
         while (pos < end) {
-            if (of.cost == 0) {
-                if (!settle(p)) return false;
-            } else if (pos >= base + of.cost * p.kvheads) {
-                of.cost = 0;
-                continue;
-            }
-            const int head = at_quotient(pos - base, of.cost);
-            const long long rest = pos - base - head * of.cost;
+            if (pos - first >= of.cost * p.kvheads && !settle(p)) return false;
+            const int head = at_quotient(pos - first, of.cost), rest = pos - first - head * of.cost;
             int b = 0;  // the last block that begins at or before it
             if (WIDE)
-                for (int hi = of.blocks - 1; b < hi;) {
+                for (int hi = of.blocks() - 1; b < hi;) {
                     const int mid = (b + hi + 1) / 2;
                     if (of.before_block(p, mid) <= rest)
                         b = mid;
                     else
                         hi = mid - 1;
                 }
-            const long long c0 = of.before_block(p, b), c1 = of.before_block(p, b + 1);
-            const long long x = rest - c0, y = min(x + end - pos, c1 - c0);
+            const int c0 = WIDE ? of.before_block(p, b) : 0, c1 = WIDE ? of.before_block(p, b + 1) : of.cost;
+            const int x = rest - c0, y = min(x + end - pos, c1 - c0);
             job.end = of.end(p, b);
             const int tiles = max(1, (job.end - of.t0 + TILE - 1) / TILE);
-            int t0 = 0, t1 = tiles;
-            if (!p.whole) {
-                t0 = (int)min((x + TILE - 1) / TILE, (long long)tiles);
-                t1 = (int)min((y + TILE - 1) / TILE, (long long)tiles);
-            }
+            const int t0 = p.whole ? 0 : min(x, tiles), t1 = p.whole ? tiles : min(y, tiles);
             pos += y - x;
             if (t0 >= t1) continue;
             job.head = head;
-            job.rho0 = b * of.block_rows();
-            job.rows = min(of.rows - job.rho0, of.block_rows());
+            job.rho0 = WIDE ? b * AT_WIDE : 0;
+            job.rows = min(of.rows - job.rho0, WIDE ? AT_WIDE : AT_NARROW);
             job.row0 = of.row0;
             job.before = of.before;
             job.table = of.table;
@@ -425,18 +448,18 @@ struct AtCursor {
             part = -1;
             if (p.whole) return true;
             if (t0 > 0 || t1 < tiles)
-                part = WIDE ? (2ll * worker + (t0 == 0)) * AT_SLABS : p.narrow_at + 2ll * worker + (t0 == 0);
+                part = WIDE ? (2 * worker + (t0 == 0)) * AT_SLABS : p.narrow_at + 2 * worker + (t0 == 0);
             else if (of.joined)
-                part = p.whole_at + slab + head * of.slabs() + (long long)b * of.block_slabs();
-            if (part + of.block_slabs() > p.slabs) continue;  // (starts that do not ascend)
-            if (t0 == 0) note(p, job, part, t1 < tiles ? c0 + (long long)(tiles - 1) * TILE - rest - (y - x) : -1);
+                part = p.whole_at + parts + head * of.slabs() + b * of.block_slabs();
+            if (part > p.slabs - of.block_slabs()) continue;  // (starts that do not ascend)
+            if (t0 == 0) note(p, job, part, t1 < tiles ? tiles - 1 - y : -1);
             return true;
         }
         return false;
     }
     // For the join: where the parts of the job's rows are.  behind: how far behind the
     // piece the last tile begins, -1 where the job is whole.
-    __device__ __forceinline__ void note(const AtPlan& p, const AtJob& job, long long part, long long behind)
+    __device__ __forceinline__ void note(const AtPlan& p, const AtJob& job, int part, int behind)
     {
         const int count = behind >= 0 ? 2 + at_quotient(behind, quota) : of.joined;
         const int n = WIDE ? threadIdx.x : threadIdx.x & 63;
@@ -446,7 +469,7 @@ struct AtCursor {
             // the number of parts, the row in its slab, whether shared parts are to be added
             const int what = count == 0 ? 0 : count | (n % AT_NARROW) << 16 | of.joined << 24 | (int)WIDE << 25;
             (job.group ? p.shared_parts : p.own)[row * p.heads + head] =
-                make_int2(part < 0 ? 0 : (int)(part + n / AT_NARROW), what);
+                make_int2(part < 0 ? 0 : part + n / AT_NARROW, what);
         }
     }
 };

@@ -45,8 +45,12 @@ template <class T, int HD, bool MIXED>
 int attn_launch(AttnArgs<T> a, hipStream_t stream)
 {
     AtPlan& p = a.p;
+    // Tiles that a line has at most.  (Where an int might not count them, no job is cut;
+    // the call takes minutes.)
+    const double blocks = (double)p.rows * p.share / AT_WIDE + p.seqs + p.groups;
+    const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE[0] + AT_OVER + 2);
     // Sequences of a piece at most are whole as they are: one launch.
-    const bool cut = p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST[0];
+    const bool cut = line < 2e9 && (p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST * AT_TILE[0]);
     const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, p.start == nullptr);
     int resident = 0;
     const int rc = resident_blocks(reinterpret_cast<const void*>(&q8_attn<T, HD, MIXED>), 256, &resident);
@@ -55,19 +59,19 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
         p.whole = ws == nullptr;
         // no more than there can be pieces
         const long long jobs = ((long long)p.rows * p.share / AT_WIDE + p.seqs) * p.kvheads;
-        const long long tiles = p.whole ? 1 : ((long long)p.ldt * p.ps + AT_LEAST[0] - 1) / AT_LEAST[0];
-        const long long most = MIXED ? jobs * tiles + p.groups : (jobs * tiles + 3) / 4;
+        const long long tiles = p.whole ? 1 : (long long)p.ldt * p.ps / AT_TILE[0] + 1 + AT_OVER;
+        const long long most = MIXED ? (jobs * tiles + p.groups + 7) / 8 * 8 : (jobs * tiles + 3) / 4;
         p.grid = (int)std::min((long long)std::min(resident, AT_GRID), std::max(1ll, most));
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
             p.own = reinterpret_cast<int2*>(at);
             p.shared_parts = reinterpret_cast<int2*>(at + space.shared);
-            p.slabs = (long long)space.slabs;
-            p.narrow_at = (long long)space.narrow;
-            p.whole_at = (long long)space.whole;
+            p.slabs = (int)space.slabs;
+            p.narrow_at = (int)space.narrow;
+            p.whole_at = (int)space.whole;
             a.slabs = reinterpret_cast<float*>(at + space.parts);
         }
-        XSYMV_HIP(launch_k(&q8_attn<T, HD, MIXED>, dim3(p.grid), dim3(256), stream, a, tc.e0, tc.e1));
+        XSYMV_HIP(launch_k(&q8_attn<T, HD, MIXED>, dim3(MIXED ? 2 * p.grid : p.grid), dim3(256), stream, a, tc.e0, tc.e1));
         if (p.whole) return 0;
         // Four waves for a row and head where there are few, else one for several.
         const long long all = (long long)p.rows * p.heads;
@@ -103,12 +107,12 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     const bool some = rows > 0 && (seqs > 0 || start == nullptr);
     if (some && q == nullptr) return -5;
     if (ldq < wide) return -6;
-    if (seqs < 0 || (start == nullptr && seqs != rows)) return -7;
+    if (seqs < 0 || (start == nullptr && seqs != rows) || seqs > AT_ENTRIES) return -7;
     const bool tokens = some && ldt > 0 && pages > 0;
     if (some && len == nullptr) return -9;
     if (tokens && table == nullptr) return -10;
     if (ldt < 0) return -11;
-    if (groups < 0) return -12;
+    if (groups < 0 || groups > AT_ENTRIES - seqs) return -12;
     if (tokens && groups > 0 && first == nullptr) return -13;
     if (tokens && groups > 0 && shared == nullptr) return -14;
     if (tokens && k == nullptr) return -15;

@@ -488,8 +488,8 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   above) the call is made without, in up to many times the time.
  *   Codes: -1 rows < 0 (or rows * heads over 2^31 - 1), -2 heads < 1 or not a
  *   multiple of kvheads (or heads * hd over 2^31 - 1), -3 kvheads < 1, -4 hd < 16 or > 256, -5 q NULL, -6 ldq, -7
- *   seqs < 0, or not rows without start, -9 len NULL, -10 table NULL, -11 ldt <
- *   0, -12 groups < 0, -13 first NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd,
+ *   seqs < 0, > 65536, or not rows without start, -9 len NULL, -10 table NULL, -11 ldt <
+ *   0, -12 groups < 0 or > 65536 - seqs, -13 first NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd,
  *   -17 ks NULL, -18 v NULL, -19 ldv < hd, -20 vs NULL, -21 pages < 0 or too many
  *   rows, -22 ps < 1, -23 scale not finite, -24 out NULL, -25 ldo, 2000 installed
  *   workspace too small.
