@@ -161,7 +161,8 @@ struct AtQuery {
     static constexpr int NF = HD / 32;
     static constexpr bool SPLIT = std::is_same<T, float>::value;
     at_h8 hi[NF], lo[SPLIT ? NF : 1];
-    float unit;  // score = sum of products * key's scale * unit
+    float unit;   // score = sum of products * key's scale * unit, which is above zero
+    float reach;  // 1 / unit
     __device__ __forceinline__ void load(const T* row, bool some, const AtLanes<HD>& a, int hd, float scale)
     {
         float v[NF][8], most = 0.0f;
@@ -184,7 +185,11 @@ struct AtQuery {
             up = __uint_as_float((unsigned)(127 + e) << 23);
             down = __uint_as_float((unsigned)(127 - e) << 23);
         }
-        unit = scale * down;
+        // a negative scale is q's sign; zero is a number that makes all scores as good as it
+        unit = fmaxf(fabsf(scale) * down, 0x1p-120f);
+        reach = 1.0f / unit;
+        if (scale < 0.0f) up = -up;
+        if (scale == 0.0f) up = 0.0f;
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -196,8 +201,9 @@ struct AtQuery {
     }
 };
 
-// Results so far of 16 rows of q, in the lanes of their columns: l, the sum of the
-// weights e^(s - m) of a lane's tokens, and out in units of `unit` / 2^14.
+// Results so far of 16 rows of q, in the lanes of their columns: the reference m as a
+// score before its row's unit, l, the sum of the weights of a lane's tokens, and out
+// in units of AtUnit's / 2^14.
 template <int HD>
 struct AtRows {
     static constexpr int CB = HD / 16;
@@ -222,53 +228,66 @@ struct AtRows {
     }
 };
 
-// Scores of one lane to weights.  x: N scores of row n in units of log 2; on
-// return e^(s - m).
-template <int N, int HD>
-__device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N])
+// The reference follows where a lane's largest score is more than a factor of two of
+// weight above it.
+template <int HD>
+__device__ __forceinline__ bool at_above(const AtRows<HD>& r, float most, float reach) { return most > r.m + reach; }
+template <int HD>
+__device__ __forceinline__ void at_follow(AtRows<HD>& r, float most, float unit)
+{
+    most = fmaxf(most, __shfl_xor(most, 16, 64));
+    most = fmaxf(most, __shfl_xor(most, 32, 64));
+    const float to = fmaxf(most, r.m), f = __builtin_amdgcn_exp2f((r.m - to) * unit);
+    r.m = to;
+    r.l *= f;
+    r.times(f);
+}
+template <int N>
+__device__ __forceinline__ float at_largest(const float (&x)[N])
 {
     float most = x[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
-    if (__ballot(most > r.m + 1.0f) != 0) {
-        most = fmaxf(most, __shfl_xor(most, 16, 64));
-        most = fmaxf(most, __shfl_xor(most, 32, 64));
-        const float to = fmaxf(most, r.m), f = __builtin_amdgcn_exp2f(r.m - to);
-        r.m = to;
-        r.l *= f;
-        r.times(f);
-    }
+    return most;
+}
+// Scores to weights e^(s - m).
+template <int N, int HD>
+__device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N], float unit)
+{
+    const float m = r.m * unit;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(x[i] - r.m);
-        r.l += x[i];
-    }
+    for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], unit, -m));
+    // (in pairs: half the additions wait for the sum)
+#pragma unroll
+    for (int i = 0; i < N; i += 2) r.l += x[i] + x[i + 1];
 }
 
 // Which of 64 tokens a row sees: those that are there (`ok`) and lie before `limit`;
-// bit 0 is a lane's first token, 4 g.  (A weight of zero is not multiplied with its
-// token's scale, which may be no number.)
+// bit 0 is a lane's first token, 4 g.
 __device__ __forceinline__ unsigned long long at_seen(unsigned long long ok, int limit, int g)
 {
     const int n = min(max(limit, 0), 64);
     return (n == 64 ? ok : ok & ((1ull << n) - 1)) >> (4 * g);
 }
 
-// The largest values' scale so far, as a power of two, for a wave.  Scales that are
-// not finite do not count: their weights are not finite in their own rows.
+// A values' scale that is no number as the largest one: nothing of a row that does not
+// see its token, and not finite in one that does.
+__device__ __forceinline__ float at_number(float v) { return fmaxf(fminf(v, -AT_LOWEST), AT_LOWEST); }
+
+// The largest values' scale so far, as a power of two, for a wave.  Scales above 2^120
+// do not count, as they are no numbers.
 struct AtUnit {
     float unit = 0x1p-100f;
     // raised to hold `v` (any lane's); the factor for what was summed in the old one
     __device__ __forceinline__ bool raise(float v, float& f)
     {
         v = fabsf(v);
-        const bool more = v > unit && v < INFINITY;
+        const bool more = v > unit && v < 0x1p120f;
         if (__ballot(more) == 0) return false;
         float most = more ? v : unit;
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-        // the next power of two (the largest ones: 2^127)
-        const unsigned e = min((__float_as_uint(most) >> 23) + 1, 254u);
+        const unsigned e = (__float_as_uint(most) >> 23) + 1;  // the next power of two
         const float to = __uint_as_float(__builtin_amdgcn_readfirstlane(e << 23));
         f = unit / to;
         unit = to;
@@ -337,10 +356,11 @@ __device__ __forceinline__ void at_write(const AtRows<HD>& r, const AtLanes<HD>&
 // A tile of 16 rows, of which the lanes' is the job's row n, to out or to its part.
 template <class T, int HD>
 __device__ __forceinline__ void at_finish(const AttnArgs<T>& a, const AtJob& job, const AtLanes<HD>& at,
-                                          AtRows<HD>& r, const AtUnit& unit, int n, float* slab)
+                                          AtRows<HD>& r, float row_unit, const AtUnit& unit, int n, float* slab)
 {
     const int hd = a.p.hd;
     r.whole();
+    r.m = r.l == 0.0f ? AT_LOWEST : r.m * row_unit;
     if (n >= job.rows) return;
     const float f = r.l == 0.0f ? 0.0f : unit.unit * AT_DOWN;
     if (slab != nullptr) {
@@ -404,7 +424,7 @@ struct AtNarrow {
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
             c.ks = a.ks[row];
-            c.vs = a.vs[row];
+            c.vs = at_number(a.vs[row]);
         }
         if (lane < STEP) tok.row[lane] = max(row, 0);
         at_wave_sync();
@@ -440,22 +460,20 @@ struct AtNarrow {
             const at_f4 vs = *(const at_f4*)&tok.vs[16 * i + 4 * at.g];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[4 * i + e] = s[e] * ks[e] * q.unit;
+                x[4 * i + e] = s[e] * ks[e];
                 w[4 * i + e] = vs[e];
             }
         }
-        if ((unsigned)c.ok == ~0u && base + STEP <= least) {
-            at_weigh(r, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= x[i];
-        } else {
+        if ((unsigned)c.ok != ~0u || base + STEP > least) {
             const unsigned mask = (unsigned)at_seen(c.ok, limit - base, at.g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = mask >> (i / 4 * 16 + i % 4) & 1 ? x[i] : -INFINITY;
-            at_weigh(r, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = x[i] == 0.0f ? 0.0f : x[i] * w[i];
         }
+        const float most = at_largest(x);
+        if (__ballot(at_above(r, most, q.reach)) != 0) at_follow(r, most, q.unit);
+        at_weigh(r, x, q.unit);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= x[i];
         const at_h8 p = at_round(w);
         at_h8 rest;
         if constexpr (SPLIT) rest = at_rest(w, p);
@@ -504,7 +522,7 @@ struct AtNarrow {
             step(c[0], c[1], lds[0], lds[1], s);
             if (s + 1 < count) step(c[1], c[0], lds[1], lds[0], s + 1);
         }
-        at_finish(a, job, at, r, unit, at.n, slab);
+        at_finish(a, job, at, r, q.unit, unit, at.n, slab);
     }
 };
 
@@ -517,6 +535,7 @@ struct AtWide {
         at_h8 k[4][NF][64];     // keys of 16 tokens each, as the lanes read them
         at_h8 v[2][CB][64];     // values of 32 tokens each
         float ks[64], vs[64];
+        float top[4];           // of each wave's tokens, the largest values' scale
         unsigned short ok[4];   // tokens that are there
     };
     struct Lds {
@@ -553,7 +572,7 @@ struct AtWide {
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
             c.ks = a.ks[row];
-            c.vs = a.vs[row];
+            c.vs = at_number(a.vs[row]);
         }
         row = max(row, 0);
         at_keys<HD>(a.k + (size_t)row * a.ldk, at, c.k);
@@ -589,7 +608,13 @@ struct AtWide {
             s.ks[wave * 16 + lane] = c.ks;
             s.vs[wave * 16 + lane] = c.vs;
         }
-        if (lane == 0) s.ok[wave] = (unsigned short)ok;
+        float top = fabsf(c.vs) < 0x1p120f ? fabsf(c.vs) : 0.0f;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        if (lane == 0) {
+            s.ok[wave] = (unsigned short)ok;
+            s.top[wave] = top;
+        }
     }
     template <int TILES>
     __device__ __forceinline__ void compute(const Step& s, int base)
@@ -615,41 +640,44 @@ struct AtWide {
 #pragma unroll
             for (int i = 0; i < TILES; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e] * q[i].unit;
-            __builtin_amdgcn_sched_barrier(0);  // (operands of one step in registers, not of all)
+                for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e];
         }
-        float v = 0.0f, f;
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v = fabsf(vs[sub][e]) < INFINITY ? fmaxf(v, fabsf(vs[sub][e])) : v;
-        if (unit.raise(v, f))
+        float f;
+        if (unit.raise(s.top[lane & 3], f))
 #pragma unroll
             for (int i = 0; i < TILES; ++i) r[i].times(f);
-        const float up = unit.up();
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
         unsigned long long ok;
         __builtin_memcpy(&ok, s.ok, 8);
-        const bool all = ok == ~0ull && base + STEP <= least;
-        at_h8 p[TILES][2], rest[TILES][SPLIT ? 2 : 1];
+        if (ok != ~0ull || base + STEP > least) {
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            if (!all) {
+            for (int i = 0; i < TILES; ++i) {
                 const unsigned long long mask = at_seen(ok, limit[i] - base, at.g);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[i][e] = mask >> (e / 4 * 16 + e % 4) & 1 ? x[i][e] : -INFINITY;
             }
-            at_weigh(r[i], x[i]);
+        }
+        float most[TILES];
+        bool above = false;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            most[i] = at_largest(x[i]);
+            above |= at_above(r[i], most[i], q[i].reach);
+        }
+        if (__ballot(above) != 0)
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) at_follow(r[i], most[i], q[i].unit);
+        const float up = unit.up();
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
+        at_h8 p[TILES][2], rest[TILES][SPLIT ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            at_weigh(r[i], x[i], q[i].unit);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = x[i][8 * h + e] * vs[2 * h + e / 4][e % 4];
-                if (!all) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = x[i][8 * h + e] == 0.0f ? 0.0f : w[e];
-                }
                 p[i][h] = at_round(w);
                 if constexpr (SPLIT) rest[i][h] = at_rest(w, p[i][h]);
             }
@@ -664,7 +692,7 @@ struct AtWide {
                     r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
                     if constexpr (SPLIT) r[i].o[j] = at_product(c, rest[i][h], r[i].o[j]);
                 }
-                if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+
             }
     }
     __device__ __forceinline__ void run(int from, int to, float* slab)
@@ -706,8 +734,8 @@ struct AtWide {
                 }
             }
         }
-        at_finish(a, job, at, r[0], unit, first + at.n, slab);
-        if (tiles == 2) at_finish(a, job, at, r[1], unit, first + 16 + at.n, slab);
+        at_finish(a, job, at, r[0], q[0].unit, unit, first + at.n, slab);
+        if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, unit, first + 16 + at.n, slab);
         __syncthreads();
     }
 };
@@ -720,30 +748,30 @@ constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
 template <class T, int HD, bool MIXED>
 __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T> a)
 {
-    struct Narrow {
+    struct None {};
+    __shared__ union {
+        AtScan<MIXED> scan;  // until the cursor is there
         typename AtNarrow<T, HD>::Lds narrow;
-    };
-    union Both {
-        typename AtNarrow<T, HD>::Lds narrow;
-        typename AtWide<T, HD>::Lds wide;
-    };
-    __shared__ AtScan<MIXED> scan;
-    __shared__ typename std::conditional<MIXED, Both, Narrow>::type lds;
+        typename std::conditional<MIXED, typename AtWide<T, HD>::Lds, None>::type wide;
+    } lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AtLanes<HD> at(a.p.hd);
     // Workgroups b, b + 8, ... are of one die: they have pieces side by side.
-    int b = (int)blockIdx.x;
+    int worker = (int)blockIdx.x % 8 * (a.p.grid / 8);
+    const int turn = (int)blockIdx.x / 8;
     AtJob job;
     int from, to, slab;
     if constexpr (MIXED) {
-        // Every other one takes wide jobs: where there are both, a compute unit runs one
-        // that waits for memory beside one that computes.
-        const bool wide = b / 8 % 2 == 0;
-        b = b / 16 * 8 + b % 8;
+        // Half of them take wide jobs: where there are both kinds, a compute unit runs one
+        // that computes beside one that waits for memory.  A die deals its workgroups to
+        // its four engines in turn, and waits for one that is full: engines get four of a
+        // kind at a time (every other one wide left half the engines idle).
+        const bool wide = ((turn >> 2 ^ turn >> 5) & 1) == 0;
+        worker += (turn >> 3) * 4 + (turn & 3);
         if (wide) {
-            const int worker = a.p.grid % 8 == 0 ? b % 8 * (a.p.grid / 8) + b / 8 : b;
-            const AtLines<true> lines(a.p, scan);
-            AtCursor<true, true> cursor(a.p, scan, lines, worker, a.p.grid);
+            const AtLines<true> lines(a.p, lds.scan);
+            AtCursor<true, true> cursor(a.p, lds.scan, lines, worker, a.p.grid);
+            __syncthreads();
             while (cursor.next(a.p, job, from, to, slab)) {
                 float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
                 AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
@@ -752,9 +780,10 @@ __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T>
             return;
         }
     }
-    const int worker = a.p.grid % 8 == 0 ? b % 8 * (a.p.grid / 8) + b / 8 : b;
-    const AtLines<MIXED> lines(a.p, scan);
-    AtCursor<MIXED, false> cursor(a.p, scan, lines, worker * 4 + wave, a.p.grid * 4);
+    if constexpr (!MIXED) worker += turn;
+    const AtLines<MIXED> lines(a.p, lds.scan);
+    AtCursor<MIXED, false> cursor(a.p, lds.scan, lines, worker * 4 + wave, a.p.grid * 4);
+    __syncthreads();
     while (cursor.next(a.p, job, from, to, slab)) {
         float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
         AtNarrow<T, HD> w{a, job, at, lds.narrow.tokens[wave], a.p.table + (size_t)job.table * a.p.ldt, lane};

@@ -60,8 +60,11 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
         // no more than there can be pieces
         const long long jobs = ((long long)p.rows * p.share / AT_WIDE + p.seqs) * p.kvheads;
         const long long tiles = p.whole ? 1 : (long long)p.ldt * p.ps / AT_TILE[0] + 1 + AT_OVER;
-        const long long most = MIXED ? (jobs * tiles + p.groups + 7) / 8 * 8 : (jobs * tiles + 3) / 4;
-        p.grid = (int)std::min((long long)std::min(resident, AT_GRID), std::max(1ll, most));
+        // (as many for every die, and for the four engines of each)
+        const long long most = MIXED ? jobs * tiles + p.groups : (jobs * tiles + 3) / 4;
+        const long long step = MIXED ? 32 : 8;
+        p.grid = (int)std::min(std::min((long long)resident, (long long)AT_GRID) / step * step,
+                               std::max(1ll, (most + step - 1) / step) * step);
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
             p.own = reinterpret_cast<int2*>(at);
