@@ -56,7 +56,6 @@ struct AttnArgs {
     float scale;  // times log2(e): scores are kept in units of log 2
     int ldq, ldk, ldv, ldo;
     float* slabs;  // parts of jobs (see AtPlan)
-    int per;       // of the join: rows and heads that a wave looks at
 };
 
 constexpr float AT_LN2 = 0.6931471805599453f;
@@ -163,16 +162,26 @@ struct AtQuery {
     at_h8 hi[NF], lo[SPLIT ? NF : 1];
     float unit;   // score = sum of products * key's scale * unit, which is above zero
     float reach;  // 1 / unit
-    __device__ __forceinline__ void load(const T* row, bool some, const AtLanes<HD>& a, int hd, float scale)
+    typedef T raw __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    raw in[NF];
+    // on their way
+    __device__ __forceinline__ void fetch(const T* row, bool some, const AtLanes<HD>& a, int hd)
+    {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            in[f] = raw{};
+            if (some && f / 2 * 64 + a.g * 16 < hd) in[f] = *(const raw*)(row + a.koff[f / 2] + (f & 1) * 8);
+        }
+    }
+    __device__ __forceinline__ void convert(const AtLanes<HD>& a, int hd, float scale)
     {
         float v[NF][8], most = 0.0f;
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
             const int from = a.koff[f / 2] + (f & 1) * 8, at = f / 2 * 64 + a.g * 16;
-            q8_load(row + from, some && at < hd ? 8 : 0, v[f]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (from + e < at) v[f][e] = 0.0f;
+                v[f][e] = from + e < at ? 0.0f : (float)in[f][e];
                 most = __builtin_elementwise_maximum(most, __builtin_fabsf(v[f][e]));
             }
         }
@@ -329,6 +338,14 @@ __device__ __forceinline__ at_h8 at_column(const int (&v)[8][N])
     const at_h2 a = at_pair<B>(v[0][W], v[1][W]), b = at_pair<B>(v[2][W], v[3][W]);
     const at_h2 c = at_pair<B>(v[4][W], v[5][W]), d = at_pair<B>(v[6][W], v[7][W]);
     return (at_h8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A barrier for what is in LDS: loads and stores of memory go on.
+__device__ __forceinline__ void at_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // A row's results to out and lse.
@@ -499,22 +516,21 @@ struct AtNarrow {
         r.clear();
         const int count = (to - from + STEP - 1) / STEP;
         Codes c[2];
-        int page = page_of(from + lane);
+        const int page = page_of(from + lane);
+        int later = page_of(from + STEP + lane);
         size_t row = 0;
         const bool some = at.n < job.rows;
         const int head = job.place(a.p, some ? at.n : 0, row);
-        if (count > 0) {
-            fetch(c[0], lds[0], from, page);
-            page = page_of(from + STEP + lane);
-        }
-        q.load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
+        q.fetch(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd);
         limit = some ? job.limit(a.p, at.n) : 0x7fffffff;
+        if (count > 0) fetch(c[0], lds[0], from, page);
+        q.convert(at, a.p.hd, a.scale);
         least = at_least(limit);
         auto step = [&](Codes& now, Codes& next, AtTokens& tn, AtTokens& tx, int s) {
             const int base = from + s * STEP;
             if (s + 1 < count) {
-                fetch(next, tx, base + STEP, page);
-                page = page_of(base + 2 * STEP + lane);
+                fetch(next, tx, base + STEP, later);
+                later = page_of(base + 2 * STEP + lane);
             }
             compute(now, tn, base);
         };
@@ -700,43 +716,46 @@ struct AtWide {
         // few rows are dealt 16 to a wave, so that all waves have some
         tiles = job.rows > 64 ? 2 : 1;
         first = wave * 16 * tiles;
-        least = 0x7fffffff;
-        most = 0;
+        const int mine = wave * 16 + at.n, page = page_of(from + mine);
+        int later = page_of(from + STEP + mine);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int n = first + 16 * i + at.n;
             const bool some = i < tiles && n < job.rows;
             size_t row = 0;
             const int head = job.place(a.p, some ? n : 0, row);
-            q[i].load(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd, a.scale);
+            q[i].fetch(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd);
             limit[i] = some ? job.limit(a.p, n) : 0x7fffffff;
-            least = min(least, at_least(limit[i]));
-            most = max(most, at_most(some ? limit[i] : 0));
             r[i].clear();
         }
         Codes c;
-        const int mine = wave * 16 + at.n;
-        if (from < to) {
-            fetch(c, from, page_of(from + mine));
-            int page = page_of(from + STEP + mine), p = 0;
-            for (int base = from; base < to; base += STEP, p ^= 1) {
-                share(c, lds.step[p]);
-                __syncthreads();
-                if (base + STEP < to) {
-                    fetch(c, base + STEP, page);
-                    page = page_of(base + 2 * STEP + mine);
-                }
-                if (base < most) {
-                    if (tiles == 2)
-                        compute<2>(lds.step[p], base);
-                    else
-                        compute<1>(lds.step[p], base);
-                }
+        if (from < to) fetch(c, from, page);
+        least = 0x7fffffff;
+        most = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            q[i].convert(at, a.p.hd, a.scale);
+            least = min(least, at_least(limit[i]));
+            most = max(most, at_most(limit[i] == 0x7fffffff ? 0 : limit[i]));
+        }
+        int p = 0;
+        for (int base = from; base < to; base += STEP, p ^= 1) {
+            share(c, lds.step[p]);
+            at_barrier();
+            if (base + STEP < to) {
+                fetch(c, base + STEP, later);
+                later = page_of(base + 2 * STEP + mine);
+            }
+            if (base < most) {
+                if (tiles == 2)
+                    compute<2>(lds.step[p], base);
+                else
+                    compute<1>(lds.step[p], base);
             }
         }
         at_finish(a, job, at, r[0], q[0].unit, unit, first + at.n, slab);
         if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, unit, first + 16 + at.n, slab);
-        __syncthreads();
+        at_barrier();
     }
 };
 
@@ -745,45 +764,47 @@ struct AtWide {
 template <class T, int HD>
 constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
 
-template <class T, int HD, bool MIXED>
-__global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T> a)
+// Workgroups b, b + 8, ... are of one die: their pieces lie side by side.
+__device__ __forceinline__ int at_worker(const AtPlan& p)
 {
-    struct None {};
+    return (int)blockIdx.x % 8 * (p.grid / 8) + (int)blockIdx.x / 8;
+}
+
+template <class T, int HD>
+__global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn_wide(AttnArgs<T> a)
+{
     __shared__ union {
-        AtScan<MIXED> scan;  // until the cursor is there
-        typename AtNarrow<T, HD>::Lds narrow;
-        typename std::conditional<MIXED, typename AtWide<T, HD>::Lds, None>::type wide;
+        AtScan<AT_WIDE_JOBS> scan;  // until the cursor is there
+        typename AtWide<T, HD>::Lds wide;
     } lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const AtLanes<HD> at(a.p.hd);
-    // Workgroups b, b + 8, ... are of one die: they have pieces side by side.
-    int worker = (int)blockIdx.x % 8 * (a.p.grid / 8);
-    const int turn = (int)blockIdx.x / 8;
+    const AtLines<AT_WIDE_JOBS> lines(a.p, lds.scan);
+    AtCursor<AT_WIDE_JOBS> cursor(a.p, lds.scan, lines, at_worker(a.p), a.p.grid);
+    __syncthreads();
     AtJob job;
     int from, to, slab;
-    if constexpr (MIXED) {
-        // Half of them take wide jobs: where there are both kinds, a compute unit runs one
-        // that computes beside one that waits for memory.  A die deals its workgroups to
-        // its four engines in turn, and waits for one that is full: engines get four of a
-        // kind at a time (every other one wide left half the engines idle).
-        const bool wide = ((turn >> 2 ^ turn >> 5) & 1) == 0;
-        worker += (turn >> 3) * 4 + (turn & 3);
-        if (wide) {
-            const AtLines<true> lines(a.p, lds.scan);
-            AtCursor<true, true> cursor(a.p, lds.scan, lines, worker, a.p.grid);
-            __syncthreads();
-            while (cursor.next(a.p, job, from, to, slab)) {
-                float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
-                AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
-                w.run(from, to, part);
-            }
-            return;
-        }
+    while (cursor.next(a.p, job, from, to, slab)) {
+        float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
+        AtWide<T, HD> w{a, job, at, lds.wide, a.p.table + (size_t)job.table * a.p.ldt, lane, wave};
+        w.run(from, to, part);
     }
-    if constexpr (!MIXED) worker += turn;
-    const AtLines<MIXED> lines(a.p, lds.scan);
-    AtCursor<MIXED, false> cursor(a.p, lds.scan, lines, worker * 4 + wave, a.p.grid * 4);
+}
+
+template <class T, int HD, AtKind KIND>
+__global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn_narrow(AttnArgs<T> a)
+{
+    __shared__ union {
+        AtScan<KIND> scan;  // until the cursor is there
+        typename AtNarrow<T, HD>::Lds narrow;
+    } lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const AtLanes<HD> at(a.p.hd);
+    const AtLines<KIND> lines(a.p, lds.scan);
+    AtCursor<KIND> cursor(a.p, lds.scan, lines, at_worker(a.p) * 4 + wave, a.p.grid * 4);
     __syncthreads();
+    AtJob job;
+    int from, to, slab;
     while (cursor.next(a.p, job, from, to, slab)) {
         float* part = slab < 0 ? nullptr : a.slabs + (size_t)slab * at_slab(a.p.hd);
         AtNarrow<T, HD> w{a, job, at, lds.narrow.tokens[wave], a.p.table + (size_t)job.table * a.p.ldt, lane};
@@ -791,88 +812,100 @@ __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn(AttnArgs<T>
     }
 }
 
-// Adds the parts of rows' results.  A wave looks at `per` rows and heads at once for
-// those that have parts; WAVES waves share the parts of each.
-template <class T, int WAVES>
+// Adds the parts of rows' results.  LANES lanes have a row and head, four of its codes
+// each, and with WAVES of four all waves of a workgroup share its parts.
+template <class T, int LANES, int WAVES>
 __global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
 {
-    constexpr int NE = AT_HD / 64, U = 4;
-    __shared__ float sums[WAVES > 1 ? 4 : 1][AT_HD + 2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd, mine = WAVES > 1 ? wave : 0;
+    constexpr int U = 4, ITEMS = 64 / LANES * (4 / WAVES);
+    __shared__ float sums[WAVES > 1 ? 4 : 1][64][6];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd;
+    const int d = threadIdx.x % LANES * 4, have = min(hd - d, 4);
     const long long all = (long long)a.p.rows * a.p.heads;
-    const long long first = ((long long)blockIdx.x * (4 / WAVES) + (WAVES > 1 ? 0 : wave)) * a.per, at = first + lane;
+    const long long item = (long long)blockIdx.x * ITEMS + (WAVES > 1 ? lane : (int)threadIdx.x) / LANES;
     int2 own{0, 0}, shared{0, 0};
-    if (lane < a.per && at < all) {
-        own = a.p.own[at];
-        if (a.p.groups > 0) shared = a.p.shared_parts[at];
-        if (a.p.start != nullptr) {
-            // rows outside the sequences hold what an earlier call left there
-            const long long row = at / a.p.heads;
-            if (row < a.p.start[0] || row >= a.p.start[a.p.seqs]) own.y = 0;
-        }
+    size_t row = 0;
+    if (item < all) {
+        own = a.p.own[item];
+        if (a.p.groups > 0) shared = a.p.shared_parts[item];
+        row = item / a.p.heads;
+        // rows outside the sequences hold what an earlier call left there
+        if (a.p.start != nullptr && ((long long)row < a.p.start[0] || (long long)row >= a.p.start[a.p.seqs])) own.y = 0;
     }
     if (!(own.y >> 24 & 1)) shared.y = 0;
-    for (unsigned long long todo = __ballot(own.y != 0); todo != 0; todo &= todo - 1) {
-        const int from = __builtin_ctzll(todo);
-        const size_t item = first + from, row = item / a.p.heads;
-        const int head = (int)(item % a.p.heads);
-        float m = AT_LOWEST, l = 0.0f, o[NE] = {};
-        auto add = [&](int2 where) {
-            const int count = where.y & 0xffff, n = where.y >> 16 & 15;
-            const long long last = a.p.slabs - 1;
-            auto slab = [&](int i) { return a.slabs + min(max(at_part(where, i), 0ll), last) * at_slab(hd); };
-            for (int base = mine; base < count; base += WAVES * U) {
-                float pm[U], pl[U], v[U][NE];
+    float m = AT_LOWEST, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](int2 where) {
+        const int count = where.y & 0xffff, n = where.y >> 16 & 15;
+        for (int base = WAVES > 1 ? wave : 0; base < count; base += WAVES * U) {
+            float pm[U], pl[U], v[U][4];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = base + u * WAVES;
-                    const float* s = slab(min(i, count - 1));
-                    pm[u] = i < count ? s[2 * n] : AT_LOWEST;
-                    pl[u] = i < count ? s[2 * n + 1] : 0.0f;
+            for (int u = 0; u < U; ++u) {
+                const int i = base + u * WAVES;
+                pm[u] = AT_LOWEST;
+                pl[u] = v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.0f;
+                if (i < count) {
+                    const long long at = min(max(at_part(where, i), 0ll), (long long)a.p.slabs - 1);
+                    const float* s = a.slabs + at * at_slab(hd);
+                    pm[u] = s[2 * n];
+                    pl[u] = s[2 * n + 1];
+                    s += 2 * AT_NARROW + n * hd + d;
+                    if (have == 4) {
+                        typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+                        const vec x = *(const vec*)s;
 #pragma unroll
-                    for (int e = 0; e < NE; ++e)
-                        v[u][e] = lane + 64 * e < hd ? s[2 * AT_NARROW + (size_t)n * hd + lane + 64 * e] : 0.0f;
-                }
+                        for (int e = 0; e < 4; ++e) v[u][e] = x[e];
+                    } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float to = fmaxf(m, pm[u]);
-                    const float f = __builtin_amdgcn_exp2f(m - to);
-                    // (a part without tokens, or none: what its place holds does not count)
-                    const float g = pl[u] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm[u] - to);
-                    m = to;
-                    l = l * f + pl[u] * g;
-#pragma unroll
-                    for (int e = 0; e < NE; ++e) o[e] = o[e] * f + (pl[u] == 0.0f ? 0.0f : v[u][e] * g);
+                        for (int e = 0; e < 4; ++e)
+                            if (e < have) v[u][e] = s[e];
+                    }
                 }
             }
-        };
-        add(make_int2(at_lane(own.x, from), at_lane(own.y, from)));
-        add(make_int2(at_lane(shared.x, from), at_lane(shared.y, from)));
-        if constexpr (WAVES > 1) {
-            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < NE; ++e) sums[wave][lane + 64 * e] = o[e];
-            if (lane == 0) {
-                sums[wave][AT_HD] = m;
-                sums[wave][AT_HD + 1] = l;
-            }
-            __syncthreads();
-            if (wave != 0) continue;
-            for (int w = 1; w < WAVES; ++w) {
-                const float pm = sums[w][AT_HD], to = fmaxf(m, pm);
-                const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(pm - to);
+            for (int u = 0; u < U; ++u) {
+                const float to = fmaxf(m, pm[u]), f = __builtin_amdgcn_exp2f(m - to);
+                // (a part without tokens, or none: what its place holds does not count)
+                const float g = pl[u] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm[u] - to);
                 m = to;
-                l = l * f + sums[w][AT_HD + 1] * g;
+                l = l * f + pl[u] * g;
 #pragma unroll
-                for (int e = 0; e < NE; ++e) o[e] = o[e] * f + sums[w][lane + 64 * e] * g;
+                for (int e = 0; e < 4; ++e) o[e] = o[e] * f + (pl[u] == 0.0f ? 0.0f : v[u][e] * g);
             }
         }
-        T* out = a.out + row * a.ldo + (size_t)head * hd;
+    };
+    add(own);
+    add(shared);
+    if constexpr (WAVES > 1) {
+        float(&mine)[6] = sums[wave][lane];
 #pragma unroll
-        for (int e = 0; e < NE; ++e)
-            if (lane + 64 * e < hd) out[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
-        if (lane == 0) at_lse(a, row, head, m, l);
+        for (int e = 0; e < 4; ++e) mine[e] = o[e];
+        mine[4] = m;
+        mine[5] = l;
+        __syncthreads();
+        if (wave != 0) return;
+        for (int w = 1; w < WAVES; ++w) {
+            const float(&p)[6] = sums[w][lane];
+            const float to = fmaxf(m, p[4]), f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(p[4] - to);
+            m = to;
+            l = l * f + p[5] * g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = o[e] * f + p[e] * g;
+        }
     }
+    if (own.y == 0) return;
+    const int head = (int)(item - (long long)row * a.p.heads);
+    if (d == 0) at_lse(a, row, head, m, l);
+    T* out = a.out + row * a.ldo + (size_t)head * hd + d;
+    typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    vec x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
+    if (have == 4)
+        *(vec*)out = x;
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < have) out[e] = x[e];
 }
 
 }  // namespace xsymv

@@ -8,8 +8,8 @@
 // entry has no more (narrow), else of 128 (wide).
 //
 // There are two lines of jobs, one after the other by entry, head and block: wide
-// jobs, of which every workgroup takes an equal piece, and narrow ones, of which
-// every wave does.  Lines are counted in tiles (32 tokens of a narrow job, 64 of a
+// jobs, of which every workgroup of q8_attn_wide takes an equal piece, and narrow
+// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens of a narrow job, 64 of a
 // wide one): a job's tiles come first in its stretch of the line, then some that
 // stand for what a job takes besides.  Stretches may be longer than need be, but have
 // to be the same for all workers, which compute them from the arrays on the device,
@@ -61,7 +61,7 @@ struct AtPlan {
     const int *start, *len, *table, *first, *shared;
     int rows, heads, kvheads, share, hd, seqs, ldt, groups, pages, ps;
     AtDivisor by_share, by_page;
-    int grid;   // workgroups of each kind
+    int grid;   // workgroups
     int whole;  // no job is cut, nothing is shared: no workspace
     // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
     // narrow ones', two a wave; of whole parts) and, for each row and head, where its
@@ -69,7 +69,7 @@ struct AtPlan {
     int slabs, narrow_at, whole_at;
     int2 *own, *shared_parts;
 
-    __device__ __forceinline__ int entries() const { return groups + seqs; }
+    int wide_entries;  // of the first, those that can be wide
     __device__ __forceinline__ int room() const { return (int)min((long long)ldt * ps, 0x7fffff00ll); }
     __device__ __forceinline__ int length(int s) const { return min(max(len[s], 0), room()); }
     __device__ __forceinline__ int row_of(int s) const
@@ -94,6 +94,7 @@ struct AtEntry {
     int before;      // tokens before the first row's own (a sequence's)
     int table;       // the row of the table that is read
     int wide, group, joined;
+    int mine;  // whether its jobs are of the kernel's kind
     int cost;  // tiles of one head
 
     __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
@@ -164,10 +165,14 @@ __device__ __forceinline__ int at_shared(const AtPlan& p, int s)
     return g.pays && s >= g.s0 && s < g.s1 ? g.tokens : 0;
 }
 
-// MIXED: the call has groups, several rows a sequence or many heads that share keys.
-template <bool MIXED>
+// Which jobs a kernel makes: wide ones, narrow ones, or all of a call that has neither
+// groups nor several rows a sequence nor many heads that share keys.
+enum AtKind { AT_WIDE_JOBS, AT_NARROW_JOBS, AT_SINGLE_JOBS };
+
+template <AtKind KIND>
 __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
 {
+    constexpr bool MIXED = KIND != AT_SINGLE_JOBS;
     AtEntry x{};
     if (MIXED && e < p.groups) {
         x.group = x.joined = 1;
@@ -198,6 +203,7 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
     }
     x.wide = MIXED && x.rows > AT_NARROW;
     x.cost = x.before_block(p, x.blocks());
+    x.mine = MIXED ? x.wide == (KIND == AT_WIDE_JOBS) : 1;
     return x;
 }
 
@@ -222,10 +228,10 @@ struct AtJob {
     }
 };
 
-// Sums of 64 entries each: narrow tiles, wide tiles, slabs.
-template <bool MIXED>
+// Sums of 64 entries each: tiles, slabs.
+template <AtKind KIND>
 struct AtScan {
-    int sums[MIXED ? 3 : 1][AT_WINDOWS];
+    int sums[KIND == AT_SINGLE_JOBS ? 1 : 2][AT_WINDOWS];
 };
 
 // Least and largest of a number that lanes n, n + 16, ... have alike.
@@ -275,64 +281,60 @@ __device__ __forceinline__ int at_sums(int v)
 }
 
 // 64 entries, one a lane, and their sums up to and with the lane's.
-template <bool MIXED>
+template <AtKind KIND>
 struct AtWindow {
-    static constexpr int N = MIXED ? 3 : 1;
+    static constexpr int N = KIND == AT_SINGLE_JOBS ? 1 : 2;
     AtEntry x;
-    int own[N], sums[N];  // narrow tiles, wide tiles, slabs
+    int own[N], sums[N];  // tiles, slabs
+    static __device__ __forceinline__ int entries(const AtPlan& p)
+    {
+        return KIND == AT_WIDE_JOBS ? p.wide_entries : p.groups + p.seqs;
+    }
     __device__ __forceinline__ void load(const AtPlan& p, int window)
     {
         const int e = window * 64 + (threadIdx.x & 63);
         x = AtEntry{};
-        if (e < p.entries()) x = at_entry<MIXED>(p, e);
-        const int cost = x.cost * p.kvheads;
-        own[0] = x.wide ? 0 : cost;
-        if constexpr (MIXED) {
-            own[1] = x.wide ? cost : 0;
-            own[2] = x.slabs() * p.kvheads;
-        }
+        if (e < entries(p)) x = at_entry<KIND>(p, e);
+        own[0] = x.mine ? x.cost * p.kvheads : 0;
+        if constexpr (N > 1) own[1] = x.slabs() * p.kvheads;
 #pragma unroll
         for (int i = 0; i < N; ++i) sums[i] = at_sums(own[i]);
     }
     __device__ __forceinline__ int all(int i) const { return at_lane(sums[i], 63); }
 };
 
-// The whole lines: their lengths, and with more than 64 entries the windows' sums.
-template <bool MIXED>
+// The whole line: its length, and with more than 64 entries the windows' sums.
+template <AtKind KIND>
 struct AtLines {
-    AtWindow<MIXED> w;
-    int total[2], windows;
-    __device__ __forceinline__ AtLines(const AtPlan& p, AtScan<MIXED>& scan)
+    AtWindow<KIND> w;
+    int total, windows;
+    __device__ __forceinline__ AtLines(const AtPlan& p, AtScan<KIND>& scan)
     {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        windows = (p.entries() + 63) / 64;
-        total[1] = 0;
+        windows = (AtWindow<KIND>::entries(p) + 63) / 64;
         if (windows <= 1) {
             w.load(p, 0);
-            total[0] = w.all(0);
-            if constexpr (MIXED) total[1] = w.all(1);
+            total = w.all(0);
             return;
         }
         for (int i = wave; i < windows; i += 4) {
             w.load(p, i);
             if (lane == 63)
 #pragma unroll
-                for (int j = 0; j < AtWindow<MIXED>::N; ++j) scan.sums[j][i] = w.sums[j];
+                for (int j = 0; j < AtWindow<KIND>::N; ++j) scan.sums[j][i] = w.sums[j];
         }
         __syncthreads();
-        total[0] = 0;
-        for (int i = 0; i < windows; i += 64) {
-            const bool some = i + lane < windows;
-            total[0] += at_lane(at_sums(some ? scan.sums[0][i + lane] : 0), 63);
-            if constexpr (MIXED) total[1] += at_lane(at_sums(some ? scan.sums[1][i + lane] : 0), 63);
-        }
+        total = 0;
+        for (int i = 0; i < windows; i += 64)
+            total += at_lane(at_sums(i + lane < windows ? scan.sums[0][i + lane] : 0), 63);
     }
 };
 
 // A worker's way through its piece of a line: a wave's (narrow jobs) or a
 // workgroup's (wide ones).
-template <bool MIXED, bool WIDE>
+template <AtKind KIND>
 struct AtCursor {
+    static constexpr bool WIDE = KIND == AT_WIDE_JOBS, MIXED = KIND != AT_SINGLE_JOBS;
     static constexpr int TILE = AT_TILE[WIDE];
     int pos, end, quota;
     int base, slab;  // where the window's tiles, and its whole parts, begin
@@ -340,12 +342,12 @@ struct AtCursor {
     int first, parts;  // the same of the entry
     AtEntry of;
 
-    __device__ __forceinline__ AtCursor(const AtPlan& p, const AtScan<MIXED>& scan, const AtLines<MIXED>& lines,
+    __device__ __forceinline__ AtCursor(const AtPlan& p, const AtScan<KIND>& scan, const AtLines<KIND>& lines,
                                         int worker_, int workers)
     {
-        AtWindow<MIXED> w = lines.w;
+        AtWindow<KIND> w = lines.w;
         worker = worker_;
-        const int lane = threadIdx.x & 63, total = lines.total[WIDE];
+        const int lane = threadIdx.x & 63, total = lines.total;
         // a little more than total / workers, which need not be exact
         quota = (int)((float)total * __builtin_amdgcn_rcpf((float)workers) * 1.00001f) + 1;
         if (!p.whole) quota = max(quota, AT_LEAST);
@@ -358,10 +360,10 @@ struct AtCursor {
         if (windows > 1) {
             for (int i = 0; i < windows; i += 64) {
                 const bool some = i + lane < windows;
-                const int v = some ? scan.sums[WIDE][i + lane] : 0, sums = at_sums(v);
+                const int v = some ? scan.sums[0][i + lane] : 0, sums = at_sums(v);
                 int part = 0, slabs = 0;
                 if constexpr (MIXED) {
-                    part = some ? scan.sums[2][i + lane] : 0;
+                    part = some ? scan.sums[1][i + lane] : 0;
                     slabs = at_sums(part);
                 }
                 const unsigned long long found = __ballot(base + sums > pos);
@@ -380,14 +382,14 @@ struct AtCursor {
         if (!find(w)) end = pos;
     }
     // The window's entry that holds pos.
-    __device__ __forceinline__ bool find(const AtWindow<MIXED>& w)
+    __device__ __forceinline__ bool find(const AtWindow<KIND>& w)
     {
-        const unsigned long long found = __ballot(base + w.sums[WIDE] > pos);
+        const unsigned long long found = __ballot(base + w.sums[0] > pos);
         if (found == 0) return false;
         const int at = __builtin_ctzll(found);
-        first = base + at_lane(w.sums[WIDE] - w.own[WIDE], at);
+        first = base + at_lane(w.sums[0] - w.own[0], at);
         parts = 0;
-        if constexpr (MIXED) parts = slab + at_lane(w.sums[2] - w.own[2], at);
+        if constexpr (MIXED) parts = slab + at_lane(w.sums[1] - w.own[1], at);
         of.row0 = at_lane(w.x.row0, at);
         of.rows = at_lane(w.x.rows, at);
         of.t0 = at_lane(w.x.t0, at);
@@ -405,11 +407,11 @@ struct AtCursor {
     __device__ __forceinline__ bool settle(const AtPlan& p)
     {
         for (; window < windows; ++window) {
-            AtWindow<MIXED> w;
+            AtWindow<KIND> w;
             w.load(p, window);
             if (find(w)) return true;
-            base += w.all(WIDE);
-            if constexpr (MIXED) slab += w.all(2);
+            base += w.all(0);
+            if constexpr (MIXED) slab += w.all(1);
         }
         return false;
     }

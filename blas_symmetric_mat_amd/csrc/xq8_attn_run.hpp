@@ -41,30 +41,42 @@ struct AttnSpace {
     }
 };
 
-template <class T, int HD, bool MIXED>
+// Workgroups of a kernel: as many for every die, and no more than can have work.
+template <class K>
+int attn_grid(K* kernel, long long most, int& grid)
+{
+    int resident = 0;
+    const int rc = resident_blocks(reinterpret_cast<const void*>(kernel), 256, &resident);
+    grid = (int)std::min(std::min((long long)resident, (long long)AT_GRID) / 8 * 8, std::max(1ll, (most + 7) / 8) * 8);
+    return rc;
+}
+
+template <class T, int LANES>
+int attn_join(const AttnArgs<T>& a, hipStream_t stream, hipEvent_t stop)
+{
+    // Four waves for rows and heads where there are few, which may have many parts.
+    const long long all = (long long)a.p.rows * a.p.heads;
+    const bool few = all <= 4096;
+    const long long each = 64 / LANES * (few ? 1 : 4);
+    XSYMV_HIP(launch_k(few ? &q8_attn_join<T, LANES, 4> : &q8_attn_join<T, LANES, 1>,
+                       dim3((unsigned)((all + each - 1) / each)), dim3(256), stream, a, nullptr, stop));
+    return 0;
+}
+
+template <class T, int HD>
 int attn_launch(AttnArgs<T> a, hipStream_t stream)
 {
     AtPlan& p = a.p;
+    const bool single = p.start == nullptr, mixed = attn_mixed(p.heads, p.kvheads, p.groups, single);
     // Tiles that a line has at most.  (Where an int might not count them, no job is cut;
     // the call takes minutes.)
     const double blocks = (double)p.rows * p.share / AT_WIDE + p.seqs + p.groups;
     const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE[0] + AT_OVER + 2);
     // Sequences of a piece at most are whole as they are: one launch.
     const bool cut = line < 2e9 && (p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST * AT_TILE[0]);
-    const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, p.start == nullptr);
-    int resident = 0;
-    const int rc = resident_blocks(reinterpret_cast<const void*>(&q8_attn<T, HD, MIXED>), 256, &resident);
-    if (rc) return rc;
+    const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, single);
     return q8_with_workspace(cut ? space.bytes : 0, true, stream, [&](void* ws, const TimedCall& tc) -> int {
         p.whole = ws == nullptr;
-        // no more than there can be pieces
-        const long long jobs = ((long long)p.rows * p.share / AT_WIDE + p.seqs) * p.kvheads;
-        const long long tiles = p.whole ? 1 : (long long)p.ldt * p.ps / AT_TILE[0] + 1 + AT_OVER;
-        // (as many for every die, and for the four engines of each)
-        const long long most = MIXED ? jobs * tiles + p.groups : (jobs * tiles + 3) / 4;
-        const long long step = MIXED ? 32 : 8;
-        p.grid = (int)std::min(std::min((long long)resident, (long long)AT_GRID) / step * step,
-                               std::max(1ll, (most + step - 1) / step) * step);
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
             p.own = reinterpret_cast<int2*>(at);
@@ -74,25 +86,30 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
             p.whole_at = (int)space.whole;
             a.slabs = reinterpret_cast<float*>(at + space.parts);
         }
-        XSYMV_HIP(launch_k(&q8_attn<T, HD, MIXED>, dim3(MIXED ? 2 * p.grid : p.grid), dim3(256), stream, a, tc.e0, tc.e1));
+        hipEvent_t start = tc.e0;
+        if (mixed) {
+            // Single tokens of few heads are narrow jobs: only groups' may be wide.
+            p.wide_entries = p.groups + (single && p.share <= AT_NARROW ? 0 : p.seqs);
+            if (p.whole && single && p.share <= AT_NARROW) p.wide_entries = 0;
+            const long long most = p.whole ? (long long)std::min(blocks * p.kvheads, 1e9) : 1ll << 30;
+            const int rc = p.wide_entries > 0 ? attn_grid(&q8_attn_wide<T, HD>, most, p.grid) : 0;
+            if (rc) return rc;
+            if (p.wide_entries > 0) {
+                XSYMV_HIP(launch_k(&q8_attn_wide<T, HD>, dim3(p.grid), dim3(256), stream, a, start, nullptr));
+                start = nullptr;
+            }
+        }
+        // A line of narrow jobs has no more tiles than this.
+        const double tiles = p.whole ? 1.0 : ((double)p.ldt * p.ps / AT_TILE[0] + 1 + AT_OVER) / AT_LEAST;
+        const long long most = (long long)std::min(((double)p.seqs + p.groups) * p.kvheads * tiles / 4 + 1, 1e9);
+        auto* narrow = mixed ? &q8_attn_narrow<T, HD, AT_NARROW_JOBS> : &q8_attn_narrow<T, HD, AT_SINGLE_JOBS>;
+        const int rc = attn_grid(narrow, most, p.grid);
+        if (rc) return rc;
+        XSYMV_HIP(launch_k(narrow, dim3(p.grid), dim3(256), stream, a, start, tc.e1));
         if (p.whole) return 0;
-        // Four waves for a row and head where there are few, else one for several.
-        const long long all = (long long)p.rows * p.heads;
-        const bool few = all <= 4096;
-        a.per = few ? 1 : (int)std::min(std::max(all / 8192, 1ll), 64ll);
-        const long long each = few ? 1 : 4 * a.per;
-        XSYMV_HIP(launch_k(few ? &q8_attn_join<T, 4> : &q8_attn_join<T, 1>, dim3((unsigned)((all + each - 1) / each)),
-                           dim3(256), stream, a, nullptr, tc.e2));
-        return 0;
+        return HD == 64 ? attn_join<T, 16>(a, stream, tc.e2)
+                        : HD == 128 ? attn_join<T, 32>(a, stream, tc.e2) : attn_join<T, 64>(a, stream, tc.e2);
     });
-}
-
-template <class T, int HD>
-int attn_width(const AttnArgs<T>& a, hipStream_t stream)
-{
-    const AtPlan& p = a.p;
-    return attn_mixed(p.heads, p.kvheads, p.groups, p.start == nullptr) ? attn_launch<T, HD, true>(a, stream)
-                                                                        : attn_launch<T, HD, false>(a, stream);
 }
 
 template <class T>
@@ -164,9 +181,9 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     a.ldk = ldk;
     a.ldv = ldv;
     a.ldo = ldo;
-    if (hd <= 64) return attn_width<T, 64>(a, stream);
-    if (hd <= 128) return attn_width<T, 128>(a, stream);
-    return attn_width<T, 256>(a, stream);
+    if (hd <= 64) return attn_launch<T, 64>(a, stream);
+    if (hd <= 128) return attn_launch<T, 128>(a, stream);
+    return attn_launch<T, 256>(a, stream);
 }
 
 }  // namespace xsymv
