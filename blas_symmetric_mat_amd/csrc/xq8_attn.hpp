@@ -27,9 +27,9 @@
 //   narrow jobs (up to 16 rows of q: single tokens): a wave takes 32 tokens at a
 //     time, whose codes come from memory to the registers that the instruction reads
 //     them from.  Waves work by themselves.  Bound by the cache's bytes.
-//   wide jobs (up to 128 rows: a group's tokens, prompts): each wave of a workgroup
+//   wide jobs (up to 256 rows: a group's tokens, prompts): each wave of a workgroup
 //     has 16 or 32 rows and every token; the waves make operands of 16 tokens each
-//     and share them through LDS, so that codes are converted once for 128 rows.
+//     and share them through LDS, so that codes are converted once for all rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -405,7 +405,7 @@ struct AtTokens {
 
 template <class T, int HD>
 struct AtNarrow {
-    static constexpr int NK = HD / 64, CB = HD / 16, NV = CB / 4, STEP = AT_TILE[0];
+    static constexpr int NK = HD / 64, CB = HD / 16, NV = CB / 4, STEP = AT_TILE;
     static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
     struct Lds {
         AtTokens tokens[4][2];
@@ -545,14 +545,18 @@ struct AtNarrow {
 // --------------------------------------------------------------------- wide
 template <class T, int HD>
 struct AtWide {
-    static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4, STEP = AT_TILE[1];
+    static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4;
     static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
+    // Eight waves on a compute unit either way: as one workgroup, whose waves convert half
+    // as much for their rows; heads of 256 codes and float's two numbers take the
+    // registers and the LDS of more.
+    static constexpr int WAVES = HD <= 128 && !SPLIT ? 8 : 4, STEP = 16 * WAVES;
     struct Step {
-        at_h8 k[4][NF][64];     // keys of 16 tokens each, as the lanes read them
-        at_h8 v[2][CB][64];     // values of 32 tokens each
-        float ks[64], vs[64];
-        float top[4];           // of each wave's tokens, the largest values' scale
-        unsigned short ok[4];   // tokens that are there
+        at_h8 k[WAVES][NF][64];      // keys of 16 tokens each, as the lanes read them
+        at_h8 v[WAVES / 2][CB][64];  // values of 32 tokens each
+        float ks[STEP], vs[STEP];
+        float top[WAVES];            // of each wave's tokens, the largest values' scale
+        unsigned short ok[WAVES];    // tokens that are there
     };
     struct Lds {
         Step step[2];
@@ -569,7 +573,7 @@ struct AtWide {
     Lds& lds;
     const int* pages;
     int lane, wave;
-    int tiles;       // tiles of 16 rows of a wave: 1 or 2
+    int tiles;       // of 16 rows, a wave's: 1 or 2
     int first;       // the wave's first row
     AtQuery<T, HD> q[2];
     AtRows<HD> r[2];
@@ -632,8 +636,9 @@ struct AtWide {
             s.top[wave] = top;
         }
     }
+    // 64 tokens, `half` of a step's
     template <int TILES>
-    __device__ __forceinline__ void compute(const Step& s, int base)
+    __device__ __forceinline__ void compute(const Step& s, int half, int base)
     {
         float x[TILES][16];
         at_f4 vs[4];
@@ -644,27 +649,27 @@ struct AtWide {
             for (int i = 0; i < TILES; ++i) acc[i] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                const at_h8 k = s.k[sub][f][lane];
+                const at_h8 k = s.k[4 * half + sub][f][lane];
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
                     acc[i] = at_product(k, q[i].hi[f], acc[i]);
                     if constexpr (SPLIT) acc[i] = at_product(k, q[i].lo[f], acc[i]);
                 }
             }
-            const at_f4 ks = *(const at_f4*)&s.ks[16 * sub + 4 * at.g];
-            vs[sub] = *(const at_f4*)&s.vs[16 * sub + 4 * at.g];
+            const at_f4 ks = *(const at_f4*)&s.ks[64 * half + 16 * sub + 4 * at.g];
+            vs[sub] = *(const at_f4*)&s.vs[64 * half + 16 * sub + 4 * at.g];
 #pragma unroll
             for (int i = 0; i < TILES; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e];
         }
         float f;
-        if (unit.raise(s.top[lane & 3], f))
+        if (unit.raise(s.top[4 * half + (lane & 3)], f))
 #pragma unroll
             for (int i = 0; i < TILES; ++i) r[i].times(f);
         unsigned long long ok;
-        __builtin_memcpy(&ok, s.ok, 8);
-        if (ok != ~0ull || base + STEP > least) {
+        __builtin_memcpy(&ok, s.ok + 4 * half, 8);
+        if (ok != ~0ull || base + 64 > least) {
 #pragma unroll
             for (int i = 0; i < TILES; ++i) {
                 const unsigned long long mask = at_seen(ok, limit[i] - base, at.g);
@@ -702,7 +707,7 @@ struct AtWide {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < CB; ++j) {
-                const at_h8 c = s.v[h][j][lane];
+                const at_h8 c = s.v[2 * half + h][j][lane];
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
                     r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
@@ -714,7 +719,7 @@ struct AtWide {
     __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         // few rows are dealt 16 to a wave, so that all waves have some
-        tiles = job.rows > 64 ? 2 : 1;
+        tiles = job.rows > STEP ? 2 : 1;
         first = wave * 16 * tiles;
         const int mine = wave * 16 + at.n, page = page_of(from + mine);
         int later = page_of(from + STEP + mine);
@@ -746,11 +751,12 @@ struct AtWide {
                 fetch(c, base + STEP, later);
                 later = page_of(base + 2 * STEP + mine);
             }
-            if (base < most) {
+#pragma unroll 1
+            for (int half = 0; half < WAVES / 4 && base + 64 * half < min(most, to); ++half) {
                 if (tiles == 2)
-                    compute<2>(lds.step[p], base);
+                    compute<2>(lds.step[p], half, base + 64 * half);
                 else
-                    compute<1>(lds.step[p], base);
+                    compute<1>(lds.step[p], half, base + 64 * half);
             }
         }
         at_finish(a, job, at, r[0], q[0].unit, unit, first + at.n, slab);
@@ -759,8 +765,8 @@ struct AtWide {
     }
 };
 
-// Workgroups a compute unit has room for: wide heads and float's two numbers take
-// the registers of two.
+// Waves that a SIMD has room for: wide heads and float's two numbers take the registers
+// of two.
 template <class T, int HD>
 constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
 
@@ -771,7 +777,7 @@ __device__ __forceinline__ int at_worker(const AtPlan& p)
 }
 
 template <class T, int HD>
-__global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn_wide(AttnArgs<T> a)
+__global__ __launch_bounds__((64 * AtWide<T, HD>::WAVES), (at_resident<T, HD>)) void q8_attn_wide(AttnArgs<T> a)
 {
     __shared__ union {
         AtScan<AT_WIDE_JOBS> scan;  // until the cursor is there
@@ -844,7 +850,7 @@ __global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
                 pm[u] = AT_LOWEST;
                 pl[u] = v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0.0f;
                 if (i < count) {
-                    const long long at = min(max(at_part(where, i), 0ll), (long long)a.p.slabs - 1);
+                    const long long at = min(max(at_part(a.p, where, i), 0ll), (long long)a.p.slabs - 1);
                     const float* s = a.slabs + at * at_slab(hd);
                     pm[u] = s[2 * n];
                     pl[u] = s[2 * n + 1];

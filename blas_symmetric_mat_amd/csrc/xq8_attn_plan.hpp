@@ -5,12 +5,12 @@
 // rows, the tokens that are not read for a group).  Each head of keys and each
 // block of an entry's rows is a job.  A row of an entry is a row of q and one of
 // the `share` heads of q that read the same keys; blocks are of 16 rows where an
-// entry has no more (narrow), else of 128 (wide).
+// entry has no more (narrow), else of 256 (wide; 128 where registers hold no more).
 //
 // There are two lines of jobs, one after the other by entry, head and block: wide
 // jobs, of which every workgroup of q8_attn_wide takes an equal piece, and narrow
-// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens of a narrow job, 64 of a
-// wide one): a job's tiles come first in its stretch of the line, then some that
+// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens of a narrow job, 16
+// for each wave of a wide one): a job's tiles come first in its stretch of the line, then some that
 // stand for what a job takes besides.  Stretches may be longer than need be, but have
 // to be the same for all workers, which compute them from the arrays on the device,
 // so that a captured call follows what these hold.  A single sequence's step waits for
@@ -28,9 +28,7 @@ namespace xsymv {
 
 constexpr int AT_LOW = 16, AT_HD = 256;  // least and widest head
 constexpr int AT_NARROW = 16;            // rows of a narrow job, and of a slab
-constexpr int AT_WIDE = 128;             // rows of a wide job
-constexpr int AT_SLABS = AT_WIDE / AT_NARROW;
-constexpr int AT_TILE[2] = {32, 64};  // tokens of a narrow and of a wide tile
+constexpr int AT_TILE = 32;              // tokens of a narrow tile
 constexpr int AT_OVER = 2;            // tiles that a job takes besides its own
 // A piece is two tiles at least, for the join's sake.
 constexpr int AT_LEAST = 2;
@@ -63,6 +61,14 @@ struct AtPlan {
     AtDivisor by_share, by_page;
     int grid;   // workgroups
     int whole;  // no job is cut, nothing is shared: no workspace
+    int wide_log;  // of a wide job's rows; a tile has half as many tokens
+    __host__ __device__ __forceinline__ int wide_rows() const { return 1 << wide_log; }
+    __host__ __device__ __forceinline__ int wide_slabs() const { return 1 << wide_log >> 4; }
+    // tiles that hold this many tokens
+    __device__ __forceinline__ int wide_tiles(int tokens) const
+    {
+        return (int)(((long long)tokens + (1 << (wide_log - 1)) - 1) >> (wide_log - 1));
+    }
     // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
     // narrow ones', two a wave; of whole parts) and, for each row and head, where its
     // own parts and its group's are.
@@ -97,27 +103,32 @@ struct AtEntry {
     int mine;  // whether its jobs are of the kernel's kind
     int cost;  // tiles of one head
 
-    __device__ __forceinline__ int block_rows() const { return wide ? AT_WIDE : AT_NARROW; }
-    __device__ __forceinline__ int block_slabs() const { return wide ? AT_SLABS : 1; }
-    __device__ __forceinline__ int blocks() const { return wide ? (rows + AT_WIDE - 1) / AT_WIDE : rows > 0; }
-    __device__ __forceinline__ int slabs() const { return joined ? blocks() * block_slabs() : 0; }
+    __device__ __forceinline__ int block_slabs(const AtPlan& p) const { return wide ? p.wide_slabs() : 1; }
+    __device__ __forceinline__ int blocks(const AtPlan& p) const
+    {
+        return wide ? (rows + p.wide_rows() - 1) >> p.wide_log : rows > 0;
+    }
+    __device__ __forceinline__ int slabs(const AtPlan& p) const { return joined ? blocks(p) * block_slabs(p) : 0; }
+    __device__ __forceinline__ int tiles(const AtPlan& p, int tokens) const
+    {
+        return wide ? p.wide_tiles(tokens) : (tokens + AT_TILE - 1) / AT_TILE;
+    }
     // length of the blocks before block b
     __device__ __forceinline__ int before_block(const AtPlan& p, int b) const
     {
         if (p.whole) return b;
-        const int tile = wide ? AT_TILE[1] : AT_TILE[0];
-        if (!wide || group) return b * (AT_OVER + (t1 - t0 + tile - 1) / tile);
+        if (!wide || group) return b * (AT_OVER + tiles(p, t1 - t0));
         // block b sees up to step * (b + 1) tokens more than what lies before the
         // rows; the sums of these are rounded down, for which one tile makes up
-        const int step = p.by_share.of(AT_WIDE + p.share - 1);
-        return b * (AT_OVER + 1 + (max(before - t0, 0) + tile - 1) / tile) +
-               (int)((long long)b * (b + 1) / 2 * step / tile);
+        const int step = p.by_share.of(p.wide_rows() + p.share - 1);
+        return b * (AT_OVER + 1 + tiles(p, max(before - t0, 0))) +
+               (int)((long long)b * (b + 1) / 2 * step >> (p.wide_log - 1));
     }
     // end of the tokens that block b sees
     __device__ __forceinline__ int end(const AtPlan& p, int b) const
     {
         if (group) return t1;
-        const int last = (int)min((long long)(b + 1) * block_rows(), (long long)rows) - 1;
+        const int last = wide ? (int)min((long long)(b + 1) << p.wide_log, (long long)rows) - 1 : rows - 1;
         return min(max(before + p.by_share.of(last) + 1, t0), t1);
     }
 };
@@ -138,13 +149,13 @@ struct AtGroup {
         pays = false;
         if (tokens > 0 && count > 1 && rows > 0) {
             const long long one = (long long)((rows + count - 1) / count) * p.share;
-            pays = work((long long)rows * p.share) < count * work(one);
+            pays = work(p, (long long)rows * p.share) < count * work(p, one);
         }
     }
-    // a wide tile of tokens takes about as long as two narrow ones
-    static __device__ __forceinline__ long long work(long long rows)
+    // a wide job takes about twice as long as a narrow one with as many tokens
+    static __device__ __forceinline__ long long work(const AtPlan& p, long long rows)
     {
-        return rows <= AT_NARROW ? 1 : (rows + AT_WIDE - 1) / AT_WIDE * 2;
+        return rows <= AT_NARROW ? 1 : (rows + p.wide_rows() - 1) >> p.wide_log << 1;
     }
 };
 
@@ -202,7 +213,7 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
         x.before = x.t1 - 1;
     }
     x.wide = MIXED && x.rows > AT_NARROW;
-    x.cost = x.before_block(p, x.blocks());
+    x.cost = x.before_block(p, x.blocks(p));
     x.mine = MIXED ? x.wide == (KIND == AT_WIDE_JOBS) : 1;
     return x;
 }
@@ -296,7 +307,7 @@ struct AtWindow {
         x = AtEntry{};
         if (e < entries(p)) x = at_entry<KIND>(p, e);
         own[0] = x.mine ? x.cost * p.kvheads : 0;
-        if constexpr (N > 1) own[1] = x.slabs() * p.kvheads;
+        if constexpr (N > 1) own[1] = x.slabs(p) * p.kvheads;
 #pragma unroll
         for (int i = 0; i < N; ++i) sums[i] = at_sums(own[i]);
     }
@@ -317,7 +328,7 @@ struct AtLines {
             total = w.all(0);
             return;
         }
-        for (int i = wave; i < windows; i += 4) {
+        for (int i = wave; i < windows; i += (int)blockDim.x >> 6) {
             w.load(p, i);
             if (lane == 63)
 #pragma unroll
@@ -335,7 +346,6 @@ struct AtLines {
 template <AtKind KIND>
 struct AtCursor {
     static constexpr bool WIDE = KIND == AT_WIDE_JOBS, MIXED = KIND != AT_SINGLE_JOBS;
-    static constexpr int TILE = AT_TILE[WIDE];
     int pos, end, quota;
     int base, slab;  // where the window's tiles, and its whole parts, begin
     int worker, window, windows;
@@ -424,7 +434,7 @@ struct AtCursor {
             const int head = at_quotient(pos - first, of.cost), rest = pos - first - head * of.cost;
             int b = 0;  // the last block that begins at or before it
             if (WIDE)
-                for (int hi = of.blocks() - 1; b < hi;) {
+                for (int hi = of.blocks(p) - 1; b < hi;) {
                     const int mid = (b + hi + 1) / 2;
                     if (of.before_block(p, mid) <= rest)
                         b = mid;
@@ -434,26 +444,26 @@ struct AtCursor {
             const int c0 = WIDE ? of.before_block(p, b) : 0, c1 = WIDE ? of.before_block(p, b + 1) : of.cost;
             const int x = rest - c0, y = min(x + end - pos, c1 - c0);
             job.end = of.end(p, b);
-            const int tiles = max(1, (job.end - of.t0 + TILE - 1) / TILE);
+            const int tiles = max(1, of.tiles(p, job.end - of.t0)), tile = WIDE ? p.wide_rows() / 2 : AT_TILE;
             const int t0 = p.whole ? 0 : min(x, tiles), t1 = p.whole ? tiles : min(y, tiles);
             pos += y - x;
             if (t0 >= t1) continue;
             job.head = head;
-            job.rho0 = WIDE ? b * AT_WIDE : 0;
-            job.rows = min(of.rows - job.rho0, WIDE ? AT_WIDE : AT_NARROW);
+            job.rho0 = WIDE ? b << p.wide_log : 0;
+            job.rows = min(of.rows - job.rho0, WIDE ? p.wide_rows() : AT_NARROW);
             job.row0 = of.row0;
             job.before = of.before;
             job.table = of.table;
             job.group = of.group;
-            from = of.t0 + t0 * TILE;
-            to = min(of.t0 + t1 * TILE, job.end);
+            from = of.t0 + t0 * tile;
+            to = min(of.t0 + t1 * tile, job.end);
             part = -1;
             if (p.whole) return true;
             if (t0 > 0 || t1 < tiles)
-                part = WIDE ? (2 * worker + (t0 == 0)) * AT_SLABS : p.narrow_at + 2 * worker + (t0 == 0);
+                part = WIDE ? (2 * worker + (t0 == 0)) * p.wide_slabs() : p.narrow_at + 2 * worker + (t0 == 0);
             else if (of.joined)
-                part = p.whole_at + parts + head * of.slabs() + b * of.block_slabs();
-            if (part > p.slabs - of.block_slabs()) continue;  // (starts that do not ascend)
+                part = p.whole_at + parts + head * of.slabs(p) + b * of.block_slabs(p);
+            if (part > p.slabs - of.block_slabs(p)) continue;  // (starts that do not ascend)
             if (t0 == 0) note(p, job, part, t1 < tiles ? tiles - 1 - y : -1);
             return true;
         }
@@ -477,9 +487,9 @@ struct AtCursor {
 };
 
 // Slab of part i of a row: the first one's, then one of each of the next workers.
-__device__ __forceinline__ long long at_part(int2 where, int i)
+__device__ __forceinline__ long long at_part(const AtPlan& p, int2 where, int i)
 {
-    const int step = where.y >> 25 & 1 ? AT_SLABS : 1;
+    const int step = where.y >> 25 & 1 ? p.wide_slabs() : 1;
     return where.x + (i == 0 ? 0ll : (2ll * i - 1) * step);
 }
 

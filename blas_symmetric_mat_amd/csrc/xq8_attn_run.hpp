@@ -19,6 +19,9 @@ inline bool attn_mixed(int heads, int kvheads, int groups, bool single)
     return !single || groups > 0 || heads / kvheads > AT_NARROW;
 }
 
+// Rows of a wide job: 256, or 128 (AtWide).
+constexpr int AT_WIDE = 256, AT_LESS = 128;
+
 // Workspace: where the rows' parts are, and their slabs: of cut jobs (two a worker),
 // and where groups share tokens of whole ones.
 struct AttnSpace {
@@ -28,14 +31,14 @@ struct AttnSpace {
         const size_t share = heads / kvheads, table = align_up((size_t)rows * heads * sizeof(int2));
         shared = table;
         parts = groups > 0 ? 2 * table : table;
-        narrow = attn_mixed(heads, kvheads, groups, single) ? 2 * (size_t)AT_GRID * AT_SLABS : 0;
+        // (256 workgroups of 256 rows, or 512 of 128)
+        narrow = attn_mixed(heads, kvheads, groups, single) ? 2 * (size_t)AT_GRID * AT_LESS / AT_NARROW : 0;
         whole = narrow + 2 * 4 * (size_t)AT_GRID;
         slabs = whole;
         if (groups > 0) {
-            const size_t blocks = (size_t)rows * share / AT_WIDE;
-            const size_t own = single ? seqs * (share <= AT_NARROW ? 1 : (share + AT_WIDE - 1) / AT_WIDE * AT_SLABS)
-                                      : (blocks + seqs) * AT_SLABS;
-            slabs += kvheads * (own + (blocks + groups) * AT_SLABS);
+            const size_t most = AT_WIDE / AT_NARROW, all = (size_t)rows * share / AT_NARROW;
+            const size_t own = single && share <= AT_NARROW ? seqs : all + seqs * most;
+            slabs += kvheads * (own + all + groups * most);
         }
         bytes = parts + slabs * at_slab(hd) * sizeof(float);
     }
@@ -43,11 +46,12 @@ struct AttnSpace {
 
 // Workgroups of a kernel: as many for every die, and no more than can have work.
 template <class K>
-int attn_grid(K* kernel, long long most, int& grid)
+int attn_grid(K* kernel, int threads, long long most, int& grid)
 {
     int resident = 0;
-    const int rc = resident_blocks(reinterpret_cast<const void*>(kernel), 256, &resident);
-    grid = (int)std::min(std::min((long long)resident, (long long)AT_GRID) / 8 * 8, std::max(1ll, (most + 7) / 8) * 8);
+    const int rc = resident_blocks(reinterpret_cast<const void*>(kernel), threads, &resident);
+    const long long room = std::min((long long)resident, (long long)AT_GRID * 256 / threads);
+    grid = (int)std::max(8ll, std::min(room / 8, std::max(1ll, (most + 7) / 8)) * 8);
     return rc;
 }
 
@@ -70,13 +74,15 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
     const bool single = p.start == nullptr, mixed = attn_mixed(p.heads, p.kvheads, p.groups, single);
     // Tiles that a line has at most.  (Where an int might not count them, no job is cut;
     // the call takes minutes.)
-    const double blocks = (double)p.rows * p.share / AT_WIDE + p.seqs + p.groups;
-    const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE[0] + AT_OVER + 2);
+    const double blocks = (double)p.rows * p.share / AT_LESS + p.seqs + p.groups;
+    const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE + AT_OVER + 2);
     // Sequences of a piece at most are whole as they are: one launch.
-    const bool cut = line < 2e9 && (p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST * AT_TILE[0]);
+    const bool cut = line < 2e9 && (p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST * AT_TILE);
     const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, single);
     return q8_with_workspace(cut ? space.bytes : 0, true, stream, [&](void* ws, const TimedCall& tc) -> int {
+        constexpr int threads = 64 * AtWide<T, HD>::WAVES;
         p.whole = ws == nullptr;
+        p.wide_log = AtWide<T, HD>::WAVES == 8 ? 8 : 7;
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
             p.own = reinterpret_cast<int2*>(at);
@@ -92,18 +98,18 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
             p.wide_entries = p.groups + (single && p.share <= AT_NARROW ? 0 : p.seqs);
             if (p.whole && single && p.share <= AT_NARROW) p.wide_entries = 0;
             const long long most = p.whole ? (long long)std::min(blocks * p.kvheads, 1e9) : 1ll << 30;
-            const int rc = p.wide_entries > 0 ? attn_grid(&q8_attn_wide<T, HD>, most, p.grid) : 0;
+            const int rc = p.wide_entries > 0 ? attn_grid(&q8_attn_wide<T, HD>, threads, most, p.grid) : 0;
             if (rc) return rc;
             if (p.wide_entries > 0) {
-                XSYMV_HIP(launch_k(&q8_attn_wide<T, HD>, dim3(p.grid), dim3(256), stream, a, start, nullptr));
+                XSYMV_HIP(launch_k(&q8_attn_wide<T, HD>, dim3(p.grid), dim3(threads), stream, a, start, nullptr));
                 start = nullptr;
             }
         }
         // A line of narrow jobs has no more tiles than this.
-        const double tiles = p.whole ? 1.0 : ((double)p.ldt * p.ps / AT_TILE[0] + 1 + AT_OVER) / AT_LEAST;
+        const double tiles = p.whole ? 1.0 : ((double)p.ldt * p.ps / AT_TILE + 1 + AT_OVER) / AT_LEAST;
         const long long most = (long long)std::min(((double)p.seqs + p.groups) * p.kvheads * tiles / 4 + 1, 1e9);
         auto* narrow = mixed ? &q8_attn_narrow<T, HD, AT_NARROW_JOBS> : &q8_attn_narrow<T, HD, AT_SINGLE_JOBS>;
-        const int rc = attn_grid(narrow, most, p.grid);
+        const int rc = attn_grid(narrow, 256, most, p.grid);
         if (rc) return rc;
         XSYMV_HIP(launch_k(narrow, dim3(p.grid), dim3(256), stream, a, start, tc.e1));
         if (p.whole) return 0;
