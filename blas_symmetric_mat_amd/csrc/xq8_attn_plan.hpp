@@ -9,8 +9,7 @@
 //
 // There are two lines of jobs, one after the other by entry, head and block: wide
 // jobs, of which every workgroup of q8_attn_wide takes an equal piece, and narrow
-// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens of a narrow job, 16
-// for each wave of a wide one): a job's tiles come first in its stretch of the line, then some that
+// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens): a job's tiles come first in its stretch of the line, then some that
 // stand for what a job takes besides.  Stretches may be longer than need be, but have
 // to be the same for all workers, which compute them from the arrays on the device,
 // so that a captured call follows what these hold.  A single sequence's step waits for
@@ -28,10 +27,12 @@ namespace xsymv {
 
 constexpr int AT_LOW = 16, AT_HD = 256;  // least and widest head
 constexpr int AT_NARROW = 16;            // rows of a narrow job, and of a slab
-constexpr int AT_TILE = 32;              // tokens of a narrow tile
-constexpr int AT_OVER = 2;            // tiles that a job takes besides its own
-// A piece is two tiles at least, for the join's sake.
-constexpr int AT_LEAST = 2;
+constexpr int AT_TILE = 32;              // tokens of a tile
+// Tiles that a job takes besides its own: a narrow one, a wide one (20 us for its rows
+// of q and its results, when a step of 128 tokens takes 7).
+constexpr int AT_OVER = 3, AT_OVER_WIDE = 12;
+// A piece is so many tiles at least, for the join's sake (narrow, wide: a step).
+constexpr int AT_LEAST = 2, AT_LEAST_WIDE = 4;
 // Entries of a call at most: windows of 64, of which LDS holds the sums.
 constexpr int AT_WINDOWS = 1024, AT_ENTRIES = 64 * AT_WINDOWS;
 
@@ -61,14 +62,9 @@ struct AtPlan {
     AtDivisor by_share, by_page;
     int grid;   // workgroups
     int whole;  // no job is cut, nothing is shared: no workspace
-    int wide_log;  // of a wide job's rows; a tile has half as many tokens
+    int wide_log;  // of a wide job's rows
     __host__ __device__ __forceinline__ int wide_rows() const { return 1 << wide_log; }
     __host__ __device__ __forceinline__ int wide_slabs() const { return 1 << wide_log >> 4; }
-    // tiles that hold this many tokens
-    __device__ __forceinline__ int wide_tiles(int tokens) const
-    {
-        return (int)(((long long)tokens + (1 << (wide_log - 1)) - 1) >> (wide_log - 1));
-    }
     // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
     // narrow ones', two a wave; of whole parts) and, for each row and head, where its
     // own parts and its group's are.
@@ -109,20 +105,18 @@ struct AtEntry {
         return wide ? (rows + p.wide_rows() - 1) >> p.wide_log : rows > 0;
     }
     __device__ __forceinline__ int slabs(const AtPlan& p) const { return joined ? blocks(p) * block_slabs(p) : 0; }
-    __device__ __forceinline__ int tiles(const AtPlan& p, int tokens) const
-    {
-        return wide ? p.wide_tiles(tokens) : (tokens + AT_TILE - 1) / AT_TILE;
-    }
+    static __device__ __forceinline__ int tiles(int tokens) { return (tokens + AT_TILE - 1) / AT_TILE; }
     // length of the blocks before block b
     __device__ __forceinline__ int before_block(const AtPlan& p, int b) const
     {
         if (p.whole) return b;
-        if (!wide || group) return b * (AT_OVER + tiles(p, t1 - t0));
+        if (!wide) return b * (AT_OVER + tiles(t1 - t0));
+        if (group) return b * (AT_OVER_WIDE + tiles(t1 - t0));
         // block b sees up to step * (b + 1) tokens more than what lies before the
         // rows; the sums of these are rounded down, for which one tile makes up
         const int step = p.by_share.of(p.wide_rows() + p.share - 1);
-        return b * (AT_OVER + 1 + tiles(p, max(before - t0, 0))) +
-               (int)((long long)b * (b + 1) / 2 * step >> (p.wide_log - 1));
+        return b * (AT_OVER_WIDE + 1 + tiles(max(before - t0, 0))) +
+               (int)((long long)b * (b + 1) / 2 * step / AT_TILE);
     }
     // end of the tokens that block b sees
     __device__ __forceinline__ int end(const AtPlan& p, int b) const
@@ -149,7 +143,8 @@ struct AtGroup {
         pays = false;
         if (tokens > 0 && count > 1 && rows > 0) {
             const long long one = (long long)((rows + count - 1) / count) * p.share;
-            pays = work(p, (long long)rows * p.share) < count * work(p, one);
+            // (a quarter less: rows that have two entries are added by the join)
+            pays = work(p, (long long)rows * p.share) * 4 <= count * work(p, one) * 3;
         }
     }
     // a wide job takes about twice as long as a narrow one with as many tokens
@@ -220,7 +215,8 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
 
 // A piece of work: rows of an entry, a head of keys.
 struct AtJob {
-    int head, rows, rho0, row0, end, before, table, group;
+    int head, rows, rho0, row0, before, table, group;
+    int end;  // of the piece's tokens
     // row n's row and head of q
     __device__ __forceinline__ int place(const AtPlan& p, int n, size_t& row) const
     {
@@ -360,7 +356,7 @@ struct AtCursor {
         const int lane = threadIdx.x & 63, total = lines.total;
         // a little more than total / workers, which need not be exact
         quota = (int)((float)total * __builtin_amdgcn_rcpf((float)workers) * 1.00001f) + 1;
-        if (!p.whole) quota = max(quota, AT_LEAST);
+        if (!p.whole) quota = max(quota, WIDE ? AT_LEAST_WIDE : AT_LEAST);
         const long long at = (long long)worker * quota;
         pos = (int)min(at, (long long)total);
         end = (int)min(at + quota, (long long)total);
@@ -444,7 +440,7 @@ struct AtCursor {
             const int c0 = WIDE ? of.before_block(p, b) : 0, c1 = WIDE ? of.before_block(p, b + 1) : of.cost;
             const int x = rest - c0, y = min(x + end - pos, c1 - c0);
             job.end = of.end(p, b);
-            const int tiles = max(1, of.tiles(p, job.end - of.t0)), tile = WIDE ? p.wide_rows() / 2 : AT_TILE;
+            const int tiles = max(1, of.tiles(job.end - of.t0));
             const int t0 = p.whole ? 0 : min(x, tiles), t1 = p.whole ? tiles : min(y, tiles);
             pos += y - x;
             if (t0 >= t1) continue;
@@ -455,8 +451,9 @@ struct AtCursor {
             job.before = of.before;
             job.table = of.table;
             job.group = of.group;
-            from = of.t0 + t0 * tile;
-            to = min(of.t0 + t1 * tile, job.end);
+            from = of.t0 + t0 * AT_TILE;
+            to = min(of.t0 + t1 * AT_TILE, job.end);
+            job.end = to;
             part = -1;
             if (p.whole) return true;
             if (t0 > 0 || t1 < tiles)

@@ -75,7 +75,7 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
     // Tiles that a line has at most.  (Where an int might not count them, no job is cut;
     // the call takes minutes.)
     const double blocks = (double)p.rows * p.share / AT_LESS + p.seqs + p.groups;
-    const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE + AT_OVER + 2);
+    const double line = blocks * p.kvheads * (((double)p.ldt * p.ps) / AT_TILE + AT_OVER_WIDE + 2);
     // Sequences of a piece at most are whole as they are: one launch.
     const bool cut = line < 2e9 && (p.groups > 0 || (long long)p.ldt * p.ps > AT_LEAST * AT_TILE);
     const AttnSpace space(p.rows, p.heads, p.kvheads, p.hd, p.seqs, p.groups, single);
