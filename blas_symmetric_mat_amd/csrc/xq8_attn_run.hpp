@@ -127,6 +127,7 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     if (rows < 0) return -1;
     if (heads < 1 || (kvheads >= 1 && heads % kvheads != 0)) return -2;
     if (kvheads < 1) return -3;
+    if ((long long)rows * heads > 0x7fffffffll) return -1;
     if (hd < AT_LOW || hd > AT_HD) return -4;
     const long long wide = (long long)heads * hd;
     if (wide > 0x7fffffffll) return -2;
@@ -155,7 +156,6 @@ int attn_run(int rows, int heads, int kvheads, int hd, const T* q, int ldq, int 
     if (some && out == nullptr) return -24;
     if (ldo < wide) return -25;
     if (!some) return 0;
-    if ((long long)rows * heads > 0x7fffffffll) return -1;
     AttnArgs<T> a{};
     AtPlan& p = a.p;
     p.start = start;
