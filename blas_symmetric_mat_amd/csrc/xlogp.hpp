@@ -8,6 +8,12 @@
 // `top` logits are found in the same pass: each thread remembers the largest of
 // its own and where, the top-th largest of these bounds the row's top-th logit
 // from below, and only the few threads that hold one above it read theirs again.
+//
+// Bound by the reads where rows are many and long: 2048 rows of 131072 bfloat16
+// logits in 101 us, 5.3 TB/s, the sums' some nine instructions a logit behind
+// them (at eleven, with room for five waves a SIMD instead of eight, 129 us).  A
+// single row of 32000 is dealt over 16 workgroups; the rest of its 12 us is the
+// two launches and what each does one after the other.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,6 +24,7 @@ namespace xsymv {
 
 constexpr int LP_THREADS = 256;
 constexpr int LP_TOP = 128;     // alternatives of one row at most
+constexpr int LP_FEW = 32;      // alternatives that 64 bounds find
 constexpr int LP_CAP = 1024;    // candidates ranked at once
 constexpr int LP_PARTS = 64;    // workgroups that share a row at most
 constexpr int LP_LISTS = 2048;  // alternatives of all parts of a row at most
@@ -58,6 +65,19 @@ __device__ __forceinline__ float lp_value(lp_key k)
 }
 __device__ __forceinline__ int lp_index(lp_key k) { return (int)(0xffffffffu - (unsigned)k); }
 
+// Of a wave's keys, those above one.
+__device__ __forceinline__ int lp_rank(lp_key k)
+{
+    int rank = 0;
+#pragma unroll
+    for (int o = 0; o < 64; ++o) {
+        const unsigned lo = __builtin_amdgcn_readlane((unsigned)k, o);
+        const unsigned hi = __builtin_amdgcn_readlane((unsigned)(k >> 32), o);
+        rank += ((lp_key)hi << 32 | lo) > k;
+    }
+    return rank;
+}
+
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
 constexpr float LP_LOWEST = -3.4028234663852886e38f;
 
@@ -91,25 +111,26 @@ __device__ __forceinline__ void lp_load(const T* x, int have, float (&v)[8])
     }
 }
 
-// -infinity as a finite number whose power is zero too; a NaN passes.
-__device__ __forceinline__ float lp_above(float z) { return __builtin_elementwise_maximum(z, -1e30f); }
-
 // Adds eight logits.  c follows where one is more than 20 above it (e^20 times
-// the number of logits is far below the largest float).
+// the number of logits is far below the largest float).  The eight are summed by
+// themselves first: a sum of n in this order is off by some n / 8 + 8 roundings.
 __device__ __forceinline__ float lp_take(LpSums& a, const float (&v)[8])
 {
-    float most = v[0];
+    float most = v[0];  // (a NaN passes: fmaxf would quiet each first)
 #pragma unroll
-    for (int e = 1; e < 8; ++e) most = fmaxf(most, v[e]);
+    for (int e = 1; e < 8; ++e) most = __builtin_elementwise_maximum(most, v[e]);
     if (most > a.c + 20.0f || (a.c == LP_LOWEST && most > a.c)) lp_move(a, most);
+    float l = 0.0f, s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         // the difference first: c itself has power 1, and masks of the type's lowest
         // value, times log2(e), would be no numbers
-        const float z = lp_above((v[e] - a.c) * LP_LOG2E), p = __builtin_amdgcn_exp2f(z);
-        a.l += p;
-        a.s = __builtin_fmaf(p, z, a.s);
+        const float z = (v[e] - a.c) * LP_LOG2E, p = __builtin_amdgcn_exp2f(z);
+        l += p;
+        s = __builtin_fmaf(p, fmaxf(z, -1e30f), s);  // -infinity has no part; p is a NaN where z is one
     }
+    a.l += l;
+    a.s += s;
     return most;
 }
 
@@ -146,7 +167,7 @@ __device__ __forceinline__ void lp_alternative(const LpArgs<T>& a, int row, int 
 }
 
 template <class T, bool TOP>
-__global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
+__global__ __launch_bounds__(LP_THREADS, 8) void logp_rows(LpArgs<T> a)
 {
     __shared__ LpSums of_wave[LP_THREADS / 64];
     __shared__ lp_key bound[TOP ? LP_THREADS : 1], found[TOP ? LP_CAP : 1], least;
@@ -160,24 +181,33 @@ __global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
         LpSums sum{LP_LOWEST, 0.0f, 0.0f};
         float best = -INFINITY;
         int best_at = t;
-        constexpr int U = 4;  // loads in flight
-        for (int v = t; v < vecs; v += LP_THREADS * U) {
-            float e[U][8];
+        auto take = [&](const float (&e)[8], int v) {
+            const float most = lp_take(sum, e);
+            if (TOP && most > best) {
+                best = most;
+                best_at = v;
+            }
+        };
+        // Four loads in flight, as they come, and whole ones; then one at a time.
+        constexpr int U = 4;
+        typedef T raw __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+        int v = t;
+        for (; (v + (U - 1) * LP_THREADS + 1) * 8 <= have; v += LP_THREADS * U) {
+            raw r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v + u * LP_THREADS < vecs) {
-                    const int at = (v + u * LP_THREADS) * 8;
-                    lp_load(x + at, have - at, e[u]);
-                }
+            for (int u = 0; u < U; ++u) r[u] = *(const raw*)(x + (v + u * LP_THREADS) * 8);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v + u * LP_THREADS < vecs) {
-                    const float most = lp_take(sum, e[u]);
-                    if (TOP && most > best) {
-                        best = most;
-                        best_at = v + u * LP_THREADS;
-                    }
-                }
+            for (int u = 0; u < U; ++u) {
+                float e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = (float)r[u][i];
+                take(e, v + u * LP_THREADS);
+            }
+        }
+        for (; v < vecs; v += LP_THREADS) {
+            float e[8];
+            lp_load(x + v * 8, have - v * 8, e);
+            take(e, v);
         }
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
@@ -203,9 +233,18 @@ __global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
         else if (t == 0)
             a.sums[item] = sum;
         if constexpr (TOP) {
-            int rank = 0;
-            for (int o = 0; o < LP_THREADS; ++o) rank += bound[o] > bound[t];
-            if (rank == a.top - 1 && bound[t] != 0) least = bound[t];
+            if (a.top <= LP_FEW) {
+                // The largest of four threads' each, by one wave.
+                if (t < 64) {
+                    const lp_key k = max(max(bound[t], bound[64 + t]), max(bound[128 + t], bound[192 + t]));
+                    if (lp_rank(k) == a.top - 1 && k != 0) least = k;
+                }
+            } else {
+                int rank = 0;
+#pragma unroll 16
+                for (int o = 0; o < LP_THREADS; ++o) rank += bound[o] > bound[t];
+                if (rank == a.top - 1 && bound[t] != 0) least = bound[t];
+            }
             __syncthreads();
             // threads that hold a logit at or above `least`
             if (t < vecs && lp_order(best, from + best_at * 8) >= least)
@@ -252,6 +291,7 @@ __global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
             for (int i = t; i < count; i += LP_THREADS) {
                 const lp_key k = found[i];
                 int before = 0;
+#pragma unroll 8
                 for (int o = 0; o < count; ++o) before += found[o] > k;
                 if (before < a.top) {
                     if (a.parts == 1)
@@ -266,41 +306,52 @@ __global__ __launch_bounds__(LP_THREADS) void logp_rows(LpArgs<T> a)
     }
 }
 
-// A row from its parts.
+// A row from its parts.  With q = top / parts, rounded up, the lists' q-th keys
+// are ranked: the (top / q)-th largest of them, rounded up, has top keys at or above
+// it, and only those that are there are ranked among each other.
 template <class T>
 __global__ __launch_bounds__(LP_THREADS) void logp_join(LpArgs<T> a)
 {
-    __shared__ lp_key keys[LP_LISTS];
-    const int t = threadIdx.x, lists = a.parts * a.top;
+    __shared__ lp_key found[LP_LISTS], least;
+    __shared__ int found_n;
+    const int t = threadIdx.x, lane = t & 63, lists = a.parts * a.top;
+    const int q = a.top > 0 ? (a.top + a.parts - 1) / a.parts : 1, r = (a.top + q - 1) / q;
     for (int row = blockIdx.x; row < a.m; row += gridDim.x) {
         const size_t first = (size_t)row * a.parts;
-        __syncthreads();
-        for (int i = t; i < lists; i += LP_THREADS) keys[i] = a.keys[first * a.top + i];
-        const int lane = t & 63;
+        const lp_key* keys = a.keys + first * a.top;
+        lp_key mine[LP_LISTS / LP_THREADS], head = 0;
         LpSums sum{LP_LOWEST, 0.0f, 0.0f};
         if (lane < a.parts) sum = a.sums[first + lane];
+        if (t < a.parts && a.top > 0) head = keys[t * a.top + q - 1];
+#pragma unroll
+        for (int i = 0; i < LP_LISTS / LP_THREADS; ++i) {
+            mine[i] = 0;
+            if (t + i * LP_THREADS < lists) mine[i] = keys[t + i * LP_THREADS];
+        }
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
             const LpSums o{__shfl_xor(sum.c, d, 64), __shfl_xor(sum.l, d, 64), __shfl_xor(sum.s, d, 64)};
             lp_add(sum, o);
         }
         const LpRow of = lp_finish(a, row, sum, t == 0);
+        if (a.top == 0) continue;
+        __syncthreads();  // the row before is done with LDS
+        if (t < 64) {
+            const bool it = lp_rank(head) == r - 1 && head != 0, any = __ballot(it) != 0;
+            if (t == 0) found_n = 0;
+            if (it || (t == 0 && !any)) least = it ? head : 1;
+        }
         __syncthreads();
-        for (int i = t; i < lists; i += LP_THREADS) {
-            const lp_key k = keys[i];
-            if (k == 0) continue;
-            int before = 0;  // larger ones: of every sorted list, those before the first below k
-            for (int p = 0; p < a.parts && before < a.top; ++p) {
-                int lo = 0, hi = a.top;
-                while (lo < hi) {
-                    const int mid = (lo + hi) / 2;
-                    if (keys[p * a.top + mid] > k)
-                        lo = mid + 1;
-                    else
-                        hi = mid;
-                }
-                before += lo;
-            }
+#pragma unroll
+        for (int i = 0; i < LP_LISTS / LP_THREADS; ++i)
+            if (mine[i] >= least) found[atomicAdd(&found_n, 1)] = mine[i];
+        __syncthreads();
+        const int count = found_n;
+        for (int i = t; i < count; i += LP_THREADS) {
+            const lp_key k = found[i];
+            int before = 0;
+#pragma unroll 8
+            for (int o = 0; o < count; ++o) before += found[o] > k;
             if (before < a.top) lp_alternative(a, row, before, k, of);
         }
     }
