@@ -1,5 +1,6 @@
 """One layer of a decoder that serves from 8 bits, on the library's 8-bit row
 operators: an example of their use together, and the path their tests run.
+Q8Layer holds one sequence, Q8Answers several answers to one prompt.
 
     python -m blas_symmetric_mat_amd.q8_layer
 
@@ -15,6 +16,15 @@ head.  A call takes a prompt's tokens or a single one:
     h  = o + h, normalised                         xsymv_q8norm_*
     g, u = h Wgu^T;  g / (1 + exp(-g)) * u         xsymv_q8gemm_*, xsymv_q8glu_*
     x  = that Wd^T; the next layer adds h          xsymv_q8gemm_*
+
+Q8Answers keeps the cache in pages that its answers share with the prompt:
+
+    the prompt's tokens get pages, the answers get the prompt's
+                                                   xsymv_q8pages_grow, _fork, _copy
+    k, v to their rows of the cache                xsymv_q8pages_slots, xsymv_q8store_*
+    attention, the prompt's tokens read once       xsymv_q8attn_*
+    an answer's next token, from logits            xsymv_logp_*
+    answers that have ended                        xsymv_q8pages_free
 """
 from __future__ import annotations
 
@@ -106,40 +116,174 @@ class Q8Layer:
         stride of rows); returns the layer's output and the new residual.
         ValueError, with nothing done, for other tensors and where the cache has
         no room for m tokens more."""
-        import torch
-        m, d, heads, hd = x.shape[0], self.d, self.heads, self.hd
+        m = x.shape[0]
         self._check("x", x, m)
         self._check("r", r, m)
         first, seen = self.used, self.used + m
         if seen > self.tokens:
             raise ValueError(f"the cache holds {self.tokens} tokens, {first} are there and {m} more "
                              "do not fit")
+        out = self._layer(x, r, lambda qkv: self._attend(qkv, first, seen))
+        self.used = seen
+        return out
+
+    def _layer(self, x, r, attend):
+        """attend: of the rows' q, k, v."""
+        m, d, f = x.shape[0], self.d, self.f
         h, rows = self._norm(m, x, r, self.norm1)
-        qkv = self._product(m, rows, self.wqkv)
-        slots, cap = self._slots(first, m), self.tokens * heads
-        past, read = self._slots(0, seen), []
+        att = attend(self._product(m, rows, self.wqkv))
+        rows = self._rows(m, d)
+        X.xsymv_q8store_b(m, d, att, d, None, m, rows[0], d, rows[1])
+        o = self._product(m, rows, self.wo)
+        h, rows = self._norm(m, o, h, self.norm2)
+        gu = self._product(m, rows, self.wgu)
+        rows = self._rows(m, f)
+        X.xsymv_q8glu_b(m, f, gu, 2 * f, gu[:, f:], 2 * f, rows[0], f, rows[1])
+        return self._product(m, rows, self.wd), h
+
+    def _store(self, qkv, slots):
+        d, heads, hd, m = self.d, self.heads, self.hd, qkv.shape[0]
         for part, (codes, scale) in enumerate(self.kv, start=1):
             new = qkv[:, part * d:(part + 1) * d].reshape(m * heads, hd)
-            X.xsymv_q8store_b(m * heads, hd, new, hd, slots, cap, codes, hd, scale)
+            X.xsymv_q8store_b(m * heads, hd, new, hd, slots, self.tokens * heads, codes, hd, scale)
+
+    def _attend(self, qkv, first, seen):
+        import torch
+        m, d, heads, hd = qkv.shape[0], self.d, self.heads, self.hd
+        self._store(qkv, self._slots(first, m))
+        past, read = self._slots(0, seen), []
+        for codes, scale in self.kv:
             out = torch.empty((seen * heads, hd), dtype=torch.float32, device=codes.device)
-            X.xsymv_q8read_s(seen * heads, hd, codes, hd, scale, past, cap, out, hd)
+            X.xsymv_q8read_s(seen * heads, hd, codes, hd, scale, past, self.tokens * heads, out, hd)
             read.append(out.view(seen, heads, hd).transpose(0, 1).double())
         q = qkv[:, :d].reshape(m, heads, hd).transpose(0, 1).double()
         score = q @ read[0].transpose(1, 2).contiguous() / math.sqrt(hd)
         token = torch.arange(seen, device=score.device)
         late = token[None, :] > token[first:, None]
         weight = torch.softmax(score.masked_fill(late, -math.inf), dim=-1)
-        att = (weight @ read[1].contiguous()).transpose(0, 1).reshape(m, d).bfloat16()
-        rows = self._rows(m, d)
-        X.xsymv_q8store_b(m, d, att, d, None, m, rows[0], d, rows[1])
-        o = self._product(m, rows, self.wo)
-        h, rows = self._norm(m, o, h, self.norm2)
-        gu, f = self._product(m, rows, self.wgu), self.f
-        rows = self._rows(m, f)
-        X.xsymv_q8glu_b(m, f, gu, 2 * f, gu[:, f:], 2 * f, rows[0], f, rows[1])
-        y = self._product(m, rows, self.wd)
-        self.used = seen
-        return y, h
+        return (weight @ read[1].contiguous()).transpose(0, 1).reshape(m, d).bfloat16()
+
+
+class Q8Answers(Q8Layer):
+    """The layer for up to `answers` answers to one prompt, `page` tokens a page
+    of the cache, which has room for `tokens` (a multiple of page).
+
+        layer.prompt(x, r)   the prompt's next tokens, all of it before:
+        layer.fork()         the answers begin, with the prompt's pages
+        layer.step(x, r)     a token of each answer
+        layer.free()         the answers end; fork may begin others
+
+    Each returns or raises as Q8Layer does."""
+
+    def __init__(self, d, heads, f, tokens, answers, page=16, seed=0, eps=1e-5):
+        super().__init__(d, heads, f, tokens, seed, eps)
+        self._pages(answers, page)
+
+    def _pages(self, answers, page):
+        import torch
+        if answers < 1 or page < 1 or self.tokens % page:
+            raise ValueError(f"{answers} answers, {self.tokens} tokens in pages of {page}")
+        self.answers, self.page, self.pages, self.seqs = answers, page, self.tokens // page, answers + 1
+
+        def ints(v):
+            return torch.tensor(v, dtype=torch.int32, device=self.place.device)
+
+        # Sequence 0 is the prompt.  What calls take as device arrays is made once.
+        self.len = ints([0] * self.seqs)
+        self.table = ints([[-1] * self.pages] * self.seqs)
+        self.refs = ints([0] * self.pages)
+        self.each, self.zeros, self.ones = ints(list(range(1, self.seqs))), ints([0] * answers), ints([1] * answers)
+        self.steps = ints([0] + list(range(self.seqs)))
+        self.all, self.shared = ints([0, self.seqs]), ints([0])
+        self.got, self.src, self.dst = (ints([0] * answers) for _ in range(3))
+        self.used = self.more = 0     # tokens of the prompt, and of each answer behind it
+        self.forked = False
+
+    def _held(self, used, more, forked):
+        """Pages that so many tokens are: a whole page of the prompt is held once."""
+        whole = used // self.page
+        own = -(-(used + more) // self.page) - whole
+        return -(-used // self.page) + (self.answers * own if forked else 0)
+
+    def _room(self, used, more, forked):
+        if self._held(used, more, forked) > self.pages:
+            raise ValueError(f"the cache holds {self.pages} pages of {self.page} tokens: {used} of a prompt"
+                             + (f" and {more} of {self.answers} answers" if forked else "") + " do not fit")
+
+    def _cache(self):
+        return self.seqs, self.len, self.table, self.pages, self.pages, self.page
+
+    def _answer(self, qkv, start, groups):
+        import torch
+        m, heads, hd = qkv.shape[0], self.heads, self.hd
+        slots = torch.empty((m * heads,), dtype=torch.int32, device=self.place.device)
+        X.xsymv_q8pages_slots(m, heads, start, self.seqs, self.len, self.table, self.pages, self.pages, self.page,
+                              slots)
+        self._store(qkv, slots)
+        att = torch.empty((m, self.d), dtype=torch.bfloat16, device=self.place.device)
+        (k, ks), (v, vs) = self.kv
+        X.xsymv_q8attn_b(m, heads, heads, hd, qkv, 3 * self.d, self.seqs, start, self.len, self.table, self.pages,
+                         groups, self.all, self.shared, k, hd, ks, v, hd, vs, self.pages, self.page,
+                         1 / math.sqrt(hd), att, self.d, None)
+        return att
+
+    def prompt(self, x, r):
+        import torch
+        m = x.shape[0]
+        self._check("x", x, m)
+        self._check("r", r, m)
+        if self.forked:
+            raise ValueError("the prompt has answers")
+        self._room(self.used + m, 0, False)
+        add = torch.tensor([m], dtype=torch.int32, device=self.place.device)
+        start = torch.tensor([0] + [m] * self.seqs, dtype=torch.int32, device=self.place.device)
+        X.xsymv_q8pages_grow(1, self.zeros, add, *self._cache(), self.refs, self.got)
+        self.used += m
+        return self._layer(x, r, lambda qkv: self._answer(qkv, start, 0))
+
+    def fork(self):
+        if self.forked:
+            raise ValueError("the prompt has answers")
+        self._room(self.used, 0, True)
+        X.xsymv_q8pages_fork(self.answers, self.zeros, self.each, *self._cache(), self.refs, self.src, self.dst)
+        rows = self.heads * self.page
+        (k, ks), (v, vs) = self.kv
+        X.xsymv_q8pages_copy(self.answers, self.src, self.dst, self.pages, rows, self.hd, k, self.hd, ks,
+                             v, self.hd, vs, 1, self.pages * rows)
+        self.shared.fill_(self.used // self.page * self.page)
+        self.more, self.forked = 0, True
+
+    def step(self, x, r):
+        """x, r: row i is the next token of answer i."""
+        self._check("x", x, self.answers)
+        self._check("r", r, self.answers)
+        if not self.forked:
+            raise ValueError("the prompt has no answers")
+        self._room(self.used, self.more + 1, True)
+        self.more += 1
+        return self._step(x, r)
+
+    def _step(self, x, r):
+        X.xsymv_q8pages_grow(self.answers, self.each, self.ones, *self._cache(), self.refs, self.got)
+        return self._layer(x, r, lambda qkv: self._answer(qkv, self.steps, 1))
+
+    def free(self):
+        if not self.forked:
+            raise ValueError("the prompt has no answers")
+        X.xsymv_q8pages_free(self.answers, self.each, *self._cache(), self.refs)
+        self.forked = False
+
+    def likely(self, x, r, head, top):
+        """The layer's output and residual as logits of `head` (a Q8Weight): the
+        `top` most likely tokens of each row and their log probabilities."""
+        import torch
+        m = x.shape[0]
+        rows = self._norm(m, x, r, self.norm1)[1]
+        logits = self._product(m, rows, head)
+        index = torch.empty((m, top), dtype=torch.int32, device=logits.device)
+        value = torch.empty((m, top), dtype=torch.float32, device=logits.device)
+        X.xsymv_logp_b(m, head.n, logits, head.n, None, None, None, None, top, index, value, top)
+        return index, value
 
 
 def plain(layer, x, r):
@@ -184,6 +328,30 @@ def main():
     torch.cuda.synchronize()
     print(f"64 single tokens: {(time.perf_counter() - t) / 64 * 1e6:.0f} us a token "
           "(attention in torch's elementary operations)")
+
+    del layer, want, want_h
+    answers, length, words = 16, 64, 32000
+    layer = Q8Answers(d=4096, heads=32, f=11008, tokens=4096, answers=answers)
+    head = Q8Weight(torch.randn((words, 4096), generator=g, device="cuda") / 64)
+
+    def rows(tokens):
+        return (head.codes[tokens].float() * head.scale[tokens, None] * 64).bfloat16()
+
+    zero = torch.zeros((answers, 4096), dtype=torch.bfloat16, device="cuda")
+    y, h = layer.prompt(x[:prompt], r[:prompt])
+    index, value = layer.likely(y[-1:], h[-1:], head, answers)
+    tokens, sums = index[0], value[0].clone()  # each answer begins with another token
+    layer.fork()
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(length):
+        y, h = layer.step(rows(tokens), zero)
+        index, value = layer.likely(y, h, head, 1)
+        tokens = index[:, 0]
+        sums += value[:, 0]
+    torch.cuda.synchronize()
+    print(f"{answers} answers of {length} tokens: {(time.perf_counter() - t) / length * 1e6:.0f} us a token of each; "
+          f"the likeliest has log probability {sums.max().item():.2f}")
 
 
 if __name__ == "__main__":
