@@ -48,16 +48,17 @@ template <class F>
 __device__ int pg_free(const PgCache& c, int want, int* waves, F&& take)
 {
     int found = 0;
-    for (int base = 0; base < c.pages && found < want; base += PG_THREADS * PG_CHUNK) {
-        const int first = base + (int)threadIdx.x * PG_CHUNK;
+    // (unsigned: the last round reaches past the largest int)
+    for (unsigned base = 0; base < (unsigned)c.pages && found < want; base += PG_THREADS * PG_CHUNK) {
+        const unsigned first = base + threadIdx.x * PG_CHUNK;
         unsigned mask = 0;
 #pragma unroll
         for (int e = 0; e < PG_CHUNK; ++e)
-            if (first + e < c.pages && c.refs[first + e] == 0) mask |= 1u << e;
+            if (first + e < (unsigned)c.pages && c.refs[first + e] == 0) mask |= 1u << e;
         int total = 0;
         int rank = found + pg_scan((int)__popc(mask), waves, total);
         while (mask != 0 && rank < want) {
-            take(first + __ffs((int)mask) - 1, rank++);
+            take((int)first + __ffs((int)mask) - 1, rank++);
             mask &= mask - 1;
         }
         found += total;
@@ -335,33 +336,33 @@ __global__ __launch_bounds__(PG_THREADS) void q8_pages_plan(PgCompactArgs a)
     __shared__ int waves[PG_THREADS / 64];
     const int half = a.pages / 2;
     constexpr int STEP = PG_THREADS * PG_CHUNK;
-    auto used = [&](int base) {
-        const int first = base + (int)threadIdx.x * PG_CHUNK;
+    auto used = [&](unsigned base) {
+        const unsigned first = base + threadIdx.x * PG_CHUNK;
         unsigned mask = 0;
 #pragma unroll
         for (int e = 0; e < PG_CHUNK; ++e)
-            if (first + e < a.pages && a.refs[first + e] != 0) mask |= 1u << e;
+            if (first + e < (unsigned)a.pages && a.refs[first + e] != 0) mask |= 1u << e;
         return mask;
     };
     int live = 0;
-    for (int base = 0; base < a.pages; base += STEP) live += __popc(used(base));
+    for (unsigned base = 0; base < (unsigned)a.pages; base += STEP) live += __popc(used(base));
     int total = 0;
     (void)pg_scan(live, waves, total);
     live = total;
     int holes = 0, movers = 0;
-    for (int base = 0; base < a.pages; base += STEP) {
-        const int first = base + (int)threadIdx.x * PG_CHUNK;
-        const int have = min(max(a.pages - first, 0), PG_CHUNK);
-        const int low = min(max(live - first, 0), have);  // of the chunk, before place `live`
+    for (unsigned base = 0; base < (unsigned)a.pages; base += STEP) {
+        const unsigned first = base + threadIdx.x * PG_CHUNK;
+        const int have = first < (unsigned)a.pages ? min(a.pages - (int)first, PG_CHUNK) : 0;
+        const int low = first < (unsigned)live ? min(live - (int)first, have) : 0;  // before place `live`
         const unsigned mask = used(base), below = (1u << low) - 1, valid = (1u << have) - 1;
         unsigned hole = ~mask & below, mover = mask & valid & ~below;
         int more = 0;
         int rank = holes + pg_scan((int)__popc(hole), waves, more);
         holes += more;
-        for (; hole != 0; hole &= hole - 1) a.dst[rank++] = first + __ffs((int)hole) - 1;
+        for (; hole != 0; hole &= hole - 1) a.dst[rank++] = (int)first + __ffs((int)hole) - 1;
         rank = movers + pg_scan((int)__popc(mover), waves, more);
         movers += more;
-        for (; mover != 0; mover &= mover - 1) a.src[rank++] = first + __ffs((int)mover) - 1;
+        for (; mover != 0; mover &= mover - 1) a.src[rank++] = (int)first + __ffs((int)mover) - 1;
     }
     for (int i = movers + (int)threadIdx.x; i < half; i += PG_THREADS) a.src[i] = a.dst[i] = -1;
     if (threadIdx.x == 0) a.live[0] = live;

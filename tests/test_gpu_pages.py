@@ -254,3 +254,31 @@ def test_a_captured_step():
             if a >= 0:
                 assert torch.equal(k[a * 32:a * 32 + 32], k[b * 32:b * 32 + 32])
                 assert torch.equal(ks[a * 32:a * 32 + 32], ks[b * 32:b * 32 + 32])
+
+
+def test_the_most_pages():
+    """As many pages as an int counts, of which the last three are free, and one used among free ones."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    pages = 2 ** 31 - 1
+    length, table = ints([0, 0, 0]), torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    refs = torch.ones((pages,), dtype=torch.int32, device="cuda")
+    refs[pages - 3:] = 0
+    got = ints([0, 0])
+    X.xsymv_q8pages_grow(2, ints([1, 0]), ints([2, 1]), 3, length, table, 4, pages, 1, refs, got)
+    torch.cuda.synchronize()
+    assert got.tolist() == [2, 1] and length.tolist() == [1, 2, 0]
+    assert table[1, :2].tolist() == [pages - 3, pages - 2] and table[0, 0].item() == pages - 1
+    assert refs[pages - 3:].tolist() == [1, 1, 1]
+    refs.zero_()
+    refs[pages - 2] = 5
+    table.fill_(-1)
+    table[2, 3] = pages - 2
+    src, dst = (torch.zeros((pages // 2,), dtype=torch.int32, device="cuda") for _ in range(2))
+    live = ints([7])
+    X.xsymv_q8pages_compact(3, table, 4, table, 4, pages, refs, refs, src, dst, live)
+    torch.cuda.synchronize()
+    assert live.tolist() == [1] and src[:2].tolist() == [pages - 2, -1] and dst[:2].tolist() == [0, -1]
+    assert refs[0].item() == 5 and not bool(refs[1:].any())
+    assert table.flatten().tolist() == [-1] * 11 + [0]
+    assert bool((src[1:] == -1).all()) and bool((dst[1:] == -1).all())
