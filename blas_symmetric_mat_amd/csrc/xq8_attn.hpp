@@ -355,6 +355,31 @@ __device__ __forceinline__ void at_lse(const AttnArgs<T>& a, size_t row, int hea
     if (a.lse != nullptr) a.lse[row * a.p.heads + head] = l == 0.0f ? -INFINITY : m * AT_LN2 + logf(l);
 }
 
+// Where in a slab lane (n, g)'s results of registers 4 j to 4 j + 3, place i, are: a
+// wave's stores of one i and j lie side by side, and of those a row's 64 bytes do.
+// (With rows one after the other a lane's 128 bytes lie together, and a store of 64
+// lanes touches as many lines: 64 rows of 32 heads over 16384 shared tokens took 85 us
+// in all, now 80.)
+__device__ __forceinline__ int at_part_of(int i, int j, int v, int n, int g)
+{
+    return 2 * AT_NARROW + ((i * v + j) * AT_NARROW + n) * 16 + g * 4;
+}
+template <bool ALL, int HD>
+__device__ __forceinline__ void at_keep(const AtRows<HD>& r, const AtLanes<HD>& at, float* slab, float f, int n, int hd)
+{
+    constexpr int V = HD / 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (!ALL && (4 * at.g + i) * AtRows<HD>::CB >= hd) continue;  // the last codes again
+            at_f4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = r.o[4 * j + e][i] * f;
+            *(at_f4*)(slab + at_part_of(i, j, V, n, at.g)) = v;
+        }
+}
+
 // One lane's codes of a row of results, times f.
 template <int HD, class O>
 __device__ __forceinline__ void at_write(const AtRows<HD>& r, const AtLanes<HD>& at, O* to, float f, int hd)
@@ -387,7 +412,10 @@ __device__ __forceinline__ void at_finish(const AttnArgs<T>& a, const AtJob& job
             part[2 * m] = r.m;
             part[2 * m + 1] = r.l;
         }
-        at_write(r, at, part + 2 * AT_NARROW + (size_t)m * hd, f, hd);
+        if (hd == HD)
+            at_keep<true>(r, at, part, f, m, hd);
+        else
+            at_keep<false>(r, at, part, f, m, hd);
     } else {
         size_t row;
         const int head = job.place(a.p, n, row);
@@ -428,7 +456,8 @@ struct AtNarrow {
 
     __device__ __forceinline__ int page_of(int t) const
     {
-        return lane < STEP && t < job.end ? pages[a.p.by_page.of(t)] : -1;
+        // (unsigned: two steps behind the last token may pass the largest int)
+        return lane < STEP && (unsigned)t < (unsigned)job.end ? pages[a.p.by_page.of(t)] : -1;
     }
     // rows of the step's tokens to LDS, and their codes and scales on their way
     __device__ __forceinline__ void fetch(Codes& c, AtTokens& tok, int base, int page)
@@ -580,7 +609,10 @@ struct AtWide {
     AtUnit unit;
     int limit[2], least, most;
 
-    __device__ __forceinline__ int page_of(int t) const { return t < job.end ? pages[a.p.by_page.of(t)] : -1; }
+    __device__ __forceinline__ int page_of(int t) const
+    {
+        return (unsigned)t < (unsigned)job.end ? pages[a.p.by_page.of(t)] : -1;
+    }
 
     __device__ __forceinline__ void fetch(Codes& c, int base, int page)
     {
@@ -819,14 +851,17 @@ __global__ __launch_bounds__(256, (at_resident<T, HD>)) void q8_attn_narrow(Attn
 }
 
 // Adds the parts of rows' results.  LANES lanes have a row and head, four of its codes
-// each, and with WAVES of four all waves of a workgroup share its parts.
+// each in the slabs' order, and with more than one of WAVES all waves of a workgroup
+// share its parts.
 template <class T, int LANES, int WAVES>
-__global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
+__global__ __launch_bounds__((WAVES > 4 ? 64 * WAVES : 256)) void q8_attn_join(AttnArgs<T> a)
 {
-    constexpr int U = 4, ITEMS = 64 / LANES * (4 / WAVES);
-    __shared__ float sums[WAVES > 1 ? 4 : 1][64][6];
+    constexpr int U = 4, ITEMS = 64 / LANES * (WAVES > 1 ? 1 : 4), HD = 4 * LANES, V = HD / 64;
+    __shared__ float sums[WAVES][64][6];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = a.p.hd;
-    const int d = threadIdx.x % LANES * 4, have = min(hd - d, 4);
+    const int at_g = threadIdx.x % 4, at_i = threadIdx.x % LANES / 4 / V, at_j = threadIdx.x % LANES / 4 % V;
+    const int d = AtLanes<HD>::at_value(4 * at_g + at_i, hd) + 4 * at_j;
+    const bool own_codes = (4 * at_g + at_i) * (HD / 16) < hd;
     const long long all = (long long)a.p.rows * a.p.heads;
     const long long item = (long long)blockIdx.x * ITEMS + (WAVES > 1 ? lane : (int)threadIdx.x) / LANES;
     int2 own{0, 0}, shared{0, 0};
@@ -854,17 +889,10 @@ __global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
                     const float* s = a.slabs + at * at_slab(hd);
                     pm[u] = s[2 * n];
                     pl[u] = s[2 * n + 1];
-                    s += 2 * AT_NARROW + n * hd + d;
-                    if (have == 4) {
-                        typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-                        const vec x = *(const vec*)s;
+                    if (!own_codes) continue;
+                    const at_f4 x = *(const at_f4*)(s + at_part_of(at_i, at_j, V, n, at_g));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[u][e] = x[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (e < have) v[u][e] = s[e];
-                    }
+                    for (int e = 0; e < 4; ++e) v[u][e] = x[e];
                 }
             }
 #pragma unroll
@@ -900,18 +928,14 @@ __global__ __launch_bounds__(256) void q8_attn_join(AttnArgs<T> a)
     }
     if (own.y == 0) return;
     const int head = (int)(item - (long long)row * a.p.heads);
-    if (d == 0) at_lse(a, row, head, m, l);
+    if (threadIdx.x % LANES == 0) at_lse(a, row, head, m, l);
+    if (!own_codes) return;
     T* out = a.out + row * a.ldo + (size_t)head * hd + d;
     typedef T vec __attribute__((ext_vector_type(4), aligned(sizeof(T))));
     vec x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = (T)(l == 0.0f ? 0.0f : o[e] / l);
-    if (have == 4)
-        *(vec*)out = x;
-    else
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < have) out[e] = x[e];
+    *(vec*)out = x;
 }
 
 }  // namespace xsymv

@@ -36,9 +36,12 @@ constexpr int AT_LEAST = 2, AT_LEAST_WIDE = 4;
 // Entries of a call at most: windows of 64, of which LDS holds the sums.
 constexpr int AT_WINDOWS = 1024, AT_ENTRIES = 64 * AT_WINDOWS;
 
-// Floats of a slab, the results of 16 rows in a part of a job: m and l of each,
-// then their out, not yet divided by l.
-__host__ __device__ inline size_t at_slab(int hd) { return (size_t)AT_NARROW * (2 + hd); }
+// Floats of a slab, the results of 16 rows in a part of a job: m and l of each, then
+// their out, not yet divided by l, in the order in which a wave stores it (at_part_of).
+__host__ __device__ inline size_t at_slab(int hd)
+{
+    return (size_t)AT_NARROW * (2 + (hd <= 64 ? 64 : hd <= 128 ? 128 : 256));
+}
 
 // Quotients of numbers below 2^31 by one that the host knows.
 struct AtDivisor {
@@ -111,7 +114,8 @@ struct AtEntry {
     {
         if (p.whole) return b;
         if (!wide) return b * (AT_OVER + tiles(t1 - t0));
-        if (group) return b * (AT_OVER_WIDE + tiles(t1 - t0));
+        // (more rows than tokens: any block as one that sees all, so that sums stay small)
+        if (group || before < 0) return b * (AT_OVER_WIDE + tiles(t1 - t0));
         // block b sees up to step * (b + 1) tokens more than what lies before the
         // rows; the sums of these are rounded down, for which one tile makes up
         const int step = p.by_share.of(p.wide_rows() + p.share - 1);
@@ -439,6 +443,8 @@ struct AtCursor {
                 }
             const int c0 = WIDE ? of.before_block(p, b) : 0, c1 = WIDE ? of.before_block(p, b + 1) : of.cost;
             const int x = rest - c0, y = min(x + end - pos, c1 - c0);
+            // (starts that do not ascend: sums that no int holds)
+            if ((unsigned)head >= (unsigned)p.kvheads || y <= x) return false;
             job.end = of.end(p, b);
             const int tiles = max(1, of.tiles(job.end - of.t0));
             const int t0 = p.whole ? 0 : min(x, tiles), t1 = p.whole ? tiles : min(y, tiles);
@@ -460,7 +466,7 @@ struct AtCursor {
                 part = WIDE ? (2 * worker + (t0 == 0)) * p.wide_slabs() : p.narrow_at + 2 * worker + (t0 == 0);
             else if (of.joined)
                 part = p.whole_at + parts + head * of.slabs(p) + b * of.block_slabs(p);
-            if (part > p.slabs - of.block_slabs(p)) continue;  // (starts that do not ascend)
+            if (part < -1 || part > p.slabs - of.block_slabs(p)) continue;  // (the same)
             if (t0 == 0) note(p, job, part, t1 < tiles ? tiles - 1 - y : -1);
             return true;
         }

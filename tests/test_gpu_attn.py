@@ -449,3 +449,21 @@ def test_any_sizes(seed):
                  off=rng.choice([0, 0, 1, 8])).spoil()
         c.call()
         c.check()
+
+
+def test_many_more_rows_than_tokens():
+    """Six million rows of a sequence of three tokens: all but the last three see nothing (how a block's
+    tokens grow with its place would not fit an int here)."""
+    import torch
+    c = Case("h", 1, 1, 16, 16, [3], [6000000])
+    c.call()
+    torch.cuda.synchronize()
+    assert not bool(c.out.t[:-3].any()) and bool((c.lse[:-3] == -math.inf).all())
+    few = Case("h", 1, 1, 16, 16, [3], [3])
+    for name in ("k", "v", "q"):
+        getattr(few, name).t.copy_(getattr(c, name).t[-getattr(few, name).m:])
+    for name in ("ks", "vs", "table"):
+        getattr(few, name).copy_(getattr(c, name))
+    few.call()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out.t[-3:], few.out.t) and torch.equal(c.lse[-3:], few.lse)
