@@ -102,6 +102,8 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
             // Single tokens of few heads are narrow jobs: only groups' may be wide.
             p.wide_entries = p.groups + (single && p.share <= AT_NARROW ? 0 : p.seqs);
             if (p.whole && single && p.share <= AT_NARROW) p.wide_entries = 0;
+            // (a launch without jobs: one token over 1000 21 us with it, 15 without)
+            if ((long long)p.rows * p.share <= AT_NARROW) p.wide_entries = 0;
             const long long most = p.whole ? (long long)std::min(blocks * p.kvheads, 1e9) : 1ll << 30;
             const int rc = p.wide_entries > 0 ? attn_grid(&q8_attn_wide<T, HD>, threads, most, p.grid) : 0;
             if (rc) return rc;
