@@ -10,9 +10,9 @@
 // from below, and only the few threads that hold one above it read theirs again.
 //
 // Bound by the reads where rows are many and long: 2048 rows of 131072 bfloat16
-// logits in 101 us, 5.3 TB/s, the sums' some nine instructions a logit behind
+// logits in 101 us, 5.4 TB/s, the sums' some nine instructions a logit behind
 // them (at eleven, with room for five waves a SIMD instead of eight, 129 us).  A
-// single row of 32000 is dealt over 16 workgroups; the rest of its 12 us is the
+// single row of 32000 is dealt over 16 workgroups; the rest of its 11 us is the
 // two launches and what each does one after the other.
 #pragma once
 

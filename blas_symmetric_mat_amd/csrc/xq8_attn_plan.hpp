@@ -9,10 +9,11 @@
 //
 // There are two lines of jobs, one after the other by entry, head and block: wide
 // jobs, of which every workgroup of q8_attn_wide takes an equal piece, and narrow
-// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32 tokens): a job's tiles come first in its stretch of the line, then some that
-// stand for what a job takes besides.  Stretches may be longer than need be, but have
-// to be the same for all workers, which compute them from the arrays on the device,
-// so that a captured call follows what these hold.  A single sequence's step waits for
+// ones, of which every wave of q8_attn_narrow does.  Lines are counted in tiles (32
+// tokens): a job's tiles come first in its stretch of the line, then some that stand
+// for what a job takes besides.  Stretches may be longer than need be, but have to be
+// the same for all workers, which compute them from the arrays on the device, so that
+// a captured call follows what these hold.  A single sequence's step waits for
 // this: it is some hundred instructions, with sums over lanes (64 entries at a time).
 //
 // Who takes a job's first tile writes down, for each of its rows, where the parts of

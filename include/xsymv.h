@@ -457,7 +457,8 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *
  * DEVICE arrays of int: table (seqs rows of ldt entries), len (tokens of each
  * sequence), refs (for each page the sequences that hold it; 0: a free page).  A
- * len below zero counts as zero, one above ldt * ps as that.  Where a call takes
+ * len below zero counts as zero, one above ldt * ps as that (in the attention, as
+ * 2^31 - 256 at most).  Where a call takes
  * `start` (seqs + 1 ascending numbers), rows start[i] to start[i + 1] - 1 of its
  * matrices are the last tokens of sequence i, of which a sequence may have none;
  * start NULL: row i is the last token of sequence i.  Rows outside start[0] to
@@ -487,12 +488,12 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   xsymv_q8attn_workspace_bytes; where it cannot be had (as for the product
  *   above) the call is made without, in up to many times the time.
  *   Codes: -1 rows < 0 (or rows * heads over 2^31 - 1), -2 heads < 1 or not a
- *   multiple of kvheads (or heads * hd over 2^31 - 1), -3 kvheads < 1, -4 hd < 16 or > 256, -5 q NULL, -6 ldq, -7
- *   seqs < 0, > 65536, or not rows without start, -9 len NULL, -10 table NULL, -11 ldt <
- *   0, -12 groups < 0 or > 65536 - seqs, -13 first NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd,
- *   -17 ks NULL, -18 v NULL, -19 ldv < hd, -20 vs NULL, -21 pages < 0 or too many
- *   rows, -22 ps < 1, -23 scale not finite, -24 out NULL, -25 ldo, 2000 installed
- *   workspace too small.
+ *   multiple of kvheads (or heads * hd over 2^31 - 1), -3 kvheads < 1, -4 hd < 16 or
+ *   > 256, -5 q NULL, -6 ldq, -7 seqs < 0, > 65536, or not rows without start, -9 len
+ *   NULL, -10 table NULL, -11 ldt < 0, -12 groups < 0 or > 65536 - seqs, -13 first
+ *   NULL, -14 shared NULL, -15 k NULL, -16 ldk < hd, -17 ks NULL, -18 v NULL, -19
+ *   ldv < hd, -20 vs NULL, -21 pages < 0 or too many rows, -22 ps < 1, -23 scale not
+ *   finite, -24 out NULL, -25 ldo, 2000 installed workspace too small.
  *
  *   xsymv_q8pages_grow:  sequence seq[i] gets add[i] tokens more (n of them, in
  *   order; n <= 8192): free pages, the lowest first, are entered in its row of
