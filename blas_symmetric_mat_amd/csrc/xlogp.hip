@@ -41,7 +41,7 @@ int logp_run(int m, int n, const T* x, int ldx, const int* token, float* logp, f
              int top, int* index, float* value, int ldt, hipStream_t stream)
 {
     if (m < 0) return -1;
-    if (n < 0) return -2;
+    if (n < 0 || n > LP_MOST) return -2;
     const bool some = m > 0 && n > 0;
     if (some && x == nullptr) return -3;
     if (ldx < std::max(1, n)) return -4;
@@ -64,7 +64,7 @@ int logp_run(int m, int n, const T* x, int ldx, const int* token, float* logp, f
 extern "C" size_t xsymv_logp_workspace_bytes(int m, int n, int top)
 {
     using namespace xsymv;
-    if (m <= 0 || n <= 0 || top < 0 || top > LP_TOP) return 0;
+    if (m <= 0 || n <= 0 || n > LP_MOST || top < 0 || top > LP_TOP) return 0;
     return logp_bytes(m, logp_parts(m, n, top), top);
 }
 

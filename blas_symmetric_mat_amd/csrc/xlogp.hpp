@@ -23,6 +23,7 @@
 namespace xsymv {
 
 constexpr int LP_THREADS = 256;
+constexpr int LP_MOST = 0x7fffffff - 4095;  // logits of a row at most: a round of loads further is an int
 constexpr int LP_TOP = 128;     // alternatives of one row at most
 constexpr int LP_FEW = 32;      // alternatives that 64 bounds find
 constexpr int LP_CAP = 1024;    // candidates ranked at once

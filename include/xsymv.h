@@ -554,8 +554,8 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   of these alone: lse, logp and value -infinity, entropy 0.  A row that holds a
  *   NaN or +infinity: NaN, and indexes of which only is said that they differ.
  *   Uses the stream's workspace, up to xsymv_logp_workspace_bytes, as xsymv_q8attn_*
- *   does.  Codes: -1 m < 0, -2 n < 0, -3 x NULL, -4 ldx, -6 logp NULL with token,
- *   -9 top < 0, > n or > 128, -10 index NULL, -12 ldt < top, 2000.
+ *   does.  Codes: -1 m < 0, -2 n < 0 or > 2^31 - 4096, -3 x NULL, -4 ldx, -6 logp
+ *   NULL with token, -9 top < 0, > n or > 128, -10 index NULL, -12 ldt < top, 2000.
  * All: 1000 + hipError_t. */
 size_t xsymv_q8attn_workspace_bytes(int rows, int heads, int kvheads, int hd, int seqs, int groups);
 size_t xsymv_logp_workspace_bytes(int m, int n, int top);

@@ -214,3 +214,22 @@ def test_many_rows_and_long_offsets():
     x.t.copy_(torch.randn((m, n), generator=gen(1), device="cuda"))
     token = torch.arange(m, device="cuda").to(torch.int32)
     check(x, token, call(x, "b", token, 10), 10)
+
+
+def test_the_longest_row():
+    """2^31 - 4096 logits: zeros but for two, the first and last of which are the largest.  l is exact up to
+    the sums of the two (whole numbers of 8 a thread's step), so the bound is that of a few roundings."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    n = 2 ** 31 - 4096
+    x = torch.zeros((1, n), dtype=torch.float16, device="cuda")
+    x[0, 7] = x[0, n - 1] = 5.0
+    token = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    f = [torch.empty((1,), device="cuda") for _ in range(3)]
+    index, value = torch.empty((1, 3), dtype=torch.int32, device="cuda"), torch.empty((1, 3), device="cuda")
+    X.xsymv_logp_h(1, n, x, n, token, *f, 3, index, value, 3)
+    torch.cuda.synchronize()
+    lse = math.log(n - 2 + 2 * math.exp(5.0))
+    assert index.tolist() == [[7, n - 1, 0]]
+    assert abs(f[2].item() - lse) < 64 * U * lse and abs(f[0].item() - (5 - lse)) < 64 * U * lse
+    assert all(abs(a - b) < 64 * U * lse for a, b in zip(value[0].tolist(), (5 - lse, 5 - lse, -lse)))

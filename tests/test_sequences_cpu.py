@@ -28,7 +28,7 @@ BAD = {
              ("ldv", 63, -19), ("vs", None, -20), ("pages", -1, -21), ("pages", BIG // 30, -21), ("ps", 0, -22),
              ("ps", BIG, -21), ("scale", float("nan"), -23), ("scale", float("inf"), -23), ("out", None, -24),
              ("ldo", 511, -25)],
-    "logp": [("m", -1, -1), ("n", -1, -2), ("x", None, -3), ("ldx", 99, -4), ("logp", None, -6), ("top", -1, -9),
+    "logp": [("m", -1, -1), ("n", -1, -2), ("n", 2 ** 31 - 4095, -2), ("x", None, -3), ("ldx", 99, -4), ("logp", None, -6), ("top", -1, -9),
              ("top", 101, -9), ("index", None, -10), ("ldt", 4, -12)],
     "grow": [("n", -1, -1), ("n", 8193, -1), ("seq", None, -2), ("add", None, -3), ("seqs", -1, -4), ("len", None, -5),
              ("table", None, -6), ("ldt", -1, -7), ("pages", -1, -8), ("ps", 0, -9), ("refs", None, -10),
