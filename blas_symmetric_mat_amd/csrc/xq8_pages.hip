@@ -6,6 +6,19 @@
 namespace xsymv {
 namespace {
 
+// A call of two kernels, the first one of one workgroup: one timing record.
+template <class A>
+int launch_two(void (*first)(A), void (*second)(A), unsigned grid, hipStream_t stream, const A& a)
+{
+    TimedCall tc{};
+    const int timing = timing_enabled();
+    if (timing) XSYMV_HIP(timed_call_create(tc, timing));
+    XSYMV_HIP(launch_k(first, dim3(1), dim3(PG_THREADS), stream, a, tc.e0, tc.e1));
+    XSYMV_HIP(launch_k(second, dim3(grid), dim3(256), stream, a, nullptr, tc.e2));
+    if (timing) timing_push(tc);
+    return 0;
+}
+
 // Rows of a cache count in an int, as slots do.
 bool too_many(int pages, int kvheads, int ps)
 {
@@ -74,9 +87,8 @@ int fork_run(int n, const int* parent, const int* child, int seqs, int* len, int
     // saves the second launch; what a single workgroup writes is bound by its own
     // latency, a table's row at a time.
     a.whole = n <= 16 && (long long)n * ldt <= 16 * PG_THREADS;
-    const int rc = q8_launch(&q8_pages_fork, 1, PG_THREADS, stream, a);
-    if (rc || a.whole) return rc;
-    return q8_launch(&q8_pages_inherit, (unsigned)n, 256, stream, a);
+    if (a.whole) return q8_launch(&q8_pages_fork, 1, PG_THREADS, stream, a);
+    return launch_two(&q8_pages_fork, &q8_pages_inherit, (unsigned)n, stream, a);
 }
 
 int free_run(int n, const int* seq, int seqs, int* len, int* table, int ldt, int pages, int ps, int* refs,
@@ -113,11 +125,9 @@ int compact_run(int seqs, const int* table, int ldt, int* out, int ldo, int page
     if (pages > 1 && dst == nullptr) return -10;
     if (live == nullptr) return -11;
     const PgCompactArgs a{table, refs, out, rout, src, dst, live, seqs, ldt, ldo, pages};
-    const int rc = q8_launch(&q8_pages_plan, 1, PG_THREADS, stream, a);
-    if (rc) return rc;
     const long long all = (long long)seqs * ldt + pages;
-    if (all == 0) return 0;
-    return q8_launch(&q8_pages_rename, (unsigned)std::min((all + 255) / 256, 4096ll), 256, stream, a);
+    if (all == 0) return q8_launch(&q8_pages_plan, 1, PG_THREADS, stream, a);
+    return launch_two(&q8_pages_plan, &q8_pages_rename, (unsigned)std::min((all + 255) / 256, 4096ll), stream, a);
 }
 
 int copy_run(int n, const int* src, const int* dst, int pages, int rows, int hd, signed char* k, int ldk,

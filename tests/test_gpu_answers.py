@@ -145,3 +145,36 @@ def test_moved_together():
     for t, u in zip(*outs):
         for row in (0, 3, 4):
             assert torch.equal(t[row], u[row])
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+def test_timing_records_each_call(mode):
+    """Calls with one kernel, with a join, with wide and narrow jobs: a record each, and the same bytes."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    many = make()
+    prompt, own = tokens(11)
+    y, h = many.prompt(*prompt)
+    many.fork()
+    head = q8_weight()
+    many.likely(y, h, head, 5)
+    many.likely(y[:1], h[:1], head, 5)
+    torch.cuda.synchronize()
+    X.timing_read()
+    X.timing_enable(mode)
+    try:
+        index, value = many.likely(y, h, head, 5)
+        single = many.likely(y[:1], h[:1], head, 5)
+        many.step(own[0][0], own[1][0])
+    finally:
+        rec = X.timing_read()
+        X.timing_enable(0)
+    # a norm, a product and the log probabilities twice; the step's 13 calls, of which grow, slots and
+    # three stores, a norm each, four products, the attention and the activation
+    assert len(rec) >= 2 * 3 + 8 and all(a > 0 and b >= 0 for a, b in rec)
+    assert torch.equal(index[:1], single[0]) and bool(((value[:1] - single[1]).abs() < 1e-5).all())
+
+
+def q8_weight():
+    from blas_symmetric_mat_amd import q8_layer
+    return q8_layer.Q8Weight(randn((5003, D), gen(12)))

@@ -282,3 +282,24 @@ def test_the_most_pages():
     assert refs[0].item() == 5 and not bool(refs[1:].any())
     assert table.flatten().tolist() == [-1] * 11 + [0]
     assert bool((src[1:] == -1).all()) and bool((dst[1:] == -1).all())
+
+
+@pytest.mark.parametrize("mode", [1, 2])
+def test_timing_records_each_call(mode):
+    import blas_symmetric_mat_amd as X
+    p = Pages(40, 30, 400, 4)
+    p.grow([0, 1], [70, 41])
+    X.timing_read()
+    X.timing_enable(mode)
+    try:
+        p.fork([0, 1], [2, 3])           # one launch
+        p.fork([0, 1] * 9, list(range(4, 22)))  # two
+        p.grow([5], [3])
+        p.free([0, 7])
+        p.compact(True)
+    finally:
+        rec = X.timing_read()
+        X.timing_enable(0)
+    assert len(rec) == 5 and all(a > 0 and b >= 0 for a, b in rec)
+    if mode == 1:
+        assert [b > 0 for _, b in rec] == [False, True, False, False, True]
