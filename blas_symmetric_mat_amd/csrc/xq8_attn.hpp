@@ -583,10 +583,14 @@ template <class T, int HD>
 struct AtWide {
     static constexpr int NK = HD / 64, NF = HD / 32, CB = HD / 16, NV = CB / 4;
     static constexpr bool SPLIT = AtQuery<T, HD>::SPLIT;
-    // Eight waves on a compute unit either way: as one workgroup, whose waves convert half
-    // as much for their rows; heads of 256 codes and float's two numbers take the
-    // registers and the LDS of more.
-    static constexpr int WAVES = HD <= 128 && !SPLIT ? 8 : 4, STEP = 16 * WAVES;
+    // Eight waves on a compute unit, as one workgroup: as two of four, each wave converts
+    // twice as much for its rows.  Two tiles of rows a wave where registers hold them, one
+    // where not (float's two numbers over 64 codes, others over 128), and over 128 codes
+    // LDS for one buffer.  4 x 1024 rows behind 8192 tokens, with four waves of two tiles
+    // and as it is: bfloat16 of 128 codes 895 us and 705, of 256 4521 and 1608; float of
+    // 64 codes 1234 and 638, of 128 1827 and 1218 (two tiles on eight waves: spilled).
+    static constexpr int WAVES = 8, STEP = 16 * WAVES;
+    static constexpr int TILES = HD <= (SPLIT ? 64 : 128) ? 2 : 1, BUFFERS = HD <= 128 ? 2 : 1, ROWS = STEP * TILES;
     struct Step {
         at_h8 k[WAVES][NF][64];      // keys of 16 tokens each, as the lanes read them
         at_h8 v[WAVES / 2][CB][64];  // values of 32 tokens each
@@ -595,7 +599,7 @@ struct AtWide {
         unsigned short ok[WAVES];    // tokens that are there
     };
     struct Lds {
-        Step step[2];
+        Step step[BUFFERS];
     };
     struct Codes {  // a wave's 16 tokens of one step
         int k[NK][4], v[4][NV];
@@ -611,10 +615,10 @@ struct AtWide {
     int lane, wave;
     int tiles;       // of 16 rows, a wave's: 1 or 2
     int first;       // the wave's first row
-    AtQuery<T, HD> q[2];
-    AtRows<HD> r[2];
+    AtQuery<T, HD> q[TILES];
+    AtRows<HD> r[TILES];
     AtUnit unit;
-    int limit[2], least, most;
+    int limit[TILES], least, most;
 
     __device__ __forceinline__ int page_of(int t) const
     {
@@ -676,21 +680,21 @@ struct AtWide {
         }
     }
     // 64 tokens, `half` of a step's
-    template <int TILES>
+    template <int N>
     __device__ __forceinline__ void compute(const Step& s, int half, int base)
     {
-        float x[TILES][16];
+        float x[N][16];
         at_f4 vs[4];
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) {
-            at_f4 acc[TILES];
+            at_f4 acc[N];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) acc[i] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < N; ++i) acc[i] = (at_f4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
                 const at_h8 k = s.k[4 * half + sub][f][lane];
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) {
+                for (int i = 0; i < N; ++i) {
                     acc[i] = at_product(k, q[i].hi[f], acc[i]);
                     if constexpr (SPLIT) acc[i] = at_product(k, q[i].lo[f], acc[i]);
                 }
@@ -698,40 +702,40 @@ struct AtWide {
             const at_f4 ks = *(const at_f4*)&s.ks[64 * half + 16 * sub + 4 * at.g];
             vs[sub] = *(const at_f4*)&s.vs[64 * half + 16 * sub + 4 * at.g];
 #pragma unroll
-            for (int i = 0; i < TILES; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e];
         }
         float f;
         if (unit.raise(s.top[4 * half + (lane & 3)], f))
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) r[i].times(f);
+            for (int i = 0; i < N; ++i) r[i].times(f);
         unsigned long long ok;
         __builtin_memcpy(&ok, s.ok + 4 * half, 8);
         if (ok != ~0ull || base + 64 > least) {
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) {
+            for (int i = 0; i < N; ++i) {
                 const unsigned long long mask = at_seen(ok, limit[i] - base, at.g);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[i][e] = mask >> (e / 4 * 16 + e % 4) & 1 ? x[i][e] : -INFINITY;
             }
         }
-        float most[TILES];
+        float most[N];
         bool above = false;
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) {
+        for (int i = 0; i < N; ++i) {
             most[i] = at_largest(x[i]);
             above |= at_above(r[i], most[i], q[i].reach);
         }
         if (__ballot(above) != 0)
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) at_follow(r[i], most[i], q[i].unit);
+            for (int i = 0; i < N; ++i) at_follow(r[i], most[i], q[i].unit);
         const float up = unit.up();
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
-        at_h8 p[TILES][2], rest[TILES][SPLIT ? 2 : 1];
+        at_h8 p[N][2], rest[N][SPLIT ? 2 : 1];
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) {
+        for (int i = 0; i < N; ++i) {
             at_weigh(r[i], x[i], q[i].unit);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -748,7 +752,7 @@ struct AtWide {
             for (int j = 0; j < CB; ++j) {
                 const at_h8 c = s.v[2 * half + h][j][lane];
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) {
+                for (int i = 0; i < N; ++i) {
                     r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
                     if constexpr (SPLIT) r[i].o[j] = at_product(c, rest[i][h], r[i].o[j]);
                 }
@@ -758,12 +762,12 @@ struct AtWide {
     __device__ __forceinline__ void run(int from, int to, float* slab)
     {
         // few rows are dealt 16 to a wave, so that all waves have some
-        tiles = job.rows > STEP ? 2 : 1;
+        tiles = TILES > 1 && job.rows > STEP ? 2 : 1;
         first = wave * 16 * tiles;
         const int mine = wave * 16 + at.n, page = page_of(from + mine);
         int later = page_of(from + STEP + mine);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < TILES; ++i) {
             const int n = first + 16 * i + at.n;
             const bool some = i < tiles && n < job.rows;
             size_t row = 0;
@@ -777,13 +781,13 @@ struct AtWide {
         least = 0x7fffffff;
         most = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < TILES; ++i) {
             q[i].convert(at, a.p.hd, a.scale);
             least = min(least, at_least(limit[i]));
             most = max(most, at_most(limit[i] == 0x7fffffff ? 0 : limit[i]));
         }
         int p = 0;
-        for (int base = from; base < to; base += STEP, p ^= 1) {
+        for (int base = from; base < to; base += STEP) {
             share(c, lds.step[p]);
             at_barrier();
             if (base + STEP < to) {
@@ -792,19 +796,25 @@ struct AtWide {
             }
 #pragma unroll 1
             for (int half = 0; half < WAVES / 4 && base + 64 * half < min(most, to); ++half) {
-                if (tiles == 2)
-                    compute<2>(lds.step[p], half, base + 64 * half);
-                else
+                if (tiles == 2) {
+                    if constexpr (TILES > 1) compute<2>(lds.step[p], half, base + 64 * half);
+                } else {
                     compute<1>(lds.step[p], half, base + 64 * half);
+                }
             }
+            if (BUFFERS > 1)
+                p ^= 1;
+            else
+                at_barrier();
         }
         at_finish(a, job, at, r[0], q[0].unit, unit, first + at.n, slab);
-        if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, unit, first + 16 + at.n, slab);
+        if constexpr (TILES > 1)
+            if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, unit, first + 16 + at.n, slab);
         at_barrier();
     }
 };
 
-// Waves that a SIMD has room for: wide heads and float's two numbers take the registers
+// Waves of narrow jobs that a SIMD has room for: wide heads and float's two numbers take the registers
 // of two.
 template <class T, int HD>
 constexpr int at_resident = HD <= 128 && !std::is_same<T, float>::value ? 2 : 1;
@@ -816,7 +826,7 @@ __device__ __forceinline__ int at_worker(const AtPlan& p)
 }
 
 template <class T, int HD>
-__global__ __launch_bounds__((64 * AtWide<T, HD>::WAVES), (at_resident<T, HD>)) void q8_attn_wide(AttnArgs<T> a)
+__global__ __launch_bounds__((64 * AtWide<T, HD>::WAVES)) void q8_attn_wide(AttnArgs<T> a)
 {
     __shared__ union {
         AtScan<AT_WIDE_JOBS> scan;  // until the cursor is there

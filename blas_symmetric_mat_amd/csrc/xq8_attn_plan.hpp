@@ -69,7 +69,7 @@ struct AtPlan {
     int wide_log;  // of a wide job's rows
     __host__ __device__ __forceinline__ int wide_rows() const { return 1 << wide_log; }
     __host__ __device__ __forceinline__ int wide_slabs() const { return 1 << wide_log >> 4; }
-    // Workspace: slabs (of cut wide jobs' parts, two of 128 rows a workgroup; of cut
+    // Workspace: slabs (of cut wide jobs' parts, two a workgroup; of cut
     // narrow ones', two a wave; of whole parts) and, for each row and head, where its
     // own parts and its group's are.
     int slabs, narrow_at, whole_at;

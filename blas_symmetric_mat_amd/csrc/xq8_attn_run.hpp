@@ -19,7 +19,7 @@ inline bool attn_mixed(int heads, int kvheads, int groups, bool single)
     return !single || groups > 0 || heads / kvheads > AT_NARROW;
 }
 
-// Rows of a wide job: 256, or 128 (AtWide).
+// Rows of a wide job: 256, or 128 (AtWide::ROWS).
 constexpr int AT_WIDE = 256, AT_LESS = 128;
 
 // Workspace: where the rows' parts are, and their slabs: of cut jobs (two a worker),
@@ -31,7 +31,7 @@ struct AttnSpace {
         const size_t share = heads / kvheads, table = align_up((size_t)rows * heads * sizeof(int2));
         shared = table;
         parts = groups > 0 ? 2 * table : table;
-        // (256 workgroups of 256 rows, or 512 of 128)
+        // (256 workgroups of 256 rows)
         narrow = attn_mixed(heads, kvheads, groups, single) ? 2 * (size_t)AT_GRID * AT_LESS / AT_NARROW : 0;
         whole = narrow + 2 * 4 * (size_t)AT_GRID;
         slabs = whole;
@@ -87,7 +87,7 @@ int attn_launch(AttnArgs<T> a, hipStream_t stream)
     return q8_with_workspace(cut ? space.bytes : 0, true, stream, [&](void* ws, const TimedCall& tc) -> int {
         constexpr int threads = 64 * AtWide<T, HD>::WAVES;
         p.whole = ws == nullptr;
-        p.wide_log = AtWide<T, HD>::WAVES == 8 ? 8 : 7;
+        p.wide_log = AtWide<T, HD>::ROWS == AT_WIDE ? 8 : 7;
         if (!p.whole) {
             char* at = static_cast<char*>(ws);
             p.own = reinterpret_cast<int2*>(at);
