@@ -285,19 +285,20 @@ __device__ __forceinline__ unsigned long long at_seen(unsigned long long ok, int
     return (n == 64 ? ok : ok & ((1ull << n) - 1)) >> (4 * g);
 }
 
-// A values' scale that is no number as the largest one: nothing of a row that does not
-// see its token, and not finite in one that does.
-__device__ __forceinline__ float at_number(float v) { return fmaxf(fminf(v, -AT_LOWEST), AT_LOWEST); }
+// A values' scale for the weights.  One that is no number (2^120 and above count as
+// such) becomes the largest number: times a weight of zero, a row's that does not see
+// the token, it is nothing, and no 16-bit number in a row that does.
+constexpr float AT_NONE = 0x1p120f;
+__device__ __forceinline__ float at_scaled(float v, float up) { return fabsf(v) < AT_NONE ? v * up : -AT_LOWEST; }
 
-// The largest values' scale so far, as a power of two, for a wave.  Scales above 2^120
-// do not count, as they are no numbers.
+// The largest values' scale so far, as a power of two, for a wave.
 struct AtUnit {
     float unit = 0x1p-100f;
     // raised to hold `v` (any lane's); the factor for what was summed in the old one
     __device__ __forceinline__ bool raise(float v, float& f)
     {
         v = fabsf(v);
-        const bool more = v > unit && v < 0x1p120f;
+        const bool more = v > unit && v < AT_NONE;
         if (__ballot(more) == 0) return false;
         float most = more ? v : unit;
 #pragma unroll
@@ -477,7 +478,7 @@ struct AtNarrow {
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
             c.ks = a.ks[row];
-            c.vs = at_number(a.vs[row]);
+            c.vs = a.vs[row];
         }
         if (lane < STEP) tok.row[lane] = max(row, 0);
         at_wave_sync();
@@ -494,7 +495,7 @@ struct AtNarrow {
         if (unit.raise(c.vs, f)) r.times(f);
         if (lane < STEP) {
             tok.ks[lane] = c.ks;
-            tok.vs[lane] = c.vs * unit.up();
+            tok.vs[lane] = at_scaled(c.vs, unit.up());
         }
         at_wave_sync();
         float x[8], w[8];
@@ -595,7 +596,8 @@ struct AtWide {
         at_h8 k[WAVES][NF][64];      // keys of 16 tokens each, as the lanes read them
         at_h8 v[WAVES / 2][CB][64];  // values of 32 tokens each
         float ks[STEP], vs[STEP];
-        float top[WAVES];            // of each wave's tokens, the largest values' scale
+        float top[WAVES];            // of each wave's tokens, the largest values' scale; below
+                                     // zero where one is no number
         unsigned short ok[WAVES];    // tokens that are there
     };
     struct Lds {
@@ -635,7 +637,7 @@ struct AtWide {
         c.ks = c.vs = 0.0f;
         if (row >= 0) {
             c.ks = a.ks[row];
-            c.vs = at_number(a.vs[row]);
+            c.vs = a.vs[row];
         }
         row = max(row, 0);
         at_keys<HD>(a.k + (size_t)row * a.ldk, at, c.k);
@@ -671,9 +673,11 @@ struct AtWide {
             s.ks[wave * 16 + lane] = c.ks;
             s.vs[wave * 16 + lane] = c.vs;
         }
-        float top = fabsf(c.vs) < 0x1p120f ? fabsf(c.vs) : 0.0f;
+        const bool number = fabsf(c.vs) < AT_NONE;
+        float top = number ? fabsf(c.vs) : 0.0f;
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        if (__ballot(!number) != 0) top = -fmaxf(top, 0x1p-126f);
         if (lane == 0) {
             s.ok[wave] = (unsigned short)ok;
             s.top[wave] = top;
@@ -707,7 +711,8 @@ struct AtWide {
                 for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e];
         }
         float f;
-        if (unit.raise(s.top[4 * half + (lane & 3)], f))
+        const float top = s.top[4 * half + (lane & 3)];
+        if (unit.raise(top, f))
 #pragma unroll
             for (int i = 0; i < N; ++i) r[i].times(f);
         unsigned long long ok;
@@ -731,8 +736,15 @@ struct AtWide {
 #pragma unroll
             for (int i = 0; i < N; ++i) at_follow(r[i], most[i], q[i].unit);
         const float up = unit.up();
+        if (__ballot(top < 0.0f) == 0) {
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
+            for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
+        } else {
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) vs[sub][e] = at_scaled(vs[sub][e], up);
+        }
         at_h8 p[N][2], rest[N][SPLIT ? 2 : 1];
 #pragma unroll
         for (int i = 0; i < N; ++i) {

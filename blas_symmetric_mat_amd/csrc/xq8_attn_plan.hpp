@@ -152,6 +152,25 @@ struct AtGroup {
             pays = work(p, (long long)rows * p.share) * 4 <= count * work(p, one) * 3;
         }
     }
+    // The sequence whose row of the table is read: the first one that has all the shared
+    // tokens, else the longest (others may have ended, and their pages be free).
+    __device__ __forceinline__ int table(const AtPlan& p) const
+    {
+        int best = s0, most = -1;
+        for (int s = s0; s < s1 && most < tokens; s += 8) {
+            int len[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) len[i] = s + i < s1 ? p.length(s + i) : -1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (most < tokens && len[i] > most) {
+                    most = len[i];
+                    best = s + i;
+                }
+            }
+        }
+        return best;
+    }
     // a wide job takes about twice as long as a narrow one with as many tokens
     static __device__ __forceinline__ long long work(const AtPlan& p, long long rows)
     {
@@ -193,7 +212,7 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
                 x.row0 = g.row0;
                 x.rows = g.rows * p.share;
                 x.t1 = g.tokens;
-                x.table = g.s0;
+                x.table = g.table(p);
             }
         }
     } else if (MIXED) {

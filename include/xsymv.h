@@ -482,8 +482,9 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   row that sees none gets zeros and -infinity.  16 <= hd <= 256.
  *   Sequences first[g] to first[g + 1] - 1 (groups + 1 ascending numbers from 0
  *   to seqs) have their first shared[g] tokens in common: their rows of the table
- *   name the same pages there, and these are read once for all of them where that
- *   takes less time.  groups == 0: nothing is shared.  Products of 16 bits
+ *   name the same pages there, as far as each one's len goes (one that has ended may
+ *   stay in its group), and these are read once for all of them where that takes less
+ *   time.  groups == 0: nothing is shared.  Products of 16 bits
  *   (letters h and b) or 22 (s), sums in 32.  Uses the stream's workspace, up to
  *   xsymv_q8attn_workspace_bytes; where it cannot be had (as for the product
  *   above) the call is made without, in up to many times the time.

@@ -467,3 +467,46 @@ def test_many_more_rows_than_tokens():
     few.call()
     torch.cuda.synchronize()
     assert torch.equal(c.out.t[-3:], few.out.t) and torch.equal(c.lse[-3:], few.lse)
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("lens", [[0, 0, 400, 500, 0, 390, 70, 450, 0, 401], [0] * 21 + [70, 384, 600] + [0] * 3,
+                                  [0, 100, 33, 64, 383, 16, 0, 250]])
+def test_groups_whose_first_sequences_have_ended(t, lens):
+    """Sequences without tokens, whose rows of the table name no page, and shorter ones than the shared
+    tokens stand before those that have all of them, or none has."""
+    for counts in (None, [min(n, 5) for n in lens]):
+        c = Case(t, 8, 2, 64, 16, lens, counts, groups=[(len(lens), 384)], seed=len(lens)).spoil()
+        c.call()
+        c.check()
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf, 1e37])
+def test_scales_of_tokens_that_some_rows_do_not_see(t, hd, bad):
+    """A values' scale that is no number: rows that see its token are not finite, the others, of the same
+    jobs, keep their bytes (few rows and many, and rows of a group)."""
+    import torch
+    for lens, counts, groups in (([90, 40], [6, 3], ()), ([700, 300], [400, 150], ()),
+                                 ([200, 215, 230], [12, 12, 12], [(3, 192)])):
+        c = Case(t, 4, 2, hd, 16, lens, counts, groups, seed=hd)
+        c.vs.clamp_(min=0.01)
+        at = []
+        for i in range(len(lens)):  # the last row's token but one or two, of each sequence
+            places, _ = c.places(i)
+            at += places[:, lens[i] - 2].tolist()
+        c.vs[at] = 1e-4  # (not the largest, so that without it nothing else changes)
+        c.call()
+        torch.cuda.synchronize()
+        clean = c.out.t.clone()
+        c.vs[at] = bad
+        c.call()
+        torch.cuda.synchronize()
+        ends = list(itertools.accumulate(counts))
+        sees = torch.zeros((c.rows,), dtype=torch.bool, device="cuda")
+        for e in ends:
+            sees[e - 2:e] = True
+        assert torch.equal(c.out.t[~sees], clean[~sees])
+        # (a code of zero times infinity, or a weight that is nothing in 16 bits, aside)
+        assert bool((~c.out.t[sees].isfinite()).any(1).all())
