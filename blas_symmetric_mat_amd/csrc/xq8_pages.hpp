@@ -49,7 +49,7 @@ template <class F>
 __device__ int pg_free(const PgCache& c, int want, int* waves, F&& take)
 {
     int found = 0;
-    // (unsigned: the last round reaches past the largest int)
+    // (unsigned: the last stretch reaches past the largest int)
     for (unsigned base = 0; base < (unsigned)c.pages && found < want; base += PG_THREADS * PG_CHUNK) {
         const unsigned first = base + threadIdx.x * PG_CHUNK;
         unsigned mask = 0;

@@ -342,15 +342,16 @@ def main():
     index, value = layer.likely(y[-1:], h[-1:], head, answers)
     tokens, sums = index[0], value[0].clone()  # each answer begins with another token
     layer.fork()
-    torch.cuda.synchronize()
-    t = time.perf_counter()
-    for _ in range(length):
+    for i in range(length + 8):
+        if i == 8:  # (the first steps make workspaces and load kernels)
+            torch.cuda.synchronize()
+            t = time.perf_counter()
         y, h = layer.step(rows(tokens), zero)
         index, value = layer.likely(y, h, head, 1)
         tokens = index[:, 0]
         sums += value[:, 0]
     torch.cuda.synchronize()
-    print(f"{answers} answers of {length} tokens: {(time.perf_counter() - t) / length * 1e6:.0f} us a token of each; "
+    print(f"{answers} answers of {length + 8} tokens: {(time.perf_counter() - t) / length * 1e6:.0f} us a token of each; "
           f"the likeliest has log probability {sums.max().item():.2f}")
 
 
