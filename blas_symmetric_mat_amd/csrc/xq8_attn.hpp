@@ -265,11 +265,13 @@ __device__ __forceinline__ float at_largest(const float (&x)[N])
     for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
     return most;
 }
-// Scores to weights e^(s - m).
+// Scores to weights e^(s - m).  A row that has seen no token yet has its reference at
+// the lowest number, which a unit above 1 would take to -infinity, and the weight of a
+// token that it does not see to that of infinity minus infinity.
 template <int N, int HD>
 __device__ __forceinline__ void at_weigh(AtRows<HD>& r, float (&x)[N], float unit)
 {
-    const float m = r.m * unit;
+    const float m = fmaxf(r.m * unit, AT_LOWEST);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], unit, -m));
     // (in pairs: half the additions wait for the sum)

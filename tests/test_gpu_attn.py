@@ -510,3 +510,79 @@ def test_scales_of_tokens_that_some_rows_do_not_see(t, hd, bad):
         assert torch.equal(c.out.t[~sees], clean[~sees])
         # (a code of zero times infinity, or a weight that is nothing in 16 bits, aside)
         assert bool((~c.out.t[sees].isfinite()).any(1).all())
+
+
+class Fine(Case):
+    """A case whose half results may be small: below 2^-14 half's numbers lie 2^-24 apart, so that an output is
+    rounded by up to 2^-25 there, whatever its size."""
+
+    def expected(self):
+        out, err, lse, lerr = super().expected()
+        return out, err + (2.0 ** -25 if self.t == "h" else 0.0), lse, lerr
+
+
+SCALES = [0.5, 0.75, 1.0, 2.0, 4.0, -1.0, -0.0625, 0.0]
+
+
+def at_scale(c, scale, bad=True):
+    """The case at another scale, its keys made smaller so that scores stay as large as they were."""
+    c.scale = scale
+    if bad:
+        c.spoil()
+    c.ks *= 0.125 / max(abs(scale), 0.125)
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("scale", SCALES)
+def test_rows_that_see_nothing_at_any_scale(t, scale):
+    """Rows without a token, of a sequence or of a piece of it: those of test_rows_that_see_nothing, and
+    sequences whose first pages are not there, for one row each and for many."""
+    at_scale(Fine(t, 4, 2, 64, 16, [3, 0, 40, 17], [5, 2, 0, 17], lead=2, tail=3), scale)
+    c = Fine(t, 4, 2, 64, 16, [100, 90, 80, 100], seed=3)
+    c.table[0, 2] = -1
+    c.table[0, 6] = c.pages
+    c.table[1] = 1 << 30
+    c.table[3, 0] = -(1 << 31)
+    c.len[2] = c.lens[2] = -5
+    at_scale(c, scale)
+    for counts in (None, [5, 3, 1], [250, 100, 60]):
+        c = Fine(t, 4, 2, 64, 16, [300, 150, 100], counts, seed=4)
+        c.table[0, :8] = -1
+        c.table[1, 4:] = -1
+        c.table[2] = c.pages
+        at_scale(c, scale)
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_cut_prompts_at_any_scale(t, scale, hd):
+    """Pieces that begin behind a row's last token: of many rows, of a few, of a group."""
+    at_scale(Fine(t, 4, 2, hd, 16, [3000, 700], [300, 500], seed=5), scale)
+    at_scale(Fine(t, 4, 2, hd, 16, [2000, 40], [5, 3], seed=6), scale)
+    at_scale(Fine(t, 4, 2, hd, 16, [200, 30, 0, 170], None, [(4, 160)]), scale, bad=False)
+    at_scale(Fine(t, 8, 2, hd, 16, [600, 370, 165, 370], [60, 30, 5, 1], [(4, 320)]), scale, bad=False)
+    at_scale(Fine(t, 8, 2, hd, 16, [2100 + i for i in range(20)] + [7, 0, 33], None, [(23, 2048)]), scale, bad=False)
+
+
+@pytest.mark.parametrize("t", ["s", "b"])
+@pytest.mark.parametrize("up,scale", [(2.0 ** 16, 1.0), (2.0 ** 100, 0.125), (2.0 ** -60, 1.0)])
+def test_rows_of_large_and_small_numbers(t, up, scale):
+    """q far from one, keys' scales by as much the other way."""
+    for lens, counts in (([3, 0, 40, 17], [5, 2, 0, 17]), ([3000, 700], [300, 500]), ([2000, 40], None)):
+        c = Fine(t, 4, 2, 64, 16, lens, counts, seed=7, spread=2.5 * up)
+        c.ks /= up
+        at_scale(c, scale)
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("up", [2.0 ** 100])
+def test_scales_far_from_one(t, up):
+    for lens, counts in (([300, 170], [30, 100]), ([2000, 40], None)):
+        c = Fine(t, 4, 2, 64, 16, lens, counts, seed=8)
+        c.scale *= up
+        c.ks /= up
+        c.call()
+        c.check()
