@@ -193,13 +193,14 @@ struct AtQuery {
         }
         most = __builtin_elementwise_maximum(most, __shfl_xor(most, 16, 64));
         most = __builtin_elementwise_maximum(most, __shfl_xor(most, 32, 64));
-        float up = 1.0f, down = 1.0f;
-        if (!std::is_same<T, q8half>::value && most > 0.0f && most < INFINITY) {
+        int e = 0;
+        if (!std::is_same<T, q8half>::value && most > 0.0f && most < INFINITY)
             // the largest between 2^14 and 2^15
-            const int e = min(max(14 + 127 - (int)(__float_as_uint(most) >> 23), -126), 126);
-            up = __uint_as_float((unsigned)(127 + e) << 23);
-            down = __uint_as_float((unsigned)(127 - e) << 23);
-        }
+            e = min(max(14 + 127 - (int)(__float_as_uint(most) >> 23), -126), 126);
+        // less where the unit would be below 2^-120: its inverse is a number
+        e = min(e, (int)(__float_as_uint(fabsf(scale)) >> 23) - 127 + 120);
+        float up = __uint_as_float((unsigned)(127 + e) << 23);
+        const float down = __uint_as_float((unsigned)(127 - e) << 23);
         // a negative scale is q's sign; zero is a number that makes all scores as good as it
         unit = fmaxf(fabsf(scale) * down, 0x1p-120f);
         reach = 1.0f / unit;

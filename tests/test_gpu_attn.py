@@ -568,7 +568,7 @@ def test_cut_prompts_at_any_scale(t, scale, hd):
 
 
 @pytest.mark.parametrize("t", ["s", "b"])
-@pytest.mark.parametrize("up,scale", [(2.0 ** 16, 1.0), (2.0 ** 100, 0.125), (2.0 ** -60, 1.0)])
+@pytest.mark.parametrize("up,scale", [(2.0 ** 16, 1.0), (2.0 ** 100, 0.125), (2.0 ** -60, 1.0), (2.0 ** -115, -0.125)])
 def test_rows_of_large_and_small_numbers(t, up, scale):
     """q far from one, keys' scales by as much the other way."""
     for lens, counts in (([3, 0, 40, 17], [5, 2, 0, 17]), ([3000, 700], [300, 500]), ([2000, 40], None)):
@@ -578,7 +578,7 @@ def test_rows_of_large_and_small_numbers(t, up, scale):
 
 
 @pytest.mark.parametrize("t", LETTERS)
-@pytest.mark.parametrize("up", [2.0 ** 100])
+@pytest.mark.parametrize("up", [2.0 ** -121, 2.0 ** -118, 2.0 ** 100])
 def test_scales_far_from_one(t, up):
     for lens, counts in (([300, 170], [30, 100]), ([2000, 40], None)):
         c = Fine(t, 4, 2, 64, 16, lens, counts, seed=8)
