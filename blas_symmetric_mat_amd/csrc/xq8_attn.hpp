@@ -113,9 +113,9 @@ struct AtLanes {
     int n, g;          // lane % 16, lane / 16
     int koff[NK];      // of the keys' pieces
     int voff;          // of the values' piece
-    __device__ AtLanes(int hd)
+    __device__ AtLanes(int hd) : AtLanes(hd, threadIdx.x & 63) {}
+    __device__ AtLanes(int hd, int lane)
     {
-        const int lane = threadIdx.x & 63;
         n = lane & 15;
         g = lane >> 4;
 #pragma unroll
@@ -219,7 +219,7 @@ struct AtQuery {
 
 // Results so far of 16 rows of q, in the lanes of their columns: the reference m as a
 // score before its row's unit, l, the sum of the weights of a lane's tokens, and out
-// in units of AtUnit's / 2^14.
+// in units of the row's AtUnit / 2^14.
 template <int HD>
 struct AtRows {
     static constexpr int CB = HD / 16;
@@ -288,32 +288,43 @@ __device__ __forceinline__ unsigned long long at_seen(unsigned long long ok, int
     return (n == 64 ? ok : ok & ((1ull << n) - 1)) >> (4 * g);
 }
 
-// A values' scale for the weights.  One that is no number (2^120 and above count as
-// such) becomes the largest number: times a weight of zero, a row's that does not see
-// the token, it is nothing, and no 16-bit number in a row that does.
-constexpr float AT_NONE = 0x1p120f;
-__device__ __forceinline__ float at_scaled(float v, float up) { return fabsf(v) < AT_NONE ? v * up : -AT_LOWEST; }
+constexpr float AT_NONE = 0x1p120f;  // values' scales from here on count as no numbers
 
-// The largest values' scale so far, as a power of two, for a wave.
+// The largest values' scale so far, as a power of two, of the tokens that a row sees:
+// others may have scales beside which its own would be nothing in half precision.  Rows
+// have it in common up to the step in which the first of them has its last token, and
+// steps from there on are taken apart.
 struct AtUnit {
     float unit = 0x1p-100f;
-    // raised to hold `v` (any lane's); the factor for what was summed in the old one
-    __device__ __forceinline__ bool raise(float v, float& f)
+    __device__ __forceinline__ bool above(float v) const { return fabsf(v) > unit && fabsf(v) < AT_NONE; }
+    // raised to hold `most`; the factor for what was summed in the old one
+    __device__ __forceinline__ float raise(float most)
     {
-        v = fabsf(v);
-        const bool more = v > unit && v < AT_NONE;
-        if (__ballot(more) == 0) return false;
-        float most = more ? v : unit;
+        const float was = unit;
+        // (the next power of two)
+        if (most > unit) unit = __uint_as_float(((__float_as_uint(most) >> 23) + 1) << 23);
+        return was / unit;
+    }
+    // The largest of the wave's scales, where one is above it.
+    __device__ __forceinline__ float largest(float v) const
+    {
+        float most = above(v) ? fabsf(v) : unit;
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-        const unsigned e = (__float_as_uint(most) >> 23) + 1;  // the next power of two
-        const float to = __uint_as_float(__builtin_amdgcn_readfirstlane(e << 23));
-        f = unit / to;
-        unit = to;
-        return true;
+        return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
     }
     __device__ __forceinline__ float up() const { return AT_UP / unit; }
+    // A scale for the weights.  One above the unit is no number or not to be seen, and
+    // becomes the largest number: times a weight of zero, a row's that does not see the
+    // token, it is nothing, and no 16-bit number in a row that does.
+    __device__ __forceinline__ float scaled(float v, float up) const { return fabsf(v) <= unit ? v * up : -AT_LOWEST; }
 };
+
+// Tokens a to b - 1 of 64.
+__device__ __forceinline__ unsigned long long at_stretch(int a, int b)
+{
+    return (~0ull << a) & (~0ull >> (64 - b));
+}
 
 template <class H8>
 __device__ __forceinline__ at_f4 at_product(H8 a, H8 b, at_f4 c)
@@ -408,14 +419,16 @@ __device__ __forceinline__ void at_write(const AtRows<HD>& r, const AtLanes<HD>&
 
 // A tile of 16 rows, of which the lanes' is the job's row n, to out or to its part.
 template <class T, int HD>
-__device__ __forceinline__ void at_finish(const AttnArgs<T>& a, const AtJob& job, const AtLanes<HD>& at,
-                                          AtRows<HD>& r, float row_unit, const AtUnit& unit, int n, float* slab)
+__device__ __forceinline__ void at_finish(const AttnArgs<T>& a, const AtJob& job, AtLanes<HD> at, AtRows<HD>& r,
+                                          float row_unit, float unit, int n, float* slab)
 {
+    // (places of results are computed here, not kept in registers while jobs run)
+    asm volatile("" : "+v"(at.g));
     const int hd = a.p.hd;
     r.whole();
     r.m = r.l == 0.0f ? AT_LOWEST : r.m * row_unit;
     if (n >= job.rows) return;
-    const float f = r.l == 0.0f ? 0.0f : unit.unit * AT_DOWN;
+    const float f = r.l == 0.0f ? 0.0f : unit * AT_DOWN;
     if (slab != nullptr) {
         float* part = slab + (size_t)(n / AT_NARROW) * at_slab(hd);
         const int m = n % AT_NARROW;
@@ -492,13 +505,29 @@ struct AtNarrow {
         for (int i = 0; i < 8; ++i)
             at_values<HD>(a.v + (size_t)tok.row[i / 4 * 16 + 4 * at.g + i % 4] * a.ldv, at, c.v[i]);
     }
+    // Apart: a row's unit by the values' scales that it sees, and these in it.
+    __device__ __forceinline__ void scale(float (&w)[8], unsigned mask)
+    {
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            most = mask >> (i / 4 * 16 + i % 4) & 1 && unit.above(w[i]) ? fmaxf(most, fabsf(w[i])) : most;
+        if (__ballot(most > 0.0f) != 0) {
+            most = fmaxf(most, __shfl_xor(most, 16, 64));
+            most = fmaxf(most, __shfl_xor(most, 32, 64));
+            r.times(unit.raise(most));
+        }
+        const float up = unit.up();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = unit.scaled(w[i], up);
+    }
     __device__ __forceinline__ void compute(Codes& c, AtTokens& tok, int base)
     {
-        float f;
-        if (unit.raise(c.vs, f)) r.times(f);
+        const bool apart = base + STEP > least;
+        if (!apart && __ballot(unit.above(c.vs)) != 0) r.times(unit.raise(unit.largest(c.vs)));
         if (lane < STEP) {
             tok.ks[lane] = c.ks;
-            tok.vs[lane] = at_scaled(c.vs, unit.up());
+            tok.vs[lane] = apart ? c.vs : unit.scaled(c.vs, unit.up());
         }
         at_wave_sync();
         float x[8], w[8];
@@ -521,10 +550,11 @@ struct AtNarrow {
                 w[4 * i + e] = vs[e];
             }
         }
-        if ((unsigned)c.ok != ~0u || base + STEP > least) {
+        if (__builtin_expect((unsigned)c.ok != ~0u || apart, 0)) {
             const unsigned mask = (unsigned)at_seen(c.ok, limit - base, at.g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = mask >> (i / 4 * 16 + i % 4) & 1 ? x[i] : -INFINITY;
+            if (__builtin_expect(apart, 0)) scale(w, mask);
         }
         const float most = at_largest(x);
         if (__ballot(at_above(r, most, q.reach)) != 0) at_follow(r, most, q.unit);
@@ -566,6 +596,7 @@ struct AtNarrow {
         if (count > 0) fetch(c[0], lds[0], from, page);
         q.convert(at, a.p.hd, a.scale);
         least = at_least(limit);
+        if (least >= job.end) least = 0x7fffffff;  // rows differ in no step
         auto step = [&](Codes& now, Codes& next, AtTokens& tn, AtTokens& tx, int s) {
             const int base = from + s * STEP;
             if (s + 1 < count) {
@@ -578,7 +609,7 @@ struct AtNarrow {
             step(c[0], c[1], lds[0], lds[1], s);
             if (s + 1 < count) step(c[1], c[0], lds[1], lds[0], s + 1);
         }
-        at_finish(a, job, at, r, q.unit, unit, at.n, slab);
+        at_finish(a, job, at, r, q.unit, unit.unit, at.n, slab);
     }
 };
 
@@ -605,6 +636,8 @@ struct AtWide {
     };
     struct Lds {
         Step step[BUFFERS];
+        float unit[ROWS];  // of rows from the first step that is apart on
+        int limit[ROWS];
     };
     struct Codes {  // a wave's 16 tokens of one step
         int k[NK][4], v[4][NV];
@@ -623,7 +656,7 @@ struct AtWide {
     AtQuery<T, HD> q[TILES];
     AtRows<HD> r[TILES];
     AtUnit unit;
-    int limit[TILES], least, most;
+    int least, most;
 
     __device__ __forceinline__ int page_of(int t) const
     {
@@ -632,7 +665,13 @@ struct AtWide {
 
     __device__ __forceinline__ void fetch(Codes& c, int base, int page)
     {
-        const int t = base + wave * 16 + at.n;
+        // (Places in rows are computed here: kept in registers, they took those of other
+        // numbers, which then had to be read back from memory in each step: 728 us for
+        // 4 x 1024 rows behind 8192 tokens where it is 670.)
+        int x = lane;
+        asm volatile("" : "+v"(x));
+        const AtLanes<HD> here(a.p.hd, x);
+        const int t = base + wave * 16 + here.n;
         int row = -1;
         if (t < job.end && (unsigned)page < (unsigned)a.p.pages)
             row = (page * a.p.kvheads + job.head) * a.p.ps + t - a.p.by_page.of(t) * a.p.ps;
@@ -643,10 +682,10 @@ struct AtWide {
             c.vs = a.vs[row];
         }
         row = max(row, 0);
-        at_keys<HD>(a.k + (size_t)row * a.ldk, at, c.k);
+        at_keys<HD>(a.k + (size_t)row * a.ldk, here, c.k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            at_values<HD>(a.v + (size_t)__shfl(row, 4 * at.g + i, 64) * a.ldv, at, c.v[i]);
+            at_values<HD>(a.v + (size_t)__shfl(row, 4 * here.g + i, 64) * a.ldv, here, c.v[i]);
     }
     __device__ __forceinline__ void share(Codes& c, Step& s)
     {
@@ -686,10 +725,39 @@ struct AtWide {
             s.top[wave] = top;
         }
     }
-    // 64 tokens, `half` of a step's
-    template <int N>
-    __device__ __forceinline__ void compute(const Step& s, int half, int base)
+    __device__ __forceinline__ int row_of(int i) const { return first + 16 * i + at.n; }
+    // The first of 64 tokens from `a` on whose scale is above the unit.
+    __device__ __forceinline__ int first_above(float v, int a) const
     {
+        const unsigned long long m = __ballot(unit.above(v)) >> a;
+        return m == 0 ? 64 : a + __builtin_ctzll(m);
+    }
+    // 64 tokens, `half` of a step's, from `a` on; the end of those that were taken
+    template <int N, bool APART>
+    __device__ __forceinline__ int compute(const Step& s, int half, int base, int a)
+    {
+        bool odd = false;
+        int b = 64;
+        unsigned long long stretch = ~0ull;
+        if constexpr (APART) {
+            // Apart: by stretches, of which each begins with a token that raises the unit, so
+            // that rows whose tokens all lie before it keep theirs.  (A unit for each row
+            // besides the two tiles' results does not fit the registers.)
+            const float v = s.vs[64 * half + lane];
+            b = first_above(v, a);
+            if (b == a) {
+                const float f = unit.raise(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fabsf(v)), a)));
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const bool sees = lds.limit[row_of(i)] > base + a;
+                    r[i].times(sees ? f : 1.0f);
+                    if (sees) lds.unit[row_of(i)] = unit.unit;
+                }
+                b = first_above(v, a);
+            }
+            stretch = at_stretch(a, b);
+            odd = b - a < 64;
+        }
         float x[N][16];
         at_f4 vs[4];
 #pragma unroll
@@ -713,17 +781,21 @@ struct AtWide {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][4 * sub + e] = acc[i][e] * ks[e];
         }
-        float f;
         const float top = s.top[4 * half + (lane & 3)];
-        if (unit.raise(top, f))
-#pragma unroll
-            for (int i = 0; i < N; ++i) r[i].times(f);
+        odd |= __ballot(top < 0.0f) != 0;
         unsigned long long ok;
         __builtin_memcpy(&ok, s.ok + 4 * half, 8);
-        if (ok != ~0ull || base + 64 > least) {
+        ok &= stretch;
+        if (!APART && __ballot(unit.above(top)) != 0) {
+            const float f = unit.raise(unit.largest(top));
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i].times(f);
+        }
+        if (ok != ~0ull || APART) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const unsigned long long mask = at_seen(ok, limit[i] - base, at.g);
+                const unsigned long long mask =
+                    APART ? at_seen(ok, lds.limit[row_of(i)] - base, at.g) : ok >> (4 * at.g);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[i][e] = mask >> (e / 4 * 16 + e % 4) & 1 ? x[i][e] : -INFINITY;
             }
@@ -739,14 +811,14 @@ struct AtWide {
 #pragma unroll
             for (int i = 0; i < N; ++i) at_follow(r[i], most[i], q[i].unit);
         const float up = unit.up();
-        if (__ballot(top < 0.0f) == 0) {
+        if (!odd) {
 #pragma unroll
             for (int sub = 0; sub < 4; ++sub) vs[sub] *= up;
         } else {
 #pragma unroll
             for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) vs[sub][e] = at_scaled(vs[sub][e], up);
+                for (int e = 0; e < 4; ++e) vs[sub][e] = unit.scaled(vs[sub][e], up);
         }
         at_h8 p[N][2], rest[N][SPLIT ? 2 : 1];
 #pragma unroll
@@ -771,8 +843,35 @@ struct AtWide {
                     r[i].o[j] = at_product(c, p[i][h], r[i].o[j]);
                     if constexpr (SPLIT) r[i].o[j] = at_product(c, rest[i][h], r[i].o[j]);
                 }
-
             }
+        return b;
+    }
+    // Steps from `base` up to `stop`.
+    template <bool APART>
+    __device__ __forceinline__ void steps(Codes& c, int& base, int stop, int to, int& p, int& later)
+    {
+        for (; base < stop; base += STEP) {
+            share(c, lds.step[p]);
+            at_barrier();
+            if (base + STEP < to) {
+                fetch(c, base + STEP, later);
+                later = page_of(base + 2 * STEP + wave * 16 + at.n);
+            }
+#pragma unroll 1
+            for (int half = 0, a = 0; half < WAVES / 4 && base + 64 * half < min(most, to);) {
+                if (tiles == 2) {
+                    if constexpr (TILES > 1) a = compute<2, APART>(lds.step[p], half, base + 64 * half, a);
+                } else {
+                    a = compute<1, APART>(lds.step[p], half, base + 64 * half, a);
+                }
+                half += a == 64;
+                a &= 63;
+            }
+            if (BUFFERS > 1)
+                p ^= 1;
+            else
+                at_barrier();
+        }
     }
     __device__ __forceinline__ void run(int from, int to, float* slab)
     {
@@ -780,7 +879,7 @@ struct AtWide {
         tiles = TILES > 1 && job.rows > STEP ? 2 : 1;
         first = wave * 16 * tiles;
         const int mine = wave * 16 + at.n, page = page_of(from + mine);
-        int later = page_of(from + STEP + mine);
+        int later = page_of(from + STEP + mine), limit[TILES];
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
             const int n = first + 16 * i + at.n;
@@ -789,6 +888,7 @@ struct AtWide {
             const int head = job.place(a.p, some ? n : 0, row);
             q[i].fetch(a.q + row * a.ldq + (size_t)head * a.p.hd, some, at, a.p.hd);
             limit[i] = some ? job.limit(a.p, n) : 0x7fffffff;
+            if (i < tiles) lds.limit[n] = limit[i];
             r[i].clear();
         }
         Codes c;
@@ -801,30 +901,18 @@ struct AtWide {
             least = min(least, at_least(limit[i]));
             most = max(most, at_most(limit[i] == 0x7fffffff ? 0 : limit[i]));
         }
-        int p = 0;
-        for (int base = from; base < to; base += STEP) {
-            share(c, lds.step[p]);
-            at_barrier();
-            if (base + STEP < to) {
-                fetch(c, base + STEP, later);
-                later = page_of(base + 2 * STEP + mine);
-            }
-#pragma unroll 1
-            for (int half = 0; half < WAVES / 4 && base + 64 * half < min(most, to); ++half) {
-                if (tiles == 2) {
-                    if constexpr (TILES > 1) compute<2>(lds.step[p], half, base + 64 * half);
-                } else {
-                    compute<1>(lds.step[p], half, base + 64 * half);
-                }
-            }
-            if (BUFFERS > 1)
-                p ^= 1;
-            else
-                at_barrier();
-        }
-        at_finish(a, job, at, r[0], q[0].unit, unit, first + at.n, slab);
+        if (least >= to) least = 0x7fffffff;  // rows differ in no step
+        // (a loop for either kind of step: what the second one takes costs the first none of
+        // its registers)
+        int p = 0, base = from;
+        steps<false>(c, base, min(to, from + (max(least, from) - from) / STEP * STEP), to, p, later);
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+            if (i < tiles) lds.unit[row_of(i)] = unit.unit;
+        steps<true>(c, base, to, to, p, later);
+        at_finish(a, job, at, r[0], q[0].unit, lds.unit[row_of(0)], first + at.n, slab);
         if constexpr (TILES > 1)
-            if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, unit, first + 16 + at.n, slab);
+            if (tiles == 2) at_finish(a, job, at, r[1], q[1].unit, lds.unit[row_of(1)], first + 16 + at.n, slab);
         at_barrier();
     }
 };

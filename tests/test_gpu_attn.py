@@ -586,3 +586,36 @@ def test_scales_far_from_one(t, up):
         c.ks /= up
         c.call()
         c.check()
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("large", [1e6, 1e12, 1e30])
+def test_large_scales_of_tokens_that_some_rows_do_not_see(t, hd, large):
+    """A token's values as large as they like: rows of the same jobs that do not see it keep their bytes, and
+    those that do are right (half, which does not hold them, aside)."""
+    import torch
+    for lens, counts, groups in (([90, 40], [6, 3], ()), ([700, 300], [400, 150], ()),
+                                 ([200, 215, 230], [12, 12, 12], [(3, 192)]),
+                                 ([200, 195, 230], [1, 1, 1], [(3, 224)])):
+        c = Fine(t, 4, 2, hd, 16, lens, counts, groups, seed=hd)
+        if groups and groups[0][1] > lens[0]:
+            # (a token that only the last sequence of the group sees; the others end before it)
+            places, _ = c.places(2)
+            at, sees = places[:, 220].tolist(), [2]
+        else:
+            at = [p for i in range(len(lens)) for p in c.places(i)[0][:, lens[i] - 2].tolist()]
+            sees = [r for e in itertools.accumulate(counts) for r in (e - 2, e - 1)]
+        c.vs[at] = 1e-4
+        c.call()
+        torch.cuda.synchronize()
+        clean = c.out.t.clone()
+        c.check()
+        c.vs[at] = large
+        c.call()
+        torch.cuda.synchronize()
+        mask = torch.zeros((c.rows,), dtype=torch.bool, device="cuda")
+        mask[sees] = True
+        assert torch.equal(c.out.t[~mask], clean[~mask])
+        if t != "h":
+            c.check()
