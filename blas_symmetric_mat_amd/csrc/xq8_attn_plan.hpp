@@ -115,8 +115,10 @@ struct AtEntry {
     {
         if (p.whole) return b;
         if (!wide) return b * (AT_OVER + tiles(t1 - t0));
-        // (more rows than tokens: any block as one that sees all, so that sums stay small)
-        if (group || before < 0) return b * (AT_OVER_WIDE + tiles(t1 - t0));
+        // (more rows than tokens, or heads of a row than a block: any block as one that sees all.
+        // The sums below are of steps of whole tokens, of which such blocks have none or less
+        // than one each, and no int would hold them: from 370000 blocks on.)
+        if (group || before < 0 || p.share >= p.wide_rows()) return b * (AT_OVER_WIDE + tiles(t1 - t0));
         // block b sees up to step * (b + 1) tokens more than what lies before the
         // rows; the sums of these are rounded down, for which one tile makes up
         const int step = p.by_share.of(p.wide_rows() + p.share - 1);

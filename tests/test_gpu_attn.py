@@ -619,3 +619,31 @@ def test_large_scales_of_tokens_that_some_rows_do_not_see(t, hd, large):
         assert torch.equal(c.out.t[~mask], clean[~mask])
         if t != "h":
             c.check()
+
+
+def test_many_more_heads_than_a_block():
+    """One row of a hundred million heads that share their keys (what its blocks see, summed over them, fits no int
+    if each counts for a token more): its first, middle and last heads are what they are among a few."""
+    import torch
+    heads, n = 100_000_000, 64
+    c = Fine("h", 1, 1, 16, 16, [100], seed=11)
+    few = Fine("h", 3 * n, 1, 16, 16, [100], seed=11)
+    q = torch.randn((heads * 16,), generator=gen(1), device="cuda", dtype=torch.float16) * 2.5
+    out, lse = torch.full_like(q, 7), torch.full((heads,), NAN, device="cuda")
+    at = [0, heads // 2, heads - n]
+    few.q.t.copy_(torch.cat([q[16 * a:16 * (a + n)] for a in at])[None])
+    for name in ("k", "v"):
+        getattr(few, name).t.copy_(getattr(c, name).t)
+    for name in ("ks", "vs", "table"):
+        getattr(few, name).copy_(getattr(c, name))
+    few.call()
+    few.check()
+    import blas_symmetric_mat_amd as X
+    X.xsymv_q8attn_h(1, heads, 1, 16, q, heads * 16, 1, None, c.len, c.table, c.ldt, 0, None, None, c.k.t, c.k.ld, c.ks,
+                     c.v.t, c.v.ld, c.vs, c.pages, c.ps, c.scale, out, heads * 16, lse)
+    torch.cuda.synchronize()
+    few.out.t.copy_(torch.cat([out[16 * a:16 * (a + n)] for a in at])[None])
+    few.lse.copy_(torch.cat([lse[a:a + n] for a in at])[None])
+    few.check()
+    left = int(lse.isnan().sum())
+    assert left == 0
