@@ -107,12 +107,14 @@ __global__ __launch_bounds__(PG_THREADS) void q8_pages_grow(PgGrowArgs a)
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS) {
         const int s = a.seq[i];
         before[i] = c.is_seq(s) ? c.length(s) : -1;
+        // (what a length out of range was is kept where the answer will be)
+        if (c.is_seq(s)) a.got[i] = c.len[s];
     }
     pg_claim(c, a.n, [&](int i) { return before[i] < 0 ? -1 : a.seq[i]; },
              [&](int i, bool yes) { start[i] = yes; });
     // the claims are off: every sequence has its length again
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS)
-        if (before[i] >= 0) c.len[a.seq[i]] = before[i];
+        if (before[i] >= 0) c.len[a.seq[i]] = a.got[i];
     __syncthreads();
     auto held = [&](long long tokens) { return (tokens + c.ps - 1) / c.ps; };
     long long sum = 0;
@@ -230,12 +232,14 @@ __global__ __launch_bounds__(PG_THREADS) void q8_pages_fork(PgForkArgs a)
         int n = -1;
         if (c.is_seq(p) && c.is_seq(s) && c.length(s) == 0) n = c.length(p);
         tokens[i] = n;
+        // (what a length below zero was is kept where the answer will be)
+        if (n >= 0) a.dst[i] = c.len[s];
     }
     pg_claim(c, a.n, [&](int i) { return tokens[i] < 0 ? -1 : a.child[i]; },
              [&](int i, bool yes) { page_of[i] = yes; });
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS) {
         if (tokens[i] < 0) continue;
-        c.len[a.child[i]] = 0;
+        c.len[a.child[i]] = a.dst[i];
         if (page_of[i] == 0) tokens[i] = -1;
     }
     __syncthreads();

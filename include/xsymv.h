@@ -501,7 +501,9 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   the table, their refs set to one, and its len raised; got[i] = add[i].
  *   A sequence that does not exist, that is listed before, whose tokens would not
  *   fit its row of the table, or for which not enough free pages are left behind
- *   those before it in the list, stays as it is: got[i] = 0.  Codes: -1 n < 0 or >
+ *   those before it in the list, stays as it is: got[i] = 0 (entries of its row
+ *   behind its pages may become -1).  While grow or fork runs, len of a sequence
+ *   that it lists (fork: as a child) may hold another number.  Codes: -1 n < 0 or >
  *   8192, -2 seq NULL, -3 add NULL, -4 seqs < 0, -5 len NULL, -6 table NULL, -7
  *   ldt < 0, -8 pages < 0, -9 ps < 1, -10 refs NULL, -11 got NULL.
  *

@@ -303,3 +303,41 @@ def test_timing_records_each_call(mode):
     assert len(rec) == 5 and all(a > 0 and b >= 0 for a, b in rec)
     if mode == 1:
         assert [b > 0 for _, b in rec] == [False, True, False, False, True]
+
+
+def test_refused_sequences_stay_as_they_are():
+    """Lengths out of range of sequences that grow or fork refuses stay what they are, also where a sequence is
+    listed twice; one that grows counts from none, or takes the place of an empty one."""
+    import torch
+    import blas_symmetric_mat_amd as X
+    seqs, ldt, pages, ps = 8, 3, 7, 4
+    table = torch.full((seqs, ldt), -1, dtype=torch.int32, device="cuda")
+    refs = ints([0] * pages)
+    big = 2000000000
+    length = ints([-5, big, -(2 ** 31), -9, 13, -1, 2 ** 31 - 1, 0])
+    got = ints([-9] * 9)
+    # 2: more than its row has room for; 3: grows; 6: has no room; 5: not enough pages are left
+    X.xsymv_q8pages_grow(9, ints([0, 1, 2, 2, 3, 4, 5, 6, 7]), ints([0, 1, 13, 1, 9, 1, 12, -1, 12]), seqs, length, table,
+                         ldt, pages, ps, refs, got)
+    torch.cuda.synchronize()
+    assert got.tolist() == [0, 0, 0, 0, 9, 0, 12, 0, 0]
+    assert length.tolist() == [-5, big, -(2 ** 31), 9, 13, 12, 2 ** 31 - 1, 0]
+    assert table[3].tolist() == [0, 1, 2] and table[5].tolist() == [3, 4, 5] and refs.tolist() == [1] * 6 + [0]
+    src, dst = ints([-9] * 7), ints([-9] * 7)
+    # 0 takes the last page; 2 finds none; 9 does not exist; 5 and 1 are not empty
+    X.xsymv_q8pages_fork(7, ints([3, 3, 3, 9, 3, 5, 5]), ints([0, 2, 2, 7, 5, 1, 9]), seqs, length, table, ldt, pages, ps,
+                         refs, src, dst)
+    torch.cuda.synchronize()
+    assert src.tolist() == [2, -2, -2, -2, -2, -2, -2] and dst.tolist() == [6, -2, -2, -2, -2, -2, -2]
+    assert length.tolist() == [9, big, -(2 ** 31), 9, 13, 12, 2 ** 31 - 1, 0]
+    assert table[0].tolist() == [0, 1, 6] and refs.tolist() == [2, 2, 1, 1, 1, 1, 1]
+    # many forks (tables in a launch of their own) of a sequence without a page left
+    n = 40
+    length, table = ints([6, -3] + [-i for i in range(n)]), torch.full((n + 2, 2), -1, dtype=torch.int32, device="cuda")
+    table[0] = ints([0, 1])
+    refs = ints([1, 1, 0])
+    src, dst = ints([-9] * n), ints([-9] * n)
+    X.xsymv_q8pages_fork(n, ints([0] * n), ints(list(range(2, n + 2))), n + 2, length, table, 2, 3, 4, refs, src, dst)
+    torch.cuda.synchronize()
+    assert src.tolist() == [1] + [-2] * (n - 1) and dst.tolist() == [2] + [-2] * (n - 1)
+    assert length.tolist() == [6, -3, 6] + [-i for i in range(1, n)] and refs.tolist() == [2, 1, 1]
