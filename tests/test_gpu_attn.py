@@ -647,3 +647,45 @@ def test_many_more_heads_than_a_block():
     few.check()
     left = int(lse.isnan().sum())
     assert left == 0
+
+
+def each_token(c):
+    """Keys of zeros, so that all tokens that a row sees have the same weight, whose sum is a whole number, and
+    values that are zero but for one code of 127 in each column, another token's in each: a column is
+    127 vs / (the tokens that the row sees), two roundings of it and the type's, or nothing.  Every token in turn."""
+    import torch
+    c.k.t.zero_()
+    c.vs.fill_(2.0 ** -6)
+    share, longest = c.heads // c.kvheads, max(c.lens)
+    for base in range(0, longest, c.hd * c.kvheads):
+        c.v.t.zero_()
+        token = base + torch.arange(c.kvheads * c.hd, device="cuda").view(c.kvheads, c.hd)
+        col = torch.arange(c.hd, device="cuda")
+        for i in range(c.seqs):
+            at, _ = c.places(i)
+            for h in range(c.kvheads):
+                some = token[h] < at.shape[1]
+                c.v.t[at[h, token[h][some]], col[some]] = 127
+        c.call()
+        torch.cuda.synchronize()
+        row = 0
+        for i, n in enumerate(c.counts):
+            limit = (c.lens[i] - n + 1 + torch.arange(n, device="cuda"))[:, None, None]
+            want = torch.where(token.repeat_interleave(share, 0) < limit, 127 * 2.0 ** -6 / limit.double(), 0.0)
+            got = c.out.t[row:row + n].reshape(n, c.heads, c.hd).double()
+            assert bool(((got - want).abs() <= want * (3 * U + half_step(c.t) * (1 + 3 * U))).all()), (base, i)
+            lse = limit[:, :, 0].double().log().expand(n, c.heads)
+            # (log l within a step and a half, and its rounding)
+            assert bool(((c.lse[row:row + n].double() - lse).abs() <= 4 * U * lse).all()), (base, i)
+            row += n
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("hd", [80, 256])
+def test_each_token_counts_once(t, hd):
+    """A sequence over all compute units, prompts, groups: no token of a piece's ends is lost or taken twice."""
+    each_token(Case(t, 8, 8, hd, 64, [12345]))
+    each_token(Case(t, 8, 8, hd, 16, [5000, 33, 700], [1, 1, 1], room=3))
+    each_token(Case(t, 16, 8, hd, 16, [3100, 900], [600, 333]))
+    each_token(Case(t, 32, 8, hd, 16, [2100 + 19 * i for i in range(9)], None, [(9, 2048)]))
+    each_token(Case(t, 16, 8, hd, 16, [1100 + 19 * i for i in range(5)], [7, 1, 40, 19, 2], [(2, 1024), (3, 800)]))
