@@ -233,3 +233,104 @@ def test_the_longest_row():
     assert index.tolist() == [[7, n - 1, 0]]
     assert abs(f[2].item() - lse) < 64 * U * lse and abs(f[0].item() - (5 - lse)) < 64 * U * lse
     assert all(abs(a - b) < 64 * U * lse for a, b in zip(value[0].tolist(), (5 - lse, 5 - lse, -lse)))
+
+
+def close(x, token, got):
+    """As `check`, with what the sums are in fact.  A row is shared by `parts` workgroups of 256 threads, which take
+    8 logits at a time: `loads` for a thread.  It adds the 8 by themselves, then to its sum; a workgroup's sums are
+    added in eight steps, the row's in six: no logit passes more than loads + 30 additions.  The reference is the
+    largest logit so far: a logit d below the row's is off by 3 u d + 2 u by its power and the reference's moves
+    together, and by 3 u more for each of these, at most loads and 15 in joining."""
+    import torch
+    v, n = x.t.double(), x.n
+    parts = max(1, min(1024 // x.m, -(-n // 2048), 64))  # (with lists of alternatives no fewer here)
+    loads = -(-n // (2048 * parts)) + 1
+    depth = loads + 30
+    m = v.amax(1)
+    d = m[:, None] - v
+    e = (-d).exp()
+    l = e.sum(1)
+    log_l = l.log()
+    some = e > 0
+    d = torch.where(some, d, 0.0)
+    rel = 3 * U * (d + loads + 15) + 2 * U
+    err_l = (e * rel).sum(1) / l + depth * U
+    # (logf within a step and a half)
+    tol = err_l + 3 * U * log_l
+    lse = m + log_l
+    assert bool(((got["lse"].double() - lse).abs() <= tol + U * (lse.abs() + tol)).all())
+    p = e / l[:, None]
+    ent = log_l + (p * d).sum(1)
+    err_s = (p * d * (rel + (depth + 4) * U)).sum(1) + (p * d).sum(1) * (err_l + 4 * U)
+    assert bool(((got["entropy"].double() - ent).abs() <= tol + err_s + U * ent).all())
+    want = v.gather(1, token.long()[:, None])[:, 0] - m - log_l
+    off = (got["logp"].double() - want).abs()
+    assert bool((off <= tol + 3 * U * want.abs()).all()), float((off - tol).max())
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m,n", [(1, 1), (3, 9), (1, 2047), (5, 2049), (1, 32000), (37, 50021), (1500, 2500), (1, 262147),
+                                 (9, 131072), (1100, 30001)])
+def test_sizes_closely(t, m, n):
+    import torch
+    x = logits(m, n, t, seed=n + 1)
+    token = torch.randint(0, n, (m,), generator=gen(m), device="cuda").to(torch.int32)
+    for top in sorted({min(n, k) for k in (0, 5)}):
+        close(x, token, call(x, t, token, top))
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m,n", [(1, 262147), (1200, 8200)])
+def test_rows_that_are_sure_of_a_token(t, m, n):
+    """Two logits, 0 and d, the second in a later load of the first one's thread; nothing else.  The reference moves to
+    the larger one, whose power is 1; the other's, below 0.78, is off by 2 u d + 5 u of itself, 5 u at most, its sum by
+    1, the logarithm, below 0.58, by 2 more; so the likely token's log probability is within 10 u, however near 0 it
+    is, the other's within 10 u and the rounding of a number as large as itself, and the entropy, which adds s / l
+    with the errors of its power, product, quotient and constant, within 20 u."""
+    import torch
+    x = Rows(m, n, dtype_of(t))
+    every = torch.linspace(0.25, 30.0, 240, device="cuda")
+    token = torch.full((m,), 2048, dtype=torch.int32, device="cuda")
+    for i in range(0, 240, 17 if m == 1 else 240):
+        x.t.fill_(-math.inf)
+        x.t[:, 0] = 0.0
+        x.t[:, 2048] = every[i] if m == 1 else every.repeat(m // 240)
+        d = x.t[:, 2048].double()
+        rest = torch.log1p((-d).exp())
+        for top in (0, 2):
+            token.fill_(2048)
+            got = call(x, t, token, top)
+            assert bool(((got["logp"].double() + rest).abs() <= 10 * U).all()), (got["logp"].double() + rest).abs().max() / U
+            assert bool(((got["lse"].double() - d - rest).abs() <= 10 * U + U * (d + 1)).all())
+            ent = rest + d * (-d - rest).exp()
+            assert bool(((got["entropy"].double() - ent).abs() <= 20 * U).all())
+            token.fill_(0)
+            got = call(x, t, token, top)
+            assert bool(((got["logp"].double() + d + rest).abs() <= 10 * U + U * (d + 1)).all())
+            if top:
+                assert bool(((got["value"][:, 0].double() + rest).abs() <= 10 * U).all())
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m,n", [(1, 40000), (2, 131073), (16, 70001), (300, 9001), (1500, 4099)])
+def test_each_logit_counts_once(t, m, n):
+    """Stretches of zeros, nothing else: l is the number of them exactly, lse and the entropy its logarithm (a step
+    and a half, and a rounding).  They begin and end around loads', workgroups' and parts' ends."""
+    import torch
+    parts = max(1, min(1024 // m, -(-n // 2048), 64))
+    each = -(-(-(-n // parts)) // 8) * 8
+    ends = sorted({min(n, max(0, a + d)) for a in range(0, n + each, each) for d in (-9, -1, 0, 1, 8)}
+                  | {min(n, 2048 * i + d) for i in range(0, 5) for d in (0, 7, 8)})
+    pairs = list(zip(ends, ends[1:])) + [(a, n) for a in ends if a < n] + [(0, b) for b in ends if b]
+    pairs += [pairs[-1]] * (-len(pairs) % m)
+    x = Rows(m, n, dtype_of(t))
+    token = torch.zeros((m,), dtype=torch.int32, device="cuda")
+    at = torch.arange(n, device="cuda")
+    for i in range(0, len(pairs), m):
+        lo, hi = (torch.tensor(v, device="cuda")[:, None] for v in zip(*pairs[i:i + m]))
+        x.t.copy_(torch.where((at >= lo) & (at < hi), 0.0, -math.inf))
+        token.copy_(hi[:, 0] - 1)
+        got = call(x, t, token, 0)
+        want = (hi - lo)[:, 0].double().log()
+        for k, sign in (("lse", 1), ("entropy", 1), ("logp", -1)):
+            assert bool(((sign * got[k].double() - want).abs() <= 4 * U * want).all()), k
