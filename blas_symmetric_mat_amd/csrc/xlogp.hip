@@ -24,8 +24,9 @@ size_t logp_bytes(int m, int parts, int top)
 template <class T>
 int logp_launch(LpArgs<T> a, int parts, void* ws, hipStream_t stream, const TimedCall& tc)
 {
-    a.each = (int)((((long long)a.n + parts - 1) / parts + 7) / 8 * 8);
-    a.parts = (int)(((long long)a.n + a.each - 1) / a.each);
+    // (a row without logits is one part too)
+    a.each = (int)std::max(8ll, (((long long)a.n + parts - 1) / parts + 7) / 8 * 8);
+    a.parts = (int)std::max(1ll, ((long long)a.n + a.each - 1) / a.each);
     a.sums = static_cast<LpSums*>(ws);
     a.keys = reinterpret_cast<lp_key*>(static_cast<char*>(ws) + align_up((size_t)a.m * parts * sizeof(LpSums)));
     const unsigned grid = (unsigned)std::min((long long)a.m * a.parts, 1ll << 20);
@@ -42,8 +43,8 @@ int logp_run(int m, int n, const T* x, int ldx, const int* token, float* logp, f
 {
     if (m < 0) return -1;
     if (n < 0 || n > LP_MOST) return -2;
-    const bool some = m > 0 && n > 0;
-    if (some && x == nullptr) return -3;
+    const bool some = m > 0;
+    if (some && n > 0 && x == nullptr) return -3;
     if (ldx < std::max(1, n)) return -4;
     if (some && token != nullptr && logp == nullptr) return -6;
     if (top < 0 || top > LP_TOP || (some && top > n)) return -9;

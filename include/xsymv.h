@@ -554,8 +554,9 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   and the lower index first of equal ones: index[i * ldt + r], value[i * ldt + r]
  *   = x - lse.  token (with logp), entropy, lse and value may be NULL; index only
  *   with top == 0.  Tokens of logit -infinity have no part in the entropy.  A row
- *   of these alone: lse, logp and value -infinity, entropy 0.  A row that holds a
- *   NaN or +infinity: NaN, and indexes of which only is said that they differ.
+ *   of these alone: lse, logp and value -infinity, entropy 0; one without tokens (n
+ *   == 0): lse -infinity, logp and entropy 0.  A row that holds a NaN or +infinity:
+ *   NaN, and indexes of which only is said that they differ.
  *   Uses the stream's workspace, up to xsymv_logp_workspace_bytes, as xsymv_q8attn_*
  *   does.  Codes: -1 m < 0, -2 n < 0 or > 2^31 - 4096, -3 x NULL, -4 ldx, -6 logp
  *   NULL with token, -9 top < 0, > n or > 128, -10 index NULL, -12 ldt < top, 2000.

@@ -334,3 +334,15 @@ def test_each_logit_counts_once(t, m, n):
         want = (hi - lo)[:, 0].double().log()
         for k, sign in (("lse", 1), ("entropy", 1), ("logp", -1)):
             assert bool(((sign * got[k].double() - want).abs() <= 4 * U * want).all()), k
+
+
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("m", [1, 3000])
+def test_rows_without_logits(t, m):
+    """Nothing is likely: every output is written."""
+    import torch
+    x = Rows(m, 0, dtype_of(t))
+    token = torch.zeros((m,), dtype=torch.int32, device="cuda")
+    got = call(x, t, token, 0)
+    assert bool((got["lse"] == -math.inf).all())
+    assert bool((got["logp"] == 0).all()) and bool((got["entropy"] == 0).all())

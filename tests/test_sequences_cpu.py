@@ -126,3 +126,13 @@ def test_the_model_by_hand():
     table, refs, src, dst, live = m.compact()
     assert (src, dst, live) == ([3, -1, -1], [1, -1, -1], 3) and refs == [1, 1, 2, 0, 0, 0]
     assert table[2][:2] == [0, 1]
+
+
+def test_rows_without_logits(way):
+    """They have outputs like others, and no alternatives."""
+    for entry in entries("logp"):
+        for change, code in ((dict(top=1), -9), (dict(top=0, logp=None), -6), (dict(top=0, ldx=0), -4)):
+            with pytest.raises(X.XsymvError) as e:
+                call(entry, "logp", **{"n": 0, "ldx": 1, "x": None, **change})
+            assert e.value.code == code
+        call(entry, "logp", m=0, n=0, ldx=1, x=None, token=None, logp=None, entropy=None, lse=None, index=None, value=None)
