@@ -173,7 +173,7 @@ class Q8Answers(Q8Layer):
         layer.step(x, r)     a token of each answer
         layer.free()         the answers end; fork may begin others
 
-    Each returns or raises as Q8Layer does."""
+    Each returns or raises as Q8Layer does, and a call that fails takes no room."""
 
     def __init__(self, d, heads, f, tokens, answers, page=16, seed=0, eps=1e-5):
         super().__init__(d, heads, f, tokens, seed, eps)
@@ -238,8 +238,24 @@ class Q8Answers(Q8Layer):
         add = torch.tensor([m], dtype=torch.int32, device=self.place.device)
         start = torch.tensor([0] + [m] * self.seqs, dtype=torch.int32, device=self.place.device)
         X.xsymv_q8pages_grow(1, self.zeros, add, *self._cache(), self.refs, self.got)
+        try:
+            out = self._layer(x, r, lambda qkv: self._answer(qkv, start, 0))
+        except BaseException:
+            self._shrink(0, 1)
+            raise
         self.used += m
-        return self._layer(x, r, lambda qkv: self._answer(qkv, start, 0))
+        return out
+
+    def _shrink(self, first, count):
+        """Sequences from `first` on give back the tokens that they were last grown by."""
+        import torch
+        n, table = self.len[first:first + count], self.table[first:first + count]
+        old = n - self.got[:count]
+        place = torch.arange(self.pages, device=n.device)
+        last = table[(place >= (old[:, None] + self.page - 1) // self.page)
+                     & (place < (n[:, None] + self.page - 1) // self.page)]
+        self.refs[last.long()] = 0
+        n.copy_(old)
 
     def fork(self):
         if self.forked:
@@ -248,9 +264,13 @@ class Q8Answers(Q8Layer):
         X.xsymv_q8pages_fork(self.answers, self.zeros, self.each, *self._cache(), self.refs, self.src, self.dst)
         rows = self.heads * self.page
         (k, ks), (v, vs) = self.kv
-        X.xsymv_q8pages_copy(self.answers, self.src, self.dst, self.pages, rows, self.hd, k, self.hd, ks,
-                             v, self.hd, vs, 1, self.pages * rows)
-        self.shared.fill_(self.used // self.page * self.page)
+        try:
+            X.xsymv_q8pages_copy(self.answers, self.src, self.dst, self.pages, rows, self.hd, k, self.hd, ks,
+                                 v, self.hd, vs, 1, self.pages * rows)
+            self.shared.fill_(self.used // self.page * self.page)
+        except BaseException:
+            X.xsymv_q8pages_free(self.answers, self.each, *self._cache(), self.refs)
+            raise
         self.more, self.forked = 0, True
 
     def step(self, x, r):
@@ -260,12 +280,25 @@ class Q8Answers(Q8Layer):
         if not self.forked:
             raise ValueError("the prompt has no answers")
         self._room(self.used, self.more + 1, True)
+        self._grow()
+        try:
+            out = self._next(x, r)
+        except BaseException:
+            self._shrink(1, self.answers)
+            raise
         self.more += 1
-        return self._step(x, r)
+        return out
+
+    def _grow(self):
+        X.xsymv_q8pages_grow(self.answers, self.each, self.ones, *self._cache(), self.refs, self.got)
+
+    def _next(self, x, r):
+        return self._layer(x, r, lambda qkv: self._answer(qkv, self.steps, 1))
 
     def _step(self, x, r):
-        X.xsymv_q8pages_grow(self.answers, self.each, self.ones, *self._cache(), self.refs, self.got)
-        return self._layer(x, r, lambda qkv: self._answer(qkv, self.steps, 1))
+        """What a step does on the device (for a graph of it, whose replays are not counted here)."""
+        self._grow()
+        return self._next(x, r)
 
     def free(self):
         if not self.forked:

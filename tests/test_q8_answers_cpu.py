@@ -5,6 +5,7 @@ import torch
 
 import blas_symmetric_mat_amd as X
 from blas_symmetric_mat_amd import q8_layer
+from tests.pages_model import Model
 from tests.test_q8_layer_cpu import D, F, HEADS, TOKENS, calls, rows  # noqa: F401
 
 ANSWERS, PAGE = 3, 2
@@ -101,3 +102,55 @@ def test_likely(calls, monkeypatch):  # noqa: F811
     assert index.shape == value.shape == (3, 7)
     assert names(calls) == ["xsymv_q8norm_b", "xsymv_q8gemm_b", "xsymv_logp_b"]
     assert (calls[-1][1][0], calls[-1][1][1], calls[-1][1][3], calls[-1][1][8]) == (3, 50, 50, 7)
+
+
+@pytest.fixture
+def pages(monkeypatch, calls):  # noqa: F811
+    """The calls that give and take pages do so, as the model does."""
+    def on(cache, name, *lists):
+        seqs, length, table, ldt, count, page, refs = cache
+        m = Model(seqs, ldt, count, page)
+        m.len, m.table, m.refs = length.tolist(), table.tolist(), refs.tolist()
+        out = getattr(m, name)(*(v.tolist() for v in lists))
+        length.copy_(torch.tensor(m.len)), table.copy_(torch.tensor(m.table)), refs.copy_(torch.tensor(m.refs))
+        return out
+
+    monkeypatch.setattr(X, "xsymv_q8pages_grow", lambda n, seq, add, *a: a[-1][:n].copy_(
+        torch.tensor(on(a[:-1], "grow", seq[:n], add[:n]))))
+
+    def fork(n, parent, child, *a):
+        for to, v in zip(a[-2:], on(a[:-2], "fork", parent[:n], child[:n])):
+            to[:n].copy_(torch.tensor(v))
+    monkeypatch.setattr(X, "xsymv_q8pages_fork", fork)
+    monkeypatch.setattr(X, "xsymv_q8pages_free", lambda n, seq, *a: on(a, "free", seq[:n]))
+
+
+def test_a_call_that_fails_takes_no_room(pages, monkeypatch):
+    """Where a later call cannot be made, pages, lengths and counts are what they were, and the same call works when it
+    can: a prompt that ends in a page and between, the fork of it, a step that fills pages and one that begins them."""
+    layer = make(tokens=32)
+
+    def state():
+        return layer.len.tolist(), layer.refs.tolist(), layer.used, layer.more, layer.forked
+
+    def fails(name, call):
+        before = state()
+        with monkeypatch.context() as m:
+            m.setattr(X, name, lambda *a: (_ for _ in ()).throw(X.XsymvError(name, 1002)))
+            for _ in range(2):
+                with pytest.raises(X.XsymvError):
+                    call()
+                assert state() == before
+        call()
+        assert state() != before
+
+    fails("xsymv_q8attn_b", lambda: layer.prompt(*tokens(1)))
+    fails("xsymv_q8glu_b", lambda: layer.prompt(*tokens(4)))
+    assert layer.len.tolist()[0] == layer.used == 5 and layer.refs.tolist() == [1] * 3 + [0] * 13
+    fails("xsymv_q8pages_copy", layer.fork)
+    assert layer.refs.tolist() == [4, 4] + [1] * 4 + [0] * 10
+    for name in ("xsymv_q8pages_slots", "xsymv_q8gemm_b", "xsymv_q8norm_b"):
+        fails(name, lambda: layer.step(*tokens(ANSWERS)))
+    assert layer.more == 3 and layer.len.tolist() == [5, 8, 8, 8] and layer.refs.tolist() == [4, 4] + [1] * 7 + [0] * 7
+    layer.free()
+    assert layer.refs.tolist() == [1] * 3 + [0] * 13 and layer.len.tolist() == [5, 0, 0, 0]
