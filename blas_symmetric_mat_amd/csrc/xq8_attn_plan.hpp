@@ -110,11 +110,12 @@ struct AtEntry {
     }
     __device__ __forceinline__ int slabs(const AtPlan& p) const { return joined ? blocks(p) * block_slabs(p) : 0; }
     static __device__ __forceinline__ int tiles(int tokens) { return (tokens + AT_TILE - 1) / AT_TILE; }
-    // length of the blocks before block b
+    // length of the blocks before block b, of an entry of the kernel's kind
+    template <bool WIDE>
     __device__ __forceinline__ int before_block(const AtPlan& p, int b) const
     {
         if (p.whole) return b;
-        if (!wide) return b * (AT_OVER + tiles(t1 - t0));
+        if constexpr (!WIDE) return b * (AT_OVER + tiles(t1 - t0));
         // (more rows than tokens, or heads of a row than a block: any block as one that sees all.
         // The sums below are of steps of whole tokens, of which such blocks have none or less
         // than one each, and no int would hold them: from 370000 blocks on.)
@@ -234,8 +235,8 @@ __device__ __forceinline__ AtEntry at_entry(const AtPlan& p, int e)
         x.before = x.t1 - 1;
     }
     x.wide = MIXED && x.rows > AT_NARROW;
-    x.cost = x.before_block(p, x.blocks(p));
     x.mine = MIXED ? x.wide == (KIND == AT_WIDE_JOBS) : 1;
+    x.cost = x.before_block<KIND == AT_WIDE_JOBS>(p, x.blocks(p));
     return x;
 }
 
@@ -458,12 +459,13 @@ struct AtCursor {
             if (WIDE)
                 for (int hi = of.blocks(p) - 1; b < hi;) {
                     const int mid = (b + hi + 1) / 2;
-                    if (of.before_block(p, mid) <= rest)
+                    if (of.template before_block<WIDE>(p, mid) <= rest)
                         b = mid;
                     else
                         hi = mid - 1;
                 }
-            const int c0 = WIDE ? of.before_block(p, b) : 0, c1 = WIDE ? of.before_block(p, b + 1) : of.cost;
+            const int c0 = WIDE ? of.template before_block<WIDE>(p, b) : 0;
+            const int c1 = WIDE ? of.template before_block<WIDE>(p, b + 1) : of.cost;
             const int x = rest - c0, y = min(x + end - pos, c1 - c0);
             // (starts that do not ascend: sums that no int holds)
             if ((unsigned)head >= (unsigned)p.kvheads || y <= x) return false;
