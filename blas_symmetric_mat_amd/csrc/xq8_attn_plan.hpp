@@ -30,9 +30,14 @@ constexpr int AT_LOW = 16, AT_HD = 256;  // least and widest head
 constexpr int AT_NARROW = 16;            // rows of a narrow job, and of a slab
 constexpr int AT_TILE = 32;              // tokens of a tile
 // Tiles that a job takes besides its own: a narrow one, a wide one (20 us for its rows
-// of q and its results, when a step of 128 tokens takes 7).
+// of q and its results, when a step of 128 tokens takes 7).  In us, one state of 32 heads
+// on 8 at a time (64 tokens behind 16384 shared ones and 600 each, 200 over 500 each; two
+// times 100 rows behind 4096): narrow 0, 3, 8: 85, 81, 84 and 45, 42, 46; wide 4, 12, 30:
+// 86, 81, 81 and 61, 58, 63.
 constexpr int AT_OVER = 3, AT_OVER_WIDE = 12;
-// A piece is so many tiles at least, for the join's sake (narrow, wide: a step).
+// A piece is so many tiles at least, for the join's sake (narrow, wide: a step).  Narrow
+// 1, 2, 6: one token over 1000 14.5, 15.2, 18.9, the 64 tokens 81, 81, 87; wide 4, 12: nine
+// sequences of 5 rows behind 1500 tokens 38, 48.
 constexpr int AT_LEAST = 2, AT_LEAST_WIDE = 4;
 // Entries of a call at most: windows of 64, of which LDS holds the sums.
 constexpr int AT_WINDOWS = 1024, AT_ENTRIES = 64 * AT_WINDOWS;
@@ -151,7 +156,12 @@ struct AtGroup {
         pays = false;
         if (tokens > 0 && count > 1 && rows > 0) {
             const long long one = (long long)((rows + count - 1) / count) * p.share;
-            // (a quarter less: rows that have two entries are added by the join)
+            // A quarter less, as rows that have two entries are added by the join.  Counted is
+            // work alone, so short stretches are shared though starts and ends then cost more
+            // than is saved: in us, never and always shared, 64 tokens behind 16384 276, 81;
+            // two and three behind 65536 56, 42 and 75, 42; but eight behind 4096 30, 37, nine
+            // sequences of 5 rows behind 1500 28, 37; prompts of 1024 rows, which the rule
+            // leaves alone, 690, 738.
             pays = work(p, (long long)rows * p.share) * 4 <= count * work(p, one) * 3;
         }
     }
@@ -174,7 +184,9 @@ struct AtGroup {
         }
         return best;
     }
-    // a wide job takes about twice as long as a narrow one with as many tokens
+    // A wide job counts as two narrow ones with as many tokens, which the times above bear out
+    // for long stretches.  (In a compute unit's time a tile of a full wide job is a quarter of 7
+    // us, one of a narrow job 0.3 us where memory is the bound.)
     static __device__ __forceinline__ long long work(const AtPlan& p, long long rows)
     {
         return rows <= AT_NARROW ? 1 : (rows + p.wide_rows() - 1) >> p.wide_log << 1;
