@@ -13,8 +13,14 @@ struct PgCache {
     // tokens of sequence s, as far as its row of the table can hold them
     __device__ __forceinline__ int length(int s) const
     {
+        int n;
+        return length(s, n);
+    }
+    // (n: what len holds)
+    __device__ __forceinline__ int length(int s, int& n) const
+    {
         const long long room = (long long)ldt * ps;
-        const int n = __hip_atomic_load(&len[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        n = __hip_atomic_load(&len[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         return n < 0 ? 0 : n > room ? (int)room : n;
     }
     __device__ __forceinline__ int* row(int s) const { return table + (size_t)s * ldt; }

@@ -100,21 +100,20 @@ struct PgGrowArgs {
 
 __global__ __launch_bounds__(PG_THREADS) void q8_pages_grow(PgGrowArgs a)
 {
-    // tokens before, of those that grow (-1: left as it is); pages of those before it
-    __shared__ int before[PG_MOST], start[PG_MOST + 1], waves[PG_THREADS / 64];
+    // tokens before, of those that grow (-1: left as it is); pages of those before it;
+    // what the lengths are, in range or not
+    __shared__ int before[PG_MOST], start[PG_MOST + 1], was[PG_MOST], waves[PG_THREADS / 64];
     __shared__ long long wide[PG_THREADS / 64];
     const PgCache& c = a.c;
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS) {
         const int s = a.seq[i];
-        before[i] = c.is_seq(s) ? c.length(s) : -1;
-        // (what a length out of range was is kept where the answer will be)
-        if (c.is_seq(s)) a.got[i] = c.len[s];
+        before[i] = c.is_seq(s) ? c.length(s, was[i]) : -1;
     }
     pg_claim(c, a.n, [&](int i) { return before[i] < 0 ? -1 : a.seq[i]; },
              [&](int i, bool yes) { start[i] = yes; });
     // the claims are off: every sequence has its length again
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS)
-        if (before[i] >= 0) c.len[a.seq[i]] = a.got[i];
+        if (before[i] >= 0) c.len[a.seq[i]] = was[i];
     __syncthreads();
     auto held = [&](long long tokens) { return (tokens + c.ps - 1) / c.ps; };
     long long sum = 0;
@@ -225,21 +224,19 @@ __device__ __forceinline__ void pg_inherit(const PgCache& c, int parent, int chi
 
 __global__ __launch_bounds__(PG_THREADS) void q8_pages_fork(PgForkArgs a)
 {
-    __shared__ int tokens[PG_MOST], page_of[PG_MOST], waves[PG_THREADS / 64];
+    __shared__ int tokens[PG_MOST], page_of[PG_MOST], was[PG_MOST], waves[PG_THREADS / 64];
     const PgCache& c = a.c;
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS) {
         const int p = a.parent[i], s = a.child[i];
         int n = -1;
-        if (c.is_seq(p) && c.is_seq(s) && c.length(s) == 0) n = c.length(p);
+        if (c.is_seq(p) && c.is_seq(s) && c.length(s, was[i]) == 0) n = c.length(p);
         tokens[i] = n;
-        // (what a length below zero was is kept where the answer will be)
-        if (n >= 0) a.dst[i] = c.len[s];
     }
     pg_claim(c, a.n, [&](int i) { return tokens[i] < 0 ? -1 : a.child[i]; },
              [&](int i, bool yes) { page_of[i] = yes; });
     for (int i = threadIdx.x; i < a.n; i += PG_THREADS) {
         if (tokens[i] < 0) continue;
-        c.len[a.child[i]] = a.dst[i];
+        c.len[a.child[i]] = was[i];
         if (page_of[i] == 0) tokens[i] = -1;
     }
     __syncthreads();
