@@ -649,6 +649,32 @@ def test_many_more_heads_than_a_block():
     assert left == 0
 
 
+@pytest.mark.parametrize("t", LETTERS)
+@pytest.mark.parametrize("hd", [64, 128, 200, 256])
+@pytest.mark.parametrize("how", ["any", "rising", "falling", "steps"])
+def test_scales_that_differ_from_token_to_token(t, hd, how):
+    """Values' scales from 2^-30 to 2^8 times the usual in any order, each larger than the one before (so that every
+    token of a step in which rows end begins another stretch), smaller, in blocks, with zeros: every row is as close
+    as the scales that it sees allow."""
+    import torch
+    for lens, counts, groups in (([300, 90], [300, 90], ()), ([700, 333], [400, 150], ()), ([100, 33], [6, 3], ()),
+                                 ([200, 215, 30, 230], [12, 12, 5, 12], [(4, 192)]), ([900, 150], [100, 1], ())):
+        c = Fine(t, 8, 2, hd, 16, lens, counts, groups, seed=hd + len(lens))
+        for i, n in reversed(list(enumerate(lens))):
+            at = torch.arange(n, device="cuda") / max(n - 1, 1)
+            if how == "any":
+                e = torch.rand((n,), generator=gen(i), device="cuda")
+            else:
+                e = {"rising": at, "falling": 1 - at, "steps": (at * 9.99).floor() / 9}[how]
+            scale = 0.02 * (e * 38 - 30).exp2()
+            if how == "any":
+                scale[::13] = 0
+            places, _ = c.places(i)
+            c.vs[places] = scale.expand_as(places)
+        c.call()
+        c.check()
+
+
 def each_token(c):
     """Keys of zeros, so that all tokens that a row sees have the same weight, whose sum is a whole number, and
     values that are zero but for one code of 127 in each column, another token's in each: a column is
