@@ -10,7 +10,7 @@
 // from below, and only the few threads that hold one above it read theirs again.
 //
 // Bound by the reads where rows are many and long: 2048 rows of 131072 bfloat16
-// logits in 101 us, 5.4 TB/s, the sums' some nine instructions a logit behind
+// logits in 100 us, 5.5 TB/s, the sums' some nine instructions a logit behind
 // them (at eleven, with room for five waves a SIMD instead of eight, 129 us).  A
 // single row of 32000 is dealt over 16 workgroups; the rest of its 11 us is the
 // two launches and what each does one after the other.
@@ -114,8 +114,8 @@ __device__ __forceinline__ void lp_load(const T* x, int have, float (&v)[8])
 
 // Adds eight logits.  c follows each larger one: results are differences of log l and
 // a logit's distance from c, which are near 0 for a row that is sure of its token, and
-// keep their bits if c is its logit (20 below it they were off by 1e-6 or more; following
-// late is no faster, 2048 rows of 131072 in 101 us, and 100 so).  The eight are summed by
+// keep their bits if c is its logit (with c up to 20 below they were off by 2e-6;
+// following late is no faster, 2048 rows of 131072 in 101 us, and 100 so).  The eight are summed by
 // themselves first: a sum of n in this order is off by some n / 8 + 8 roundings.
 __device__ __forceinline__ float lp_take(LpSums& a, const float (&v)[8])
 {

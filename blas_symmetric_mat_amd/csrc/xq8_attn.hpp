@@ -32,15 +32,17 @@
 //   narrow jobs (up to 16 rows of q: single tokens): a wave takes 32 tokens at a
 //     time, whose codes come from memory to the registers that the instruction reads
 //     them from.  Waves work by themselves.  Bound by the cache's bytes: two rows of
-//     32 heads on 8, 131072 tokens each (406 MB), in 79 us, 5.2 TB/s (the call took
+//     32 heads on 8, 131072 tokens each (406 MB), in 78 us, 5.2 TB/s (the call took
 //     152 where a workgroup shared such a job, 120 with a wave each, 88 without a
 //     launch for wide jobs and with sixteen waves in the join).
 //   wide jobs (up to 256 rows: a group's tokens, prompts): each wave of a workgroup
 //     has 16 or 32 rows and every token; the waves make operands of 16 tokens each
 //     and share them through LDS, so that codes are converted once for all rows.
-//     Bound by the vector ALU (60 % busy) and the matrix cores (29 %), which take turns:
-//     4 x 1024 rows of 32 heads behind 8192 shared tokens in 0.67 ms, 680 T/s.  With
-//     128 rows on four waves it was 895 us; wide and narrow jobs in one kernel, 1475.
+//     4 x 1024 rows of 32 heads behind 8192 shared tokens in 0.67 ms, 680 T/s.  The vector
+//     ALU is busy 59 % of the time and the matrix cores 28 % (in runs of 0.72 ms, with
+//     counters): neither is full, as one follows on the other's results and a SIMD has two
+//     waves to overlap.  With 128 rows on four waves it was 895 us; wide and narrow jobs in
+//     one kernel, 1475.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -627,8 +629,8 @@ struct AtWide {
     // twice as much for its rows.  Two tiles of rows a wave where registers hold them, one
     // where not (float's two numbers over 64 codes, others over 128), and over 128 codes
     // LDS for one buffer.  4 x 1024 rows behind 8192 tokens, with four waves of two tiles
-    // and as it is: bfloat16 of 128 codes 895 us and 668, of 256 4521 and 1608; float of
-    // 64 codes 1234 and 638, of 128 1827 and 1218 (two tiles on eight waves: spilled).
+    // and as it is: bfloat16 of 128 codes 895 us and 669, of 256 4521 and 1570; float of
+    // 64 codes 1234 and 655, of 128 1827 and 1185 (two tiles on eight waves: spilled).
     static constexpr int WAVES = 8, STEP = 16 * WAVES;
     static constexpr int TILES = HD <= (SPLIT ? 64 : 128) ? 2 : 1, BUFFERS = HD <= 128 ? 2 : 1, ROWS = STEP * TILES;
     struct Step {

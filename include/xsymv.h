@@ -479,7 +479,9 @@ int xsymv_q8gemm_b(int m, int n, int k, const signed char *a, int lda, const flo
  *   them, from 0): a row sees the tokens up to its own.  Head h of row r is at
  *   q[r * ldq + h * hd] and out[r * ldo + h * hd], and at lse[r * heads + h] (lse
  *   NULL: not kept).  Tokens whose page is outside [0, pages) are passed over; a
- *   row that sees none gets zeros and -infinity.  16 <= hd <= 256.
+ *   row that sees none gets zeros and -infinity.  Scales of tokens that a row does
+ *   not see mean nothing to it, whatever they are; in vs 2^120 and more count as no
+ *   numbers.  16 <= hd <= 256.
  *   Sequences first[g] to first[g + 1] - 1 (groups + 1 ascending numbers from 0
  *   to seqs) have their first shared[g] tokens in common: their rows of the table
  *   name the same pages there, as far as each one's len goes (one that has ended may
